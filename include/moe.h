@@ -159,6 +159,56 @@ MOE_API int moe_route_grouped(const moe_shape_t* shape, int T, int n_groups, int
                               const void* w_router, const float* bias, const float* logits_in, float* logits_out,
                               int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- scored routing
+ * Routing whose scores, selection and weights are separate steps (the form of
+ * routers trained without an auxiliary balance loss).
+ *   score      s[t,e] = sigmoid(l[t,e]) or softmax over all E logits;
+ *   selection  c[t,e] = s[t,e] + select_bias[e] (select_bias NULL: 0).  With
+ *              topk_groups < n_groups the E experts form n_groups contiguous
+ *              groups; a group scores its largest c (MOE_GROUP_MAX) or the sum of
+ *              its two largest (MOE_GROUP_TOP2; its largest where a second is
+ *              missing or masked); the best topk_groups groups are kept (ties ->
+ *              lower group).  topk_idx[t,0..k-1]: the k largest c of the kept
+ *              groups, descending, ties -> lower expert.  The bias moves the
+ *              selection and never the weights.  Orders are those of the exact
+ *              values: where fp32 cannot tell two c apart they are compared in
+ *              fp64.
+ *   weight     topk_w[t,j] = scale * s_j, or with renormalize scale * s_j / sum_i s_i
+ *              over the selected (computed relative to the largest, so a row of
+ *              tiny scores keeps its ratios).
+ * A logit of -inf or NaN masks its expert: score 0, selected only when fewer
+ * than k others remain in the kept groups (then the lowest masked experts of
+ * those groups), weight 0.  A row with no unmasked expert gets weights 0.
+ * x, w_router, logits_in, logits_out, outputs and workspace as moe_route (there
+ * is no bias on the logits).  Limits: those of moe_route_grouped. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2 1
+typedef struct {
+    int32_t score;        /* MOE_SCORE_* */
+    int32_t n_groups;     /* 1: no groups */
+    int32_t topk_groups;
+    int32_t group_score;  /* MOE_GROUP_* */
+    int32_t renormalize;  /* 0 | 1 */
+    float scale;          /* finite */
+} moe_router_t;
+MOE_API int moe_route_scored(const moe_shape_t* shape, const moe_router_t* router, int T, const void* x,
+                             const void* w_router, const float* select_bias, const float* logits_in,
+                             float* logits_out, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* Gradient of topk_w with respect to the logits, the selection held fixed
+ * (select_bias has none).  logits [T,E] fp32 as used by moe_route_scored,
+ * topk_idx [T,k] its selection, d_topk_w [T,k] fp32; d_logits [T,E] fp32 is
+ * written whole (zeros where there is no gradient; masked logits get 0).
+ *   d_s_j = scale * d_w_j, or scale / S * (d_w_j - sum_i d_w_i s_i / S);
+ *   sigmoid: d_l_j = d_s_j s_j (1 - s_j);  softmax: d_l_e = s_e (d_s_e - sum_i d_s_i s_i).
+ * An id outside [0, E) sets the device status and contributes nothing. */
+MOE_API int moe_route_scored_backward(const moe_shape_t* shape, const moe_router_t* router, int T,
+                                      const float* logits, const int32_t* topk_idx, const float* d_topk_w,
+                                      float* d_logits, void* stream);
+
 /* ---------------------------------------------------------------- EPLB monitor
  * "专家并行(EP)" section 6.2 ("monitor": tokens arriving at each expert; a
  * rank's load = sum over its experts) for one batch, and section 6.3 (a token

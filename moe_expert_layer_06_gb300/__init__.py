@@ -40,7 +40,14 @@ EXPORTS = (
     "moe_eplb_copy_replicas", "moe_quantize_rows_fp8", "moe_dispatch_fp8", "moe_expert_gate_up_fp8",
     "moe_workspace_size_fp8", "moe_forward_fp8", "moe_expert_down_fp8", "moe_dispatch_workspace_size",
     "moe_expert_down_fp8_payload", "moe_combine_fp8", "moe_ep_plan", "moe_gather_rows",
+    "moe_route_scored", "moe_route_scored_backward",
 )
+
+# router scores and group scores of moe_route_scored
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
 
 # columns per scale of the E4M3 combine payload (MOE_PAYLOAD_BLOCK in include/moe.h)
 MOE_PAYLOAD_BLOCK = 128
@@ -65,6 +72,16 @@ class Shape(ctypes.Structure):
         return cls(w.hidden, w.inter, w.n_experts, w.top_k, w.n_shared, w.inter_shared, w.n_slots, w.n_blocks)
 
 
+class Router(ctypes.Structure):
+    """How moe_route_scored scores, selects and weights (moe_router_t)."""
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    def __init__(self, score=MOE_SCORE_SIGMOID, n_groups=1, topk_groups=1, group_score=MOE_GROUP_TOP2, renormalize=1,
+                 scale=1.0):
+        super().__init__(score, n_groups, topk_groups, group_score, renormalize, scale)
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
@@ -79,6 +96,8 @@ _SIG = {
     "moe_route_workspace_size": (_Z, [_P, _I]),
     "moe_route": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "moe_route_grouped": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_route_scored": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_route_scored_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _P]),
     "moe_expert_histogram": (_I, [_P, _I, _P, _P, _P, _P, _P]),
     "moe_eplb_imbalance": (ctypes.c_double, [_P, _I]),
     "moe_eplb_window_bytes": (_Z, [_P, _I]),
@@ -198,6 +217,33 @@ def moe_route_grouped(shape, T, n_groups, topk_groups, x, w_router, bias, logits
     _check(lib().moe_route_grouped(_shape(shape), T, n_groups, topk_groups, _ptr(x), _ptr(w_router), _ptr(bias),
                                    _ptr(logits_in), _ptr(logits_out), _ptr(topk_idx), _ptr(topk_w), _ptr(ws),
                                    ws_bytes, _stream(stream)))
+
+
+def _dense(t, name, shape, dtype):
+    """Pointer of a device tensor whose sizes and type are checked (None passes)."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return _ptr(t)
+
+
+def moe_route_scored(shape, router, T, x, w_router, select_bias, logits_in, logits_out, topk_idx, topk_w, ws=None,
+                     stream=None):
+    E, k, f32 = shape.n_experts, shape.top_k, torch.float32
+    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(lib().moe_route_scored(
+        _shape(shape), ctypes.byref(router), T, _dense(x, "x", (T, shape.hidden), torch.bfloat16),
+        _dense(w_router, "w_router", (E, shape.hidden), torch.bfloat16), _dense(select_bias, "select_bias", (E,), f32),
+        _dense(logits_in, "logits_in", (T, E), f32), _dense(logits_out, "logits_out", (T, E), f32),
+        _dense(topk_idx, "topk_idx", (T, k), torch.int32), _dense(topk_w, "topk_w", (T, k), f32), _ptr(ws), ws_bytes,
+        _stream(stream)))
+
+
+def moe_route_scored_backward(shape, router, T, logits, topk_idx, d_topk_w, d_logits, stream=None):
+    E, k, f32 = shape.n_experts, shape.top_k, torch.float32
+    _check(lib().moe_route_scored_backward(
+        _shape(shape), ctypes.byref(router), T, _dense(logits, "logits", (T, E), f32),
+        _dense(topk_idx, "topk_idx", (T, k), torch.int32), _dense(d_topk_w, "d_topk_w", (T, k), f32),
+        _dense(d_logits, "d_logits", (T, E), f32), _stream(stream)))
 
 
 def moe_expert_histogram(shape, T, topk_idx, replica_of, counts, block_counts, stream=None):

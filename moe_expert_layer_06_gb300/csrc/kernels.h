@@ -209,5 +209,12 @@ int num_sms();
 // outside moe_api.cu.
 int api_fail(int code, const char* fmt, ...);
 int api_check_shape(const moe_shape_t* shape, int T);
+int api_device_status(DevStatus* st);
+// The router GEMM into ws (checked against moe_route_workspace_size): *ksplit partial
+// logits [ksplit][T][E], to be added in order.
+int api_router_gemm(const moe_shape_t* shape, int T, const void* x, const void* w_router, void* ws, size_t ws_bytes,
+                    int* ksplit, cudaStream_t stream);
+// Pointer checks: 0, or the error code with its text set.
+int api_need(const void* p, const char* name, unsigned align = 16);
 
 }  // namespace moe

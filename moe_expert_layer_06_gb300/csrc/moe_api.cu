@@ -248,6 +248,31 @@ static size_t route_ws(const moe_shape_t* s, int T) {
     return align256(need);
 }
 
+// The router GEMM: *ksplit K-split partial logits [ksplit][T][E] in ws (route_ws bytes).
+static int router_gemm(const moe_shape_t* s, int T, const void* x, const void* w_router, void* ws, const DevStatus& st,
+                       int* ksplit, cudaStream_t stream) {
+    const RoutePlan p = route_plan(s, T);
+    GemmArgs g;
+    memset(&g, 0, sizeof g);
+    if (int rc = tmap_weights(&g.a0, w_router, 1, s->n_experts, s->hidden)) return rc;
+    if (int rc = tmap_rows(g.b, x, T, s->hidden)) return rc;
+    g.a1 = g.a0;
+    g.sa0 = g.sa1 = g.a0;
+    for (int j = 0; j < 4; ++j) g.sb[j] = g.b[j];
+    g.T = T;
+    g.m_routed = s->n_experts;
+    g.kc_routed = (s->hidden + 63) / 64;
+    g.ksplit = p.ksplit;
+    g.kc_split = p.kc_split;
+    g.out = ws;
+    g.out_ld = s->n_experts;
+    g.st = st;
+    const int items = p.tiles * p.ksplit;
+    MOE_CUDA(launch_gemm(kRouter, p.bn, g, std::min(items, num_sms()), stream), "router gemm launch");
+    *ksplit = p.ksplit;
+    return MOE_OK;
+}
+
 static int route_impl(const moe_shape_t* s, int T, int n_groups, int topk_groups, const void* x,
                       const void* w_router, const float* bias, const float* logits_in, float* logits_out,
                       int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, cudaStream_t stream) {
@@ -274,25 +299,9 @@ static int route_impl(const moe_shape_t* s, int T, int n_groups, int topk_groups
                  "topk launch");
         return MOE_OK;
     }
-    const RoutePlan p = route_plan(s, T);
-    GemmArgs g;
-    memset(&g, 0, sizeof g);
-    if ((rc = tmap_weights(&g.a0, w_router, 1, s->n_experts, s->hidden))) return rc;
-    if ((rc = tmap_rows(g.b, x, T, s->hidden))) return rc;
-    g.a1 = g.a0;
-    g.sa0 = g.sa1 = g.a0;
-    for (int j = 0; j < 4; ++j) g.sb[j] = g.b[j];
-    g.T = T;
-    g.m_routed = s->n_experts;
-    g.kc_routed = (s->hidden + 63) / 64;
-    g.ksplit = p.ksplit;
-    g.kc_split = p.kc_split;
-    g.out = ws;
-    g.out_ld = s->n_experts;
-    g.st = st;
-    const int items = p.tiles * p.ksplit;
-    MOE_CUDA(launch_gemm(kRouter, p.bn, g, std::min(items, num_sms()), stream), "router gemm launch");
-    MOE_CUDA(launch_topk(static_cast<const float*>(ws), p.ksplit, bias, T, s->n_experts, s->top_k, logits_out,
+    int ksplit;
+    if ((rc = router_gemm(s, T, x, w_router, ws, st, &ksplit, stream))) return rc;
+    MOE_CUDA(launch_topk(static_cast<const float*>(ws), ksplit, bias, T, s->n_experts, s->top_k, logits_out,
                          topk_idx, topk_w, n_groups, topk_groups, st, stream),
              "topk launch");
     return MOE_OK;
@@ -704,6 +713,25 @@ int api_fail(int code, const char* fmt, ...) {
 }
 
 int api_check_shape(const moe_shape_t* shape, int T) { return check_shape(shape, T); }
+
+int api_need(const void* p, const char* name, unsigned align) {
+    if (!p) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) & (align - 1))
+        return fail(MOE_ERR_INVALID_ARG, "%s is not %u-byte aligned", name, align);
+    return MOE_OK;
+}
+
+int api_device_status(DevStatus* st) { return device_status(st); }
+
+int api_router_gemm(const moe_shape_t* s, int T, const void* x, const void* w_router, void* ws, size_t ws_bytes,
+                    int* ksplit, cudaStream_t stream) {
+    const size_t need = route_ws(s, T);
+    if (!ws || ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "route workspace %zu < %zu bytes", ws_bytes, need);
+    if (!aligned16(ws)) return fail(MOE_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    DevStatus st;
+    if (int rc = device_status(&st)) return rc;
+    return router_gemm(s, T, x, w_router, ws, st, ksplit, stream);
+}
 
 }  // namespace moe
 
