@@ -483,6 +483,44 @@ MOE_API int moe_ep_plan(const moe_shape_t* shape, int world, const int32_t* coun
 MOE_API int moe_gather_rows(int n_rows, int row_bytes, const void* src, const int32_t* index, void* dst,
                             void* stream);
 
+/* ---------------------------------------------------------------- low-rank adapters
+ * One projection W [N,K] shared by a whole batch, and beside it the low-rank
+ * adapter (A_i [r,K], B_i [N,r]) of each token's request: serving many tenants
+ * from one set of weights, and training adapters on frozen weights.
+ *   i = adapter_of[t] (-1: no adapter)
+ *   v[t] = bf16(scaling[i] * A_i x[t])          (0 without an adapter)
+ *   out[t] = W x[t] + B_i v[t]                  (fp32 accumulation, one rounding)
+ * Tokens may come in any order; a batch whose requests are runs of consecutive
+ * tokens, or of few tokens each, is what the kernels are fast for.
+ * x [T,K]; w [N,K]; a [n_adapters,r,K]; b [n_adapters,N,r]; scaling
+ * [n_adapters] fp32 or NULL (1); adapter_of [T] int32; out [T,N] bf16, or fp32
+ * with out_fp32 = 1 (the y_shared that moe_combine takes); v_out [T,r] bf16 or
+ * NULL receives v, which the backward pass reads.  All others bf16.
+ * An id outside [-1, n_adapters) sets the device status and counts as -1.
+ * moe_adapter_project_backward: W has no gradient,
+ *   dv[t] = bf16(scaling[i] * B_i^T dy[t]),  dx[t] = W^T dy[t] + A_i^T dv[t],
+ *   da_i = sum over i's tokens of dv[t] x[t]^T,  db_i = the same of dy[t] v[t]^T.
+ * dx [T,K], da [n_adapters,r,K], db [n_adapters,N,r] bf16, written whole (zeros
+ * for an adapter without tokens); dx may be NULL, and so may da and db together
+ * (x and v are then not read).  T = 0 writes zeros to da and db.  Sums run in an
+ * order that the sizes alone fix: results repeat bit for bit.
+ * ws: device scratch of moe_adapter_workspace_size() bytes (it serves both
+ * directions).  Limits: K, N and r multiples of 8, r <= 256, n_adapters <= 4096. */
+typedef struct {
+    int32_t in_features;   /* K */
+    int32_t out_features;  /* N */
+    int32_t n_adapters;
+    int32_t rank;          /* r */
+} moe_adapter_t;
+MOE_API size_t moe_adapter_workspace_size(const moe_adapter_t* adapter, int T);
+MOE_API int moe_adapter_project(const moe_adapter_t* adapter, int T, const void* x, const void* w, const void* a,
+                                const void* b, const float* scaling, const int32_t* adapter_of, void* out,
+                                int out_fp32, void* v_out, void* ws, size_t ws_bytes, void* stream);
+MOE_API int moe_adapter_project_backward(const moe_adapter_t* adapter, int T, const void* dy, const void* x,
+                                         const void* w, const void* a, const void* b, const float* scaling,
+                                         const int32_t* adapter_of, const void* v, void* dx, void* da, void* db,
+                                         void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- whole layer
  * moe_route (from x), moe_dispatch, moe_expert_ffn, moe_combine on one stream
  * (7 kernel launches; capturable in a CUDA graph).  Intermediates live in the

@@ -40,7 +40,8 @@ EXPORTS = (
     "moe_eplb_copy_replicas", "moe_quantize_rows_fp8", "moe_dispatch_fp8", "moe_expert_gate_up_fp8",
     "moe_workspace_size_fp8", "moe_forward_fp8", "moe_expert_down_fp8", "moe_dispatch_workspace_size",
     "moe_expert_down_fp8_payload", "moe_combine_fp8", "moe_ep_plan", "moe_gather_rows",
-    "moe_route_scored", "moe_route_scored_backward",
+    "moe_route_scored", "moe_route_scored_backward", "moe_adapter_workspace_size", "moe_adapter_project",
+    "moe_adapter_project_backward",
 )
 
 # router scores and group scores of moe_route_scored
@@ -82,6 +83,11 @@ class Router(ctypes.Structure):
         super().__init__(score, n_groups, topk_groups, group_score, renormalize, scale)
 
 
+class Adapter(ctypes.Structure):
+    """Sizes of a shared projection and the low-rank adapters beside it (moe_adapter_t)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "n_adapters", "rank")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
@@ -98,6 +104,9 @@ _SIG = {
     "moe_route_grouped": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "moe_route_scored": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "moe_route_scored_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _P]),
+    "moe_adapter_workspace_size": (_Z, [_P, _I]),
+    "moe_adapter_project": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _Z, _P]),
+    "moe_adapter_project_backward": (_I, [_P, _I] + [_P] * 12 + [_Z, _P]),
     "moe_expert_histogram": (_I, [_P, _I, _P, _P, _P, _P, _P]),
     "moe_eplb_imbalance": (ctypes.c_double, [_P, _I]),
     "moe_eplb_window_bytes": (_Z, [_P, _I]),
@@ -244,6 +253,35 @@ def moe_route_scored_backward(shape, router, T, logits, topk_idx, d_topk_w, d_lo
         _shape(shape), ctypes.byref(router), T, _dense(logits, "logits", (T, E), f32),
         _dense(topk_idx, "topk_idx", (T, k), torch.int32), _dense(d_topk_w, "d_topk_w", (T, k), f32),
         _dense(d_logits, "d_logits", (T, E), f32), _stream(stream)))
+
+
+def moe_adapter_workspace_size(adapter, T: int) -> int:
+    return lib().moe_adapter_workspace_size(ctypes.byref(adapter), T)
+
+
+def moe_adapter_project(adapter, T, x, w, a, b, scaling, adapter_of, out, v_out=None, ws=None, stream=None):
+    K, N, n, r = adapter.in_features, adapter.out_features, adapter.n_adapters, adapter.rank
+    bf16 = torch.bfloat16
+    fp32 = out is not None and out.dtype == torch.float32
+    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(lib().moe_adapter_project(
+        ctypes.byref(adapter), T, _dense(x, "x", (T, K), bf16), _dense(w, "w", (N, K), bf16),
+        _dense(a, "a", (n, r, K), bf16), _dense(b, "b", (n, N, r), bf16),
+        _dense(scaling, "scaling", (n,), torch.float32), _dense(adapter_of, "adapter_of", (T,), torch.int32),
+        _dense(out, "out", (T, N), torch.float32 if fp32 else bf16), int(fp32), _dense(v_out, "v_out", (T, r), bf16),
+        _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_adapter_project_backward(adapter, T, dy, x, w, a, b, scaling, adapter_of, v, dx, da, db, ws=None, stream=None):
+    K, N, n, r = adapter.in_features, adapter.out_features, adapter.n_adapters, adapter.rank
+    bf16 = torch.bfloat16
+    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(lib().moe_adapter_project_backward(
+        ctypes.byref(adapter), T, _dense(dy, "dy", (T, N), bf16), _dense(x, "x", (T, K), bf16),
+        _dense(w, "w", (N, K), bf16), _dense(a, "a", (n, r, K), bf16), _dense(b, "b", (n, N, r), bf16),
+        _dense(scaling, "scaling", (n,), torch.float32), _dense(adapter_of, "adapter_of", (T,), torch.int32),
+        _dense(v, "v", (T, r), bf16), _dense(dx, "dx", (T, K), bf16), _dense(da, "da", (n, r, K), bf16),
+        _dense(db, "db", (n, N, r), bf16), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def moe_expert_histogram(shape, T, topk_idx, replica_of, counts, block_counts, stream=None):
