@@ -4,7 +4,12 @@
 //   s_e = sigmoid(l_e) | softmax(l)_e,  c_e = s_e + b_e,
 //   idx = top-k of c over the best groups,  w_j = scale * s_j [/ sum_i s_i].
 //
-// One warp per token.
+// One warp per token.  Lane maxima give a threshold that few logits pass; those
+// candidates are ranked against one another, so the cost hardly grows with k.
+// The selection is made on fp32 values whose error is bounded; a row where two
+// values that decide the selection or its order lie within that bound of one
+// another is decided again in fp64 (about one row in a thousand).
+#include <float.h>
 #include <math.h>
 
 #include "kernels.h"
@@ -13,6 +18,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 4;  // tokens per CTA
+constexpr int kCand = 64;  // candidates of one row (two per lane)
 
 struct RouteArgs {
     const float* partials;  // [ksplit][T][E] logits (added in order)
@@ -79,146 +85,417 @@ __device__ __forceinline__ float share_of(float l, bool in, int sigmoid) {
 // exp(l - mx) with the limit at infinite logits (l = mx = inf gives 1)
 __device__ __forceinline__ float exp_rel(float l, float mx) { return l == mx ? 1.0f : expf(l - mx); }
 
-__global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const RouteArgs a) {
+// The j-th selected expert's weight on lane j < k (mine: its id), written out.  mx, den:
+// the softmax statistics of the row (weights that are not renormalised).
+__device__ __forceinline__ void write_selection(const RouteArgs& a, int t, int lane, int mine, float l, float mx,
+                                                float den) {
+    const bool in = lane < a.k;
+    float w;
+    if (a.renormalize) w = share_of(l, in, a.sigmoid);
+    else if (l == -INFINITY) w = 0.0f;
+    else w = a.sigmoid ? sigmoid_f(l) : exp_rel(l, mx) / den;
+    if (in) {
+        a.topk_idx[(size_t)t * a.k + lane] = mine;
+        a.topk_w[(size_t)t * a.k + lane] = a.scale * w;
+    }
+}
+
+__device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int e) {
+    const float* p = a.partials + (size_t)t * a.E + e;
+    float l = *p;
+    for (int s = 1; s < a.ksplit; ++s) l += p[(size_t)s * a.T * a.E];
+    return l;
+}
+
+// One row in fp64 from its logits, k arg-max rounds: rows that fp32 cannot decide, and
+// shapes outside the fast kernel's layout.  c: E doubles of this warp's shared memory.
+__device__ __noinline__ void select_fp64(const RouteArgs& a, int t, double* c) {
+    const int lane = threadIdx.x & 31;
+    float mx = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) {
+        const float l = masked_logit(logit_at(a, t, e));
+        c[e] = l;
+        mx = fmaxf(mx, l);
+    }
+    mx = warp_max(mx);
+    double den = 0.0;
+    if (!a.sigmoid) {
+        for (int e = lane; e < a.E; e += 32)
+            if (c[e] != -INFINITY) den += c[e] == mx ? 1.0 : exp(c[e] - (double)mx);
+        den = warp_sum(den);
+    }
+    for (int e = lane; e < a.E; e += 32) {
+        const double l = c[e];
+        if (l == -INFINITY) continue;
+        double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : (l == mx ? 1.0 : exp(l - (double)mx)) / den;
+        if (a.bias) s += a.bias[e];
+        c[e] = s;
+    }
+    __syncwarp();
+    uint32_t kept = 0xffffffffu;
+    const int gs = a.E / a.n_groups;
+    if (a.topk_groups < a.n_groups) {
+        double b0 = -INFINITY, b1 = -INFINITY;
+        if (lane < a.n_groups) {
+            for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
+                const double v = c[e];
+                if (v > b0) {
+                    b1 = b0;
+                    b0 = v;
+                } else if (v > b1) {
+                    b1 = v;
+                }
+            }
+            if (a.top2 && b1 != -INFINITY) b0 += b1;
+        }
+        kept = 0;
+        for (int r = 0; r < a.topk_groups; ++r) {
+            double v = b0;
+            int i = lane < a.n_groups && !((kept >> lane) & 1u) ? lane : 0x7fffffff;
+            warp_best(v, i);
+            kept |= 1u << i;
+        }
+    }
+    // lane j keeps the j-th selected expert; taken experts are marked NaN
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double v = 0.0;
+        int i = 0x7fffffff;
+        for (int e = lane; e < a.E; e += 32) {
+            const double u = c[e];
+            if (u != u || !((kept >> (e / gs)) & 1u)) continue;
+            if (i == 0x7fffffff || u > v) {
+                v = u;
+                i = e;
+            }
+        }
+        warp_best(v, i);
+        if ((i & 31) == lane) c[i] = NAN;
+        if (lane == j) mine = i;
+    }
+    const float l = lane < a.k ? masked_logit(logit_at(a, t, mine)) : -INFINITY;
+    write_selection(a, t, lane, mine, l, mx, (float)den);
+    __syncwarp();
+}
+
+__global__ void __launch_bounds__(kWarps * 32) scored_topk_fp64_kernel(const RouteArgs a) {
     pdl_begin();
     extern __shared__ double c_all[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double* c = c_all + (size_t)warp * a.E;
-    const size_t slice = (size_t)a.T * a.E;
     for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
-        const float* row = a.partials + (size_t)t * a.E;
-        float* lo = a.logits_out ? a.logits_out + (size_t)t * a.E : nullptr;
-        auto logit = [&](int e) {
-            float l = row[e];
-            for (int s = 1; s < a.ksplit; ++s) l += row[(size_t)s * slice + e];
-            return l;
-        };
-        float mx = -INFINITY;
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit(e);
-            if (lo) lo[e] = l;
-            c[e] = masked_logit(l);
-            mx = fmaxf(mx, masked_logit(l));
+        if (a.logits_out)
+            for (int e = lane; e < a.E; e += 32) a.logits_out[(size_t)t * a.E + e] = logit_at(a, t, e);
+        select_fp64(a, t, c_all + (size_t)warp * a.E);
+    }
+}
+
+// Monotone map of a float (no NaN) to an unsigned word that is never 0.
+__device__ __forceinline__ uint32_t key_of(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// What the fp32 selection value of an expert is.
+enum KeyKind : int {
+    kKeyLogit,    // the logit itself: orders as the score does, and exactly (no bias, no sum of two)
+    kKeySigmoid,  // sigmoid + bias
+    kKeySoftmax,  // softmax + bias
+};
+
+// Lanes are laid out by groups: lpg (a power of two) lanes per group, PER consecutive
+// experts per lane; what passes the group's end is empty (key 0).
+template <int PER, int KIND>
+__global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const RouteArgs a, int lpg, int vec) {
+    pdl_begin();
+    extern __shared__ double c_all[];
+    __shared__ uint64_t cand_all[kWarps][kCand];
+    __shared__ uint64_t sorted_all[kWarps][kCand];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t* cand = cand_all[warp];
+    uint64_t* sorted = sorted_all[warp];
+    const int gs = a.E / a.n_groups;
+    const int group = lane / lpg;
+    const int in_group = (lane & (lpg - 1)) * PER;  // first of this lane's experts within its group
+    const int n_mine = group < a.n_groups ? min(PER, max(0, gs - in_group)) : 0;
+    const int e0 = group * gs + in_group;
+    const bool grouped = a.topk_groups < a.n_groups;
+    const bool stats = KIND == kKeySoftmax || (!a.sigmoid && !a.renormalize);
+    float b[PER];
+    if (KIND != kKeyLogit) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) b[i] = a.bias && i < n_mine ? a.bias[e0 + i] : 0.0f;
+    }
+
+    float l[PER];
+    auto load = [&](int t) {
+        const float* p = a.partials + (size_t)t * a.E + e0;
+        if (PER >= 4 && vec) {
+            // rows and groups are whole float4s, so a lane's experts are too
+#pragma unroll
+            for (int i = 0; i < PER; i += 4)
+                if (i < n_mine) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+                    l[i] = v.x;
+                    l[(i + 1) % PER] = v.y;
+                    l[(i + 2) % PER] = v.z;
+                    l[(i + 3) % PER] = v.w;
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i < n_mine) l[i] = p[i];
+            for (int s = 1; s < a.ksplit; ++s) {
+                p += (size_t)a.T * a.E;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (i < n_mine) l[i] += p[i];
+            }
         }
-        mx = warp_max(mx);
-        double den = 0.0;
-        if (!a.sigmoid) {
-            for (int e = lane; e < a.E; e += 32)
-                if (c[e] != -INFINITY) den += c[e] == mx ? 1.0 : exp(c[e] - (double)mx);
+    };
+    int t = blockIdx.x * kWarps + warp;
+    if (t < a.T) load(t);
+    for (; t < a.T; t += gridDim.x * kWarps) {
+        if (a.logits_out) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i < n_mine) a.logits_out[(size_t)t * a.E + e0 + i] = l[i];
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) l[i] = masked_logit(l[i]);
+        if (KIND == kKeyLogit && !a.sigmoid) {
+            // beside an infinite logit every finite one has softmax 0: they tie
+            bool inf = false;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) inf |= i < n_mine && l[i] == INFINITY;
+            if (__any_sync(0xffffffffu, inf)) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (isfinite(l[i])) l[i] = -FLT_MAX;
+            }
+        }
+        float mx = -INFINITY, den = 1.0f;
+        if (stats) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i < n_mine) mx = fmaxf(mx, l[i]);
+            mx = warp_max(mx);
+            den = 0.0f;
+        }
+        // keys, and the error bound of a value: err (times the value's own rounding below)
+        uint32_t key[PER];
+        float sc[PER];
+        if (KIND == kKeySoftmax || stats) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                sc[i] = i < n_mine && l[i] != -INFINITY ? exp_rel(l[i], mx) : 0.0f;
+                den += sc[i];
+            }
             den = warp_sum(den);
         }
-        for (int e = lane; e < a.E; e += 32) {
-            const double l = c[e];
-            if (l == -INFINITY) continue;
-            double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : (l == mx ? 1.0 : exp(l - (double)mx)) / den;
-            if (a.bias) s += a.bias[e];
-            c[e] = s;
+        const float inv_den = 1.0f / den;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            float c = l[i];
+            if (KIND == kKeySigmoid) c = __fdividef(1.0f, 1.0f + __expf(-l[i])) + b[i];
+            if (KIND == kKeySoftmax) c = sc[i] * inv_den + b[i];
+            if (KIND != kKeyLogit && l[i] == -INFINITY) c = -INFINITY;
+            key[i] = i < n_mine ? key_of(c) : 0u;
         }
-        __syncwarp();
-        uint32_t kept = 0xffffffffu;
-        const int gs = a.E / a.n_groups;
-        if (a.topk_groups < a.n_groups) {
-            double b0 = -INFINITY, b1 = -INFINITY;
-            if (lane < a.n_groups) {
-                for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
-                    const double v = c[e];
-                    if (v > b0) {
-                        b1 = b0;
-                        b0 = v;
-                    } else if (v > b1) {
-                        b1 = v;
-                    }
+        // the next row's loads run while this one is selected
+        const int cur = t;
+        if (t + (int)gridDim.x * kWarps < a.T) load(t + gridDim.x * kWarps);
+
+        // Bound of |fp32 value - exact value| before the bias is added.  Sigmoid: the fast
+        // exponential is off by 2 + 1.18 |l| steps, which 1 / (1 + e) takes s (1 - s) of
+        // (at most 0.63 steps of 2^-23), the sum and the fast division by 1.5 more: 3 in
+        // all.  Softmax: 2 steps of the exponential, |l - mx| / 2 of its argument, those
+        // of the sum ((PER + 5) / 2), of 1 / den and the product, all relative to a
+        // value of at most 1 / den: below 32.  The sum with the bias adds half a step.
+        const float err = KIND == kKeyLogit ? 0.0f : 0x1p-23f * (KIND == kKeySigmoid ? 3.0f : 32.0f * inv_den);
+        bool unsure = false;
+        if (grouped) {
+            uint32_t k0 = 0, k1 = 0;  // the two largest of the group
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                k1 = max(k1, min(k0, key[i]));
+                k0 = max(k0, key[i]);
+            }
+            for (int d = 1; d < lpg; d <<= 1) {
+                const uint32_t o0 = __shfl_xor_sync(0xffffffffu, k0, d), o1 = __shfl_xor_sync(0xffffffffu, k1, d);
+                k1 = max(max(k1, o1), min(k0, o0));
+                k0 = max(k0, o0);
+            }
+            float g = k0 ? value_of(k0) : 0.0f;
+            if (KIND != kKeyLogit && a.top2 && k1 && value_of(k1) != -INFINITY) g += value_of(k1);
+            const uint32_t gk = group < a.n_groups ? key_of(g) : 0u;
+            int rank = 0;
+            for (int o = 0; o < a.n_groups; ++o) {
+                const uint32_t ok = __shfl_sync(0xffffffffu, gk, o * lpg);
+                rank += ok > gk || (ok == gk && o < group) ? 1 : 0;
+            }
+            const bool keep = group < a.n_groups && rank < a.topk_groups;
+            if (KIND != kKeyLogit) {
+                const uint32_t in_k = __reduce_min_sync(0xffffffffu, keep ? gk : 0xffffffffu);
+                const uint32_t out_k = __reduce_max_sync(0xffffffffu, keep ? 0u : gk);
+                const float in = value_of(in_k), out = value_of(out_k);
+                // (two groups without an unmasked expert tie exactly)
+                if (out != -INFINITY && in - out <= 2.0f * (2.0f * err + 0x1p-22f * fabsf(in))) unsure = true;
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (!keep) key[i] = 0u;
+        }
+        // threshold: the (k+1)-th largest lane maximum (the largest k+1 keys pass it)
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) m = max(m, key[i]);
+        uint32_t tau = 0, top = 0;
+        for (int j = 0; j <= a.k; ++j) {
+            tau = __reduce_max_sync(0xffffffffu, m);
+            if (j == 0) top = tau;
+            if (m == tau) m = 0;
+        }
+        const float mag = fmaxf(fabsf(value_of(top)), tau ? fabsf(value_of(tau)) : 0.0f);
+        const float eps = 2.0f * err + (KIND == kKeyLogit || mag == INFINITY ? 0.0f : 0x1p-22f * mag);
+        if (KIND != kKeyLogit && tau && value_of(tau) != -INFINITY) tau = key_of(value_of(tau) - 2.0f * eps);
+        if (tau == 0) tau = 1;
+        // candidates in expert order
+        int cnt = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) cnt += key[i] >= tau ? 1 : 0;
+        int incl = cnt;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const int n = __shfl_sync(0xffffffffu, incl, 31);
+        if (n > kCand) unsure = true;
+        if (!unsure) {
+            int at = incl - cnt;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (key[i] >= tau) cand[at++] = ((uint64_t)key[i] << 32) | (uint32_t)~(e0 + i);
+            __syncwarp();
+            for (int q = lane; q < n; q += 32) {
+                const uint64_t mine = cand[q];
+                int rank = 0;
+                for (int o = 0; o < n; ++o) rank += cand[o] > mine ? 1 : 0;
+                sorted[rank] = mine;
+            }
+            __syncwarp();
+            if (KIND != kKeyLogit) {
+                // neighbours of the first k + 1 in order, too close for fp32?
+                const uint32_t mine = lane < n ? (uint32_t)(sorted[lane] >> 32) : 0u;
+                const uint32_t next = lane + 1 < n ? (uint32_t)(sorted[lane + 1] >> 32) : 0u;
+                const bool close = lane < a.k && next && value_of(next) != -INFINITY &&
+                                   value_of(mine) - value_of(next) <= eps;
+                unsure = __any_sync(0xffffffffu, close);
+                if (unsure && KIND == kKeySigmoid && n <= 32) {
+                    // the candidates again in fp64 (every exact value above the k-th is among them)
+                    __syncwarp();
+                    const int e = lane < n ? (int)~(uint32_t)cand[lane] : 0;
+                    const double x = lane < n ? (double)masked_logit(logit_at(a, cur, e)) : 0.0;
+                    const double c = x == -INFINITY ? x : 1.0 / (1.0 + exp(-x)) + (a.bias ? (double)a.bias[e] : 0.0);
+                    __syncwarp();
+                    double* c64 = reinterpret_cast<double*>(cand);
+                    if (lane < n) c64[lane] = c;
+                    __syncwarp();
+                    int rank = 0;  // candidates are in expert order: ties to the lower position
+                    for (int o = 0; o < n; ++o) rank += c64[o] > c || (c64[o] == c && o < lane) ? 1 : 0;
+                    if (lane < n) sorted[rank] = (uint32_t)~e;
+                    __syncwarp();
+                    unsure = false;
                 }
-                if (a.top2 && b1 != -INFINITY) b0 += b1;
-            }
-            kept = 0;
-            for (int r = 0; r < a.topk_groups; ++r) {
-                double v = b0;
-                int i = lane < a.n_groups && !((kept >> lane) & 1u) ? lane : 0x7fffffff;
-                warp_best(v, i);
-                kept |= 1u << i;
             }
         }
-        // lane j keeps the j-th selected expert; taken experts are marked NaN
-        int mine = -1;
-        for (int j = 0; j < a.k; ++j) {
-            double v = 0.0;
-            int i = 0x7fffffff;
-            for (int e = lane; e < a.E; e += 32) {
-                const double u = c[e];
-                if (u != u || !((kept >> (e / gs)) & 1u)) continue;
-                if (i == 0x7fffffff || u > v) {
-                    v = u;
-                    i = e;
-                }
-            }
-            warp_best(v, i);
-            if ((i & 31) == lane) c[i] = NAN;
-            if (lane == j) mine = i;
+        if (unsure) {
+            select_fp64(a, cur, c_all + (size_t)warp * a.E);
+            continue;
         }
-        const bool in = lane < a.k;
-        const float l = in ? masked_logit(logit(mine)) : -INFINITY;
-        float w;
-        if (a.renormalize) w = share_of(l, in, a.sigmoid);
-        else if (l == -INFINITY) w = 0.0f;
-        else w = a.sigmoid ? sigmoid_f(l) : (float)(exp_rel(l, mx) / den);
-        if (in) {
-            a.topk_idx[(size_t)t * a.k + lane] = mine;
-            a.topk_w[(size_t)t * a.k + lane] = a.scale * w;
-        }
+        const int mine = lane < a.k ? (int)~(uint32_t)sorted[lane] : 0;
+        const float lw = lane < a.k ? masked_logit(logit_at(a, cur, mine)) : -INFINITY;
+        write_selection(a, cur, lane, mine, lw, mx, den);
         __syncwarp();
     }
 }
 
-// One warp per token: lane j < k holds the j-th selected expert.
+// The gradient of one row.  Lane j < k holds the j-th selected expert; V: float or float4,
+// NV of them per lane (V vec = lane + 32 i of the row).  Sparse gradients (sigmoid, or
+// renormalised) are zeros and k values; a softmax as it is reads the row once.
+template <typename V, int NV>
 __global__ void __launch_bounds__(kWarps * 32) scored_backward_kernel(const float* __restrict__ logits,
                                                                       const int32_t* __restrict__ topk_idx,
                                                                       const float* __restrict__ dw, int T, int E,
                                                                       int k, int sigmoid, int renormalize, float scale,
                                                                       float* __restrict__ dl, DevStatus st) {
     pdl_begin();
+    constexpr int W = sizeof(V) / 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool dense = !sigmoid && !renormalize;
+    const int nv = E / W;
     for (int t = blockIdx.x * kWarps + warp; t < T; t += gridDim.x * kWarps) {
         const float* row = logits + (size_t)t * E;
         float* out = dl + (size_t)t * E;
-        int e = lane < k ? topk_idx[(size_t)t * k + lane] : -1;
+        const int e = lane < k ? topk_idx[(size_t)t * k + lane] : -1;
         const bool in = e >= 0 && e < E;
         if (lane < k && !in) raise_status(st, kStatusInvalidExpert);
         const float g = in ? dw[(size_t)t * k + lane] : 0.0f;
         const float l = in ? masked_logit(row[e]) : -INFINITY;
         const bool live = l != -INFINITY;
-        const float rest = sigmoid && live ? 1.0f / (1.0f + expf(l)) : 1.0f;  // 1 - sigmoid(l)
-        float d;  // gradient through the selected scores
-        if (renormalize) {
-            const float w = share_of(l, in, sigmoid);
-            d = scale * w * (g - warp_sum(w * g)) * rest;
-        } else if (sigmoid) {
-            d = live ? scale * g * sigmoid_f(l) * rest : 0.0f;
-        } else {
-            float mx = -INFINITY;
-            for (int i = lane; i < E; i += 32) mx = fmaxf(mx, masked_logit(row[i]));
-            mx = warp_max(mx);
-            float den = 0.0f;
-            for (int i = lane; i < E; i += 32) {
-                const float v = masked_logit(row[i]);
-                if (v != -INFINITY) den += exp_rel(v, mx);
+        if (!dense) {
+            const float rest = sigmoid && live ? 1.0f / (1.0f + expf(l)) : 1.0f;  // 1 - sigmoid(l)
+            float d;
+            if (renormalize) {
+                const float w = share_of(l, in, sigmoid);
+                d = scale * w * (g - warp_sum(w * g)) * rest;
+            } else {
+                d = live ? scale * g * sigmoid_f(l) * rest : 0.0f;
             }
-            den = warp_sum(den);
-            const float p = live ? exp_rel(l, mx) / den : 0.0f;
-            const float dot = warp_sum(scale * g * p);
-            for (int i = lane; i < E; i += 32) {
-                const float v = masked_logit(row[i]);
-                out[i] = v == -INFINITY ? 0.0f : -(exp_rel(v, mx) / den) * dot;
-            }
+            V zero;
+            float* z = reinterpret_cast<float*>(&zero);
+#pragma unroll
+            for (int u = 0; u < W; ++u) z[u] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (lane + 32 * i < nv) reinterpret_cast<V*>(out)[lane + 32 * i] = zero;
             __syncwarp();
-            if (live) out[e] = p * (scale * g - dot);
-            __syncwarp();
+            if (in) out[e] = d;
             continue;
         }
-        for (int i = lane; i < E; i += 32) out[i] = 0.0f;
+        V v[NV];
+        float* p = reinterpret_cast<float*>(v);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane + 32 * i < nv) v[i] = reinterpret_cast<const V*>(row)[lane + 32 * i];
+#pragma unroll
+        for (int i = 0; i < NV * W; ++i) {
+            p[i] = lane + 32 * (i / W) < nv ? masked_logit(p[i]) : -INFINITY;
+            mx = fmaxf(mx, p[i]);
+        }
+        mx = warp_max(mx);
+        float den = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV * W; ++i) {
+            p[i] = p[i] == -INFINITY ? 0.0f : exp_rel(p[i], mx);
+            den += p[i];
+        }
+        den = warp_sum(den);
+        const float inv_den = den > 0.0f ? 1.0f / den : 0.0f;
+        const float pe = live ? exp_rel(l, mx) * inv_den : 0.0f;
+        const float dot = warp_sum(scale * g * pe);
+#pragma unroll
+        for (int i = 0; i < NV * W; ++i) p[i] *= -dot * inv_den;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane + 32 * i < nv) reinterpret_cast<V*>(out)[lane + 32 * i] = v[i];
         __syncwarp();
-        if (in) out[e] = d;
-        __syncwarp();
+        if (in) out[e] = pe * (scale * g - dot);
     }
 }
 
@@ -245,6 +522,36 @@ int grid_for(int T) {
     const long want = ((long)T + kWarps - 1) / kWarps;
     const long cap = (long)num_sms() * 16;
     return (int)(want < cap ? want : cap);
+}
+
+template <int PER>
+cudaError_t launch_scored_per(const RouteArgs& a, int kind, int lpg, int vec, cudaStream_t stream) {
+    const dim3 grid(grid_for(a.T)), block(kWarps * 32);
+    const size_t smem = (size_t)kWarps * a.E * sizeof(double);
+    if (kind == kKeyLogit) return launch_pdl(scored_topk_kernel<PER, kKeyLogit>, grid, block, smem, stream, a, lpg, vec);
+    if (kind == kKeySigmoid)
+        return launch_pdl(scored_topk_kernel<PER, kKeySigmoid>, grid, block, smem, stream, a, lpg, vec);
+    return launch_pdl(scored_topk_kernel<PER, kKeySoftmax>, grid, block, smem, stream, a, lpg, vec);
+}
+
+cudaError_t launch_scored(const RouteArgs& a, cudaStream_t stream) {
+    const bool grouped = a.topk_groups < a.n_groups;
+    const int kind = !a.bias && !(grouped && a.top2) ? kKeyLogit : a.sigmoid ? kKeySigmoid : kKeySoftmax;
+    const int gs = a.E / a.n_groups;
+    int lpg = 32;
+    while (lpg * a.n_groups > 32) lpg >>= 1;
+    const int per = (gs + lpg - 1) / lpg;
+    const int vec = a.ksplit == 1 && gs % 4 == 0 && (reinterpret_cast<uintptr_t>(a.partials) & 15) == 0;
+    // more than 31 selected (no lane left for the next one) or more experts than a lane holds
+    if (a.k > 31 || per > 32)
+        return launch_pdl(scored_topk_fp64_kernel, dim3(grid_for(a.T)), dim3(kWarps * 32),
+                          (size_t)kWarps * a.E * sizeof(double), stream, a);
+    if (per <= 1) return launch_scored_per<1>(a, kind, lpg, vec, stream);
+    if (per <= 2) return launch_scored_per<2>(a, kind, lpg, vec, stream);
+    if (per <= 4) return launch_scored_per<4>(a, kind, lpg, vec, stream);
+    if (per <= 8) return launch_scored_per<8>(a, kind, lpg, vec, stream);
+    if (per <= 16) return launch_scored_per<16>(a, kind, lpg, vec, stream);
+    return launch_scored_per<32>(a, kind, lpg, vec, stream);
 }
 
 }  // namespace
@@ -289,8 +596,7 @@ int moe_route_scored(const moe_shape_t* shape, const moe_router_t* router, int T
     a.logits_out = logits_out;
     a.topk_idx = topk_idx;
     a.topk_w = topk_w;
-    const cudaError_t e = launch_pdl(scored_topk_kernel, dim3(grid_for(T)), dim3(kWarps * 32),
-                                     (size_t)kWarps * a.E * sizeof(double), reinterpret_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = launch_scored(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "scored top-k launch: %s", cudaGetErrorString(e));
     return MOE_OK;
 }
@@ -306,11 +612,19 @@ int moe_route_scored_backward(const moe_shape_t* shape, const moe_router_t* rout
         return rc;
     DevStatus st;
     if ((rc = api_device_status(&st))) return rc;
-    const cudaError_t e =
-        launch_pdl(scored_backward_kernel, dim3(grid_for(T)), dim3(kWarps * 32), 0,
-                   reinterpret_cast<cudaStream_t>(stream), logits, topk_idx, d_topk_w, T, shape->n_experts,
-                   shape->top_k, (int)(router->score == MOE_SCORE_SIGMOID), (int)router->renormalize, router->scale,
-                   d_logits, st);
+    const int E = shape->n_experts;
+    // rows as float4s where they start on 16 bytes
+    const bool vec = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(d_logits)) & 15) == 0;
+    auto launch = [&](auto kern) {
+        return launch_pdl(kern, dim3(grid_for(T)), dim3(kWarps * 32), 0, reinterpret_cast<cudaStream_t>(stream), logits,
+                          topk_idx, d_topk_w, T, E, (int)shape->top_k, (int)(router->score == MOE_SCORE_SIGMOID),
+                          (int)router->renormalize, router->scale, d_logits, st);
+    };
+    const cudaError_t e = !vec       ? launch(scored_backward_kernel<float, 32>)
+                          : E <= 128 ? launch(scored_backward_kernel<float4, 1>)
+                          : E <= 256 ? launch(scored_backward_kernel<float4, 2>)
+                          : E <= 512 ? launch(scored_backward_kernel<float4, 4>)
+                                     : launch(scored_backward_kernel<float4, 8>);
     if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "scored backward launch: %s", cudaGetErrorString(e));
     return MOE_OK;
 }
