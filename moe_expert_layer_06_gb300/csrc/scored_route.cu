@@ -72,12 +72,15 @@ __device__ __forceinline__ float sigmoid_f(float l) { return 1.0f / (1.0f + expf
 // s_j / sum s_i relative to the largest: exp(l) for a softmax; for a sigmoid
 // exp(min(l, 0)) / (1 + exp(-|l|)), whose small factor exp(min(l, 0)) is taken
 // relative to the row's largest.  A row of masked logits gets 0.
+__device__ __forceinline__ float share_term(float l, float top, int sigmoid) {
+    const float low = sigmoid ? fminf(l, 0.0f) : l;
+    const float e = low == top ? 1.0f : expf(low - top);
+    return sigmoid ? e / (1.0f + expf(-fabsf(l))) : e;
+}
+
 __device__ __forceinline__ float share_of(float l, bool in, int sigmoid) {
-    const float low = in ? (sigmoid ? fminf(l, 0.0f) : l) : -INFINITY;
-    const float m = warp_max(low);
-    float e = low == m ? 1.0f : expf(low - m);
-    if (sigmoid) e /= 1.0f + expf(-fabsf(l));
-    if (!in || l == -INFINITY) e = 0.0f;
+    const float m = warp_max(in ? (sigmoid ? fminf(l, 0.0f) : l) : -INFINITY);
+    const float e = in && l != -INFINITY ? share_term(l, m, sigmoid) : 0.0f;
     const float sum = warp_sum(e);
     return sum > 0.0f ? e / sum : 0.0f;
 }
@@ -178,7 +181,7 @@ __device__ __noinline__ void select_fp64(const RouteArgs& a, int t, double* c) {
     __syncwarp();
 }
 
-__global__ void __launch_bounds__(kWarps * 32) scored_topk_fp64_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) scored_topk_fp64_kernel(const __grid_constant__ RouteArgs a) {
     pdl_begin();
     extern __shared__ double c_all[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -192,12 +195,56 @@ __global__ void __launch_bounds__(kWarps * 32) scored_topk_fp64_kernel(const Rou
 // Monotone map of a float (no NaN) to an unsigned word that is never 0.
 __device__ __forceinline__ uint32_t key_of(float f) {
     const uint32_t u = __float_as_uint(f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+
+// 1 / (1 + exp(-l)) from the hardware's approximate 2^x and reciprocal.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.442695041f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// Reductions over the LPT consecutive lanes of one token (every lane gets the result).
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
+    if constexpr (LPT == 32) {
+        return __reduce_max_sync(0xffffffffu, v);
+    } else {
+#pragma unroll
+        for (int d = LPT / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    }
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_max(float v) {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v) {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ bool token_any(bool p) {
+    const uint32_t b = __ballot_sync(0xffffffffu, p);
+    if (LPT == 32) return b != 0;
+    return ((b >> (threadIdx.x & 31 & ~(LPT - 1))) & ((1u << (LPT & 31)) - 1u)) != 0;
+}
+
+// fp64 scratch of a warp: a row, or a value per candidate.
+__host__ __device__ __forceinline__ int scratch_doubles(int E) { return E > kCand ? E : kCand; }
 
 // What the fp32 selection value of an expert is.
 enum KeyKind : int {
@@ -206,38 +253,50 @@ enum KeyKind : int {
     kKeySoftmax,  // softmax + bias
 };
 
-// Lanes are laid out by groups: lpg (a power of two) lanes per group, PER consecutive
-// experts per lane; what passes the group's end is empty (key 0).
-template <int PER, int KIND>
-__global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const RouteArgs a, int lpg, int vec) {
+// LPT lanes per token (32 / LPT tokens per warp).  A token's lanes are laid out by
+// groups: lpg (a power of two) lanes per group, PER consecutive experts per lane; what
+// passes the group's end is empty (key 0).
+template <int LPT, int PER, int KIND>
+__global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const __grid_constant__ RouteArgs a, int lpg, int vec) {
     pdl_begin();
+    constexpr int TPW = 32 / LPT;                // tokens per warp
+    // experts per block maximum: at least 32 blocks of a full row, at most 8 experts each
+    constexpr int BLK = PER * LPT >= 256 ? 8 : PER * LPT >= 64 ? PER * LPT / 32 : 1;
+    constexpr int NB = PER / BLK;
     extern __shared__ double c_all[];
-    __shared__ uint64_t cand_all[kWarps][kCand];
-    __shared__ uint64_t sorted_all[kWarps][kCand];
+    __shared__ __align__(16) uint32_t cand_all[kWarps * TPW][kCand];
+    __shared__ uint16_t cand_e_all[kWarps * TPW][kCand];
+    __shared__ uint16_t sorted_all[kWarps * TPW][kCand];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t* cand = cand_all[warp];
-    uint64_t* sorted = sorted_all[warp];
+    const int sub = lane & (LPT - 1), slot = lane / LPT;
+    uint32_t* cand = cand_all[warp * TPW + slot];      // keys of the candidates, in expert order
+    uint16_t* cand_e = cand_e_all[warp * TPW + slot];  // their experts
+    uint16_t* sorted = sorted_all[warp * TPW + slot];  // candidate of each rank
     const int gs = a.E / a.n_groups;
-    const int group = lane / lpg;
-    const int in_group = (lane & (lpg - 1)) * PER;  // first of this lane's experts within its group
+    const int group = sub / lpg;
+    const int in_group = (sub & (lpg - 1)) * PER;  // first of this lane's experts within its group
     const int n_mine = group < a.n_groups ? min(PER, max(0, gs - in_group)) : 0;
     const int e0 = group * gs + in_group;
     const bool grouped = a.topk_groups < a.n_groups;
     const bool stats = KIND == kKeySoftmax || (!a.sigmoid && !a.renormalize);
-    float b[PER];
+    // bias, a lane's experts together and lanes apart by PER + 4 words (16-byte reads without bank conflicts)
+    double* scratch = c_all + (size_t)warp * scratch_doubles(a.E);
+    float* bias = reinterpret_cast<float*>(c_all + (size_t)kWarps * scratch_doubles(a.E));
     if (KIND != kKeyLogit) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) b[i] = a.bias && i < n_mine ? a.bias[e0 + i] : 0.0f;
+        if (warp == 0 && lane < LPT)
+            for (int i = 0; i < PER; ++i) bias[sub * (PER + 4) + i] = a.bias && i < n_mine ? a.bias[e0 + i] : 0.0f;
+        __syncthreads();
     }
 
     float l[PER];
     auto load = [&](int t) {
         const float* p = a.partials + (size_t)t * a.E + e0;
+        const int n = t < a.T ? n_mine : 0;
         if (PER >= 4 && vec) {
             // rows and groups are whole float4s, so a lane's experts are too
 #pragma unroll
             for (int i = 0; i < PER; i += 4)
-                if (i < n_mine) {
+                if (i < n) {
                     const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
                     l[i] = v.x;
                     l[(i + 1) % PER] = v.y;
@@ -247,75 +306,112 @@ __global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const RouteArg
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (i < n_mine) l[i] = p[i];
+                if (i < n) l[i] = p[i];
             for (int s = 1; s < a.ksplit; ++s) {
                 p += (size_t)a.T * a.E;
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    if (i < n_mine) l[i] += p[i];
+                    if (i < n) l[i] += p[i];
             }
         }
     };
-    int t = blockIdx.x * kWarps + warp;
-    if (t < a.T) load(t);
-    for (; t < a.T; t += gridDim.x * kWarps) {
-        if (a.logits_out) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = 0.0f;
+    const int stride = gridDim.x * kWarps * TPW;
+    int tw = (blockIdx.x * kWarps + warp) * TPW;  // the warp's first token
+    load(tw + slot);
+    for (; tw < a.T; tw += stride) {
+        const int t = tw + slot;
+        const bool alive = t < a.T;
+        if (a.logits_out && alive) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (i < n_mine) a.logits_out[(size_t)t * a.E + e0 + i] = l[i];
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) l[i] = masked_logit(l[i]);
+        float mx = -INFINITY, den = 1.0f;
         if (KIND == kKeyLogit && !a.sigmoid) {
             // beside an infinite logit every finite one has softmax 0: they tie
             bool inf = false;
 #pragma unroll
             for (int i = 0; i < PER; ++i) inf |= i < n_mine && l[i] == INFINITY;
-            if (__any_sync(0xffffffffu, inf)) {
+            if (token_any<LPT>(inf)) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
                     if (isfinite(l[i])) l[i] = -FLT_MAX;
             }
         }
-        float mx = -INFINITY, den = 1.0f;
+        uint32_t key[PER];
         if (stats) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (i < n_mine) mx = fmaxf(mx, l[i]);
-            mx = warp_max(mx);
-            den = 0.0f;
-        }
-        // keys, and the error bound of a value: err (times the value's own rounding below)
-        uint32_t key[PER];
-        float sc[PER];
-        if (KIND == kKeySoftmax || stats) {
+            mx = token_max<LPT>(mx);
+            float part[PER];  // summed in pairs: log2(E) roundings
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                sc[i] = i < n_mine && l[i] != -INFINITY ? exp_rel(l[i], mx) : 0.0f;
-                den += sc[i];
+                part[i] = i < n_mine && l[i] != -INFINITY ? exp_rel(l[i], mx) : 0.0f;
+                if (KIND == kKeySoftmax) key[i] = __float_as_uint(part[i]);
             }
-            den = warp_sum(den);
+#pragma unroll
+            for (int w = PER / 2; w > 0; w >>= 1)
+#pragma unroll
+                for (int i = 0; i < w; ++i) part[i] += part[i + w];
+            den = token_sum<LPT>(part[0]);
         }
         const float inv_den = 1.0f / den;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            float c = l[i];
-            if (KIND == kKeySigmoid) c = __fdividef(1.0f, 1.0f + __expf(-l[i])) + b[i];
-            if (KIND == kKeySoftmax) c = sc[i] * inv_den + b[i];
-            if (KIND != kKeyLogit && l[i] == -INFINITY) c = -INFINITY;
-            key[i] = i < n_mine ? key_of(c) : 0u;
+        for (int i = 0; i < PER; i += (PER >= 4 ? 4 : 1)) {
+            float b4[4];
+            if (KIND != kKeyLogit) {
+                if (PER >= 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(bias + sub * (PER + 4) + i);
+                    b4[0] = v.x;
+                    b4[1] = v.y;
+                    b4[2] = v.z;
+                    b4[3] = v.w;
+                } else {
+                    b4[0] = bias[sub * (PER + 4) + i];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < (PER >= 4 ? 4 : 1); ++u) {
+                float c = l[i + u];
+                if (KIND == kKeySigmoid) c = fast_sigmoid(c) + b4[u];
+                if (KIND == kKeySoftmax) c = fmaf(__uint_as_float(key[i + u]), inv_den, b4[u]);
+                if (KIND != kKeyLogit && l[i + u] == -INFINITY) c = -INFINITY;
+                key[i + u] = i + u < n_mine ? key_of(c) : 0u;
+            }
         }
         // the next row's loads run while this one is selected
-        const int cur = t;
-        if (t + (int)gridDim.x * kWarps < a.T) load(t + gridDim.x * kWarps);
+        load(tw + stride + slot);
 
-        // Bound of |fp32 value - exact value| before the bias is added.  Sigmoid: the fast
+        // Bound of |fp32 value - exact value| before the bias is added.  Sigmoid: the
         // exponential is off by 2 + 1.18 |l| steps, which 1 / (1 + e) takes s (1 - s) of
-        // (at most 0.63 steps of 2^-23), the sum and the fast division by 1.5 more: 3 in
+        // (at most 0.63 steps of 2^-23), the sum and the reciprocal by 1.5 more: 3 in
         // all.  Softmax: 2 steps of the exponential, |l - mx| / 2 of its argument, those
-        // of the sum ((PER + 5) / 2), of 1 / den and the product, all relative to a
-        // value of at most 1 / den: below 32.  The sum with the bias adds half a step.
-        const float err = KIND == kKeyLogit ? 0.0f : 0x1p-23f * (KIND == kKeySigmoid ? 3.0f : 32.0f * inv_den);
+        // of den (`rel` below), of 1 / den and the product, all relative to a value of
+        // at most 1 / den: below 16.  The sum with the bias adds half a step.
+        const float err = KIND == kKeyLogit ? 0.0f : 0x1p-23f * (KIND == kKeySigmoid ? 3.0f : 16.0f * inv_den);
+        // exact scores: the softmax's sum in fp64, then one logit at a time
+        double den64 = 0.0;
+        auto sum64 = [&](bool need) {
+            if (KIND != kKeySoftmax) return;
+            double d = 0.0;
+            if (need)
+                for (int i = 0; i < n_mine; ++i) {
+                    const float x = masked_logit(logit_at(a, t, e0 + i));
+                    if (x != -INFINITY) d += x == mx ? 1.0 : exp((double)x - (double)mx);
+                }
+#pragma unroll
+            for (int w = LPT / 2; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
+            if (need) den64 = d;
+        };
+        auto score64 = [&](float x) -> double {
+            if (KIND == kKeySoftmax) return (x == mx ? 1.0 : exp((double)x - (double)mx)) / den64;
+            return 1.0 / (1.0 + exp(-(double)x));
+        };
         bool unsure = false;
         if (grouped) {
             uint32_t k0 = 0, k1 = 0;  // the two largest of the group
@@ -330,34 +426,73 @@ __global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const RouteArg
                 k0 = max(k0, o0);
             }
             float g = k0 ? value_of(k0) : 0.0f;
-            if (KIND != kKeyLogit && a.top2 && k1 && value_of(k1) != -INFINITY) g += value_of(k1);
+            const bool two = a.top2 && k1 && value_of(k1) != -INFINITY;
+            if (KIND != kKeyLogit && two) g += value_of(k1);
             const uint32_t gk = group < a.n_groups ? key_of(g) : 0u;
             int rank = 0;
             for (int o = 0; o < a.n_groups; ++o) {
-                const uint32_t ok = __shfl_sync(0xffffffffu, gk, o * lpg);
+                const uint32_t ok = __shfl_sync(0xffffffffu, gk, o * lpg, LPT);
                 rank += ok > gk || (ok == gk && o < group) ? 1 : 0;
             }
-            const bool keep = group < a.n_groups && rank < a.topk_groups;
+            bool keep = group < a.n_groups && rank < a.topk_groups;
             if (KIND != kKeyLogit) {
-                const uint32_t in_k = __reduce_min_sync(0xffffffffu, keep ? gk : 0xffffffffu);
-                const uint32_t out_k = __reduce_max_sync(0xffffffffu, keep ? 0u : gk);
-                const float in = value_of(in_k), out = value_of(out_k);
+                const float in = value_of(~token_max<LPT>(keep ? ~gk : 0u)), out = value_of(token_max<LPT>(keep ? 0u : gk));
                 // (two groups without an unmasked expert tie exactly)
-                if (out != -INFINITY && in - out <= 2.0f * (2.0f * err + 0x1p-22f * fabsf(in))) unsure = true;
+                const bool close = out != -INFINITY && in - out <= 4.0f * err + 0x1p-21f * fabsf(in);
+                if (__any_sync(0xffffffffu, close)) {
+                    // the group scores in fp64, from the experts that fp32 leaves for the two best
+                    const float low = value_of(a.top2 && k1 ? k1 : k0);
+                    const float margin = 2.0f * err + 0x1p-22f * fabsf(low);
+                    double d0 = -INFINITY, d1 = -INFINITY;
+                    sum64(close);
+                    if (close && k0) {
+                        for (int i = 0; i < n_mine; ++i) {
+                            const float x = masked_logit(logit_at(a, t, e0 + i));
+                            uint32_t ki = 0;
+#pragma unroll
+                            for (int u = 0; u < PER; ++u) ki = u == i ? key[u] : ki;
+                            if (x == -INFINITY || value_of(ki) < low - margin) continue;
+                            const double c = score64(x) + (double)bias[sub * (PER + 4) + i];
+                            d1 = fmax(d1, fmin(d0, c));
+                            d0 = fmax(d0, c);
+                        }
+                    }
+                    for (int d = 1; d < lpg; d <<= 1) {
+                        const double o0 = __shfl_xor_sync(0xffffffffu, d0, d), o1 = __shfl_xor_sync(0xffffffffu, d1, d);
+                        d1 = fmax(fmax(d1, o1), fmin(d0, o0));
+                        d0 = fmax(d0, o0);
+                    }
+                    if (a.top2 && d1 != -INFINITY) d0 += d1;
+                    int exact = 0;
+                    for (int o = 0; o < a.n_groups; ++o) {
+                        const double od = __shfl_sync(0xffffffffu, d0, o * lpg, LPT);
+                        exact += od > d0 || (od == d0 && o < group) ? 1 : 0;
+                    }
+                    if (close) keep = group < a.n_groups && exact < a.topk_groups;
+                }
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (!keep) key[i] = 0u;
         }
-        // threshold: the (k+1)-th largest lane maximum (the largest k+1 keys pass it)
-        uint32_t m = 0;
+        // threshold: the (k+1)-th largest block maximum (the largest k+1 keys pass it)
+        uint32_t m[NB];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) m = max(m, key[i]);
+        for (int q = 0; q < NB; ++q) {
+            m[q] = 0;
+#pragma unroll
+            for (int i = 0; i < BLK; ++i) m[q] = max(m[q], key[q * BLK + i]);
+        }
         uint32_t tau = 0, top = 0;
         for (int j = 0; j <= a.k; ++j) {
-            tau = __reduce_max_sync(0xffffffffu, m);
+            uint32_t mine = m[0];
+#pragma unroll
+            for (int q = 1; q < NB; ++q) mine = max(mine, m[q]);
+            tau = token_max<LPT>(mine);
             if (j == 0) top = tau;
-            if (m == tau) m = 0;
+#pragma unroll
+            for (int q = 0; q < NB; ++q)
+                if (m[q] == tau) m[q] = 0;
         }
         const float mag = fmaxf(fabsf(value_of(top)), tau ? fabsf(value_of(tau)) : 0.0f);
         const float eps = 2.0f * err + (KIND == kKeyLogit || mag == INFINITY ? 0.0f : 0x1p-22f * mag);
@@ -369,57 +504,122 @@ __global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const RouteArg
         for (int i = 0; i < PER; ++i) cnt += key[i] >= tau ? 1 : 0;
         int incl = cnt;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
+        for (int d = 1; d < LPT; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d, LPT);
+            if (sub >= d) incl += o;
         }
-        const int n = __shfl_sync(0xffffffffu, incl, 31);
-        if (n > kCand) unsure = true;
-        if (!unsure) {
+        int n = __shfl_sync(0xffffffffu, incl, LPT - 1, LPT);
+        if (n > kCand) {
+            unsure = true;
+            n = 0;
+        }
+        if (n > 0) {
             int at = incl - cnt;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (key[i] >= tau) cand[at++] = ((uint64_t)key[i] << 32) | (uint32_t)~(e0 + i);
-            __syncwarp();
-            for (int q = lane; q < n; q += 32) {
-                const uint64_t mine = cand[q];
-                int rank = 0;
-                for (int o = 0; o < n; ++o) rank += cand[o] > mine ? 1 : 0;
-                sorted[rank] = mine;
+                if (key[i] >= tau) {
+                    cand[at] = key[i];
+                    cand_e[at] = (uint16_t)(e0 + i);
+                    ++at;
+                }
+            // whole vectors of four
+            for (int q = n + sub; q < ((n + 3) & ~3); q += LPT) cand[q] = 0u;
+        }
+        __syncwarp();
+        for (int q = sub; q < n; q += LPT) {
+            // ties in expert order: an equal key at a lower position counts as larger
+            const uint32_t mine = cand[q];
+            int rank = 0;
+            for (int o = 0; o < n; o += 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(cand + o);
+                rank += v.x > mine || (v.x == mine && o < q) ? 1 : 0;
+                rank += v.y > mine || (v.y == mine && o + 1 < q) ? 1 : 0;
+                rank += v.z > mine || (v.z == mine && o + 2 < q) ? 1 : 0;
+                rank += v.w > mine || (v.w == mine && o + 3 < q) ? 1 : 0;
             }
-            __syncwarp();
-            if (KIND != kKeyLogit) {
-                // neighbours of the first k + 1 in order, too close for fp32?
-                const uint32_t mine = lane < n ? (uint32_t)(sorted[lane] >> 32) : 0u;
-                const uint32_t next = lane + 1 < n ? (uint32_t)(sorted[lane + 1] >> 32) : 0u;
-                const bool close = lane < a.k && next && value_of(next) != -INFINITY &&
-                                   value_of(mine) - value_of(next) <= eps;
-                unsure = __any_sync(0xffffffffu, close);
-                if (unsure && KIND == kKeySigmoid && n <= 32) {
-                    // the candidates again in fp64 (every exact value above the k-th is among them)
+            sorted[rank] = (uint16_t)q;
+        }
+        __syncwarp();
+        if (KIND != kKeyLogit) {
+            // neighbours of the first k + 1 in order, too close for fp32?
+            bool close = false;
+            for (int j = sub; j < min(a.k, n - 1); j += LPT) {
+                const float next = value_of(cand[sorted[j + 1]]);
+                close |= next != -INFINITY && value_of(cand[sorted[j]]) - next <= eps;
+            }
+            const bool again = token_any<LPT>(close);
+            if (__any_sync(0xffffffffu, again)) {
+                // the candidates again in fp64 (every exact value above the k-th is among them), in
+                // the warp's fp64 scratch: values and scores
+                sum64(again);
+                for (int w = 0; w < TPW; ++w) {
+                    // one token of the warp after the other
+                    const bool turn = again && slot == w;
+                    if (turn)
+                        for (int q = sub; q < n; q += LPT) {
+                            const int e = cand_e[q];
+                            const float x = masked_logit(logit_at(a, t, e));
+                            scratch[q] = x == -INFINITY ? -INFINITY : score64(x) + (a.bias ? (double)a.bias[e] : 0.0);
+                        }
                     __syncwarp();
-                    const int e = lane < n ? (int)~(uint32_t)cand[lane] : 0;
-                    const double x = lane < n ? (double)masked_logit(logit_at(a, cur, e)) : 0.0;
-                    const double c = x == -INFINITY ? x : 1.0 / (1.0 + exp(-x)) + (a.bias ? (double)a.bias[e] : 0.0);
+                    if (turn)
+                        for (int q = sub; q < n; q += LPT) {
+                            int rank = 0;
+                            for (int o = 0; o < n; ++o)
+                                rank += scratch[o] > scratch[q] || (scratch[o] == scratch[q] && o < q) ? 1 : 0;
+                            sorted[rank] = (uint16_t)q;
+                        }
                     __syncwarp();
-                    double* c64 = reinterpret_cast<double*>(cand);
-                    if (lane < n) c64[lane] = c;
-                    __syncwarp();
-                    int rank = 0;  // candidates are in expert order: ties to the lower position
-                    for (int o = 0; o < n; ++o) rank += c64[o] > c || (c64[o] == c && o < lane) ? 1 : 0;
-                    if (lane < n) sorted[rank] = (uint32_t)~e;
-                    __syncwarp();
-                    unsure = false;
                 }
             }
         }
-        if (unsure) {
-            select_fp64(a, cur, c_all + (size_t)warp * a.E);
-            continue;
+        unsure = token_any<LPT>(unsure);
+        // weights: lane sub holds the selected experts sub, sub + LPT, ... of its token
+        constexpr int KPL = 32 / LPT;
+        float lw[KPL], sh[KPL];
+        int me[KPL];
+        float low = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < KPL; ++q) {
+            const int j = sub + q * LPT;
+            const bool in = j < a.k && alive && !unsure;
+            me[q] = in ? cand_e[sorted[j]] : 0;
+            lw[q] = in ? masked_logit(logit_at(a, t, me[q])) : -INFINITY;
+            if (j < a.k) low = fmaxf(low, a.sigmoid ? fminf(lw[q], 0.0f) : lw[q]);
         }
-        const int mine = lane < a.k ? (int)~(uint32_t)sorted[lane] : 0;
-        const float lw = lane < a.k ? masked_logit(logit_at(a, cur, mine)) : -INFINITY;
-        write_selection(a, cur, lane, mine, lw, mx, den);
+        if (a.renormalize) {
+            low = token_max<LPT>(low);
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < KPL; ++q) {
+                sh[q] = 0.0f;
+                if (lw[q] != -INFINITY) sh[q] = share_term(lw[q], low, a.sigmoid);
+                sum += sh[q];
+            }
+            sum = token_sum<LPT>(sum);
+            const float f = sum > 0.0f ? a.scale / sum : 0.0f;
+#pragma unroll
+            for (int q = 0; q < KPL; ++q) sh[q] *= f;
+        } else {
+#pragma unroll
+            for (int q = 0; q < KPL; ++q) {
+                sh[q] = 0.0f;
+                if (lw[q] != -INFINITY) sh[q] = a.scale * (a.sigmoid ? sigmoid_f(lw[q]) : exp_rel(lw[q], mx) * inv_den);
+            }
+        }
+        if (alive && !unsure) {
+#pragma unroll
+            for (int q = 0; q < KPL; ++q) {
+                const int j = sub + q * LPT;
+                if (j < a.k) {
+                    a.topk_idx[(size_t)t * a.k + j] = me[q];
+                    a.topk_w[(size_t)t * a.k + j] = sh[q];
+                }
+            }
+        }
+        uint32_t redo = __ballot_sync(0xffffffffu, alive && unsure && sub == 0);
+        for (; redo; redo &= redo - 1)
+            select_fp64(a, tw + (__ffs(redo) - 1) / LPT, scratch);
         __syncwarp();
     }
 }
@@ -518,40 +718,54 @@ int check_router(const moe_shape_t* s, const moe_router_t* r, int T) {
     return MOE_OK;
 }
 
-int grid_for(int T) {
-    const long want = ((long)T + kWarps - 1) / kWarps;
+int grid_for(int T, int per_cta = kWarps) {
+    const long want = ((long)T + per_cta - 1) / per_cta;
     const long cap = (long)num_sms() * 16;
     return (int)(want < cap ? want : cap);
 }
 
-template <int PER>
+template <int LPT, int PER>
 cudaError_t launch_scored_per(const RouteArgs& a, int kind, int lpg, int vec, cudaStream_t stream) {
-    const dim3 grid(grid_for(a.T)), block(kWarps * 32);
-    const size_t smem = (size_t)kWarps * a.E * sizeof(double);
-    if (kind == kKeyLogit) return launch_pdl(scored_topk_kernel<PER, kKeyLogit>, grid, block, smem, stream, a, lpg, vec);
-    if (kind == kKeySigmoid)
-        return launch_pdl(scored_topk_kernel<PER, kKeySigmoid>, grid, block, smem, stream, a, lpg, vec);
-    return launch_pdl(scored_topk_kernel<PER, kKeySoftmax>, grid, block, smem, stream, a, lpg, vec);
+    const size_t smem = (size_t)kWarps * scratch_doubles(a.E) * sizeof(double) + LPT * (PER + 4) * sizeof(float);
+    auto launch = [&](auto kern) {
+        return launch_pdl(kern, dim3(grid_for(a.T, kWarps * (32 / LPT))), dim3(kWarps * 32), smem, stream, a, lpg, vec);
+    };
+    if (kind == kKeyLogit) return launch(scored_topk_kernel<LPT, PER, kKeyLogit>);
+    if (kind == kKeySigmoid) return launch(scored_topk_kernel<LPT, PER, kKeySigmoid>);
+    return launch(scored_topk_kernel<LPT, PER, kKeySoftmax>);
 }
 
 cudaError_t launch_scored(const RouteArgs& a, cudaStream_t stream) {
     const bool grouped = a.topk_groups < a.n_groups;
     const int kind = !a.bias && !(grouped && a.top2) ? kKeyLogit : a.sigmoid ? kKeySigmoid : kKeySoftmax;
     const int gs = a.E / a.n_groups;
-    int lpg = 32;
-    while (lpg * a.n_groups > 32) lpg >>= 1;
-    const int per = (gs + lpg - 1) / lpg;
+    // lanes per group and experts per lane when a token has `lanes` lanes (0: does not fit)
+    int lpg = 0;
+    auto fit = [&](int lanes) {
+        if (a.n_groups > lanes) return 0;
+        lpg = lanes;
+        while (lpg * a.n_groups > lanes) lpg >>= 1;
+        return (gs + lpg - 1) / lpg;
+    };
     const int vec = a.ksplit == 1 && gs % 4 == 0 && (reinterpret_cast<uintptr_t>(a.partials) & 15) == 0;
-    // more than 31 selected (no lane left for the next one) or more experts than a lane holds
+    // Two tokens per warp once every SM has dozens of tokens (65536 x 256: 77 against 88 us);
+    // below, one per warp ends sooner (4096: 12 against 15 us).
+    const int per16 = a.T >= 16384 ? fit(16) : 0;
+    if (per16 > 4 && per16 <= 16 && a.k <= 31) {
+        if (per16 <= 8) return launch_scored_per<16, 8>(a, kind, lpg, vec, stream);
+        return launch_scored_per<16, 16>(a, kind, lpg, vec, stream);
+    }
+    const int per = fit(32);
+    // more than 31 selected (no block left for the next one) or more experts than a lane holds
     if (a.k > 31 || per > 32)
         return launch_pdl(scored_topk_fp64_kernel, dim3(grid_for(a.T)), dim3(kWarps * 32),
                           (size_t)kWarps * a.E * sizeof(double), stream, a);
-    if (per <= 1) return launch_scored_per<1>(a, kind, lpg, vec, stream);
-    if (per <= 2) return launch_scored_per<2>(a, kind, lpg, vec, stream);
-    if (per <= 4) return launch_scored_per<4>(a, kind, lpg, vec, stream);
-    if (per <= 8) return launch_scored_per<8>(a, kind, lpg, vec, stream);
-    if (per <= 16) return launch_scored_per<16>(a, kind, lpg, vec, stream);
-    return launch_scored_per<32>(a, kind, lpg, vec, stream);
+    if (per <= 1) return launch_scored_per<32, 1>(a, kind, lpg, vec, stream);
+    if (per <= 2) return launch_scored_per<32, 2>(a, kind, lpg, vec, stream);
+    if (per <= 4) return launch_scored_per<32, 4>(a, kind, lpg, vec, stream);
+    if (per <= 8) return launch_scored_per<32, 8>(a, kind, lpg, vec, stream);
+    if (per <= 16) return launch_scored_per<32, 16>(a, kind, lpg, vec, stream);
+    return launch_scored_per<32, 32>(a, kind, lpg, vec, stream);
 }
 
 }  // namespace
