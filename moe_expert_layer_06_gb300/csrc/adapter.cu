@@ -491,64 +491,538 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     if (warp == 1) tmem_dealloc(tbase, C::kTmemCols);
 }
 
-// The token's adapter, or -1.
-__device__ __forceinline__ int adapter_id(const int32_t* adapter_of, int t, int n_adapters, const DevStatus& st) {
-    const int id = adapter_of[t];
-    if (id >= -1 && id < n_adapters) return id;
-    raise_status(st, kStatusInvalidExpert);
-    return -1;
-}
+// ---------------------------------------------------------------- v = s A x, few tokens
+// One CTA per adapter (or, with fewer tokens than adapters, per first token of an adapter)
+// and JR of its rows: the rows stream from memory once for up to NT tokens at a time, the
+// eight warps share the contraction.  The rows are what there is to read, so many small
+// CTAs keep them coming.
+constexpr int kFewTokens = 64;
+constexpr int JR = 2, NT = 4;
 
-// v[t][j] = s_i A_i[j] . x[t]: one warp per (token, j).
-__global__ void __launch_bounds__(256) shrink_kernel(const uint16_t* x, const uint16_t* m, const float* scaling,
-                                                     const int32_t* adapter_of, int T, int C, int r, int n_adapters,
-                                                     uint16_t* v, DevStatus st) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    for (long w = (long)blockIdx.x * 8 + (threadIdx.x >> 5); w < (long)T * r; w += (long)gridDim.x * 8) {
-        const int t = (int)(w / r), j = (int)(w % r);
-        const int i = adapter_id(adapter_of, t, n_adapters, st);
-        float sum = 0.0f;
-        if (i >= 0) {
-            const uint16_t* row = m + ((size_t)i * r + j) * C;
-            for (int k = lane; k < C; k += 32) sum += bf(x[(size_t)t * C + k]) * bf(row[k]);
-        }
+__device__ __forceinline__ void dot8(float& acc, const uint4& p, const uint4& q) {
+    const uint32_t* x = &p.x;
+    const uint32_t* y = &q.x;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) v[(size_t)t * r + j] = to_bf(i >= 0 ? sum * (scaling ? scaling[i] : 1.0f) : 0.0f);
+    for (int i = 0; i < 4; ++i) {
+        acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
+        acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
     }
 }
 
-// dv[t][j] = s_i sum_n dy[t][n] B_i[n][j]: one CTA per token, a thread per j.
-__global__ void __launch_bounds__(256) shrink_back_kernel(const uint16_t* dy, const uint16_t* b, const float* scaling,
-                                                          const int32_t* adapter_of, int T, int N, int r,
-                                                          int n_adapters, uint16_t* dv, DevStatus st) {
+template <int N>
+__device__ __forceinline__ void few_dots(const uint4* const (&xr)[NT], const uint4* const (&ar)[JR], int nv, int tid,
+                                         float (&acc)[NT][JR]) {
+#pragma unroll 2
+    for (int k = tid; k < nv; k += 256) {
+        uint4 av[JR], xv[N];
+#pragma unroll
+        for (int j = 0; j < JR; ++j) av[j] = __ldg(ar[j] + k);
+#pragma unroll
+        for (int n = 0; n < N; ++n) xv[n] = __ldg(xr[n] + k);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int j = 0; j < JR; ++j) dot8(acc[n][j], xv[n], av[j]);
+    }
+}
+
+__global__ void __launch_bounds__(256) shrink_few_kernel(const uint16_t* x, const uint16_t* m, const float* scaling,
+                                                         const int32_t* adapter_of, int T, int C, int r, int n_adapters,
+                                                         uint16_t* v, DevStatus st) {
     pdl_wait();
     pdl_launch_dependents();
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
-        const int i = adapter_id(adapter_of, t, n_adapters, st);
-        for (int j = threadIdx.x; j < r; j += blockDim.x) {
-            float sum = 0.0f;
-            if (i >= 0)
-                for (int n = 0; n < N; ++n) sum += bf(dy[(size_t)t * N + n]) * bf(b[((size_t)i * N + n) * r + j]);
-            dv[(size_t)t * r + j] = to_bf(i >= 0 ? sum * (scaling ? scaling[i] : 1.0f) : 0.0f);
+    __shared__ float part[8][NT][JR];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool by_token = T < n_adapters;
+    const int id0 = lane < T ? adapter_of[lane] : -2, id1 = 32 + lane < T ? adapter_of[32 + lane] : -2;
+    const int id = by_token ? __shfl_sync(0xffffffffu, blockIdx.x < 32 ? id0 : id1, blockIdx.x & 31) : (int)blockIdx.x;
+    if (blockIdx.y == 0 && (by_token || blockIdx.x == 0) && warp == 0) {
+        // tokens without adapter: v = 0
+        for (int h = 0; h < 2; ++h) {
+            const int t = h * 32 + lane, of = h ? id1 : id0;
+            if (t >= T || (of >= 0 && of < n_adapters) || (by_token && t != (int)blockIdx.x)) continue;
+            if (of != -1) raise_status(st, kStatusInvalidExpert);
+            for (int j = 0; j < r; j += 8) *reinterpret_cast<uint4*>(v + (size_t)t * r + j) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (id < 0 || id >= n_adapters) return;
+    uint32_t m0 = __ballot_sync(0xffffffffu, id0 == id), m1 = __ballot_sync(0xffffffffu, id1 == id);
+    if (by_token) {  // an earlier token of the same adapter does the work
+        const int f = m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
+        if (f != (int)blockIdx.x) return;
+    }
+    const int j0 = blockIdx.y * JR;
+    const uint4* ar[JR];
+#pragma unroll
+    for (int j = 0; j < JR; ++j) ar[j] = reinterpret_cast<const uint4*>(m + ((size_t)id * r + j0 + j) * C);
+    const float scale = scaling ? scaling[id] : 1.0f;
+    while (m0 | m1) {
+        int tok[NT], n = 0;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            tok[q] = 0;
+            if (m0) {
+                tok[q] = __ffs(m0) - 1;
+                m0 &= m0 - 1;
+                ++n;
+            } else if (m1) {
+                tok[q] = 31 + __ffs(m1);
+                m1 &= m1 - 1;
+                ++n;
+            }
+        }
+        const uint4* xr[NT];
+#pragma unroll
+        for (int q = 0; q < NT; ++q) xr[q] = reinterpret_cast<const uint4*>(x + (size_t)tok[q] * C);
+        float acc[NT][JR] = {};
+        if (n == 1) few_dots<1>(xr, ar, C / 8, tid, acc);
+        else if (n == 2) few_dots<2>(xr, ar, C / 8, tid, acc);
+        else few_dots<NT>(xr, ar, C / 8, tid, acc);
+        __syncthreads();  // part is free
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            if (q >= n) break;
+#pragma unroll
+            for (int j = 0; j < JR; ++j) {
+                float f = acc[q][j];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) f += __shfl_xor_sync(0xffffffffu, f, d);
+                if (lane == 0) part[warp][q][j] = f;
+            }
+        }
+        __syncthreads();
+        if (tid < n * JR) {
+            const int q = tid / JR, j = tid % JR;
+            float f = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) f += part[w][q][j];
+            int t = tok[0];
+#pragma unroll
+            for (int u = 1; u < NT; ++u) t = q == u ? tok[u] : t;
+            v[(size_t)t * r + j0 + j] = to_bf(f * scale);
         }
     }
 }
 
-// da_i[j][k] = sum over i's tokens of u[t][j] z[t][k] (transposed: db_i[k][j]).
-__global__ void __launch_bounds__(256) grad_kernel(const uint16_t* u, const uint16_t* z, const int32_t* adapter_of, int T,
-                                                   int C, int r, int n_adapters, int transposed, uint16_t* out) {
-    pdl_begin();
-    const int k = blockIdx.x * 256 + threadIdx.x;
-    const int j = blockIdx.y, i = blockIdx.z;
-    if (k >= C) return;
-    float sum = 0.0f;
-    for (int t = 0; t < T; ++t)
-        if (adapter_of[t] == i) sum += bf(u[(size_t)t * r + j]) * bf(z[(size_t)t * C + k]);
-    if (transposed) out[((size_t)i * C + k) * r + j] = to_bf(sum);
-    else out[((size_t)i * r + j) * C + k] = to_bf(sum);
+// ---------------------------------------------------------------- v and dv, many tokens
+// D[128 tokens][columns] = X tile . [A_i of the tile's adapters, stacked]^T on the tensor
+// cores: every token is multiplied with every adapter of its tile and keeps its own
+// columns, so the tokens are read once whatever their order.  Up to 256 columns at a time
+// (`per_pass` adapters); clusters share the contraction.  Backward: dY . B_i, with B_i
+// read MN-major.
+struct ShrinkArgs {
+    CUtensorMap x;   // box {64, 1, 128} of x [T][K] | dy [T][N]
+    CUtensorMap m;   // forward: box {64 k, cols} of A [n][r][K]; backward: box {64 r, 64 n} of B [n][N][r]
+    const float* scaling;
+    const int32_t* adapter_of;
+    int T, C, r, n_adapters;
+    int cols;        // columns of one adapter: r rounded up to 16 (forward) or 64 (backward)
+    int per_pass;    // 256 / cols
+    int splits, passes;  // CTAs per cluster; passes that run at the same time
+    uint16_t* v;     // [T][r]
+    DevStatus st;
+};
+constexpr int kShrinkStageBytes = 16384 + 32768;
+constexpr int kShrinkStages = 4;
+constexpr int kShrinkThreads = 192;
+constexpr int kShrinkSmem = 1024 + kShrinkStages * kShrinkStageBytes + 256 + 128 * 8 + kMaxAdapters / 8;
+
+template <bool BWD>
+__global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_constant__ ShrinkArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kShrinkStages * kShrinkStageBytes);
+    uint64_t* empty = full + kShrinkStages;
+    uint64_t* tfull = empty + kShrinkStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* count = reinterpret_cast<int*>(tmem_slot + 2);
+    int* ids = reinterpret_cast<int*>(smem + kShrinkStages * kShrinkStageBytes + 256);
+    int* list = ids + 128;
+    uint32_t* bits = reinterpret_cast<uint32_t*>(list + 128);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned long long limit = a.st.limit_ns;
+    const int S = a.splits;
+    const int rank = S > 1 ? (int)cluster_rank() : 0;
+    const int pass0 = (blockIdx.x / S) % a.passes;
+    const int row0 = (blockIdx.x / S / a.passes) * 128, rows = min(128, a.T - row0);
+    const int kc = (a.C + 63) / 64;
+    const int c0 = (int)((long)kc * rank / S), c1 = (int)((long)kc * (rank + 1) / S);
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kShrinkStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(tfull), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.x);
+        tma_prefetch_desc(&a.m);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 256);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    tile_adapters(a.adapter_of, row0, rows, a.n_adapters, 128, ids, list, bits, count, a.st, threadIdx.x, kShrinkThreads, 1);
+    const int n_list = *count;
+    if (pass0 == 0 && rank == 0)
+        for (int q = threadIdx.x; q < rows * (a.r / 8); q += kShrinkThreads)
+            if (ids[q / (a.r / 8)] < 0)
+                *reinterpret_cast<uint4*>(a.v + (size_t)row0 * a.r + (size_t)q * 8) = make_uint4(0, 0, 0, 0);
+
+    int stage = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    uint32_t armed = 0, armed_phase = 0;  // stages ever armed, and the parity of their last use
+    bool ok = true;
+    for (int pass = pass0; pass * a.per_pass < n_list; pass += a.passes) {
+        const int cnt = min(a.per_pass, n_list - pass * a.per_pass);
+        const int* mine = list + pass * a.per_pass;
+        if (warp == 0) {
+            if (lane == 0 && ok) {
+                const uint64_t pol = policy_evict_normal();
+                for (int c = c0; c < c1; ++c) {
+                    if (*abort_flag || !mbar_wait(smem_u32(&empty[stage]), phase ^ 1, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sx = smem_u32(smem + stage * kShrinkStageBytes), sm = sx + 16384;
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    mbar_arrive_expect_tx(fb, 16384 + cnt * a.cols * 128);
+                    armed |= 1u << stage;
+                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                    tma_load_3d(sx, &a.x, fb, c * 64, 0, row0, pol);
+                    for (int p = 0; p < cnt; ++p) {
+                        if (BWD) {
+                            for (int j0 = 0; j0 < a.cols; j0 += 64)
+                                tma_load_3d(sm + (p * a.cols + j0) * 128, &a.m, fb, j0, c * 64, mine[p], pol);
+                        } else {
+                            tma_load_3d(sm + p * a.cols * 128, &a.m, fb, c * 64, 0, mine[p], pol);
+                        }
+                    }
+                    if (++stage == kShrinkStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && ok) {
+                const uint32_t idesc = umma_idesc_bf16(128, cnt * a.cols) | (BWD ? kIdescBMnMajor : 0u);
+                for (int c = c0; c < c1; ++c) {
+                    if (*abort_flag || !mbar_wait(smem_u32(&full[stage]), phase, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sx = smem_u32(smem + stage * kShrinkStageBytes), sm = sx + 16384;
+                    const uint64_t ad = umma_desc_sw128(sx);
+                    const uint64_t bd = BWD ? umma_desc_mn_sw128(sm, 8192) : umma_desc_sw128(sm);
+                    const int steps = min(4, (a.C - c * 64 + 15) >> 4);
+                    for (int k = 0; k < steps; ++k)
+                        umma_bf16(tbase, ad + 2 * k, bd + (BWD ? 128 : 2) * k, idesc, c > c0 || k > 0);
+                    umma_commit(smem_u32(&empty[stage]));
+                    if (++stage == kShrinkStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                umma_commit(smem_u32(tfull));  // on a failure too: the products issued so far end
+            }
+        } else {
+            // each token's own columns into this CTA's share, [column][token]
+            if (ok) ok = mbar_wait(smem_u32(tfull), acc_phase, limit) && !*abort_flag;
+            if (ok) {
+                tc_fence_after();
+                const int q = warp & 3, row = q * 32 + lane;
+                float* part = reinterpret_cast<float*>(smem) + row;
+                for (int p = 0; p < cnt; ++p) {
+                    const bool own = ids[row] == mine[p];
+                    for (int g = 0; g * 16 < a.r; ++g) {
+                        float f[16];
+                        tmem_ld16(tbase + ((uint32_t)(q * 32) << 16) + p * a.cols + g * 16, f);
+                        tmem_ld_wait();
+                        if (own) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) part[(g * 16 + j) * 128] = f[j];
+                        }
+                        __syncwarp();
+                    }
+                }
+                tc_fence_before();
+            }
+        }
+        acc_phase ^= 1;
+        if (!ok) {
+            *abort_flag = 1;
+            raise_status(a.st, kStatusWaitTimeout);
+        }
+        __syncwarp();
+        if (S > 1) cluster_sync();
+        else __syncthreads();
+        tc_fence_after();
+        const int items = 128 * (a.r / 8);
+        const int i0 = (int)((long)items * rank / S), i1 = (int)((long)items * (rank + 1) / S);
+        for (int i = i0 + threadIdx.x; i < i1 && !*abort_flag; i += kShrinkThreads) {
+            const int row = i & 127, j0 = (i >> 7) * 8;
+            const int id = ids[row];
+            if (row >= rows || id < mine[0] || id > mine[cnt - 1]) continue;  // (the list ascends)
+            const float scale = a.scaling ? a.scaling[id] : 1.0f;
+            float f[8];
+            const uint32_t addr = smem_u32(smem) + (j0 * 128 + row) * 4;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[j] += S > 1 ? ld_peer(addr + j * 512, s) : reinterpret_cast<const float*>(smem)[(j0 + j) * 128 + row];
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = (uint32_t)to_bf(f[2 * j] * scale) | ((uint32_t)to_bf(f[2 * j + 1] * scale) << 16);
+            *reinterpret_cast<uint4*>(a.v + (size_t)(row0 + row) * a.r + j0) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        // the shares have been read before the next pass writes the stages
+        fence_async_smem();
+        if (S > 1) cluster_sync();
+        else __syncthreads();
+    }
+    if (warp == 0 && lane == 0)
+        for (int s = 0; s < kShrinkStages; ++s)
+            if ((armed >> s) & 1u) mbar_wait(smem_u32(&full[s]), (armed_phase >> s) & 1u, limit);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tbase, 256);
+}
+
+// ---------------------------------------------------------------- dA and dB
+// dA_i^T [features][r] = sum over i's tokens of x[t] dv[t]^T (dB_i: dy[t] v[t]^T): one CTA
+// per adapter and 128 features walks the 64-token chunks that hold tokens of its adapter.
+// Both operands are MN-major (the contraction runs over tokens).  In a chunk with other
+// tokens too, their rows are set to zero in shared memory, in both operands, so whatever
+// they hold stays out.
+struct GradArgs {
+    CUtensorMap z[2];  // box {64 features, 64 tokens} of x [T][K], dy [T][N]
+    CUtensorMap u[2];  // box {64 r, 64 tokens} of dv, v [T][r]
+    const int32_t* adapter_of;
+    int T, r;
+    int F[2];          // K, N
+    uint16_t* out[2];  // da [n][r][K], db [n][N][r]
+    DevStatus st;
+};
+constexpr int kGradThreads = 192;
+constexpr int kGradSegment = 4096;  // chunks whose marks are held at a time
+
+template <int RB>  // 64-column blocks of the rank
+struct GradCfg {
+    static constexpr int kStageBytes = 16384 + RB * 8192;
+    static constexpr int kStages = RB == 4 ? 4 : 3;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256 + kGradSegment;
+};
+
+template <int RB>
+__global__ void __launch_bounds__(kGradThreads, RB <= 2 ? 2 : 1) grad_kernel(const __grid_constant__ GradArgs a) {
+    using C = GradCfg<RB>;
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* landed = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+    uint64_t* full = landed + C::kStages;
+    uint64_t* empty = full + C::kStages;
+    uint64_t* done = empty + C::kStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* none = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    uint8_t* marks = smem + C::kStages * C::kStageBytes + 256;  // per chunk: 0 no token of the adapter, 1 some, 2 all
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned long long limit = a.st.limit_ns;
+    const int id = blockIdx.y;
+    const int blocks0 = (a.F[0] + 127) / 128;
+    const int side = (int)blockIdx.x >= blocks0;
+    const int f0 = ((int)blockIdx.x - (side ? blocks0 : 0)) * 128;
+    const int F = a.F[side];
+    const int chunks = (a.T + 63) / 64;
+    constexpr int kTmemCols = RB * 64;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(smem_u32(&landed[s]), 1);
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(done), 1);
+        *abort_flag = 0;
+        *none = 1;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.z[side]);
+        tma_prefetch_desc(&a.u[side]);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    pdl_wait();
+
+    int stage = 0;
+    uint32_t phase = 0, accum = 0;
+    uint32_t armed = 0, armed_phase = 0;
+    bool ok = true;
+    for (int seg = 0; seg < chunks; seg += kGradSegment) {
+        const int n = min(kGradSegment, chunks - seg);
+        for (int c = warp; c < n; c += kGradThreads / 32) {
+            const int t = (seg + c) * 64 + lane;
+            const bool b0 = t < a.T, b1 = t + 32 < a.T;
+            const bool e0 = b0 && a.adapter_of[t] == id, e1 = b1 && a.adapter_of[t + 32] == id;
+            const bool any = __any_sync(0xffffffffu, e0 || e1), all = __all_sync(0xffffffffu, e0 == b0 && e1 == b1);
+            if (lane == 0) {
+                marks[c] = any ? (all ? 2 : 1) : 0;
+                if (any) *none = 0;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            if (lane == 0 && ok) {
+                const uint64_t pol = policy_evict_normal();
+                for (int c = 0; c < n; ++c) {
+                    if (!marks[c]) continue;
+                    if (*abort_flag || !mbar_wait(smem_u32(&empty[stage]), phase ^ 1, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sz = smem_u32(smem + stage * C::kStageBytes), lb = smem_u32(&landed[stage]);
+                    const int t0 = (seg + c) * 64;
+                    mbar_arrive_expect_tx(lb, C::kStageBytes);
+                    armed |= 1u << stage;
+                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                    tma_load_3d(sz, &a.z[side], lb, f0, t0, 0, pol);
+                    tma_load_3d(sz + 8192, &a.z[side], lb, f0 + 64, t0, 0, pol);
+                    for (int b = 0; b < RB; ++b) tma_load_3d(sz + 16384 + b * 8192, &a.u[side], lb, b * 64, t0, 0, pol);
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && ok) {
+                const uint32_t idesc =
+                    umma_idesc_bf16(128, (a.r + 15) & ~15) | kIdescAMnMajor | kIdescBMnMajor;
+                for (int c = 0; c < n; ++c) {
+                    if (!marks[c]) continue;
+                    if (*abort_flag || !mbar_wait(smem_u32(&full[stage]), phase, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sz = smem_u32(smem + stage * C::kStageBytes);
+                    const uint64_t ad = umma_desc_mn_sw128(sz, 8192), bd = umma_desc_mn_sw128(sz + 16384, 8192);
+                    for (int k = 0; k < 4; ++k) {
+                        umma_bf16(tbase, ad + 128 * k, bd + 128 * k, idesc, accum);
+                        accum = 1;
+                    }
+                    umma_commit(smem_u32(&empty[stage]));
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        } else if (ok) {
+            const int tid = threadIdx.x - 64;
+            for (int c = 0; c < n; ++c) {
+                if (!marks[c]) continue;
+                if (*abort_flag || !mbar_wait(smem_u32(&landed[stage]), phase, limit)) {
+                    ok = false;
+                    break;
+                }
+                if (marks[c] == 1) {
+                    const int t0 = (seg + c) * 64;
+                    uint8_t* sz = smem + stage * C::kStageBytes;
+                    // 8 threads per token row; the 128-byte rows of all blocks
+                    for (int row = tid >> 3; row < 64; row += 16) {
+                        if (t0 + row < a.T && a.adapter_of[t0 + row] == id) continue;
+#pragma unroll
+                        for (int b = 0; b < 2 + RB; ++b)
+                            *reinterpret_cast<uint4*>(sz + b * 8192 + row * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    named_sync(1, 128);
+                }
+                if (tid == 0) mbar_arrive(smem_u32(&full[stage]));
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            raise_status(a.st, kStatusWaitTimeout);
+        }
+        __syncthreads();  // the marks are rewritten
+    }
+    if (warp == 0 && lane == 0)
+        for (int s = 0; s < C::kStages; ++s)
+            if ((armed >> s) & 1u) mbar_wait(smem_u32(&landed[s]), (armed_phase >> s) & 1u, limit);
+    if (warp == 1 && lane == 0) umma_commit(smem_u32(done));
+    if (warp == 1) {
+        if (lane == 0) mbar_wait(smem_u32(done), 0, limit);
+    } else if (warp >= 2) {
+        if (mbar_wait(smem_u32(done), 0, limit) && !*abort_flag) {
+            tc_fence_after();
+            const int q = warp & 3, feat = f0 + q * 32 + lane;
+            uint16_t* out = a.out[side];
+            for (int g = 0; g * 16 < a.r; ++g) {
+                float f[16];
+                tmem_ld16(tbase + ((uint32_t)(q * 32) << 16) + g * 16, f);
+                tmem_ld_wait();
+                if (*none) {  // no token: the accumulator was never written
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+                }
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = (uint32_t)to_bf(f[2 * j]) | ((uint32_t)to_bf(f[2 * j + 1]) << 16);
+                if (side) {  // db_i [feature][r]
+                    if (feat < F) {
+                        uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)id * F + feat) * a.r + g * 16);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (g * 16 + 8 < a.r) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                } else {  // da_i [r][feature], words of two features (as in the projection)
+                    const bool odd = lane & 1;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t o = __shfl_xor_sync(0xffffffffu, w[j], 1);
+                        const uint32_t p = __byte_perm(w[j], o, odd ? 0x3276 : 0x5410);
+                        const int col = g * 16 + 2 * j + (odd ? 1 : 0);
+                        if (feat < F && col < a.r)
+                            *reinterpret_cast<uint32_t*>(out + ((size_t)id * a.r + col) * F + (feat & ~1)) = p;
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tbase, kTmemCols);
 }
 
 int check_adapter(const moe_adapter_t* p, int T) {
@@ -653,6 +1127,93 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     return MOE_OK;
 }
 
+// v = scaling * (the token's A) . x, or dv = scaling * (the token's B)^T . dy
+template <bool BWD>
+int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, const float* scaling,
+           const int32_t* adapter_of, void* v, const DevStatus& st, cudaStream_t stream) {
+    const int C = BWD ? p->out_features : p->in_features;
+    cudaError_t e;
+    // Up to 64 tokens the adapters' rows are what is read, and no tile of 128 tokens fills.
+    if (!BWD && T <= kFewTokens) {
+        e = launch_pdl(shrink_few_kernel, dim3(std::min(T, p->n_adapters), p->rank / JR), dim3(256), 0, stream,
+                       static_cast<const uint16_t*>(tokens), static_cast<const uint16_t*>(m), scaling, adapter_of, T, C,
+                       (int)p->rank, (int)p->n_adapters, static_cast<uint16_t*>(v), st);
+    } else {
+        ShrinkArgs a;
+        const uint64_t c = C, r = p->rank, n = p->n_adapters;
+        int rc = make_tmap_3d(&a.x, tokens, c, 1, (uint64_t)T, c * 2, c * 2, 64, 1, 128);
+        if (rc) return rc;
+        a.cols = BWD ? (p->rank + 63) / 64 * 64 : (p->rank + 15) / 16 * 16;
+        a.per_pass = 256 / a.cols;
+        if (BWD) rc = make_tmap_3d(&a.m, m, r, c, n, r * 2, r * c * 2, 64, 64, 1);
+        else rc = make_tmap_3d(&a.m, m, c, r, n, c * 2, c * r * 2, 64, a.cols, 1);
+        if (rc) return rc;
+        a.scaling = scaling;
+        a.adapter_of = adapter_of;
+        a.T = T;
+        a.C = C;
+        a.r = p->rank;
+        a.n_adapters = p->n_adapters;
+        a.v = static_cast<uint16_t*>(v);
+        a.st = st;
+        // clusters share the contraction (four chunks per CTA at least) and a tile's passes run
+        // side by side as far as there are SMs
+        const int sms = num_sms(), tiles = (T + 127) / 128, kc = (C + 63) / 64;
+        a.splits = 1;
+        while (a.splits < 8 && tiles * (a.splits + 1) <= sms && (a.splits + 1) * 4 <= kc) ++a.splits;
+        const int most = (std::min(std::min(T, 128), p->n_adapters) + a.per_pass - 1) / a.per_pass;
+        a.passes = std::max(1, std::min(most, sms / (tiles * a.splits)));
+        auto kern = shrink_kernel<BWD>;
+        static std::atomic<uint64_t> configured{0};
+        e = configure_once(configured, [&] {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkSmem);
+        });
+        if (e == cudaSuccess)
+            e = launch_pdl_cluster(kern, dim3(tiles * a.passes * a.splits), dim3(kShrinkThreads), kShrinkSmem, stream,
+                                   a.splits, a);
+    }
+    if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "adapter rank-product launch: %s", cudaGetErrorString(e));
+    return MOE_OK;
+}
+
+template <int RB>
+cudaError_t launch_grad_rb(const GradArgs& a, int n_adapters, cudaStream_t stream) {
+    auto kern = grad_kernel<RB>;
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = configure_once(configured, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GradCfg<RB>::kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((a.F[0] + 127) / 128 + (a.F[1] + 127) / 128, n_adapters), dim3(kGradThreads),
+                      GradCfg<RB>::kSmemBytes, stream, a);
+}
+
+int gradients(const moe_adapter_t* p, int T, const void* dy, const void* x, const void* dv, const void* v,
+              const int32_t* adapter_of, void* da, void* db, const DevStatus& st, cudaStream_t stream) {
+    GradArgs a;
+    const uint64_t K = p->in_features, N = p->out_features, r = p->rank, t = T;
+    int rc;
+    if ((rc = make_tmap_3d(&a.z[0], x, K, t, 1, K * 2, K * t * 2, 64, 64, 1)) ||
+        (rc = make_tmap_3d(&a.z[1], dy, N, t, 1, N * 2, N * t * 2, 64, 64, 1)) ||
+        (rc = make_tmap_3d(&a.u[0], dv, r, t, 1, r * 2, r * t * 2, 64, 64, 1)) ||
+        (rc = make_tmap_3d(&a.u[1], v, r, t, 1, r * 2, r * t * 2, 64, 64, 1)))
+        return rc;
+    a.adapter_of = adapter_of;
+    a.T = T;
+    a.r = p->rank;
+    a.F[0] = p->in_features;
+    a.F[1] = p->out_features;
+    a.out[0] = static_cast<uint16_t*>(da);
+    a.out[1] = static_cast<uint16_t*>(db);
+    a.st = st;
+    const int rb = (p->rank + 63) / 64;
+    const cudaError_t e = rb == 1   ? launch_grad_rb<1>(a, p->n_adapters, stream)
+                          : rb == 2 ? launch_grad_rb<2>(a, p->n_adapters, stream)
+                                    : launch_grad_rb<4>(a, p->n_adapters, stream);
+    if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "adapter gradient launch: %s", cudaGetErrorString(e));
+    return MOE_OK;
+}
+
 #define ADAPTER_CUDA(call, what)                                                                          \
     do {                                                                                                  \
         const cudaError_t e_ = (call);                                                                    \
@@ -688,11 +1249,7 @@ int moe_adapter_project(const moe_adapter_t* adapter, int T, const void* x, cons
     if ((rc = api_device_status(&st))) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint16_t* v = static_cast<uint16_t*>(v_out ? v_out : ws);
-    const long warps = (long)T * adapter->rank;
-    ADAPTER_CUDA(launch_pdl(shrink_kernel, dim3((unsigned)std::min<long>((warps + 7) / 8, num_sms() * 8L)), dim3(256), 0,
-                            s, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(a), scaling, adapter_of, T,
-                            adapter->in_features, adapter->rank, adapter->n_adapters, v, st),
-                 "adapter shrink launch");
+    if ((rc = shrink<false>(adapter, T, x, a, scaling, adapter_of, v, st, s))) return rc;
     return project<false>(adapter, T, x, w, b, adapter_of, v, out, out_fp32, st, s);
 }
 
@@ -722,20 +1279,10 @@ int moe_adapter_project_backward(const moe_adapter_t* adapter, int T, const void
     if (!dx && !da) return MOE_OK;
     DevStatus st;
     if ((rc = api_device_status(&st))) return rc;
-    uint16_t* dv = static_cast<uint16_t*>(ws);
-    ADAPTER_CUDA(launch_pdl(shrink_back_kernel, dim3(std::min(T, num_sms() * 8)), dim3(256), 0, s,
-                            static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(b), scaling, adapter_of, T, N, r,
-                            n, dv, st),
-                 "adapter backward shrink launch");
+    void* dv = ws;
+    if ((rc = shrink<true>(adapter, T, dy, b, scaling, adapter_of, dv, st, s))) return rc;
     if (dx && (rc = project<true>(adapter, T, dy, w, a, adapter_of, dv, dx, 0, st, s))) return rc;
-    if (da) {
-        ADAPTER_CUDA(launch_pdl(grad_kernel, dim3((K + 255) / 256, r, n), dim3(256), 0, s, (const uint16_t*)dv,
-                                static_cast<const uint16_t*>(x), adapter_of, T, K, r, n, 0, static_cast<uint16_t*>(da)),
-                     "adapter gradient launch");
-        ADAPTER_CUDA(launch_pdl(grad_kernel, dim3((N + 255) / 256, r, n), dim3(256), 0, s, static_cast<const uint16_t*>(v),
-                                static_cast<const uint16_t*>(dy), adapter_of, T, N, r, n, 1, static_cast<uint16_t*>(db)),
-                     "adapter gradient launch");
-    }
+    if (da) return gradients(adapter, T, dy, x, dv, v, adapter_of, da, db, st, s);
     return MOE_OK;
 }
 

@@ -137,6 +137,20 @@ def test_backward_matches_the_definition(T, K, N, r, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r,n", [(1500, 136, 8200, 24, 3), (1100, 8200, 264, 40, 2), (2100, 264, 520, 16, 700)])
+def test_more_tiles_than_processors_and_many_adapters_per_tile(T, K, N, r, n):
+    """Forward and backward with several tiles per CTA, and with nearly every token's adapter its own."""
+    for ids in ("runs", "each"):
+        c = Case(T, K, N, r, n, ids)
+        y, v = c.forward()
+        dx, da, db = c.backward(v)
+        assert m.moe_check_status() == 0
+        ref = c.reference()
+        for name, got in (("y", y), ("dx", dx), ("da", da), ("db", db)):
+            close(got, *ref[name], name=name + " " + ids)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_no_adapters_no_scaling_and_fp32_output(T):
     c = Case(T, 264, 392, 16, 4, "none", scaled=False)
