@@ -45,6 +45,26 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// One lane of the (converged) warp.  TMA and UMMA operands have to sit in uniform
+// registers: where the whole warp runs a loop and only the issue is guarded this way, they
+// stay there (a loop inside `if (lane == 0)` took 540 cycles more per K chunk).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The whole warp waits for the phase: false on a timeout, or when another warp gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
+                                          unsigned long long limit) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        if (!ok) ok = !*abort_flag && mbar_wait(bar, parity, limit);
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    return ok;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -53,6 +73,24 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Tiled load of a box into every CTA of `mask` (same offsets), completing on each one's mbarrier.
+__device__ __forceinline__ void tma_load_3d_mcast(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                                  uint16_t mask, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "h"(mask), "l"(policy)
+        : "memory");
+}
+
+// Arrive on the mbarrier at this offset of every CTA of `mask` when this thread's tcgen05 ops are done.
+__device__ __forceinline__ void umma_commit_mcast(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
 }
 
 // fp32 at the same shared-memory address in CTA `rank` of the cluster
@@ -113,13 +151,14 @@ __device__ __forceinline__ void tile_adapters(const int32_t* adapter_of, int row
 struct ProjArgs {
     CUtensorMap w;      // forward: box {64 k, 128 n} of W [N][K]; backward: box {64 k, 64 n}
     CUtensorMap lr;     // forward: box {64 r, 128 n} of B [n][N][r]; backward: box {64 k, 64 r} of A [n][r][K]
-    CUtensorMap x;      // tokens: box {64, 1, bn} of x [T][K] | dy [T][N]
+    CUtensorMap x;      // tokens: box {64, 1, bn / mcast} of x [T][K] | dy [T][N]
     const int32_t* adapter_of;
     const uint16_t* v;  // [T][r] v | dv
     const uint16_t* lr_ptr;  // what `lr` maps
     int T, O, C, r, n_adapters;  // O output features, C contracted features
     int bn;             // tokens of a tile (a multiple of 16)
-    int splits;         // CTAs of a cluster that share one tile's contraction
+    int splits;         // CTAs of a cluster that share one tile's contraction, or
+    int mcast;          // CTAs of a cluster with 128 features each that share their tokens' loads
     void* out;          // [T][O]
     int out_fp32;
     DevStatus st;
@@ -149,6 +188,9 @@ struct ProjCfg {
 // tokens in turn; the accumulator is double buffered, so a tile's stores run under the
 // next tile's products.  A cluster's CTAs take a share of the contraction each and one
 // tile only; their fp32 sums meet in distributed shared memory, added in rank order.
+// With many tiles what runs out first is the path from L2 to the SMs (a 128 x 256 tile
+// takes 48 KB per 64 of the contraction): clusters of `mcast` CTAs, neighbours along the
+// features, each load a slice of the tokens into all of them (24 KB for 4).
 // The kernel before this one in the stream writes only v (it waited for its own
 // predecessors before it let this one start), so only the readers of v wait for it.
 template <bool BWD, int BN>
@@ -174,17 +216,20 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
     const int S = a.splits;
+    const int M = a.mcast;
     const int rank = S > 1 ? (int)cluster_rank() : 0;
-    const int m_tiles = (a.O + 127) / 128;
+    const int peer = M > 1 ? (int)cluster_rank() : 0;
+    const uint16_t mask = (uint16_t)((1 << M) - 1);
+    const int m_tiles = ((a.O + 127) / 128 + M - 1) / M;  // per cluster
     const int n_tiles = m_tiles * ((a.T + a.bn - 1) / a.bn);
-    const int first = blockIdx.x / S, step = gridDim.x / S;
+    const int first = blockIdx.x / (S * M), step = gridDim.x / (S * M);
     const int kc = (a.C + 63) / 64, rc = (a.r + 63) / 64;
     const int c0 = (int)((long)kc * rank / S), c1 = (int)((long)kc * (rank + 1) / S);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&empty[s]), M);
             mbar_init(smem_u32(&landed[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -206,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     }
     tc_fence_before();
     __syncthreads();
+    if (M > 1) cluster_sync();  // the barriers of every CTA exist before any of them is signalled
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
     auto give_up = [&]() {
@@ -213,110 +259,126 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         raise_status(a.st, kStatusWaitTimeout);
     };
 
+    const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed);
+    const uint32_t stage_u = smem_u32(smem);
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t pol = policy_evict_normal();
-            bool ok = true;
-            int stage = 0;
-            uint32_t phase = 0, land_phase = 0;
-            uint32_t armed[C::kStages];  // per stage: 0 never, else 1 + parity, + 2 for an adapter tile
-            for (int s = 0; s < C::kStages; ++s) armed[s] = 0;
-            for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
-                const int m0 = (i % m_tiles) * 128, row0 = (i / m_tiles) * a.bn;
-                for (int c = c0; c < c1; ++c) {
-                    if (*abort_flag || !mbar_wait(smem_u32(&empty[stage]), phase ^ 1, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = smem_u32(smem + stage * C::kStageBytes), fb = smem_u32(&full[stage]);
+        const uint64_t pol = policy_evict_normal();
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0, land_phase = 0;
+        uint32_t used = 0, used_land = 0, used_phase = 0;  // stages filled, whether by an adapter tile, parity
+        auto advance = [&](bool land) {
+            const uint32_t bit = 1u << stage, par = land ? (land_phase >> stage) & 1u : phase;
+            used |= bit;
+            used_land = land ? used_land | bit : used_land & ~bit;
+            used_phase = par ? used_phase | bit : used_phase & ~bit;
+            if (land) land_phase ^= bit;
+            if (++stage == C::kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        };
+        for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
+            const int m0 = ((i % m_tiles) * M + peer) * 128, row0 = (i / m_tiles) * a.bn;
+            for (int c = c0; c < c1; ++c) {
+                if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
+                if (elect_one()) {
+                    const uint32_t sa = stage_u + stage * C::kStageBytes, fb = full_u + stage * 8;
                     mbar_arrive_expect_tx(fb, kABytes + a.bn * 128);
-                    armed[stage] = 1 + phase;
                     if (BWD) {
                         tma_load_3d(sa, &a.w, fb, m0, c * 64, 0, pol);
                         tma_load_3d(sa + kABytes / 2, &a.w, fb, m0 + 64, c * 64, 0, pol);
                     } else {
                         tma_load_3d(sa, &a.w, fb, c * 64, m0, 0, pol);
                     }
-                    tma_load_3d(sa + kABytes, &a.x, fb, c * 64, 0, row0, pol);
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1;
+                    if (M > 1) {
+                        const int slice = a.bn / M * peer;
+                        tma_load_3d_mcast(sa + kABytes + slice * 128, &a.x, fb, c * 64, 0, row0 + slice, mask, pol);
+                    } else {
+                        tma_load_3d(sa + kABytes, &a.x, fb, c * 64, 0, row0, pol);
                     }
                 }
-                if (!ok || !(ok = mbar_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, limit))) break;
-                const TileList& tl = lists[n & 1];
-                for (int e = rank; e < tl.count * rc; e += S) {
-                    if (*abort_flag || !mbar_wait(smem_u32(&empty[stage]), phase ^ 1, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = smem_u32(smem + stage * C::kStageBytes), lb = smem_u32(&landed[stage]);
+                __syncwarp();
+                advance(false);
+            }
+            if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
+            const TileList& tl = lists[n & 1];
+            for (int e = rank; e < tl.count * rc; e += S) {
+                if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
+                if (elect_one()) {
+                    const uint32_t sa = stage_u + stage * C::kStageBytes, lb = landed_u + stage * 8;
                     const int id = tl.list[e / rc], j0 = (e % rc) * 64;
                     mbar_arrive_expect_tx(lb, kABytes);
-                    armed[stage] = 3 + ((land_phase >> stage) & 1u);
-                    land_phase ^= 1u << stage;
                     if (BWD) {
                         tma_load_3d(sa, &a.lr, lb, m0, j0, id, pol);
                         tma_load_3d(sa + kABytes / 2, &a.lr, lb, m0 + 64, j0, id, pol);
                     } else {
                         tma_load_3d(sa, &a.lr, lb, j0, m0, id, pol);
                     }
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                advance(true);
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        // every copy has landed before the CTA exits
+        for (int s = 0; s < C::kStages; ++s)
+            if ((used >> s) & 1u)
+                mbar_wait(((used_land >> s) & 1u ? landed_u : full_u) + s * 8, (used_phase >> s) & 1u, limit);
+        // and every CTA's products of this one's last stages have been signalled here
+        if (M > 1 && ok)
+            for (int s = 0; s < C::kStages; ++s) {
+                mbar_wait(empty_u + stage * 8, phase ^ 1, limit);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok) give_up();
-            // every copy has landed before the CTA exits
-            for (int s = 0; s < C::kStages; ++s)
-                if (armed[s]) mbar_wait(smem_u32(armed[s] >= 3 ? &landed[s] : &full[s]), (armed[s] - 1) & 1, limit);
-        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = umma_idesc_bf16(128, a.bn) | (BWD ? kIdescAMnMajor : 0u);
-            bool ok = true;
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
-                const uint32_t d = tbase + (n & 1) * BN;
-                if (*abort_flag || !mbar_wait(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, limit)) {
-                    ok = false;
-                    break;
-                }
+        const uint32_t idesc = umma_idesc_bf16(128, a.bn) | (BWD ? kIdescAMnMajor : 0u);
+        const uint64_t ad0 = BWD ? umma_desc_mn_sw128(stage_u, kABytes / 2) : umma_desc_sw128(stage_u);
+        const uint64_t bd0 = umma_desc_sw128(stage_u + kABytes);
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
+            const uint32_t d = tbase + (n & 1) * BN;
+            if (!(ok = warp_wait(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, limit))) break;
+            tc_fence_after();
+            uint32_t accum = 0;
+            auto chunk = [&](int left) {
+                if (!(ok = warp_wait(full_u + stage * 8, phase, abort_flag, limit))) return;
                 tc_fence_after();
-                uint32_t accum = 0;
-                auto chunk = [&](int left) {
-                    if (*abort_flag || !mbar_wait(smem_u32(&full[stage]), phase, limit)) {
-                        ok = false;
-                        return;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * C::kStageBytes);
-                    const uint64_t ad = BWD ? umma_desc_mn_sw128(sa, kABytes / 2) : umma_desc_sw128(sa);
-                    const uint64_t bd = umma_desc_sw128(sa + kABytes);
-                    const int steps = min(4, (left + 15) >> 4);
-                    for (int k = 0; k < steps; ++k) {  // 16 of the contraction: 32 bytes along K, or 16 K rows
-                        umma_bf16(d, ad + (BWD ? 128 : 2) * k, bd + 2 * k, idesc, accum);
-                        accum = 1;
-                    }
-                    umma_commit(smem_u32(&empty[stage]));
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                };
-                for (int c = c0; c < c1 && ok; ++c) chunk(a.C - c * 64);
-                if (!ok || !(ok = mbar_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, limit))) break;
-                const int n_ext = lists[n & 1].count * rc;
-                for (int e = rank; e < n_ext && ok; e += S) chunk(a.r - (e % rc) * 64);
-                umma_commit(smem_u32(&tfull[n & 1]));
-            }
-            if (!ok) give_up();
-            // all MMAs of this thread are complete before TMEM is freed
-            umma_commit(smem_u32(done));
-            mbar_wait(smem_u32(done), 0, limit);
+                if (elect_one()) {
+                    const uint64_t ad = ad0 + stage * (C::kStageBytes >> 4), bd = bd0 + stage * (C::kStageBytes >> 4);
+                    // 16 of the contraction per instruction: 32 bytes along K, or 16 K rows
+                    constexpr int kAStep = BWD ? 128 : 2;
+                    umma_bf16(d, ad, bd, idesc, accum);
+                    if (left > 16) umma_bf16(d, ad + kAStep, bd + 2, idesc, 1);
+                    if (left > 32) umma_bf16(d, ad + 2 * kAStep, bd + 4, idesc, 1);
+                    if (left > 48) umma_bf16(d, ad + 3 * kAStep, bd + 6, idesc, 1);
+                    if (M > 1) umma_commit_mcast(empty_u + stage * 8, mask);
+                    else umma_commit(empty_u + stage * 8);
+                }
+                __syncwarp();
+                accum = 1;
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            for (int c = c0; c < c1 && ok; ++c) chunk(a.C - c * 64);
+            if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
+            const int n_ext = lists[n & 1].count * rc;
+            for (int e = rank; e < n_ext && ok; e += S) chunk(a.r - (e % rc) * 64);
+            if (elect_one()) umma_commit(smem_u32(&tfull[n & 1]));
+            __syncwarp();
         }
+        if (!ok && lane == 0) give_up();
+        // all MMAs of this warp are complete before TMEM is freed
+        if (elect_one()) umma_commit(smem_u32(done));
+        __syncwarp();
+        mbar_wait(smem_u32(done), 0, limit);
     } else if (warp < 6) {
         // ---- adapter lists and v chunks
         const int tid = threadIdx.x - 64;  // 0..127
@@ -383,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         const int q = warp & 3;
         bool ok = true;
         for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
-            const int m0 = (i % m_tiles) * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
+            const int m0 = ((i % m_tiles) * M + peer) * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             const TileList& tl = lists[n & 1];
             if (*abort_flag || !mbar_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, limit)) {
                 ok = false;
@@ -483,6 +545,10 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 }
             }
         cluster_sync();  // no CTA leaves while another reads its shared memory
+    }
+    if (M > 1) {
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another may signal it
     }
     pdl_wait();  // the grid is complete only when the v kernel is
     tc_fence_before();
@@ -1057,12 +1123,40 @@ cudaError_t launch_project_bn(const ProjArgs& a, int grid, cudaStream_t stream) 
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ProjCfg<BN>::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(kern, dim3(grid), dim3(kThreads), ProjCfg<BN>::kSmemBytes, stream, a.splits, a);
+    return launch_pdl_cluster(kern, dim3(grid), dim3(kThreads), ProjCfg<BN>::kSmemBytes, stream, a.splits * a.mcast, a);
 }
 
-// How a projection of T tokens to O features is cut: tokens per tile, CTAs per tile, grid.
+// Clusters of 4 CTAs that fill an SM each and are resident at a time (per device, asked once).
+int clusters_of_4() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / 8;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = ProjCfg<256>::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto kern = project_kernel<false, 256>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ProjCfg<256>::kSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = num_sms() / 8;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// How a projection of T tokens to O features is cut: token capacity and tokens per tile,
+// CTAs per cluster (sharing the contraction, or the token loads), grid.
 struct ProjPlan {
-    int cap, bn, splits, grid;
+    int cap, bn, splits, mcast, grid;
 };
 
 ProjPlan project_plan(int T, int O, int C) {
@@ -1070,21 +1164,32 @@ ProjPlan project_plan(int T, int O, int C) {
     const int sms = num_sms(), m_tiles = (O + 127) / 128, kc = (C + 63) / 64;
     p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
     p.bn = p.cap;
-    p.splits = 1;
+    p.splits = p.mcast = 1;
+    int slots = sms, units = m_tiles;  // CTAs (or clusters) at a time; tiles (or groups of them) per token tile
+    // more tiles than SMs: clusters of four along the features
+    if ((long)m_tiles * ((T + 255) / 256) > sms) {
+        p.mcast = 4;
+        slots = clusters_of_4();
+        units = (m_tiles + 3) / 4;
+    }
     if (T > 256) {
-        // the tile height whose rounds over the SMs cost least: rounds x (tokens + a
+        // the tile height whose rounds over the slots cost least: rounds x (tokens + a
         // fixed 16 for the accumulator's hand-over)
         long best = -1;
-        for (int bn = 256; bn >= 128; bn -= 16) {
-            const long tiles = (long)m_tiles * ((T + bn - 1) / bn);
-            const long cost = (tiles + sms - 1) / sms * (bn + 16);
+        for (int bn = 256; bn >= 128; bn -= 32) {
+            const long tiles = (long)units * ((T + bn - 1) / bn);
+            const long cost = (tiles + slots - 1) / slots * (bn + 16);
             if (best < 0 || cost < best) {
                 best = cost;
                 p.bn = bn;
             }
         }
     }
-    const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
+    const long tiles = (long)units * ((T + p.bn - 1) / p.bn);
+    if (p.mcast > 1) {
+        p.grid = (int)std::min<long>(tiles, slots) * p.mcast;
+        return p;
+    }
     const int resident = p.cap <= 64 ? 2 : 1;
     // few tiles: clusters share a tile's contraction, four chunks of it per CTA at least
     while (p.splits < 8 && tiles * (p.splits + 1) <= (long)sms * resident && (p.splits + 1) * 4 <= kc) ++p.splits;
@@ -1106,13 +1211,14 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     const ProjPlan plan = project_plan(T, a.O, a.C);
     a.bn = plan.bn;
     a.splits = plan.splits;
+    a.mcast = plan.mcast;
     int rc = make_tmap_3d(&a.w, w, K, N, 1, K * 2, K * N * 2, 64, BWD ? 64 : 128, 1);
     if (rc) return rc;
     if (BWD) rc = make_tmap_3d(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, 64, 1);
     else rc = make_tmap_3d(&a.lr, lr, r, N, n, r * 2, r * N * 2, 64, 128, 1);
     if (rc) return rc;
     const uint64_t C = a.C;
-    if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.bn))) return rc;
+    if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.bn / plan.mcast))) return rc;
     a.lr_ptr = static_cast<const uint16_t*>(lr);
     a.adapter_of = adapter_of;
     a.v = static_cast<const uint16_t*>(v);
