@@ -75,21 +75,65 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Tiled load of a box into every CTA of `mask` (same offsets), completing on each one's mbarrier.
-__device__ __forceinline__ void tma_load_3d_mcast(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
-                                                  uint16_t mask, uint64_t policy) {
+// ---- CTA pairs (cta_group::2): one product over the shared memory and tensor memory of both
+// The address of `addr` in the pair's leader.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(addr));
+    return a;
+}
+
+// Tiled load into this CTA, completing on an mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                                 uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "h"(mask), "l"(policy)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
         : "memory");
 }
 
-// Arrive on the mbarrier at this offset of every CTA of `mask` when this thread's tcgen05 ops are done.
-__device__ __forceinline__ void umma_commit_mcast(uint32_t bar, uint16_t mask) {
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(mask)
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// D (+)= A B^T over the pair: 128 rows of A and half the rows of B in each CTA.
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on the mbarrier at this offset of both CTAs when this thread's products are done.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
         : "memory");
 }
 
@@ -151,14 +195,13 @@ __device__ __forceinline__ void tile_adapters(const int32_t* adapter_of, int row
 struct ProjArgs {
     CUtensorMap w;      // forward: box {64 k, 128 n} of W [N][K]; backward: box {64 k, 64 n}
     CUtensorMap lr;     // forward: box {64 r, 128 n} of B [n][N][r]; backward: box {64 k, 64 r} of A [n][r][K]
-    CUtensorMap x;      // tokens: box {64, 1, bn / mcast} of x [T][K] | dy [T][N]
+    CUtensorMap x;      // tokens: box {64, 1, tokens of one CTA} of x [T][K] | dy [T][N]
     const int32_t* adapter_of;
     const uint16_t* v;  // [T][r] v | dv
     const uint16_t* lr_ptr;  // what `lr` maps
     int T, O, C, r, n_adapters;  // O output features, C contracted features
     int bn;             // tokens of a tile (a multiple of 16)
-    int splits;         // CTAs of a cluster that share one tile's contraction, or
-    int mcast;          // CTAs of a cluster with 128 features each that share their tokens' loads
+    int splits;         // CTAs of a cluster that share one tile's contraction
     void* out;          // [T][O]
     int out_fp32;
     DevStatus st;
@@ -171,6 +214,88 @@ struct TileList {
     int list[kMaxTile];  // distinct adapters
     uint32_t odd[kMaxExtra / 32];  // adapter chunks with an infinity or NaN in this tile
 };
+
+// One adapter chunk of a tile, by 128 threads: sb gets v[.., j0..] of the tokens of adapter
+// id (`n` tokens from row0 with adapters ids[]), zeros elsewhere.  Zero times an infinity
+// or NaN of this adapter would reach the other adapters' tokens: such elements leave its
+// tile st_a here (true: there were some) and are added to their own tokens in the epilogue.
+__device__ __forceinline__ bool fill_v(const ProjArgs& a, const int* ids, int n, int row0, int id, int j0, uint8_t* st_a,
+                                       uint8_t* sb, int tid) {
+    for (int q = tid; q < n * 8; q += 128) {
+        const int row = q >> 3, seg = q & 7;
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (ids[row] == id && j0 + seg * 8 < a.r)
+            val = *reinterpret_cast<const uint4*>(a.v + (size_t)(row0 + row) * a.r + j0 + seg * 8);
+        *reinterpret_cast<uint4*>(sb + row * 128 + ((seg ^ (row & 7)) << 4)) = val;
+    }
+    bool hit = false;
+    for (int q = tid; q < kABytes / 16; q += 128) {
+        uint4* at = reinterpret_cast<uint4*>(st_a) + q;
+        uint4 val = *at;
+        if (not_finite(val.x) | not_finite(val.y) | not_finite(val.z) | not_finite(val.w)) {
+            val.x = finite_part(val.x);
+            val.y = finite_part(val.y);
+            val.z = finite_part(val.z);
+            val.w = finite_part(val.w);
+            *at = val;
+            hit = true;
+        }
+    }
+    return hit;
+}
+
+__device__ __forceinline__ bool has_odd(const TileList& tl, int n_ext) {
+    bool any = false;
+    for (int w = 0; w * 32 < n_ext; ++w) any |= tl.odd[w] != 0;
+    return any;
+}
+
+// The infinities and NaN that were taken out of the adapter tiles, for 16 tokens from t0
+// (position at in the tile) and one feature.
+template <bool BWD>
+__device__ __noinline__ void add_odd(const ProjArgs& a, const TileList& tl, int n_ext, int rc, int t0, int at, int feat,
+                                     float (&y)[16]) {
+    pdl_wait();  // v
+    for (int w = 0; w * 32 < n_ext; ++w) {
+        for (uint32_t b = tl.odd[w]; b; b &= b - 1) {
+            const int e = w * 32 + __ffs(b) - 1;
+            const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+            for (int j = 0; j < 16; ++j) {
+                if (tl.ids[at + j] != id) continue;
+                for (int l = j0; l < min(a.r, j0 + 64); ++l) {
+                    const size_t el = BWD ? ((size_t)id * a.r + l) * a.O + feat : ((size_t)id * a.O + feat) * a.r + l;
+                    const float u = bf(a.lr_ptr[el]);
+                    if (!isfinite(u)) y[j] += u * bf(a.v[(size_t)(t0 + j) * a.r + l]);
+                }
+            }
+        }
+    }
+}
+
+// Feature `feat` (this lane's) of up to 16 tokens from t0, `n` of them valid.
+__device__ __forceinline__ void store_group(const ProjArgs& a, int t0, int n, int feat, const float (&v)[16]) {
+    if (a.out_fp32) {
+        float* dst = reinterpret_cast<float*>(a.out) + (size_t)t0 * a.O + feat;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (feat < a.O && j < n) dst[(size_t)j * a.O] = v[j];
+        return;
+    }
+    // words of two features: lanes 2m and 2m+1 swap half their tokens, so the even lane
+    // holds the even tokens of features (2m, 2m+1) and the odd lane the odd ones
+    // (O % 8 == 0: both features of a pair are valid together)
+    const bool odd = threadIdx.x & 1;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + (size_t)t0 * a.O + (feat & ~1));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 p2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        const uint32_t p = *reinterpret_cast<const uint32_t*>(&p2);
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, p, 1);
+        const uint32_t w = __byte_perm(p, o, odd ? 0x3276 : 0x5410);
+        const int col = 2 * j + (odd ? 1 : 0);
+        if (feat < a.O && col < n) dst[(size_t)col * (a.O >> 1)] = w;
+    }
+}
 
 // BN: capacity of the token operand.  Up to 64 tokens two CTAs share an SM.
 template <int BN>
@@ -188,9 +313,6 @@ struct ProjCfg {
 // tokens in turn; the accumulator is double buffered, so a tile's stores run under the
 // next tile's products.  A cluster's CTAs take a share of the contraction each and one
 // tile only; their fp32 sums meet in distributed shared memory, added in rank order.
-// With many tiles what runs out first is the path from L2 to the SMs (a 128 x 256 tile
-// takes 48 KB per 64 of the contraction): clusters of `mcast` CTAs, neighbours along the
-// features, each load a slice of the tokens into all of them (24 KB for 4).
 // The kernel before this one in the stream writes only v (it waited for its own
 // predecessors before it let this one start), so only the readers of v wait for it.
 template <bool BWD, int BN>
@@ -216,20 +338,17 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
     const int S = a.splits;
-    const int M = a.mcast;
     const int rank = S > 1 ? (int)cluster_rank() : 0;
-    const int peer = M > 1 ? (int)cluster_rank() : 0;
-    const uint16_t mask = (uint16_t)((1 << M) - 1);
-    const int m_tiles = ((a.O + 127) / 128 + M - 1) / M;  // per cluster
+    const int m_tiles = (a.O + 127) / 128;
     const int n_tiles = m_tiles * ((a.T + a.bn - 1) / a.bn);
-    const int first = blockIdx.x / (S * M), step = gridDim.x / (S * M);
+    const int first = blockIdx.x / S, step = gridDim.x / S;
     const int kc = (a.C + 63) / 64, rc = (a.r + 63) / 64;
     const int c0 = (int)((long)kc * rank / S), c1 = (int)((long)kc * (rank + 1) / S);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), M);
+            mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -251,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     }
     tc_fence_before();
     __syncthreads();
-    if (M > 1) cluster_sync();  // the barriers of every CTA exist before any of them is signalled
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
     auto give_up = [&]() {
@@ -279,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             }
         };
         for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
-            const int m0 = ((i % m_tiles) * M + peer) * 128, row0 = (i / m_tiles) * a.bn;
+            const int m0 = (i % m_tiles) * 128, row0 = (i / m_tiles) * a.bn;
             for (int c = c0; c < c1; ++c) {
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 if (elect_one()) {
@@ -291,12 +409,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                     } else {
                         tma_load_3d(sa, &a.w, fb, c * 64, m0, 0, pol);
                     }
-                    if (M > 1) {
-                        const int slice = a.bn / M * peer;
-                        tma_load_3d_mcast(sa + kABytes + slice * 128, &a.x, fb, c * 64, 0, row0 + slice, mask, pol);
-                    } else {
-                        tma_load_3d(sa + kABytes, &a.x, fb, c * 64, 0, row0, pol);
-                    }
+                    tma_load_3d(sa + kABytes, &a.x, fb, c * 64, 0, row0, pol);
                 }
                 __syncwarp();
                 advance(false);
@@ -325,15 +438,6 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         for (int s = 0; s < C::kStages; ++s)
             if ((used >> s) & 1u)
                 mbar_wait(((used_land >> s) & 1u ? landed_u : full_u) + s * 8, (used_phase >> s) & 1u, limit);
-        // and every CTA's products of this one's last stages have been signalled here
-        if (M > 1 && ok)
-            for (int s = 0; s < C::kStages; ++s) {
-                mbar_wait(empty_u + stage * 8, phase ^ 1, limit);
-                if (++stage == C::kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
     } else if (warp == 1) {
         const uint32_t idesc = umma_idesc_bf16(128, a.bn) | (BWD ? kIdescAMnMajor : 0u);
         const uint64_t ad0 = BWD ? umma_desc_mn_sw128(stage_u, kABytes / 2) : umma_desc_sw128(stage_u);
@@ -357,8 +461,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                     if (left > 16) umma_bf16(d, ad + kAStep, bd + 2, idesc, 1);
                     if (left > 32) umma_bf16(d, ad + 2 * kAStep, bd + 4, idesc, 1);
                     if (left > 48) umma_bf16(d, ad + 3 * kAStep, bd + 6, idesc, 1);
-                    if (M > 1) umma_commit_mcast(empty_u + stage * 8, mask);
-                    else umma_commit(empty_u + stage * 8);
+                    umma_commit(empty_u + stage * 8);
                 }
                 __syncwarp();
                 accum = 1;
@@ -408,30 +511,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 land_phase ^= 1u << stage;
                 uint8_t* st_a = smem + stage * C::kStageBytes;
                 uint8_t* sb = st_a + kABytes;
-                // v of this adapter's tokens, zeros elsewhere
-                for (int q = tid; q < a.bn * 8; q += 128) {
-                    const int row = q >> 3, seg = q & 7;
-                    uint4 val = make_uint4(0, 0, 0, 0);
-                    if (tl.ids[row] == id && j0 + seg * 8 < a.r)
-                        val = *reinterpret_cast<const uint4*>(a.v + (size_t)(row0 + row) * a.r + j0 + seg * 8);
-                    *reinterpret_cast<uint4*>(sb + row * 128 + ((seg ^ (row & 7)) << 4)) = val;
-                }
-                // Zero times an infinity or NaN of this adapter would reach the other adapters'
-                // tokens: such elements leave the tile here and are added to their own
-                // tokens in the epilogue.
-                bool hit = false;
-                for (int q = tid; q < kABytes / 16; q += 128) {
-                    uint4* at = reinterpret_cast<uint4*>(st_a) + q;
-                    uint4 val = *at;
-                    if (not_finite(val.x) | not_finite(val.y) | not_finite(val.z) | not_finite(val.w)) {
-                        val.x = finite_part(val.x);
-                        val.y = finite_part(val.y);
-                        val.z = finite_part(val.z);
-                        val.w = finite_part(val.w);
-                        *at = val;
-                        hit = true;
-                    }
-                }
+                const bool hit = fill_v(a, tl.ids, a.bn, row0, id, j0, st_a, sb, tid);
                 if (hit) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
@@ -445,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         const int q = warp & 3;
         bool ok = true;
         for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
-            const int m0 = ((i % m_tiles) * M + peer) * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
+            const int m0 = (i % m_tiles) * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             const TileList& tl = lists[n & 1];
             if (*abort_flag || !mbar_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, limit)) {
                 ok = false;
@@ -456,58 +536,20 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             const int feat = m0 + q * 32 + lane;
             const int n_ext = tl.count * rc;
             const uint32_t tmem = tbase + (n & 1) * BN + ((uint32_t)(q * 32) << 16);
-            bool any_odd = false;
-            for (int w = 0; w * 32 < n_ext; ++w) any_odd |= tl.odd[w] != 0;
-            if (any_odd) pdl_wait();  // reads v
-            // the infinities and NaN that were taken out of the adapter tiles
-            auto add_odd = [&](int g, float (&y)[16]) {
-                for (int w = 0; w * 32 < n_ext; ++w) {
-                    for (uint32_t b = tl.odd[w]; b; b &= b - 1) {
-                        const int e = w * 32 + __ffs(b) - 1;
-                        const int id = tl.list[e / rc], j0 = (e % rc) * 64;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (tl.ids[g * 16 + j] != id) continue;
-                            for (int l = j0; l < min(a.r, j0 + 64); ++l) {
-                                const size_t at = BWD ? ((size_t)id * a.r + l) * a.O + feat : ((size_t)id * a.O + feat) * a.r + l;
-                                const float u = bf(a.lr_ptr[at]);
-                                if (!isfinite(u)) y[j] += u * bf(a.v[(size_t)(row0 + g * 16 + j) * a.r + l]);
-                            }
-                        }
-                    }
-                }
-            };
+            const bool any_odd = has_odd(tl, n_ext);
             for (int g = 0; g * 16 < rows; ++g) {
                 float v[16];
                 tmem_ld16(tmem + g * 16, v);
                 tmem_ld_wait();
-                if (any_odd && feat < a.O) add_odd(g, v);
+                if (any_odd && feat < a.O) add_odd<BWD>(a, tl, n_ext, rc, row0 + g * 16, g * 16, feat, v);
                 __syncwarp();
                 if (S > 1) {
                     // this CTA's share of the sum, [token][feature]
                     float* part = reinterpret_cast<float*>(smem) + (size_t)g * 16 * 128 + q * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part[j * 128] = v[j];
-                } else if (a.out_fp32) {
-                    float* dst = reinterpret_cast<float*>(a.out) + feat;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (feat < a.O && g * 16 + j < rows) dst[(size_t)(row0 + g * 16 + j) * a.O] = v[j];
                 } else {
-                    // words of two features: lanes 2m and 2m+1 swap half their tokens, so the even
-                    // lane holds the even tokens of features (2m, 2m+1) and the odd lane the odd
-                    // ones (O % 8 == 0: both features of a pair are valid together)
-                    const bool odd = lane & 1;
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + (feat & ~1));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const __nv_bfloat162 p2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                        const uint32_t p = *reinterpret_cast<const uint32_t*>(&p2);
-                        const uint32_t o = __shfl_xor_sync(0xffffffffu, p, 1);
-                        const uint32_t w = __byte_perm(p, o, odd ? 0x3276 : 0x5410);
-                        const int col = g * 16 + 2 * j + (odd ? 1 : 0);
-                        if (feat < a.O && col < rows) dst[(size_t)(row0 + col) * (a.O >> 1)] = w;
-                    }
+                    store_group(a, row0 + g * 16, rows - g * 16, feat, v);
                 }
             }
             tc_fence_before();
@@ -546,15 +588,289 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             }
         cluster_sync();  // no CTA leaves while another reads its shared memory
     }
-    if (M > 1) {
-        __syncwarp();
-        cluster_sync();  // no CTA leaves while another may signal it
-    }
     pdl_wait();  // the grid is complete only when the v kernel is
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tbase, C::kTmemCols);
+}
+
+// Many tiles: a pair of CTAs computes 256 features x bn tokens with one product per 16 of
+// the contraction (cta_group::2).  Each CTA holds 128 rows of W and half of the tokens,
+// 32 KB per 64 of the contraction, so six stages (3072 cycles of products) fit where a CTA
+// on its own has four of 48 KB (2048 cycles, less than the round trip of a stage).
+// The leader (rank 0) issues the products; both load, write v and drain their own half.
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = kABytes + 128 * 128;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 512 + 2 * (int)sizeof(TileList) + kMaxAdapters / 8;
+static_assert(kPairSmem <= 227 * 1024, "shared memory overflow");
+
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_constant__ ProjArgs a) {
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);  // (the leader's)
+    uint64_t* empty = full + kPairStages;
+    uint64_t* landed = empty + kPairStages;
+    uint64_t* other = landed + kPairStages;  // (the leader's) the other CTA's half of an adapter chunk is in place
+    uint64_t* tfull = other + kPairStages;
+    uint64_t* tempty = tfull + 2;  // (the leader's)
+    uint64_t* listed = tempty + 2;
+    uint64_t* lfree = listed + 2;
+    uint64_t* done = lfree + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((4 * kPairStages + 9) * 8 + 8 <= 512, "barriers");
+    TileList* lists = reinterpret_cast<TileList*>(smem + kPairStages * kPairStageBytes + 512);
+    uint32_t* bits = reinterpret_cast<uint32_t*>(lists + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned long long limit = a.st.limit_ns;
+    const int rank = (int)cluster_rank();
+    const int half = a.bn / 2;
+    const int m_tiles = (a.O + 255) / 256;
+    const int n_tiles = m_tiles * ((a.T + a.bn - 1) / a.bn);
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    const int kc = (a.C + 63) / 64, rc = (a.r + 63) / 64;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&other[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&landed[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&tfull[s]), 1);
+            mbar_init(smem_u32(&tempty[s]), 8);
+            mbar_init(smem_u32(&listed[s]), 1);
+            mbar_init(smem_u32(&lfree[s]), 4);
+        }
+        mbar_init(smem_u32(done), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.w);
+        tma_prefetch_desc(&a.x);
+        tma_prefetch_desc(&a.lr);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the barriers of both CTAs exist before either is signalled
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        raise_status(a.st, kStatusWaitTimeout);
+    };
+    const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed);
+    const uint32_t stage_u = smem_u32(smem);
+    const uint32_t lead_full = leader_addr(full_u), lead_tempty = leader_addr(smem_u32(tempty));
+    const uint32_t lead_other = leader_addr(smem_u32(other));
+
+    if (warp == 0) {
+        const uint64_t pol = policy_evict_normal();
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0, land_phase = 0, used = 0, used_land = 0;
+        auto advance = [&](bool land) {
+            const uint32_t bit = 1u << stage;
+            used |= bit;
+            used_land = land ? used_land | bit : used_land & ~bit;
+            if (land) land_phase ^= bit;
+            if (++stage == kPairStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        };
+        for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
+            const int m0 = (i % m_tiles) * 256 + rank * 128, row0 = (i / m_tiles) * a.bn + rank * half;
+            for (int c = 0; c < kc; ++c) {
+                if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
+                if (elect_one()) {
+                    const uint32_t sa = stage_u + stage * kPairStageBytes, fb = lead_full + stage * 8;
+                    // the leader expects the bytes of both (an arrival from the other CTA takes it 500 cycles)
+                    if (rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * kABytes + a.bn * 128);
+                    if (BWD) {
+                        tma_load_3d_pair(sa, &a.w, fb, m0, c * 64, 0, pol);
+                        tma_load_3d_pair(sa + kABytes / 2, &a.w, fb, m0 + 64, c * 64, 0, pol);
+                    } else {
+                        tma_load_3d_pair(sa, &a.w, fb, c * 64, m0, 0, pol);
+                    }
+                    tma_load_3d_pair(sa + kABytes, &a.x, fb, c * 64, 0, row0, pol);
+                }
+                __syncwarp();
+                advance(false);
+            }
+            if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
+            const TileList& tl = lists[n & 1];
+            for (int e = 0; e < tl.count * rc; ++e) {
+                if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
+                if (elect_one()) {
+                    const uint32_t sa = stage_u + stage * kPairStageBytes, lb = landed_u + stage * 8;
+                    const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+                    mbar_arrive_expect_tx(lb, kABytes);
+                    if (BWD) {
+                        tma_load_3d(sa, &a.lr, lb, m0, j0, id, pol);
+                        tma_load_3d(sa + kABytes / 2, &a.lr, lb, m0 + 64, j0, id, pol);
+                    } else {
+                        tma_load_3d(sa, &a.lr, lb, j0, m0, id, pol);
+                    }
+                }
+                __syncwarp();
+                advance(true);
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        // every stage's last products are done, so its copies have landed
+        for (int s = 0; s < kPairStages; ++s) {
+            const int bit = stage;
+            if ((used >> bit) & 1u) {
+                if (!ok && ((used_land >> bit) & 1u)) mbar_wait(landed_u + bit * 8, ((land_phase >> bit) & 1u) ^ 1, limit);
+                mbar_wait(empty_u + bit * 8, phase ^ 1, limit);
+            }
+            if (++stage == kPairStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t idesc = umma_idesc_bf16(256, a.bn) | (BWD ? kIdescAMnMajor : 0u);
+            const uint64_t ad0 = BWD ? umma_desc_mn_sw128(stage_u, kABytes / 2) : umma_desc_sw128(stage_u);
+            const uint64_t bd0 = umma_desc_sw128(stage_u + kABytes);
+            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0, other_phase = 0;
+            // what the other CTA wrote and signalled is read: the waits acquire for the cluster
+            auto wait_cluster = [&](uint32_t bar, uint32_t parity) {
+                bool done_ = mbar_try_wait_cluster(bar, parity);
+                if (!__all_sync(0xffffffffu, done_)) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (!done_ && !*abort_flag && globaltimer_ns() - t0 <= limit) done_ = mbar_try_wait_cluster(bar, parity);
+                    done_ = __all_sync(0xffffffffu, done_);
+                }
+                return done_;
+            };
+            for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
+                const uint32_t d = tbase + (n & 1) * 256;
+                if (!(ok = wait_cluster(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1))) break;
+                tc_fence_after();
+                uint32_t accum = 0;
+                auto chunk = [&](int left, bool ext) {
+                    if (!(ok = wait_cluster(full_u + stage * 8, phase))) return;
+                    if (ext) {
+                        if (!(ok = wait_cluster(smem_u32(&other[stage]), (other_phase >> stage) & 1u))) return;
+                        other_phase ^= 1u << stage;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t ad = ad0 + stage * (kPairStageBytes >> 4), bd = bd0 + stage * (kPairStageBytes >> 4);
+                        constexpr int kAStep = BWD ? 128 : 2;
+                        umma_bf16_pair(d, ad, bd, idesc, accum);
+                        if (left > 16) umma_bf16_pair(d, ad + kAStep, bd + 2, idesc, 1);
+                        if (left > 32) umma_bf16_pair(d, ad + 2 * kAStep, bd + 4, idesc, 1);
+                        if (left > 48) umma_bf16_pair(d, ad + 3 * kAStep, bd + 6, idesc, 1);
+                        umma_commit_pair(empty_u + stage * 8);
+                    }
+                    __syncwarp();
+                    accum = 1;
+                    if (++stage == kPairStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                };
+                for (int c = 0; c < kc && ok; ++c) chunk(a.C - c * 64, false);
+                if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
+                const int n_ext = lists[n & 1].count * rc;
+                for (int e = 0; e < n_ext && ok; ++e) chunk(a.r - (e % rc) * 64, true);
+                if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]));
+                __syncwarp();
+            }
+            if (!ok && lane == 0) give_up();
+            // all products are complete before TMEM is freed
+            if (elect_one()) umma_commit_pair(smem_u32(done));
+            __syncwarp();
+        }
+        mbar_wait(smem_u32(done), 0, limit);
+    } else if (warp < 6) {
+        const int tid = threadIdx.x - 64;
+        bool ok = true;
+        int stage = 0;
+        uint32_t land_phase = 0;
+        for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
+            const int row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
+            TileList& tl = lists[n & 1];
+            if (*abort_flag || !mbar_wait(smem_u32(&lfree[n & 1]), ((n >> 1) & 1) ^ 1, limit)) {
+                ok = false;
+                break;
+            }
+            for (int q = tid; q < kMaxExtra / 32; q += 128) tl.odd[q] = 0;
+            tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st, tid, 128, 1);
+            if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
+            stage = (stage + kc) % kPairStages;
+            const int n_ext = tl.count * rc;
+            if (n_ext) pdl_wait();  // v
+            for (int e = 0; e < n_ext; ++e) {
+                const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+                if (*abort_flag || !mbar_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, limit)) {
+                    ok = false;
+                    break;
+                }
+                land_phase ^= 1u << stage;
+                uint8_t* st_a = smem + stage * kPairStageBytes;
+                const bool hit = fill_v(a, tl.ids + rank * half, half, row0 + rank * half, id, j0, st_a, st_a + kABytes, tid);
+                if (hit) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
+                fence_async_smem();
+                named_sync(1, 128);
+                if (tid == 0) {
+                    if (rank == 0) mbar_arrive(full_u + stage * 8);
+                    else mbar_arrive_cluster(lead_other + stage * 8);
+                }
+                if (++stage == kPairStages) stage = 0;
+            }
+        }
+        if (!ok) give_up();
+    } else {
+        const int q = warp & 3;
+        bool ok = true;
+        for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
+            const int m0 = (i % m_tiles) * 256 + rank * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
+            const TileList& tl = lists[n & 1];
+            // (the list is read here and, in the leader, by the product warp: both before lfree)
+            if (!(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit)) ||
+                !(ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit)))
+                break;
+            tc_fence_after();
+            const int feat = m0 + q * 32 + lane;
+            const int n_ext = tl.count * rc;
+            const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
+            const bool any_odd = has_odd(tl, n_ext);
+            for (int g = 0; g * 16 < rows; ++g) {
+                float v[16];
+                tmem_ld16(tmem + g * 16, v);
+                tmem_ld_wait();
+                if (any_odd && feat < a.O) add_odd<BWD>(a, tl, n_ext, rc, row0 + g * 16, g * 16, feat, v);
+                __syncwarp();
+                store_group(a, row0 + g * 16, rows - g * 16, feat, v);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_cluster(lead_tempty + (n & 1) * 8);
+                mbar_arrive(smem_u32(&lfree[n & 1]));
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may signal it or read its memory
+    pdl_wait();      // the grid is complete only when the v kernel is
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tbase, 512);
 }
 
 // ---------------------------------------------------------------- v = s A x, few tokens
@@ -1115,81 +1431,65 @@ int check_ws(const moe_adapter_t* p, int T, const void* ws, size_t ws_bytes) {
     return api_need(ws, "workspace");
 }
 
-template <bool BWD, int BN>
-cudaError_t launch_project_bn(const ProjArgs& a, int grid, cudaStream_t stream) {
-    auto kern = project_kernel<BWD, BN>;
-    static std::atomic<uint64_t> configured{0};
-    const cudaError_t e = configure_once(configured, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ProjCfg<BN>::kSmemBytes);
-    });
+template <typename Kern>
+cudaError_t launch_project(Kern kern, std::atomic<uint64_t>& configured, int smem, int grid, int cluster,
+                           cudaStream_t stream, const ProjArgs& a) {
+    const cudaError_t e = configure_once(
+        configured, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(kern, dim3(grid), dim3(kThreads), ProjCfg<BN>::kSmemBytes, stream, a.splits * a.mcast, a);
+    return launch_pdl_cluster(kern, dim3(grid), dim3(kThreads), smem, stream, cluster, a);
 }
 
-// Clusters of 4 CTAs that fill an SM each and are resident at a time (per device, asked once).
-int clusters_of_4() {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / 8;
-    int n = known[dev].load(std::memory_order_relaxed);
-    if (n) return n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = ProjCfg<256>::kSmemBytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 4;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    auto kern = project_kernel<false, 256>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ProjCfg<256>::kSmemBytes) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        n = num_sms() / 8;
-    }
-    known[dev].store(n, std::memory_order_relaxed);
-    return n;
+template <bool BWD, int BN>
+cudaError_t launch_project_bn(const ProjArgs& a, int grid, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    return launch_project(project_kernel<BWD, BN>, configured, ProjCfg<BN>::kSmemBytes, grid, a.splits, stream, a);
+}
+
+template <bool BWD>
+cudaError_t launch_project_pair(const ProjArgs& a, int grid, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    return launch_project(project_pair_kernel<BWD>, configured, kPairSmem, grid, 2, stream, a);
 }
 
 // How a projection of T tokens to O features is cut: token capacity and tokens per tile,
-// CTAs per cluster (sharing the contraction, or the token loads), grid.
+// CTAs that share a tile's contraction, or pairs of CTAs; grid.
 struct ProjPlan {
-    int cap, bn, splits, mcast, grid;
+    int cap, bn, splits, pair, grid;
 };
+
+// The tile height, a multiple of `by` in [128, 256], whose rounds over `slots` cost least:
+// rounds x (tokens + 16 for the accumulator's hand-over).
+int tile_height(int T, int units, int slots, int by) {
+    int at = 256;
+    long best = -1;
+    for (int bn = 256; bn >= 128; bn -= by) {
+        const long tiles = (long)units * ((T + bn - 1) / bn);
+        const long cost = (tiles + slots - 1) / slots * (bn + 16);
+        if (best < 0 || cost < best) {
+            best = cost;
+            at = bn;
+        }
+    }
+    return at;
+}
 
 ProjPlan project_plan(int T, int O, int C) {
     ProjPlan p;
     const int sms = num_sms(), m_tiles = (O + 127) / 128, kc = (C + 63) / 64;
-    p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-    p.bn = p.cap;
-    p.splits = p.mcast = 1;
-    int slots = sms, units = m_tiles;  // CTAs (or clusters) at a time; tiles (or groups of them) per token tile
-    // more tiles than SMs: clusters of four along the features
-    if ((long)m_tiles * ((T + 255) / 256) > sms) {
-        p.mcast = 4;
-        slots = clusters_of_4();
-        units = (m_tiles + 3) / 4;
-    }
-    if (T > 256) {
-        // the tile height whose rounds over the slots cost least: rounds x (tokens + a
-        // fixed 16 for the accumulator's hand-over)
-        long best = -1;
-        for (int bn = 256; bn >= 128; bn -= 32) {
-            const long tiles = (long)units * ((T + bn - 1) / bn);
-            const long cost = (tiles + slots - 1) / slots * (bn + 16);
-            if (best < 0 || cost < best) {
-                best = cost;
-                p.bn = bn;
-            }
-        }
-    }
-    const long tiles = (long)units * ((T + p.bn - 1) / p.bn);
-    if (p.mcast > 1) {
-        p.grid = (int)std::min<long>(tiles, slots) * p.mcast;
+    p.splits = 1;
+    // as many tiles as SMs: pairs of CTAs
+    p.pair = T > 128 && (long)m_tiles * ((T + 255) / 256) >= sms;
+    if (p.pair) {
+        const int units = (O + 255) / 256, slots = sms / 2;
+        p.cap = 256;
+        p.bn = tile_height(T, units, slots, 32);
+        p.grid = 2 * (int)std::min<long>((long)units * ((T + p.bn - 1) / p.bn), slots);
         return p;
     }
+    p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+    p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : p.cap;
+    const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
     const int resident = p.cap <= 64 ? 2 : 1;
     // few tiles: clusters share a tile's contraction, four chunks of it per CTA at least
     while (p.splits < 8 && tiles * (p.splits + 1) <= (long)sms * resident && (p.splits + 1) * 4 <= kc) ++p.splits;
@@ -1211,21 +1511,21 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     const ProjPlan plan = project_plan(T, a.O, a.C);
     a.bn = plan.bn;
     a.splits = plan.splits;
-    a.mcast = plan.mcast;
     int rc = make_tmap_3d(&a.w, w, K, N, 1, K * 2, K * N * 2, 64, BWD ? 64 : 128, 1);
     if (rc) return rc;
     if (BWD) rc = make_tmap_3d(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, 64, 1);
     else rc = make_tmap_3d(&a.lr, lr, r, N, n, r * 2, r * N * 2, 64, 128, 1);
     if (rc) return rc;
     const uint64_t C = a.C;
-    if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.bn / plan.mcast))) return rc;
+    if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.pair ? plan.bn / 2 : plan.bn))) return rc;
     a.lr_ptr = static_cast<const uint16_t*>(lr);
     a.adapter_of = adapter_of;
     a.v = static_cast<const uint16_t*>(v);
     a.out = out;
     a.out_fp32 = out_fp32;
     a.st = st;
-    const cudaError_t e = plan.cap == 32    ? launch_project_bn<BWD, 32>(a, plan.grid, stream)
+    const cudaError_t e = plan.pair         ? launch_project_pair<BWD>(a, plan.grid, stream)
+                          : plan.cap == 32  ? launch_project_bn<BWD, 32>(a, plan.grid, stream)
                           : plan.cap == 64  ? launch_project_bn<BWD, 64>(a, plan.grid, stream)
                           : plan.cap == 128 ? launch_project_bn<BWD, 128>(a, plan.grid, stream)
                                             : launch_project_bn<BWD, 256>(a, plan.grid, stream);
