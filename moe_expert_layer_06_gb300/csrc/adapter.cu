@@ -1004,22 +1004,23 @@ struct ShrinkArgs {
     uint16_t* v;     // [T][r]
     DevStatus st;
 };
-constexpr int kShrinkStageBytes = 16384 + 32768;
-constexpr int kShrinkStages = 4;
+// A stage is the tokens' 16 KB and as much of A as the pass needs: as many as fit, up to 12.
+constexpr int kShrinkRing = 192 * 1024;
+constexpr int kShrinkStages = 12;
 constexpr int kShrinkThreads = 192;
-constexpr int kShrinkSmem = 1024 + kShrinkStages * kShrinkStageBytes + 256 + 128 * 8 + kMaxAdapters / 8;
+constexpr int kShrinkSmem = 1024 + kShrinkRing + 256 + 128 * 8 + kMaxAdapters / 8;
 
 template <bool BWD>
 __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_constant__ ShrinkArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kShrinkStages * kShrinkStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kShrinkRing);
     uint64_t* empty = full + kShrinkStages;
     uint64_t* tfull = empty + kShrinkStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* count = reinterpret_cast<int*>(tmem_slot + 2);
-    int* ids = reinterpret_cast<int*>(smem + kShrinkStages * kShrinkStageBytes + 256);
+    int* ids = reinterpret_cast<int*>(smem + kShrinkRing + 256);
     int* list = ids + 128;
     uint32_t* bits = reinterpret_cast<uint32_t*>(list + 128);
 
@@ -1060,26 +1061,23 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
             if (ids[q / (a.r / 8)] < 0)
                 *reinterpret_cast<uint4*>(a.v + (size_t)row0 * a.r + (size_t)q * 8) = make_uint4(0, 0, 0, 0);
 
-    int stage = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    uint32_t armed = 0, armed_phase = 0;  // stages ever armed, and the parity of their last use
+    uint32_t phase = 0, acc_phase = 0;  // phase: parity of each stage's next use
+    uint32_t armed = 0;                 // stages ever filled
+    const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), ring_u = smem_u32(smem);
     bool ok = true;
     for (int pass = pass0; pass * a.per_pass < n_list; pass += a.passes) {
         const int cnt = min(a.per_pass, n_list - pass * a.per_pass);
         const int* mine = list + pass * a.per_pass;
+        const int stage_bytes = 16384 + cnt * a.cols * 128;
+        const int stages = min(kShrinkStages, kShrinkRing / stage_bytes);
+        int stage = 0;
         if (warp == 0) {
-            if (lane == 0 && ok) {
-                const uint64_t pol = policy_evict_normal();
-                for (int c = c0; c < c1; ++c) {
-                    if (*abort_flag || !mbar_wait(smem_u32(&empty[stage]), phase ^ 1, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sx = smem_u32(smem + stage * kShrinkStageBytes), sm = sx + 16384;
-                    const uint32_t fb = smem_u32(&full[stage]);
-                    mbar_arrive_expect_tx(fb, 16384 + cnt * a.cols * 128);
-                    armed |= 1u << stage;
-                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+            const uint64_t pol = policy_evict_normal();
+            for (int c = c0; c < c1 && ok; ++c) {
+                if (!(ok = warp_wait(empty_u + stage * 8, ((phase >> stage) & 1u) ^ 1, abort_flag, limit))) break;
+                if (elect_one()) {
+                    const uint32_t sx = ring_u + stage * stage_bytes, sm = sx + 16384, fb = full_u + stage * 8;
+                    mbar_arrive_expect_tx(fb, stage_bytes);
                     tma_load_3d(sx, &a.x, fb, c * 64, 0, row0, pol);
                     for (int p = 0; p < cnt; ++p) {
                         if (BWD) {
@@ -1089,35 +1087,35 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
                             tma_load_3d(sm + p * a.cols * 128, &a.m, fb, c * 64, 0, mine[p], pol);
                         }
                     }
-                    if (++stage == kShrinkStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
                 }
+                __syncwarp();
+                armed |= 1u << stage;
+                phase ^= 1u << stage;
+                if (++stage == stages) stage = 0;
             }
         } else if (warp == 1) {
-            if (lane == 0 && ok) {
-                const uint32_t idesc = umma_idesc_bf16(128, cnt * a.cols) | (BWD ? kIdescBMnMajor : 0u);
-                for (int c = c0; c < c1; ++c) {
-                    if (*abort_flag || !mbar_wait(smem_u32(&full[stage]), phase, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sx = smem_u32(smem + stage * kShrinkStageBytes), sm = sx + 16384;
-                    const uint64_t ad = umma_desc_sw128(sx);
-                    const uint64_t bd = BWD ? umma_desc_mn_sw128(sm, 8192) : umma_desc_sw128(sm);
-                    const int steps = min(4, (a.C - c * 64 + 15) >> 4);
-                    for (int k = 0; k < steps; ++k)
-                        umma_bf16(tbase, ad + 2 * k, bd + (BWD ? 128 : 2) * k, idesc, c > c0 || k > 0);
-                    umma_commit(smem_u32(&empty[stage]));
-                    if (++stage == kShrinkStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+            const uint32_t idesc = umma_idesc_bf16(128, cnt * a.cols) | (BWD ? kIdescBMnMajor : 0u);
+            const uint64_t ad0 = umma_desc_sw128(ring_u);
+            const uint64_t bd0 = BWD ? umma_desc_mn_sw128(ring_u + 16384, 8192) : umma_desc_sw128(ring_u + 16384);
+            for (int c = c0; c < c1 && ok; ++c) {
+                if (!(ok = warp_wait(full_u + stage * 8, (phase >> stage) & 1u, abort_flag, limit))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t ad = ad0 + stage * (stage_bytes >> 4), bd = bd0 + stage * (stage_bytes >> 4);
+                    constexpr int kBStep = BWD ? 128 : 2;
+                    const int left = a.C - c * 64;
+                    umma_bf16(tbase, ad, bd, idesc, c > c0);
+                    if (left > 16) umma_bf16(tbase, ad + 2, bd + kBStep, idesc, 1);
+                    if (left > 32) umma_bf16(tbase, ad + 4, bd + 2 * kBStep, idesc, 1);
+                    if (left > 48) umma_bf16(tbase, ad + 6, bd + 3 * kBStep, idesc, 1);
+                    umma_commit(empty_u + stage * 8);
                 }
-                umma_commit(smem_u32(tfull));  // on a failure too: the products issued so far end
+                __syncwarp();
+                phase ^= 1u << stage;
+                if (++stage == stages) stage = 0;
             }
+            if (elect_one()) umma_commit(smem_u32(tfull));  // on a failure too: the products issued so far end
+            __syncwarp();
         } else {
             // each token's own columns into this CTA's share, [column][token]
             if (ok) ok = mbar_wait(smem_u32(tfull), acc_phase, limit) && !*abort_flag;
@@ -1176,9 +1174,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
         if (S > 1) cluster_sync();
         else __syncthreads();
     }
-    if (warp == 0 && lane == 0)
+    if (warp == 0)
         for (int s = 0; s < kShrinkStages; ++s)
-            if ((armed >> s) & 1u) mbar_wait(smem_u32(&full[s]), (armed_phase >> s) & 1u, limit);
+            if ((armed >> s) & 1u) mbar_wait(full_u + s * 8, ((phase >> s) & 1u) ^ 1, limit);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -1188,31 +1186,34 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
 
 // ---------------------------------------------------------------- dA and dB
 // dA_i^T [features][r] = sum over i's tokens of x[t] dv[t]^T (dB_i: dy[t] v[t]^T): one CTA
-// per adapter and 128 features walks the 64-token chunks that hold tokens of its adapter.
-// Both operands are MN-major (the contraction runs over tokens).  In a chunk with other
-// tokens too, their rows are set to zero in shared memory, in both operands, so whatever
-// they hold stays out.
+// (or cluster, splitting the tokens) per adapter and 256 features walks the 64-token chunks
+// that hold tokens of its adapter, and reads nothing else.  Both operands are MN-major (the
+// contraction runs over tokens).  In a chunk with other tokens too, their rows are set to
+// zero in shared memory, in both operands, so whatever they hold stays out.  What bounds
+// it is reading the tokens: 40 KB a chunk at rank 64, five in flight.
 struct GradArgs {
     CUtensorMap z[2];  // box {64 features, 64 tokens} of x [T][K], dy [T][N]
     CUtensorMap u[2];  // box {64 r, 64 tokens} of dv, v [T][r]
     const int32_t* adapter_of;
     int T, r;
     int F[2];          // K, N
+    int splits;        // CTAs of a cluster
     uint16_t* out[2];  // da [n][r][K], db [n][N][r]
     DevStatus st;
 };
 constexpr int kGradThreads = 192;
-constexpr int kGradSegment = 4096;  // chunks whose marks are held at a time
+constexpr int kGradSegment = 4096;  // chunks whose list is held at a time
 
 template <int RB>  // 64-column blocks of the rank
 struct GradCfg {
-    static constexpr int kStageBytes = 16384 + RB * 8192;
-    static constexpr int kStages = RB == 4 ? 4 : 3;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256 + kGradSegment;
+    static constexpr int kStageBytes = 32768 + RB * 8192;
+    static constexpr int kStages = RB == 1 ? 5 : RB == 2 ? 4 : 3;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256 + kGradSegment * 2;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory overflow");
 };
 
 template <int RB>
-__global__ void __launch_bounds__(kGradThreads, RB <= 2 ? 2 : 1) grad_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_constant__ GradArgs a) {
     using C = GradCfg<RB>;
     pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
@@ -1223,18 +1224,22 @@ __global__ void __launch_bounds__(kGradThreads, RB <= 2 ? 2 : 1) grad_kernel(con
     uint64_t* done = empty + C::kStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* none = reinterpret_cast<volatile int*>(tmem_slot + 2);
-    uint8_t* marks = smem + C::kStages * C::kStageBytes + 256;  // per chunk: 0 no token of the adapter, 1 some, 2 all
+    volatile int* count = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    // chunks of the segment with tokens of the adapter, + 0x8000 where there are others too
+    uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kStages * C::kStageBytes + 256);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
     const int id = blockIdx.y;
-    const int blocks0 = (a.F[0] + 127) / 128;
-    const int side = (int)blockIdx.x >= blocks0;
-    const int f0 = ((int)blockIdx.x - (side ? blocks0 : 0)) * 128;
+    const int S = a.splits;
+    const int rank = S > 1 ? (int)cluster_rank() : 0;
+    const int blocks0 = (a.F[0] + 255) / 256;
+    const int block = blockIdx.x / S;
+    const int side = block >= blocks0;
+    const int f0 = (block - (side ? blocks0 : 0)) * 256;
     const int F = a.F[side];
     const int chunks = (a.T + 63) / 64;
-    constexpr int kTmemCols = RB * 64;
+    constexpr int kTmemCols = 2 * RB * 64;
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -1244,7 +1249,6 @@ __global__ void __launch_bounds__(kGradThreads, RB <= 2 ? 2 : 1) grad_kernel(con
         }
         mbar_init(smem_u32(done), 1);
         *abort_flag = 0;
-        *none = 1;
         fence_mbar_init();
         tma_prefetch_desc(&a.z[side]);
         tma_prefetch_desc(&a.u[side]);
@@ -1257,94 +1261,110 @@ __global__ void __launch_bounds__(kGradThreads, RB <= 2 ? 2 : 1) grad_kernel(con
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
+    const uint32_t landed_u = smem_u32(landed), full_u = smem_u32(full), empty_u = smem_u32(empty), stage_u = smem_u32(smem);
     pdl_wait();
 
     int stage = 0;
-    uint32_t phase = 0, accum = 0;
-    uint32_t armed = 0, armed_phase = 0;
-    bool ok = true;
+    uint32_t phase = 0, accum = 0, armed = 0, armed_phase = 0;
+    bool ok = true, none = true;
+    int ordinal = 0;  // of the segment's first listed chunk among all
     for (int seg = 0; seg < chunks; seg += kGradSegment) {
         const int n = min(kGradSegment, chunks - seg);
-        for (int c = warp; c < n; c += kGradThreads / 32) {
-            const int t = (seg + c) * 64 + lane;
-            const bool b0 = t < a.T, b1 = t + 32 < a.T;
-            const bool e0 = b0 && a.adapter_of[t] == id, e1 = b1 && a.adapter_of[t + 32] == id;
-            const bool any = __any_sync(0xffffffffu, e0 || e1), all = __all_sync(0xffffffffu, e0 == b0 && e1 == b1);
-            if (lane == 0) {
-                marks[c] = any ? (all ? 2 : 1) : 0;
-                if (any) *none = 0;
+        // marks, eight chunks of a warp at a time: 0 no token of the adapter, 1 some, 2 all
+        for (int c0 = warp * 8; c0 < n; c0 += kGradThreads / 32 * 8) {
+            int of[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const long t = (long)(seg + c0) * 64 + q * 32 + lane;
+                of[q] = t < a.T ? a.adapter_of[t] : -2;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const bool any = __any_sync(0xffffffffu, of[2 * q] == id || of[2 * q + 1] == id);
+                const bool all = __all_sync(0xffffffffu, (of[2 * q] == id || of[2 * q] == -2) &&
+                                                             (of[2 * q + 1] == id || of[2 * q + 1] == -2));
+                if (lane == 0 && c0 + q < n) list[c0 + q] = any ? (all ? 2 : 1) : 0;
             }
         }
         __syncthreads();
+        if (warp == 0) {  // compacted in place, in order
+            int at = 0;
+            for (int c = lane; c - lane < n; c += 32) {
+                const int mark = c < n ? list[c] : 0;
+                const uint32_t b = __ballot_sync(0xffffffffu, mark != 0);
+                __syncwarp();
+                if (mark) list[at + __popc(b & ((1u << lane) - 1u))] = (uint16_t)(c | (mark == 1 ? 0x8000 : 0));
+                at += __popc(b);
+                __syncwarp();
+            }
+            if (lane == 0) *count = at;
+        }
+        __syncthreads();
+        const int cnt = *count;
+        if (cnt) none = false;
+        const int q0 = (rank - ordinal % S + S) % S;  // every S-th listed chunk is this CTA's
+        ordinal += cnt;
         if (warp == 0) {
-            if (lane == 0 && ok) {
-                const uint64_t pol = policy_evict_normal();
-                for (int c = 0; c < n; ++c) {
-                    if (!marks[c]) continue;
-                    if (*abort_flag || !mbar_wait(smem_u32(&empty[stage]), phase ^ 1, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sz = smem_u32(smem + stage * C::kStageBytes), lb = smem_u32(&landed[stage]);
-                    const int t0 = (seg + c) * 64;
+            const uint64_t pol = policy_evict_normal();
+            for (int q = q0; q < cnt && ok; q += S) {
+                if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
+                if (elect_one()) {
+                    const uint32_t sz = stage_u + stage * C::kStageBytes, lb = landed_u + stage * 8;
+                    const int t0 = (seg + (list[q] & 0x7fff)) * 64;
                     mbar_arrive_expect_tx(lb, C::kStageBytes);
-                    armed |= 1u << stage;
-                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-                    tma_load_3d(sz, &a.z[side], lb, f0, t0, 0, pol);
-                    tma_load_3d(sz + 8192, &a.z[side], lb, f0 + 64, t0, 0, pol);
-                    for (int b = 0; b < RB; ++b) tma_load_3d(sz + 16384 + b * 8192, &a.u[side], lb, b * 64, t0, 0, pol);
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) tma_load_3d(sz + b * 8192, &a.z[side], lb, f0 + b * 64, t0, 0, pol);
+#pragma unroll
+                    for (int b = 0; b < RB; ++b) tma_load_3d(sz + 32768 + b * 8192, &a.u[side], lb, b * 64, t0, 0, pol);
+                }
+                __syncwarp();
+                armed |= 1u << stage;
+                armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
         } else if (warp == 1) {
-            if (lane == 0 && ok) {
-                const uint32_t idesc =
-                    umma_idesc_bf16(128, (a.r + 15) & ~15) | kIdescAMnMajor | kIdescBMnMajor;
-                for (int c = 0; c < n; ++c) {
-                    if (!marks[c]) continue;
-                    if (*abort_flag || !mbar_wait(smem_u32(&full[stage]), phase, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sz = smem_u32(smem + stage * C::kStageBytes);
-                    const uint64_t ad = umma_desc_mn_sw128(sz, 8192), bd = umma_desc_mn_sw128(sz + 16384, 8192);
+            const uint32_t idesc = umma_idesc_bf16(128, (a.r + 15) & ~15) | kIdescAMnMajor | kIdescBMnMajor;
+            const uint64_t ad0 = umma_desc_mn_sw128(stage_u, 8192), bd0 = umma_desc_mn_sw128(stage_u + 32768, 8192);
+            for (int q = q0; q < cnt && ok; q += S) {
+                if (!(ok = warp_wait(full_u + stage * 8, phase, abort_flag, limit))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t ad = ad0 + stage * (C::kStageBytes >> 4), bd = bd0 + stage * (C::kStageBytes >> 4);
+#pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        umma_bf16(tbase, ad + 128 * k, bd + 128 * k, idesc, accum);
-                        accum = 1;
+                        umma_bf16(tbase, ad + 128 * k, bd + 128 * k, idesc, k > 0 ? 1 : accum);
+                        umma_bf16(tbase + RB * 64, ad + 1024 + 128 * k, bd + 128 * k, idesc, k > 0 ? 1 : accum);
                     }
-                    umma_commit(smem_u32(&empty[stage]));
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    umma_commit(empty_u + stage * 8);
+                }
+                __syncwarp();
+                accum = 1;
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-        } else if (ok) {
+        } else {
             const int tid = threadIdx.x - 64;
-            for (int c = 0; c < n; ++c) {
-                if (!marks[c]) continue;
-                if (*abort_flag || !mbar_wait(smem_u32(&landed[stage]), phase, limit)) {
-                    ok = false;
-                    break;
-                }
-                if (marks[c] == 1) {
-                    const int t0 = (seg + c) * 64;
+            for (int q = q0; q < cnt && ok; q += S) {
+                if (!(ok = warp_wait(landed_u + stage * 8, phase, abort_flag, limit))) break;
+                if (list[q] & 0x8000) {
+                    const int t0 = (seg + (list[q] & 0x7fff)) * 64;
                     uint8_t* sz = smem + stage * C::kStageBytes;
                     // 8 threads per token row; the 128-byte rows of all blocks
                     for (int row = tid >> 3; row < 64; row += 16) {
                         if (t0 + row < a.T && a.adapter_of[t0 + row] == id) continue;
 #pragma unroll
-                        for (int b = 0; b < 2 + RB; ++b)
+                        for (int b = 0; b < 4 + RB; ++b)
                             *reinterpret_cast<uint4*>(sz + b * 8192 + row * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_smem();
                     named_sync(1, 128);
                 }
-                if (tid == 0) mbar_arrive(smem_u32(&full[stage]));
+                if (tid == 0) mbar_arrive(full_u + stage * 8);
                 if (++stage == C::kStages) {
                     stage = 0;
                     phase ^= 1;
@@ -1355,53 +1375,89 @@ __global__ void __launch_bounds__(kGradThreads, RB <= 2 ? 2 : 1) grad_kernel(con
             *abort_flag = 1;
             raise_status(a.st, kStatusWaitTimeout);
         }
-        __syncthreads();  // the marks are rewritten
+        __syncthreads();  // the list is rewritten
     }
-    if (warp == 0 && lane == 0)
+    // this CTA's share of the chunks may be empty: its accumulators were then never written
+    const bool empty_share = none || ordinal <= rank;
+    if (warp == 0) {
         for (int s = 0; s < C::kStages; ++s)
-            if ((armed >> s) & 1u) mbar_wait(smem_u32(&landed[s]), (armed_phase >> s) & 1u, limit);
-    if (warp == 1 && lane == 0) umma_commit(smem_u32(done));
-    if (warp == 1) {
-        if (lane == 0) mbar_wait(smem_u32(done), 0, limit);
-    } else if (warp >= 2) {
-        if (mbar_wait(smem_u32(done), 0, limit) && !*abort_flag) {
-            tc_fence_after();
-            const int q = warp & 3, feat = f0 + q * 32 + lane;
-            uint16_t* out = a.out[side];
-            for (int g = 0; g * 16 < a.r; ++g) {
-                float f[16];
-                tmem_ld16(tbase + ((uint32_t)(q * 32) << 16) + g * 16, f);
-                tmem_ld_wait();
-                if (*none) {  // no token: the accumulator was never written
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = 0.0f;
-                }
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = (uint32_t)to_bf(f[2 * j]) | ((uint32_t)to_bf(f[2 * j + 1]) << 16);
-                if (side) {  // db_i [feature][r]
-                    if (feat < F) {
-                        uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)id * F + feat) * a.r + g * 16);
-                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        if (g * 16 + 8 < a.r) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
-                } else {  // da_i [r][feature], words of two features (as in the projection)
-                    const bool odd = lane & 1;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t o = __shfl_xor_sync(0xffffffffu, w[j], 1);
-                        const uint32_t p = __byte_perm(w[j], o, odd ? 0x3276 : 0x5410);
-                        const int col = g * 16 + 2 * j + (odd ? 1 : 0);
-                        if (feat < F && col < a.r)
-                            *reinterpret_cast<uint32_t*>(out + ((size_t)id * a.r + col) * F + (feat & ~1)) = p;
-                    }
-                }
-            }
-            tc_fence_before();
-        }
+            if ((armed >> s) & 1u) mbar_wait(landed_u + s * 8, (armed_phase >> s) & 1u, limit);
+    } else if (warp == 1) {
+        if (elect_one()) umma_commit(smem_u32(done));
+        __syncwarp();
+        mbar_wait(smem_u32(done), 0, limit);
+    } else {
+        ok = mbar_wait(smem_u32(done), 0, limit) && !*abort_flag;
     }
     __syncwarp();
     tc_fence_before();
+    __syncthreads();  // also: the drained stages may hold the shares of a split sum
+    tc_fence_after();
+    const int q = warp & 3;
+    uint16_t* out = a.out[side];
+    // 16 columns of this lane's feature, in words of two columns
+    auto store16 = [&](int feat, int j0, const float (&f)[16]) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = (uint32_t)to_bf(f[2 * j]) | ((uint32_t)to_bf(f[2 * j + 1]) << 16);
+        if (side) {  // db_i [feature][r]
+            if (feat < F) {
+                uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)id * F + feat) * a.r + j0);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (j0 + 8 < a.r) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            return;
+        }
+        // da_i [r][feature], words of two features (as in the projection)
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, w[j], 1);
+            const uint32_t p = __byte_perm(w[j], o, odd ? 0x3276 : 0x5410);
+            const int col = j0 + 2 * j + (odd ? 1 : 0);
+            if (feat < F && col < a.r)
+                *reinterpret_cast<uint32_t*>(out + ((size_t)id * a.r + col) * F + (feat & ~1)) = p;
+        }
+    };
+    float* part = reinterpret_cast<float*>(smem);  // split sums: [column][256 features]
+    if (warp >= 2 && ok) {
+        for (int h = 0; h < 2; ++h)
+            for (int g = 0; g * 16 < a.r; ++g) {
+                float f[16];
+                tmem_ld16(tbase + h * RB * 64 + ((uint32_t)(q * 32) << 16) + g * 16, f);
+                tmem_ld_wait();
+                if (empty_share) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+                }
+                const int feat = h * 128 + q * 32 + lane;
+                if (S > 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(g * 16 + j) * 256 + feat] = f[j];
+                } else {
+                    store16(f0 + feat, g * 16, f);
+                }
+            }
+        tc_fence_before();
+    }
+    if (S > 1) {
+        __syncwarp();
+        cluster_sync();
+        // (16 columns, 32 features) at a time, the warps of the cluster in turn
+        const int groups = (a.r + 15) / 16 * 8;
+        for (int w = rank * (kGradThreads / 32) + warp; w < groups && !*abort_flag; w += S * (kGradThreads / 32)) {
+            const int g = w >> 3, feat = (w & 7) * 32 + lane;
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] += ld_peer(stage_u + ((g * 16 + j) * 256 + feat) * 4, s);
+            store16(f0 + feat, g * 16, f);
+        }
+        cluster_sync();
+    }
+    __syncwarp();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tbase, kTmemCols);
@@ -1590,8 +1646,8 @@ cudaError_t launch_grad_rb(const GradArgs& a, int n_adapters, cudaStream_t strea
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GradCfg<RB>::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((a.F[0] + 127) / 128 + (a.F[1] + 127) / 128, n_adapters), dim3(kGradThreads),
-                      GradCfg<RB>::kSmemBytes, stream, a);
+    return launch_pdl_cluster(kern, dim3(((a.F[0] + 255) / 256 + (a.F[1] + 255) / 256) * a.splits, n_adapters),
+                              dim3(kGradThreads), GradCfg<RB>::kSmemBytes, stream, a.splits, a);
 }
 
 int gradients(const moe_adapter_t* p, int T, const void* dy, const void* x, const void* dv, const void* v,
@@ -1613,6 +1669,10 @@ int gradients(const moe_adapter_t* p, int T, const void* dy, const void* x, cons
     a.out[1] = static_cast<uint16_t*>(db);
     a.st = st;
     const int rb = (p->rank + 63) / 64;
+    // few adapters: clusters split the tokens (the shares of ranks above 128 do not fit shared memory)
+    const int ctas = ((a.F[0] + 255) / 256 + (a.F[1] + 255) / 256) * p->n_adapters;
+    a.splits = 1;
+    while (a.splits < 4 && rb <= 2 && ctas * (a.splits + 1) <= num_sms() && (T + 63) / 64 >= 4 * (a.splits + 1)) ++a.splits;
     const cudaError_t e = rb == 1   ? launch_grad_rb<1>(a, p->n_adapters, stream)
                           : rb == 2 ? launch_grad_rb<2>(a, p->n_adapters, stream)
                                     : launch_grad_rb<4>(a, p->n_adapters, stream);
