@@ -146,6 +146,17 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
 // The tile's adapter ids (-1: none) and the list of distinct ones, ascending; *count
 // their number.  `n_threads` threads call it (tid 0..), synchronised by barrier `bar`;
 // `bits` holds kMaxAdapters bits.
@@ -215,22 +226,49 @@ struct TileList {
     uint32_t odd[kMaxExtra / 32];  // adapter chunks with an infinity or NaN in this tile
 };
 
-// One adapter chunk of a tile, by 128 threads: sb gets v[.., j0..] of the tokens of adapter
-// id (`n` tokens from row0 with adapters ids[]), zeros elsewhere.  Zero times an infinity
-// or NaN of this adapter would reach the other adapters' tokens: such elements leave its
-// tile st_a here (true: there were some) and are added to their own tokens in the epilogue.
-__device__ __forceinline__ bool fill_v(const ProjArgs& a, const int* ids, int n, int row0, int id, int j0, uint8_t* st_a,
-                                       uint8_t* sb, int tid) {
-    for (int q = tid; q < n * 8; q += 128) {
-        const int row = q >> 3, seg = q & 7;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (ids[row] == id && j0 + seg * 8 < a.r)
-            val = *reinterpret_cast<const uint4*>(a.v + (size_t)(row0 + row) * a.r + j0 + seg * 8);
-        *reinterpret_cast<uint4*>(sb + row * 128 + ((seg ^ (row & 7)) << 4)) = val;
+// The v rows of a thread's tokens, 64 of their rank, held in registers while the tile's
+// adapters pass: the thread of 128 with index tid has the tokens tid and (RPT = 2) tid + 128.
+template <int RPT>
+struct VRows {
+    int id[RPT];
+    uint4 v[RPT][8];
+
+    __device__ __forceinline__ void ids(const int* of, int n, int tid) {
+#pragma unroll
+        for (int q = 0; q < RPT; ++q) id[q] = tid + q * 128 < n ? of[tid + q * 128] : -1;
     }
+    __device__ __forceinline__ void load(const ProjArgs& a, int row0, int j0, int tid) {
+#pragma unroll
+        for (int q = 0; q < RPT; ++q)
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                v[q][g] = make_uint4(0, 0, 0, 0);
+                if (id[q] >= 0 && j0 + g * 8 < a.r)
+                    v[q][g] = *reinterpret_cast<const uint4*>(a.v + (size_t)(row0 + tid + q * 128) * a.r + j0 + g * 8);
+            }
+    }
+    // sb: the rows of adapter `of`, zeros elsewhere (n rows, swizzled as TMA would)
+    __device__ __forceinline__ void store(uint8_t* sb, int n, int of, int tid) const {
+#pragma unroll
+        for (int q = 0; q < RPT; ++q) {
+            const int row = tid + q * 128;
+            if (row >= n) continue;
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+                *reinterpret_cast<uint4*>(sb + row * 128 + ((g ^ (row & 7)) << 4)) =
+                    id[q] == of ? v[q][g] : make_uint4(0, 0, 0, 0);
+        }
+    }
+};
+
+// Zero times an infinity or NaN of an adapter would reach the other adapters' tokens: such
+// elements leave its tile here (true: there were some) and are added to their own tokens
+// in the epilogue.
+__device__ __forceinline__ bool take_odd(uint8_t* st_a, int tid) {
     bool hit = false;
-    for (int q = tid; q < kABytes / 16; q += 128) {
-        uint4* at = reinterpret_cast<uint4*>(st_a) + q;
+#pragma unroll
+    for (int q = 0; q < kABytes / 16 / 128; ++q) {
+        uint4* at = reinterpret_cast<uint4*>(st_a) + q * 128 + tid;
         uint4 val = *at;
         if (not_finite(val.x) | not_finite(val.y) | not_finite(val.z) | not_finite(val.w)) {
             val.x = finite_part(val.x);
@@ -253,13 +291,13 @@ __device__ __forceinline__ bool has_odd(const TileList& tl, int n_ext) {
 // The infinities and NaN that were taken out of the adapter tiles, for 16 tokens from t0
 // (position at in the tile) and one feature.
 template <bool BWD>
-__device__ __noinline__ void add_odd(const ProjArgs& a, const TileList& tl, int n_ext, int rc, int t0, int at, int feat,
+__device__ __noinline__ void add_odd(const ProjArgs& a, const TileList& tl, int n_ext, int t0, int at, int feat,
                                      float (&y)[16]) {
     pdl_wait();  // v
     for (int w = 0; w * 32 < n_ext; ++w) {
         for (uint32_t b = tl.odd[w]; b; b &= b - 1) {
             const int e = w * 32 + __ffs(b) - 1;
-            const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+            const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
             for (int j = 0; j < 16; ++j) {
                 if (tl.ids[at + j] != id) continue;
                 for (int l = j0; l < min(a.r, j0 + 64); ++l) {
@@ -301,11 +339,13 @@ __device__ __forceinline__ void store_group(const ProjArgs& a, int t0, int n, in
 template <int BN>
 struct ProjCfg {
     static constexpr int kStageBytes = kABytes + BN * 128;
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 4;
+    // Up to 64 tokens two CTAs fit an SM, if only the next launch's beside the last one's:
+    // nine stages and one CTA took 17.5 us a call at one token, where this takes 13.
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 4 : 5;
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int kBarBytes = 256;
+    static constexpr int kBarBytes = 512;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + 2 * (int)sizeof(TileList) + kMaxAdapters / 8;
-    static_assert(kSmemBytes <= 227 * 1024, "shared memory overflow");
+    static_assert(kSmemBytes <= (BN <= 64 ? 113 : 227) * 1024, "shared memory overflow");
     static_assert(kStages * kStageBytes >= BN * 128 * 4, "the split sums fit the stages");
 };
 
@@ -319,20 +359,21 @@ template <bool BWD, int BN>
 __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(const __grid_constant__ ProjArgs a) {
     using C = ProjCfg<BN>;
     pdl_launch_dependents();
+    constexpr int stages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
-    uint64_t* empty = full + C::kStages;
-    uint64_t* landed = empty + C::kStages;  // the adapter tile of a stage, before the v writers are done with it
-    uint64_t* tfull = landed + C::kStages;  // accumulator complete / drained
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + stages * C::kStageBytes);
+    uint64_t* empty = full + stages;
+    uint64_t* landed = empty + stages;  // the adapter tile of a stage, before the v writers are done with it
+    uint64_t* tfull = landed + stages;  // accumulator complete / drained
     uint64_t* tempty = tfull + 2;
     uint64_t* listed = tempty + 2;          // a tile's adapter list written / no longer read
     uint64_t* lfree = listed + 2;
     uint64_t* done = lfree + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((3 * 6 + 9) * 8 + 8 <= C::kBarBytes, "barriers");
-    TileList* lists = reinterpret_cast<TileList*>(smem + C::kStages * C::kStageBytes + C::kBarBytes);
+    static_assert((3 * C::kStages + 9) * 8 + 8 <= C::kBarBytes, "barriers");
+    TileList* lists = reinterpret_cast<TileList*>(smem + stages * C::kStageBytes + C::kBarBytes);
     uint32_t* bits = reinterpret_cast<uint32_t*>(lists + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -346,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     const int c0 = (int)((long)kc * rank / S), c1 = (int)((long)kc * (rank + 1) / S);
 
     if (warp == 0 && lane == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
@@ -391,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             used_land = land ? used_land | bit : used_land & ~bit;
             used_phase = par ? used_phase | bit : used_phase & ~bit;
             if (land) land_phase ^= bit;
-            if (++stage == C::kStages) {
+            if (++stage == stages) {
                 stage = 0;
                 phase ^= 1;
             }
@@ -420,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 if (elect_one()) {
                     const uint32_t sa = stage_u + stage * C::kStageBytes, lb = landed_u + stage * 8;
-                    const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+                    const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
                     mbar_arrive_expect_tx(lb, kABytes);
                     if (BWD) {
                         tma_load_3d(sa, &a.lr, lb, m0, j0, id, pol);
@@ -435,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         }
         if (!ok && lane == 0) give_up();
         // every copy has landed before the CTA exits
-        for (int s = 0; s < C::kStages; ++s)
+        for (int s = 0; s < stages; ++s)
             if ((used >> s) & 1u)
                 mbar_wait(((used_land >> s) & 1u ? landed_u : full_u) + s * 8, (used_phase >> s) & 1u, limit);
     } else if (warp == 1) {
@@ -465,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 }
                 __syncwarp();
                 accum = 1;
-                if (++stage == C::kStages) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1;
                 }
@@ -473,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             for (int c = c0; c < c1 && ok; ++c) chunk(a.C - c * 64);
             if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
             const int n_ext = lists[n & 1].count * rc;
-            for (int e = rank; e < n_ext && ok; e += S) chunk(a.r - (e % rc) * 64);
+            for (int e = rank; e < n_ext && ok; e += S) chunk(a.r - e / lists[n & 1].count * 64);
             if (elect_one()) umma_commit(smem_u32(&tfull[n & 1]));
             __syncwarp();
         }
@@ -498,11 +539,15 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             for (int q = tid; q < kMaxExtra / 32; q += 128) tl.odd[q] = 0;
             tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st, tid, 128, 1);
             if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
-            stage = (stage + c1 - c0) % C::kStages;
+            stage = (stage + c1 - c0) % stages;
             const int n_ext = tl.count * rc;
             if (rank < n_ext) pdl_wait();  // v
+            VRows<BN == 256 ? 2 : 1> vr;
+            vr.ids(tl.ids, a.bn, tid);
+            int held = -1;
             for (int e = rank; e < n_ext; e += S) {
-                const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+                const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
+                if (j0 != held) vr.load(a, row0, held = j0, tid);
                 // the adapter tile has landed: the stage is free of its last use, too
                 if (*abort_flag || !mbar_wait(smem_u32(&landed[stage]), (land_phase >> stage) & 1u, limit)) {
                     ok = false;
@@ -511,12 +556,12 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 land_phase ^= 1u << stage;
                 uint8_t* st_a = smem + stage * C::kStageBytes;
                 uint8_t* sb = st_a + kABytes;
-                const bool hit = fill_v(a, tl.ids, a.bn, row0, id, j0, st_a, sb, tid);
-                if (hit) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
+                vr.store(sb, a.bn, id, tid);
+                if (take_odd(st_a, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
                 if (tid == 0) mbar_arrive(smem_u32(&full[stage]));
-                if (++stage == C::kStages) stage = 0;
+                if (++stage == stages) stage = 0;
             }
         }
         if (!ok) give_up();
@@ -541,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 float v[16];
                 tmem_ld16(tmem + g * 16, v);
                 tmem_ld_wait();
-                if (any_odd && feat < a.O) add_odd<BWD>(a, tl, n_ext, rc, row0 + g * 16, g * 16, feat, v);
+                if (any_odd && feat < a.O) add_odd<BWD>(a, tl, n_ext, row0 + g * 16, g * 16, feat, v);
                 __syncwarp();
                 if (S > 1) {
                     // this CTA's share of the sum, [token][feature]
@@ -566,24 +611,33 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         __syncwarp();
         cluster_sync();
         const int m0 = (first % m_tiles) * 128, row0 = (first / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
-        const int pairs = rows * 64;  // words of two features
-        const int p0 = (int)((long)pairs * rank / S), p1 = (int)((long)pairs * (rank + 1) / S);
+        const int quads = rows * 32;  // four features of a token
+        const int p0 = (int)((long)quads * rank / S), p1 = (int)((long)quads * (rank + 1) / S);
         if (!*abort_flag)
             for (int p = p0 + threadIdx.x; p < p1; p += kThreads) {
-                const uint32_t addr = smem_u32(smem) + p * 8;
-                float u = 0.0f, w = 0.0f;
-                for (int s = 0; s < S; ++s) {
-                    u += ld_peer(addr, s);
-                    w += ld_peer(addr + 4, s);
-                }
-                const int feat = m0 + (p & 63) * 2;
-                const size_t at = (size_t)(row0 + (p >> 6)) * a.O + feat;
-                if (feat >= a.O) continue;
+                const uint32_t addr = stage_u + p * 16;
+                float4 f[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < S) f[s] = ld_peer4(addr, s);
+                float4 y = f[0];
+#pragma unroll
+                for (int s = 1; s < 8; ++s)
+                    if (s < S) {
+                        y.x += f[s].x;
+                        y.y += f[s].y;
+                        y.z += f[s].z;
+                        y.w += f[s].w;
+                    }
+                const int feat = m0 + (p & 31) * 4;
+                if (feat >= a.O) continue;  // (O % 8 == 0: the four are valid together)
+                const size_t at = (size_t)(row0 + (p >> 5)) * a.O + feat;
                 if (a.out_fp32) {
-                    *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at) = make_float2(u, w);
+                    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = y;
                 } else {
-                    const __nv_bfloat162 p2 = __floats2bfloat162_rn(u, w);
-                    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at) = *reinterpret_cast<const uint32_t*>(&p2);
+                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+                        make_uint2((uint32_t)to_bf(y.x) | ((uint32_t)to_bf(y.y) << 16),
+                                   (uint32_t)to_bf(y.z) | ((uint32_t)to_bf(y.w) << 16));
                 }
             }
         cluster_sync();  // no CTA leaves while another reads its shared memory
@@ -709,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 if (elect_one()) {
                     const uint32_t sa = stage_u + stage * kPairStageBytes, lb = landed_u + stage * 8;
-                    const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+                    const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
                     mbar_arrive_expect_tx(lb, kABytes);
                     if (BWD) {
                         tma_load_3d(sa, &a.lr, lb, m0, j0, id, pol);
@@ -784,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 for (int c = 0; c < kc && ok; ++c) chunk(a.C - c * 64, false);
                 if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
                 const int n_ext = lists[n & 1].count * rc;
-                for (int e = 0; e < n_ext && ok; ++e) chunk(a.r - (e % rc) * 64, true);
+                for (int e = 0; e < n_ext && ok; ++e) chunk(a.r - e / lists[n & 1].count * 64, true);
                 if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]));
                 __syncwarp();
             }
@@ -812,16 +866,20 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             stage = (stage + kc) % kPairStages;
             const int n_ext = tl.count * rc;
             if (n_ext) pdl_wait();  // v
+            VRows<1> vr;
+            vr.ids(tl.ids + rank * half, half, tid);
+            int held = -1;
             for (int e = 0; e < n_ext; ++e) {
-                const int id = tl.list[e / rc], j0 = (e % rc) * 64;
+                const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
+                if (j0 != held) vr.load(a, row0 + rank * half, held = j0, tid);
                 if (*abort_flag || !mbar_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, limit)) {
                     ok = false;
                     break;
                 }
                 land_phase ^= 1u << stage;
                 uint8_t* st_a = smem + stage * kPairStageBytes;
-                const bool hit = fill_v(a, tl.ids + rank * half, half, row0 + rank * half, id, j0, st_a, st_a + kABytes, tid);
-                if (hit) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
+                vr.store(st_a + kABytes, half, id, tid);
+                if (take_odd(st_a, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
                 if (tid == 0) {
@@ -851,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 float v[16];
                 tmem_ld16(tmem + g * 16, v);
                 tmem_ld_wait();
-                if (any_odd && feat < a.O) add_odd<BWD>(a, tl, n_ext, rc, row0 + g * 16, g * 16, feat, v);
+                if (any_odd && feat < a.O) add_odd<BWD>(a, tl, n_ext, row0 + g * 16, g * 16, feat, v);
                 __syncwarp();
                 store_group(a, row0 + g * 16, rows - g * 16, feat, v);
             }
@@ -1159,6 +1217,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
             const uint32_t addr = smem_u32(smem) + (j0 * 128 + row) * 4;
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+#pragma unroll 4
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
