@@ -12,6 +12,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace moe {
@@ -192,36 +194,38 @@ __global__ void __launch_bounds__(kWarps * 32) scored_topk_fp64_kernel(const __g
     }
 }
 
-// Monotone map of a float (no NaN) to an unsigned word that is never 0.
-__device__ __forceinline__ uint32_t key_of(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-
-__device__ __forceinline__ float value_of(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
-
-// 1 / (1 + exp(-l)) from the hardware's approximate 2^x and reciprocal.
-__device__ __forceinline__ float fast_sigmoid(float l) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.442695041f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+// ---------------------------------------------------------------- the fast selection
+// max of three in one instruction (NaN loses against a number)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
-// Reductions over the LPT consecutive lanes of one token (every lane gets the result).
-template <int LPT>
-__device__ __forceinline__ uint32_t token_max(uint32_t v) {
-    if constexpr (LPT == 32) {
-        return __reduce_max_sync(0xffffffffu, v);
-    } else {
+template <int N>
+__device__ __forceinline__ float max_of(const float* v) {
+    float m = v[0];
 #pragma unroll
-        for (int d = LPT / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
-        return v;
-    }
+    for (int i = 1; i + 1 < N; i += 2) m = max3(m, v[i], v[i + 1]);
+    if (N % 2 == 0) m = fmaxf(m, v[N - 1]);
+    return m;
 }
 
+__device__ __forceinline__ float fast_exp2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Reductions over the LPT consecutive lanes of one token (every lane gets the result).
 template <int LPT>
 __device__ __forceinline__ float token_max(float v) {
 #pragma unroll
@@ -236,272 +240,434 @@ __device__ __forceinline__ float token_sum(float v) {
     return v;
 }
 
-template <int LPT>
-__device__ __forceinline__ bool token_any(bool p) {
-    const uint32_t b = __ballot_sync(0xffffffffu, p);
-    if (LPT == 32) return b != 0;
-    return ((b >> (threadIdx.x & 31 & ~(LPT - 1))) & ((1u << (LPT & 31)) - 1u)) != 0;
-}
-
-// fp64 scratch of a warp: a row, or a value per candidate.
-__host__ __device__ __forceinline__ int scratch_doubles(int E) { return E > kCand ? E : kCand; }
-
-// What the fp32 selection value of an expert is.
+// What the fp32 selection value c of an expert is.
 enum KeyKind : int {
     kKeyLogit,    // the logit itself: orders as the score does, and exactly (no bias, no sum of two)
     kKeySigmoid,  // sigmoid + bias
     kKeySoftmax,  // softmax + bias
 };
 
-// LPT lanes per token (32 / LPT tokens per warp).  A token's lanes are laid out by
-// groups: lpg (a power of two) lanes per group, PER consecutive experts per lane; what
-// passes the group's end is empty (key 0).
+// How a row lies in the lanes of its token: lpg (a power of two) lanes per group, `per`
+// consecutive experts per lane; what passes the group's end is empty.
+struct Layout {
+    int gs, lpg, per;
+};
+
+// The exact score of one logit; den: the softmax's exact sum relative to mx.
+__device__ __forceinline__ double score64(const RouteArgs& a, float l, float mx, double den) {
+    if (a.sigmoid) return 1.0 / (1.0 + exp(-(double)l));
+    return (l == mx ? 1.0 : exp((double)l - (double)mx)) / den;
+}
+
+// The softmax's sum of row t in fp64, by the whole warp (1 for a sigmoid).
+__device__ __forceinline__ double sum64(const RouteArgs& a, int t, float mx) {
+    if (a.sigmoid) return 1.0;
+    double d = 0.0;
+#pragma unroll 4
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+        const float x = masked_logit(logit_at(a, t, e));
+        d += x == mx ? 1.0 : exp((double)x - (double)mx);
+    }
+    return warp_sum(d);
+}
+
+// Row t, by the whole warp: which groups are kept, decided in fp64 from the experts that
+// fp32 (values c of the row, off by `err` at most and half a step) leaves for the two best.
+// 0: a group has more of them than kGroupCand (the row is left to select_fp64).
+constexpr int kGroupCand = 4;
+__device__ __noinline__ uint32_t resolve_groups(const RouteArgs& a, int t, const float* c, Layout lay, float mx, float err) {
+    const int lane = threadIdx.x & 31;
+    const double den = sum64(a, t, mx);
+    double score = -INFINITY;
+    bool over = false;
+    if (lane < a.n_groups) {
+        // the group's values: lpg lanes' rows of per + 4 floats
+        float k0 = -INFINITY, k1 = -INFINITY;
+        const float* row = c + lane * lay.lpg * (lay.per + 4);
+        for (int l = 0; l < lay.lpg; ++l)
+            for (int i = 0; i < lay.per; ++i) {  // (empty ones are -inf)
+                const float v = fmaxf(row[l * (lay.per + 4) + i], -INFINITY);
+                k1 = fmaxf(k1, fminf(k0, v));
+                k0 = fmaxf(k0, v);
+            }
+        const float low = a.top2 && k1 != -INFINITY ? k1 : k0;
+        const float from = low - 2.0f * err - 0x1p-21f * fabsf(low);
+        // collected first, so that the lanes' evaluations run together (they are what takes time)
+        int at[kGroupCand], n = 0;
+        for (int l = 0; l < lay.lpg && k0 != -INFINITY; ++l)
+            for (int i = 0; i < lay.per; ++i) {
+                if (!(row[l * (lay.per + 4) + i] >= from)) continue;
+#pragma unroll
+                for (int q = 0; q < kGroupCand; ++q) at[q] = q == n ? lane * lay.gs + l * lay.per + i : at[q];
+                ++n;
+            }
+        over = n > kGroupCand;
+        double d0 = -INFINITY, d1 = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kGroupCand; ++q) {
+            if (q >= n) continue;
+            const double v = score64(a, masked_logit(logit_at(a, t, at[q])), mx, den) + (a.bias ? (double)a.bias[at[q]] : 0.0);
+            d1 = fmax(d1, fmin(d0, v));
+            d0 = fmax(d0, v);
+        }
+        score = d0;
+        if (a.top2 && d1 != -INFINITY) score += d1;
+    }
+    __syncwarp();
+    if (__any_sync(0xffffffffu, over)) return 0;
+    int rank = 0;
+    for (int o = 0; o < a.n_groups; ++o) {
+        const double v = __shfl_sync(0xffffffffu, score, o);
+        rank += v > score || (v == score && o < lane) ? 1 : 0;
+    }
+    return __ballot_sync(0xffffffffu, lane < a.n_groups && rank < a.topk_groups);
+}
+
+// Row t, by the whole warp: the order of its n <= 64 candidates (in ascending order of
+// experts, e[]) in fp64; sorted[rank] = candidate.  v: 128 doubles.  A softmax's sum is
+// first taken of fp32 exponentials (the rounding of l - mx made good, so 2 steps each; 1024
+// fp64 ones take ten times as long), which decides unless two neighbours differ by no
+// more than that error makes of the difference of their scores.
+__device__ __noinline__ void resolve_order(const RouteArgs& a, int t, const uint16_t* e, int n, float mx, double* v,
+                                           uint16_t* sorted) {
+    const int lane = threadIdx.x & 31;
+    double* s = v + kCand;
+    double den = 1.0, rel = 0.0;
+    if (!a.sigmoid) {
+        den = 0.0;
+        for (int i = lane; i < a.E; i += 32) {
+            const float l = masked_logit(logit_at(a, t, i));
+            const float x = l - mx, back = x + mx;
+            const float rest = l == -INFINITY ? 0.0f : (l - back) - (mx - (back - x));
+            den += (double)(expf(x) * (1.0f + rest));
+        }
+        den = warp_sum(den);
+        rel = 0x1p-21;
+    }
+    for (bool again = true; again;) {
+        for (int q = lane; q < n; q += 32) {
+            s[q] = score64(a, masked_logit(logit_at(a, t, e[q])), mx, den);
+            v[q] = s[q] + (a.bias ? (double)a.bias[e[q]] : 0.0);
+        }
+        __syncwarp();
+        for (int q = lane; q < n; q += 32) {
+            int rank = 0;
+            for (int o = 0; o < n; ++o) rank += v[o] > v[q] || (v[o] == v[q] && o < q) ? 1 : 0;
+            sorted[rank] = (uint16_t)q;
+        }
+        __syncwarp();
+        bool open = false;
+        if (rel > 0.0)
+            for (int j = lane; j < min(a.k, n - 1); j += 32) {
+                const int q = sorted[j], r = sorted[j + 1];
+                open |= v[q] - v[r] <= rel * fabs(s[q] - s[r]) + 0x1p-45;
+            }
+        again = __any_sync(0xffffffffu, open);
+        if (again) {
+            den = sum64(a, t, mx);
+            rel = 0.0;
+        }
+    }
+}
+
+// Shared memory of a warp: two buffers of 32 lanes x `row` floats, or select_fp64's E doubles
+// (resolve_order's 2 kCand doubles fit one buffer from rows of 8 floats, and both of less).
+__host__ __device__ __forceinline__ int warp_smem(int E, int row) {
+    const int b = 2 * 32 * row * 4, d = (E * 8 + 15) & ~15;
+    return b > d ? b : d;
+}
+
+// LPT lanes per token, 32 / LPT tokens per warp.  What bounds it is issuing instructions:
+// most of a token's (threshold, ranking, weights) cost the same for one token per warp or
+// four, and the ones per expert are kept to the score and three more: a maximum of
+// blocks, a comparison with the threshold and its bit.
 template <int LPT, int PER, int KIND>
-__global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const __grid_constant__ RouteArgs a, int lpg, int vec) {
+__global__ void __launch_bounds__(kWarps * 32)
+    scored_topk_kernel(const __grid_constant__ RouteArgs a, int lpg, int vec) {
     pdl_begin();
-    constexpr int TPW = 32 / LPT;                // tokens per warp
+    constexpr int TPW = 32 / LPT;  // tokens per warp
     // experts per block maximum: at least 32 blocks of a full row, at most 8 experts each
     constexpr int BLK = PER * LPT >= 256 ? 8 : PER * LPT >= 64 ? PER * LPT / 32 : 1;
     constexpr int NB = PER / BLK;
-    extern __shared__ double c_all[];
-    __shared__ __align__(16) uint32_t cand_all[kWarps * TPW][kCand];
+    constexpr int ROW = PER + 4;  // floats of a lane in shared memory (16-byte accesses without bank conflicts)
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ __align__(16) float cand_all[kWarps * TPW][kCand];
     __shared__ uint16_t cand_e_all[kWarps * TPW][kCand];
     __shared__ uint16_t sorted_all[kWarps * TPW][kCand];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane & (LPT - 1), slot = lane / LPT;
-    uint32_t* cand = cand_all[warp * TPW + slot];      // keys of the candidates, in expert order
+    float* cand = cand_all[warp * TPW + slot];         // values of the candidates, in expert order
     uint16_t* cand_e = cand_e_all[warp * TPW + slot];  // their experts
     uint16_t* sorted = sorted_all[warp * TPW + slot];  // candidate of each rank
-    const int gs = a.E / a.n_groups;
+    // Two buffers of 32 lanes x ROW: the logits, then the values of the warp's tokens, and
+    // the logits of its next ones.  Also the fp64 scratch.
+    const int warp_bytes = warp_smem(a.E, ROW);
+    float* stage = reinterpret_cast<float*>(dyn + warp * warp_bytes);
+    float* rows = stage;
+    float* bias = reinterpret_cast<float*>(dyn + kWarps * warp_bytes);
+    Layout lay;
+    lay.gs = a.E / a.n_groups;
+    lay.lpg = lpg;
+    lay.per = PER;
     const int group = sub / lpg;
     const int in_group = (sub & (lpg - 1)) * PER;  // first of this lane's experts within its group
-    const int n_mine = group < a.n_groups ? min(PER, max(0, gs - in_group)) : 0;
-    const int e0 = group * gs + in_group;
+    const int n_mine = group < a.n_groups ? min(PER, max(0, lay.gs - in_group)) : 0;
+    const int e0 = group * lay.gs + in_group;
     const bool grouped = a.topk_groups < a.n_groups;
     const bool stats = KIND == kKeySoftmax || (!a.sigmoid && !a.renormalize);
-    // bias, a lane's experts together and lanes apart by PER + 4 words (16-byte reads without bank conflicts)
-    double* scratch = c_all + (size_t)warp * scratch_doubles(a.E);
-    float* bias = reinterpret_cast<float*>(c_all + (size_t)kWarps * scratch_doubles(a.E));
+    float bmax = -INFINITY;
     if (KIND != kKeyLogit) {
         if (warp == 0 && lane < LPT)
-            for (int i = 0; i < PER; ++i) bias[sub * (PER + 4) + i] = a.bias && i < n_mine ? a.bias[e0 + i] : 0.0f;
+            for (int i = 0; i < PER; ++i) bias[sub * ROW + i] = a.bias && i < n_mine ? a.bias[e0 + i] : 0.0f;
         __syncthreads();
+        for (int i = 0; i < n_mine; ++i) bmax = fmaxf(bmax, bias[sub * ROW + i]);
+        bmax = token_max<LPT>(bmax);
     }
 
-    float l[PER];
+    auto bias_of = [&](int e) { return a.bias ? __ldg(a.bias + e) : 0.0f; };
+
+    float c[PER];  // logits, then values
+    // Whole float4s (vec): rows come by asynchronous 16-byte copies, coalesced, into the
+    // places of their lanes, the next tokens' while these are selected.
+    auto clear = [&]() {  // the empty places stay so
+        for (int i = lane; i < 64 * ROW; i += 32) stage[i] = -INFINITY;
+        __syncwarp();
+    };
+    int dst[PER >= 4 ? PER / 4 : 1];
+    const int per_token = a.E / 4;
+    if (PER >= 4 && vec) {
+        if (a.E == LPT * PER) {  // no empty places: consecutive experts fill consecutive lanes
+#pragma unroll
+            for (int q = 0; q < (PER >= 4 ? PER / 4 : 1); ++q) {
+                const int e = (lane + q * 32) * 4;
+                dst[q] = e / PER * ROW + e % PER;
+            }
+        } else {
+            clear();
+        }
+#pragma unroll
+        for (int q = 0; q < (PER >= 4 ? PER / 4 : 1) && a.E != LPT * PER; ++q) {
+            const int f = lane + q * 32, tok = f / per_token, e = (f - tok * per_token) * 4;
+            const int g = e / lay.gs, i = e - g * lay.gs;
+            dst[q] = tok < TPW ? (tok * LPT + g * lpg + i / PER) * ROW + i % PER : -1;
+        }
+    }
+    auto prefetch = [&](int tw, int buf) {
+        const float4* src = reinterpret_cast<const float4*>(a.partials + (size_t)tw * a.E);
+        const int valid = min(TPW, a.T - tw) * per_token;  // float4s of tokens that exist
+#pragma unroll
+        for (int q = 0; q < (PER >= 4 ? PER / 4 : 1); ++q)
+            if (dst[q] >= 0 && lane + q * 32 < valid)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage + buf * 32 * ROW + dst[q])),
+                             "l"(src + lane + q * 32)
+                             : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     auto load = [&](int t) {
         const float* p = a.partials + (size_t)t * a.E + e0;
         const int n = t < a.T ? n_mine : 0;
-        if (PER >= 4 && vec) {
-            // rows and groups are whole float4s, so a lane's experts are too
 #pragma unroll
-            for (int i = 0; i < PER; i += 4)
-                if (i < n) {
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
-                    l[i] = v.x;
-                    l[(i + 1) % PER] = v.y;
-                    l[(i + 2) % PER] = v.z;
-                    l[(i + 3) % PER] = v.w;
-                }
-        } else {
+        for (int i = 0; i < PER; ++i) c[i] = i < n ? p[i] : -INFINITY;
+        for (int s = 1; s < a.ksplit; ++s) {
+            p += (size_t)a.T * a.E;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (i < n) l[i] = p[i];
-            for (int s = 1; s < a.ksplit; ++s) {
-                p += (size_t)a.T * a.E;
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (i < n) l[i] += p[i];
-            }
+                if (i < n) c[i] += p[i];
         }
     };
-#pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = 0.0f;
     const int stride = gridDim.x * kWarps * TPW;
     int tw = (blockIdx.x * kWarps + warp) * TPW;  // the warp's first token
-    load(tw + slot);
+    int buf = 0;
+    if (PER >= 4 && vec && tw < a.T) prefetch(tw, 0);
     for (; tw < a.T; tw += stride) {
         const int t = tw + slot;
+        if (PER >= 4 && vec) {
+            if (tw + stride < a.T) prefetch(tw + stride, buf ^ 1);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
+            rows = stage + buf * 32 * ROW;
+            const float* r = rows + lane * ROW;
+#pragma unroll
+            for (int i = 0; i < PER; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(r + i);
+                c[i] = v.x;
+                c[(i + 1) % PER] = v.y;
+                c[(i + 2) % PER] = v.z;
+                c[(i + 3) % PER] = v.w;
+            }
+            buf ^= 1;
+            __syncwarp();
+        } else {
+            load(t);
+        }
         const bool alive = t < a.T;
         if (a.logits_out && alive) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (i < n_mine) a.logits_out[(size_t)t * a.E + e0 + i] = l[i];
+                if (i < n_mine) a.logits_out[(size_t)t * a.E + e0 + i] = c[i];
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) l[i] = masked_logit(l[i]);
-        float mx = -INFINITY, den = 1.0f;
-        if (KIND == kKeyLogit && !a.sigmoid) {
-            // beside an infinite logit every finite one has softmax 0: they tie
-            bool inf = false;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) inf |= i < n_mine && l[i] == INFINITY;
-            if (token_any<LPT>(inf)) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (isfinite(l[i])) l[i] = -FLT_MAX;
-            }
-        }
-        uint32_t key[PER];
+        // ---- values.  A NaN stays a NaN, which no maximum and no comparison takes: masked.
+        bool unsure = !alive;  // the row is left to select_fp64 (or does not exist)
+        float mx = 0.0f, inv_den = 1.0f;
+        float e[KIND == kKeySoftmax ? PER : 1];
         if (stats) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (i < n_mine) mx = fmaxf(mx, l[i]);
-            mx = token_max<LPT>(mx);
+            mx = token_max<LPT>(max_of<PER>(c));
+            unsure |= !(fabsf(mx) < INFINITY);  // an infinite logit, or none at all
             float part[PER];  // summed in pairs: log2(E) roundings
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                part[i] = i < n_mine && l[i] != -INFINITY ? exp_rel(l[i], mx) : 0.0f;
-                if (KIND == kKeySoftmax) key[i] = __float_as_uint(part[i]);
+                part[i] = fmaxf(fast_exp2((c[i] - mx) * kLog2e), 0.0f);
+                if (KIND == kKeySoftmax) e[i % (KIND == kKeySoftmax ? PER : 1)] = part[i];
             }
 #pragma unroll
             for (int w = PER / 2; w > 0; w >>= 1)
 #pragma unroll
                 for (int i = 0; i < w; ++i) part[i] += part[i + w];
-            den = token_sum<LPT>(part[0]);
+            inv_den = 1.0f / token_sum<LPT>(part[0]);
         }
-        const float inv_den = 1.0f / den;
+        if (KIND != kKeyLogit) {
 #pragma unroll
-        for (int i = 0; i < PER; i += (PER >= 4 ? 4 : 1)) {
-            float b4[4];
-            if (KIND != kKeyLogit) {
+            for (int i = 0; i < PER; i += (PER >= 4 ? 4 : 1)) {
+                float b4[4];
                 if (PER >= 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(bias + sub * (PER + 4) + i);
+                    const float4 v = *reinterpret_cast<const float4*>(bias + sub * ROW + i);
                     b4[0] = v.x;
                     b4[1] = v.y;
                     b4[2] = v.z;
                     b4[3] = v.w;
                 } else {
-                    b4[0] = bias[sub * (PER + 4) + i];
+                    b4[0] = bias[sub * ROW + i];
                 }
-            }
 #pragma unroll
-            for (int u = 0; u < (PER >= 4 ? 4 : 1); ++u) {
-                float c = l[i + u];
-                if (KIND == kKeySigmoid) c = fast_sigmoid(c) + b4[u];
-                if (KIND == kKeySoftmax) c = fmaf(__uint_as_float(key[i + u]), inv_den, b4[u]);
-                if (KIND != kKeyLogit && l[i + u] == -INFINITY) c = -INFINITY;
-                key[i + u] = i + u < n_mine ? key_of(c) : 0u;
+                for (int u = 0; u < (PER >= 4 ? 4 : 1); ++u) {
+                    // 2^-149 l: nothing beside the bias, but for -inf, which stays -inf
+                    const float base = fmaf(c[i + u], 0x1p-149f, b4[u]);
+                    if (KIND == kKeySigmoid) c[i + u] = base + fast_rcp(1.0f + fast_exp2(c[i + u] * -kLog2e));
+                    else c[i + u] = fmaf(e[(i + u) % (KIND == kKeySoftmax ? PER : 1)], inv_den, base);
+                }
             }
         }
-        // the next row's loads run while this one is selected
-        load(tw + stride + slot);
-
-        // Bound of |fp32 value - exact value| before the bias is added.  Sigmoid: the
-        // exponential is off by 2 + 1.18 |l| steps, which 1 / (1 + e) takes s (1 - s) of
-        // (at most 0.63 steps of 2^-23), the sum and the reciprocal by 1.5 more: 3 in
-        // all.  Softmax: 2 steps of the exponential, |l - mx| / 2 of its argument, those
-        // of den (`rel` below), of 1 / den and the product, all relative to a value of
-        // at most 1 / den: below 16.  The sum with the bias adds half a step.
+        // Bound of |c - exact| before the sum with the bias rounds (half a step).  Sigmoid: the
+        // exponential is off by 2 steps and 1.5 |l| of its argument, which 1 / (1 + e) takes
+        // s (1 - s) of (at most 0.75 steps of 2^-23), the sum and the reciprocal by 1.5
+        // more: 3 in all.  Softmax: 2 steps of the exponential and 1.5 |l - mx| of its
+        // argument (at most 0.6 of the value 1 / den), log2(1024) / 2 of the sum and 3 of
+        // its terms, 2 of 1 / den and the product: 16.  Where a logit is near -FLT_MAX
+        // 2^-149 of it adds 4 steps to its bias; only rows whose threshold is not above the
+        // largest bias can select such an expert.
         const float err = KIND == kKeyLogit ? 0.0f : 0x1p-23f * (KIND == kKeySigmoid ? 3.0f : 16.0f * inv_den);
-        // exact scores: the softmax's sum in fp64, then one logit at a time
-        double den64 = 0.0;
-        auto sum64 = [&](bool need) {
-            if (KIND != kKeySoftmax) return;
-            double d = 0.0;
-            if (need)
-                for (int i = 0; i < n_mine; ++i) {
-                    const float x = masked_logit(logit_at(a, t, e0 + i));
-                    if (x != -INFINITY) d += x == mx ? 1.0 : exp((double)x - (double)mx);
-                }
+
+        // ---- groups
+        float m[NB];
 #pragma unroll
-            for (int w = LPT / 2; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
-            if (need) den64 = d;
+        for (int q = 0; q < NB; ++q) m[q] = max_of<BLK>(c + q * BLK);
+        auto write_rows = [&]() {
+            float* r = rows + lane * ROW;
+            if constexpr (PER >= 4) {
+#pragma unroll
+                for (int i = 0; i < PER; i += 4)
+                    *reinterpret_cast<float4*>(r + i) = make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) r[i] = c[i];
+            }
+            __syncwarp();
         };
-        auto score64 = [&](float x) -> double {
-            if (KIND == kKeySoftmax) return (x == mx ? 1.0 : exp((double)x - (double)mx)) / den64;
-            return 1.0 / (1.0 + exp(-(double)x));
-        };
-        bool unsure = false;
+        write_rows();
         if (grouped) {
-            uint32_t k0 = 0, k1 = 0;  // the two largest of the group
+            float k0, k1 = -INFINITY;  // the two largest of the group
+            if (KIND != kKeyLogit && a.top2) {
+                k0 = -INFINITY;
+                if constexpr (PER >= 2) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                k1 = max(k1, min(k0, key[i]));
-                k0 = max(k0, key[i]);
+                    for (int i = 0; i < PER; i += 2) {
+                        const float x = fmaxf(c[i], -INFINITY), y = fmaxf(c[i + 1], -INFINITY);
+                        const float hi = fmaxf(x, y);
+                        k1 = max3(k1, fminf(x, y), fminf(k0, hi));
+                        k0 = fmaxf(k0, hi);
+                    }
+                } else {
+                    k0 = fmaxf(c[0], -INFINITY);
+                }
+            } else {
+                k0 = fmaxf(max_of<NB>(m), -INFINITY);
             }
             for (int d = 1; d < lpg; d <<= 1) {
-                const uint32_t o0 = __shfl_xor_sync(0xffffffffu, k0, d), o1 = __shfl_xor_sync(0xffffffffu, k1, d);
-                k1 = max(max(k1, o1), min(k0, o0));
-                k0 = max(k0, o0);
+                const float o0 = __shfl_xor_sync(0xffffffffu, k0, d), o1 = __shfl_xor_sync(0xffffffffu, k1, d);
+                k1 = max3(k1, o1, fminf(k0, o0));
+                k0 = fmaxf(k0, o0);
             }
-            float g = k0 ? value_of(k0) : 0.0f;
-            const bool two = a.top2 && k1 && value_of(k1) != -INFINITY;
-            if (KIND != kKeyLogit && two) g += value_of(k1);
-            const uint32_t gk = group < a.n_groups ? key_of(g) : 0u;
+            const float g = KIND != kKeyLogit && a.top2 && k1 != -INFINITY ? k0 + k1 : k0;
             int rank = 0;
             for (int o = 0; o < a.n_groups; ++o) {
-                const uint32_t ok = __shfl_sync(0xffffffffu, gk, o * lpg, LPT);
-                rank += ok > gk || (ok == gk && o < group) ? 1 : 0;
+                const float v = __shfl_sync(0xffffffffu, g, o * lpg, LPT);
+                rank += v > g || (v == g && o < group) ? 1 : 0;
             }
             bool keep = group < a.n_groups && rank < a.topk_groups;
             if (KIND != kKeyLogit) {
-                const float in = value_of(~token_max<LPT>(keep ? ~gk : 0u)), out = value_of(token_max<LPT>(keep ? 0u : gk));
+                const float in = -token_max<LPT>(keep ? -g : -INFINITY);
+                const float out = token_max<LPT>(keep || group >= a.n_groups ? -INFINITY : g);
                 // (two groups without an unmasked expert tie exactly)
-                const bool close = out != -INFINITY && in - out <= 4.0f * err + 0x1p-21f * fabsf(in);
-                if (__any_sync(0xffffffffu, close)) {
-                    // the group scores in fp64, from the experts that fp32 leaves for the two best
-                    const float low = value_of(a.top2 && k1 ? k1 : k0);
-                    const float margin = 2.0f * err + 0x1p-22f * fabsf(low);
-                    double d0 = -INFINITY, d1 = -INFINITY;
-                    sum64(close);
-                    if (close && k0) {
-                        for (int i = 0; i < n_mine; ++i) {
-                            const float x = masked_logit(logit_at(a, t, e0 + i));
-                            uint32_t ki = 0;
-#pragma unroll
-                            for (int u = 0; u < PER; ++u) ki = u == i ? key[u] : ki;
-                            if (x == -INFINITY || value_of(ki) < low - margin) continue;
-                            const double c = score64(x) + (double)bias[sub * (PER + 4) + i];
-                            d1 = fmax(d1, fmin(d0, c));
-                            d0 = fmax(d0, c);
-                        }
+                const float far = err + (out <= 2.0f * bmax + 0x1p-10f ? 0x1p-21f : 0.0f);
+                const bool close = out != -INFINITY && in - out <= 4.0f * far + 0x1p-21f * fabsf(in);
+                for (uint32_t todo = __ballot_sync(0xffffffffu, close && sub == 0 && !unsure); todo; todo &= todo - 1) {
+                    const int s = (__ffs(todo) - 1) / LPT;
+                    const uint32_t kept = resolve_groups(a, tw + s, rows + s * LPT * ROW, lay,
+                                                         __shfl_sync(0xffffffffu, mx, s * LPT),
+                                                         __shfl_sync(0xffffffffu, far, s * LPT));
+                    if (slot == s) {
+                        keep = group < a.n_groups && ((kept >> group) & 1u);
+                        unsure |= kept == 0;
                     }
-                    for (int d = 1; d < lpg; d <<= 1) {
-                        const double o0 = __shfl_xor_sync(0xffffffffu, d0, d), o1 = __shfl_xor_sync(0xffffffffu, d1, d);
-                        d1 = fmax(fmax(d1, o1), fmin(d0, o0));
-                        d0 = fmax(d0, o0);
-                    }
-                    if (a.top2 && d1 != -INFINITY) d0 += d1;
-                    int exact = 0;
-                    for (int o = 0; o < a.n_groups; ++o) {
-                        const double od = __shfl_sync(0xffffffffu, d0, o * lpg, LPT);
-                        exact += od > d0 || (od == d0 && o < group) ? 1 : 0;
-                    }
-                    if (close) keep = group < a.n_groups && exact < a.topk_groups;
                 }
             }
+            if (!keep) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (!keep) key[i] = 0u;
+                for (int q = 0; q < NB; ++q) m[q] = -INFINITY;
+            }
         }
-        // threshold: the (k+1)-th largest block maximum (the largest k+1 keys pass it)
-        uint32_t m[NB];
-#pragma unroll
-        for (int q = 0; q < NB; ++q) {
-            m[q] = 0;
-#pragma unroll
-            for (int i = 0; i < BLK; ++i) m[q] = max(m[q], key[q * BLK + i]);
-        }
-        uint32_t tau = 0, top = 0;
+        // ---- threshold: the (k+1)-th largest block maximum (the largest k+1 values pass it)
+        const bool mine_out = !(max_of<NB>(m) > -INFINITY);  // no expert of this lane can be selected
+        float tau = INFINITY, top = -INFINITY;
         for (int j = 0; j <= a.k; ++j) {
-            uint32_t mine = m[0];
-#pragma unroll
-            for (int q = 1; q < NB; ++q) mine = max(mine, m[q]);
-            tau = token_max<LPT>(mine);
+            tau = token_max<LPT>(max_of<NB>(m));
             if (j == 0) top = tau;
 #pragma unroll
-            for (int q = 0; q < NB; ++q)
-                if (m[q] == tau) m[q] = 0;
+            for (int q = 0; q < NB; ++q) m[q] = m[q] == tau ? -INFINITY : m[q];
         }
-        const float mag = fmaxf(fabsf(value_of(top)), tau ? fabsf(value_of(tau)) : 0.0f);
-        const float eps = 2.0f * err + (KIND == kKeyLogit || mag == INFINITY ? 0.0f : 0x1p-22f * mag);
-        if (KIND != kKeyLogit && tau && value_of(tau) != -INFINITY) tau = key_of(value_of(tau) - 2.0f * eps);
-        if (tau == 0) tau = 1;
-        // candidates in expert order
-        int cnt = 0;
+        float eps = 0.0f;
+        if (KIND != kKeyLogit) {
+            const float far = err + (tau <= bmax + 0x1p-10f ? 0x1p-21f : 0.0f);
+            eps = 2.0f * far + 0x1p-22f * fmaxf(fabsf(top), tau > -INFINITY ? fabsf(tau) : 0.0f);
+            tau -= 2.0f * eps;
+        } else if (!a.sigmoid) {
+            unsure |= top == INFINITY;  // beside an infinite logit every other has softmax 0: they tie
+        }
+        tau = fmaxf(tau, -FLT_MAX);
+        // ---- candidates in expert order
+        uint32_t part_bits[4] = {0, 0, 0, 0};
+        auto mark = [&](int i, float v) {
+            asm("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, %2;\n\t@p or.b32 %0, %0, %3;\n\t}"
+                : "+r"(part_bits[i & 3])
+                : "f"(v), "f"(tau), "r"(1u << (i & 31)));
+        };
+        if constexpr (PER >= 4) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) cnt += key[i] >= tau ? 1 : 0;
+            for (int i = 0; i < PER; i += 4) {  // from `rows`: the registers are free for the calls above
+                const float4 v = *reinterpret_cast<const float4*>(rows + lane * ROW + i);
+                mark(i, v.x);
+                mark(i + 1, v.y);
+                mark(i + 2, v.z);
+                mark(i + 3, v.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mark(i, rows[lane * ROW + i]);
+        }
+        uint32_t bits = (part_bits[0] | part_bits[1]) | (part_bits[2] | part_bits[3]);
+        if (mine_out) bits = 0;
+        const int cnt = __popc(bits);
         int incl = cnt;
 #pragma unroll
         for (int d = 1; d < LPT; d <<= 1) {
@@ -509,117 +675,122 @@ __global__ void __launch_bounds__(kWarps * 32) scored_topk_kernel(const __grid_c
             if (sub >= d) incl += o;
         }
         int n = __shfl_sync(0xffffffffu, incl, LPT - 1, LPT);
-        if (n > kCand) {
+        if (unsure || n > kCand || n < a.k) {  // too many, or masked experts are among the selected
             unsure = true;
             n = 0;
+            bits = 0;
         }
-        if (n > 0) {
-            int at = incl - cnt;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (key[i] >= tau) {
-                    cand[at] = key[i];
-                    cand_e[at] = (uint16_t)(e0 + i);
-                    ++at;
-                }
-            // whole vectors of four
-            for (int q = n + sub; q < ((n + 3) & ~3); q += LPT) cand[q] = 0u;
+        for (int at = incl - cnt; bits; ++at, bits &= bits - 1) {
+            const int i = __ffs(bits) - 1;
+            cand[at] = rows[lane * ROW + i];
+            cand_e[at] = (uint16_t)(e0 + i);
         }
+        // whole vectors of four
+        for (int q = n + sub; q < ((n + 3) & ~3); q += LPT) cand[q] = -INFINITY;
         __syncwarp();
+        // ---- order: rank of each candidate among all
+        bool dirty = false;  // the rows hold fp64 scratch
+        bool tie = false;
         for (int q = sub; q < n; q += LPT) {
-            // ties in expert order: an equal key at a lower position counts as larger
-            const uint32_t mine = cand[q];
-            int rank = 0;
+            const float mine = cand[q];
+            int rank = 0, same = 0;
             for (int o = 0; o < n; o += 4) {
-                const uint4 v = *reinterpret_cast<const uint4*>(cand + o);
-                rank += v.x > mine || (v.x == mine && o < q) ? 1 : 0;
-                rank += v.y > mine || (v.y == mine && o + 1 < q) ? 1 : 0;
-                rank += v.z > mine || (v.z == mine && o + 2 < q) ? 1 : 0;
-                rank += v.w > mine || (v.w == mine && o + 3 < q) ? 1 : 0;
+                const float4 v = *reinterpret_cast<const float4*>(cand + o);
+                rank += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+                same += (v.x == mine) + (v.y == mine) + (v.z == mine) + (v.w == mine);
             }
+            tie |= same > 1;
             sorted[rank] = (uint16_t)q;
+        }
+        if (__any_sync(0xffffffffu, tie)) {
+            // ties in expert order: an equal value at a lower position goes first
+            __syncwarp();
+            for (int q = sub; q < n; q += LPT) {
+                const float mine = cand[q];
+                int rank = 0;
+                for (int o = 0; o < n; ++o) rank += cand[o] > mine || (cand[o] == mine && o < q) ? 1 : 0;
+                sorted[rank] = (uint16_t)q;
+            }
         }
         __syncwarp();
         if (KIND != kKeyLogit) {
             // neighbours of the first k + 1 in order, too close for fp32?
             bool close = false;
             for (int j = sub; j < min(a.k, n - 1); j += LPT) {
-                const float next = value_of(cand[sorted[j + 1]]);
-                close |= next != -INFINITY && value_of(cand[sorted[j]]) - next <= eps;
-            }
-            const bool again = token_any<LPT>(close);
-            if (__any_sync(0xffffffffu, again)) {
-                // the candidates again in fp64 (every exact value above the k-th is among them), in
-                // the warp's fp64 scratch: values and scores
-                sum64(again);
-                for (int w = 0; w < TPW; ++w) {
-                    // one token of the warp after the other
-                    const bool turn = again && slot == w;
-                    if (turn)
-                        for (int q = sub; q < n; q += LPT) {
-                            const int e = cand_e[q];
-                            const float x = masked_logit(logit_at(a, t, e));
-                            scratch[q] = x == -INFINITY ? -INFINITY : score64(x) + (a.bias ? (double)a.bias[e] : 0.0);
-                        }
-                    __syncwarp();
-                    if (turn)
-                        for (int q = sub; q < n; q += LPT) {
-                            int rank = 0;
-                            for (int o = 0; o < n; ++o)
-                                rank += scratch[o] > scratch[q] || (scratch[o] == scratch[q] && o < q) ? 1 : 0;
-                            sorted[rank] = (uint16_t)q;
-                        }
-                    __syncwarp();
+                const int q = sorted[j], r = sorted[j + 1];
+                float near = eps;
+                if (KIND == kKeySoftmax) {
+                    // the error is relative to the scores: those of the pair, where the largest is 1 / den
+                    const float pq = cand[q] - bias_of(cand_e[q]), pr = cand[r] - bias_of(cand_e[r]);
+                    near = eps - 2.0f * err + 0x1p-23f * 16.0f * (fabsf(pq) + fabsf(pr));
                 }
+                close |= cand[q] - cand[r] <= near;
+            }
+            uint32_t todo = __ballot_sync(0xffffffffu, close);
+            dirty = todo != 0;
+            while (todo) {
+                // (every exact value above the k-th is among the candidates)
+                const int s = (__ffs(todo) - 1) / LPT, w = warp * TPW + s;
+                resolve_order(a, tw + s, cand_e_all[w], __shfl_sync(0xffffffffu, n, s * LPT),
+                              __shfl_sync(0xffffffffu, mx, s * LPT), reinterpret_cast<double*>(rows), sorted_all[w]);
+                todo &= ~(((LPT == 32 ? 0u : 1u << (LPT & 31)) - 1u) << (s * LPT));
             }
         }
-        unsure = token_any<LPT>(unsure);
-        // weights: lane sub holds the selected experts sub, sub + LPT, ... of its token
-        constexpr int KPL = 32 / LPT;
-        float lw[KPL], sh[KPL];
-        int me[KPL];
-        float low = -INFINITY;
+        // ---- weights: lane sub holds the selected experts sub, sub + LPT, ... of its token
+        for (int j0 = 0; j0 < (a.renormalize ? 1 : a.k); j0 += LPT) {
+            if (!a.renormalize) {
+                const int j = j0 + sub;
+                if (j < a.k && !unsure) {
+                    const int id = cand_e[sorted[j]];
+                    const float l = logit_at(a, t, id);
+                    a.topk_idx[(size_t)t * a.k + j] = id;
+                    a.topk_w[(size_t)t * a.k + j] = a.scale * (a.sigmoid ? sigmoid_f(l) : exp_rel(l, mx) * inv_den);
+                }
+            } else {
+                constexpr int KPL = 32 / LPT;
+                float l[KPL], sh[KPL];
+                float low = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int q = 0; q < KPL; ++q) {
-            const int j = sub + q * LPT;
-            const bool in = j < a.k && alive && !unsure;
-            me[q] = in ? cand_e[sorted[j]] : 0;
-            lw[q] = in ? masked_logit(logit_at(a, t, me[q])) : -INFINITY;
-            if (j < a.k) low = fmaxf(low, a.sigmoid ? fminf(lw[q], 0.0f) : lw[q]);
-        }
-        if (a.renormalize) {
-            low = token_max<LPT>(low);
-            float sum = 0.0f;
+                for (int q = 0; q < KPL; ++q) {
+                    l[q] = -INFINITY;
+                    const int j = sub + q * LPT;
+                    if (j < a.k && !unsure) {
+                        const int id = cand_e[sorted[j]];
+                        l[q] = logit_at(a, t, id);
+                        a.topk_idx[(size_t)t * a.k + j] = id;
+                        low = fmaxf(low, a.sigmoid ? fminf(l[q], 0.0f) : l[q]);
+                    }
+                }
+                low = token_max<LPT>(low);
 #pragma unroll
-            for (int q = 0; q < KPL; ++q) {
-                sh[q] = 0.0f;
-                if (lw[q] != -INFINITY) sh[q] = share_term(lw[q], low, a.sigmoid);
-                sum += sh[q];
-            }
-            sum = token_sum<LPT>(sum);
-            const float f = sum > 0.0f ? a.scale / sum : 0.0f;
+                for (int q = 0; q < KPL; ++q) {
+                    sh[q] = 0.0f;
+                    if (sub + q * LPT < a.k && !unsure) sh[q] = share_term(l[q], low, a.sigmoid);
+                    sum += sh[q];
+                }
+                sum = token_sum<LPT>(sum);
+                const float f = a.scale / sum;
 #pragma unroll
-            for (int q = 0; q < KPL; ++q) sh[q] *= f;
-        } else {
-#pragma unroll
-            for (int q = 0; q < KPL; ++q) {
-                sh[q] = 0.0f;
-                if (lw[q] != -INFINITY) sh[q] = a.scale * (a.sigmoid ? sigmoid_f(lw[q]) : exp_rel(lw[q], mx) * inv_den);
-            }
-        }
-        if (alive && !unsure) {
-#pragma unroll
-            for (int q = 0; q < KPL; ++q) {
-                const int j = sub + q * LPT;
-                if (j < a.k) {
-                    a.topk_idx[(size_t)t * a.k + j] = me[q];
-                    a.topk_w[(size_t)t * a.k + j] = sh[q];
+                for (int q = 0; q < KPL; ++q) {
+                    const int j = sub + q * LPT;
+                    if (j < a.k && !unsure) a.topk_w[(size_t)t * a.k + j] = sh[q] * f;
                 }
             }
         }
         uint32_t redo = __ballot_sync(0xffffffffu, alive && unsure && sub == 0);
-        for (; redo; redo &= redo - 1)
-            select_fp64(a, tw + (__ffs(redo) - 1) / LPT, scratch);
+        if (redo) {
+            // (its scratch is both buffers: the copies under way end first and start again)
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
+            for (; redo; redo &= redo - 1) select_fp64(a, tw + (__ffs(redo) - 1) / LPT, reinterpret_cast<double*>(stage));
+            if (PER >= 4 && vec && tw + stride < a.T) {
+                clear();
+                prefetch(tw + stride, buf);
+            }
+        } else if (dirty) {
+            // empty places are not copied over
+            for (int i = n_mine; i < PER; ++i) rows[lane * ROW + i] = -INFINITY;
+        }
         __syncwarp();
     }
 }
@@ -718,17 +889,23 @@ int check_router(const moe_shape_t* s, const moe_router_t* r, int T) {
     return MOE_OK;
 }
 
-int grid_for(int T, int per_cta = kWarps) {
+int grid_for(int T, int per_cta = kWarps, int per_sm = 16) {
     const long want = ((long)T + per_cta - 1) / per_cta;
-    const long cap = (long)num_sms() * 16;
+    const long cap = (long)num_sms() * per_sm;
     return (int)(want < cap ? want : cap);
 }
 
 template <int LPT, int PER>
 cudaError_t launch_scored_per(const RouteArgs& a, int kind, int lpg, int vec, cudaStream_t stream) {
-    const size_t smem = (size_t)kWarps * scratch_doubles(a.E) * sizeof(double) + LPT * (PER + 4) * sizeof(float);
+    const size_t smem = (size_t)kWarps * warp_smem(a.E, PER + 4) + LPT * (PER + 4) * sizeof(float);
     auto launch = [&](auto kern) {
-        return launch_pdl(kern, dim3(grid_for(a.T, kWarps * (32 / LPT))), dim3(kWarps * 32), smem, stream, a, lpg, vec);
+        static std::atomic<uint64_t> configured[3];
+        const cudaError_t e = configure_once(configured[kind], [&] {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        });
+        if (e != cudaSuccess) return e;
+        // four CTAs an SM are resident (registers), each taking several turns: its set-up is paid once
+        return launch_pdl(kern, dim3(grid_for(a.T, kWarps * (32 / LPT), 4)), dim3(kWarps * 32), smem, stream, a, lpg, vec);
     };
     if (kind == kKeyLogit) return launch(scored_topk_kernel<LPT, PER, kKeyLogit>);
     if (kind == kKeySigmoid) return launch(scored_topk_kernel<LPT, PER, kKeySigmoid>);
@@ -748,12 +925,13 @@ cudaError_t launch_scored(const RouteArgs& a, cudaStream_t stream) {
         return (gs + lpg - 1) / lpg;
     };
     const int vec = a.ksplit == 1 && gs % 4 == 0 && (reinterpret_cast<uintptr_t>(a.partials) & 15) == 0;
-    // Two tokens per warp once every SM has dozens of tokens (65536 x 256: 77 against 88 us);
-    // below, one per warp ends sooner (4096: 12 against 15 us).
-    const int per16 = a.T >= 16384 ? fit(16) : 0;
-    if (per16 > 4 && per16 <= 16 && a.k <= 31) {
-        if (per16 <= 8) return launch_scored_per<16, 8>(a, kind, lpg, vec, stream);
-        return launch_scored_per<16, 16>(a, kind, lpg, vec, stream);
+    // Four tokens per warp once every SM has sixteen (65536 x 256, sigmoid and groups: 50
+    // against 102 us; 4096: 12.2 against 13.3); below, one ends sooner (512: 6.8 against 5.5).
+    const int per8 = a.T >= 16 * num_sms() ? fit(8) : 0;
+    if (per8 > 4 && per8 <= 32 && a.k <= 16) {
+        if (per8 <= 8) return launch_scored_per<8, 8>(a, kind, lpg, vec, stream);
+        if (per8 <= 16) return launch_scored_per<8, 16>(a, kind, lpg, vec, stream);
+        return launch_scored_per<8, 32>(a, kind, lpg, vec, stream);
     }
     const int per = fit(32);
     // more than 31 selected (no block left for the next one) or more experts than a lane holds
