@@ -213,6 +213,7 @@ struct ProjArgs {
     int T, O, C, r, n_adapters;  // O output features, C contracted features
     int bn;             // tokens of a tile (a multiple of 16)
     int splits;         // CTAs of a cluster that share one tile's contraction
+    int v_ready;        // v was complete before this kernel could start
     void* out;          // [T][O]
     int out_fp32;
     DevStatus st;
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
             stage = (stage + c1 - c0) % stages;
             const int n_ext = tl.count * rc;
-            if (rank < n_ext) pdl_wait();  // v
+            if (rank < n_ext && !a.v_ready) pdl_wait();
             VRows<BN == 256 ? 2 : 1> vr;
             vr.ids(tl.ids, a.bn, tid);
             int held = -1;
@@ -865,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
             stage = (stage + kc) % kPairStages;
             const int n_ext = tl.count * rc;
-            if (n_ext) pdl_wait();  // v
+            if (n_ext && !a.v_ready) pdl_wait();
             VRows<1> vr;
             vr.ids(tl.ids + rank * half, half, tid);
             int held = -1;
@@ -932,11 +933,15 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------- v = s A x, few tokens
-// One CTA per adapter (or, with fewer tokens than adapters, per first token of an adapter)
-// and JR of its rows: the rows stream from memory once for up to NT tokens at a time, the
-// eight warps share the contraction.  The rows are what there is to read, so many small
-// CTAs keep them coming.
-constexpr int kFewTokens = 64;
+// One CTA per adapter (or, with fewer tokens than adapters, per first token of an adapter),
+// JR of its rows and a share of its tokens: the rows stream from memory once for up to NT
+// tokens at a time, the eight warps share the contraction.  The rows are what there is to
+// read, so many small CTAs keep them coming.  It ends sooner than the tensor-core kernel,
+// whose 128-token tiles multiply every token with every adapter of the tile, while tokens
+// x rank is small (32 tokens, rank 16: 4 against 13 us; 192 tokens, rank 32: 5 against 12).
+constexpr int kFewTokens = 256;
+constexpr int kFewProducts = 8192;  // tokens x rank
+constexpr int kFewShares = 4;       // of an adapter's tokens, from 64 tokens
 constexpr int JR = 2, NT = 4;
 
 __device__ __forceinline__ void dot8(float& acc, const uint4& p, const uint4& q) {
@@ -972,48 +977,42 @@ __global__ void __launch_bounds__(256) shrink_few_kernel(const uint16_t* x, cons
     pdl_wait();
     pdl_launch_dependents();
     __shared__ float part[8][NT][JR];
+    __shared__ uint16_t mine[kFewTokens];  // the adapter's tokens, ascending
+    __shared__ int counts[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool by_token = T < n_adapters;
-    const int id0 = lane < T ? adapter_of[lane] : -2, id1 = 32 + lane < T ? adapter_of[32 + lane] : -2;
-    const int id = by_token ? __shfl_sync(0xffffffffu, blockIdx.x < 32 ? id0 : id1, blockIdx.x & 31) : (int)blockIdx.x;
-    if (blockIdx.y == 0 && (by_token || blockIdx.x == 0) && warp == 0) {
-        // tokens without adapter: v = 0
-        for (int h = 0; h < 2; ++h) {
-            const int t = h * 32 + lane, of = h ? id1 : id0;
-            if (t >= T || (of >= 0 && of < n_adapters) || (by_token && t != (int)blockIdx.x)) continue;
-            if (of != -1) raise_status(st, kStatusInvalidExpert);
-            for (int j = 0; j < r; j += 8) *reinterpret_cast<uint4*>(v + (size_t)t * r + j) = make_uint4(0, 0, 0, 0);
-        }
+    const int of = tid < T ? adapter_of[tid] : -2;
+    const int id = by_token ? adapter_of[blockIdx.x] : (int)blockIdx.x;
+    if (blockIdx.y == 0 && blockIdx.z == 0 && tid < T && (of < 0 || of >= n_adapters) &&
+        (by_token ? tid == (int)blockIdx.x : blockIdx.x == 0)) {
+        // a token without adapter: v = 0
+        if (of != -1) raise_status(st, kStatusInvalidExpert);
+        for (int j = 0; j < r; j += 8) *reinterpret_cast<uint4*>(v + (size_t)tid * r + j) = make_uint4(0, 0, 0, 0);
     }
     if (id < 0 || id >= n_adapters) return;
-    uint32_t m0 = __ballot_sync(0xffffffffu, id0 == id), m1 = __ballot_sync(0xffffffffu, id1 == id);
-    if (by_token) {  // an earlier token of the same adapter does the work
-        const int f = m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
-        if (f != (int)blockIdx.x) return;
+    const uint32_t here = __ballot_sync(0xffffffffu, of == id);
+    if (lane == 0) counts[warp] = __popc(here);
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        before += w < warp ? counts[w] : 0;
+        total += counts[w];
     }
+    if (of == id) mine[before + __popc(here & ((1u << lane) - 1u))] = (uint16_t)tid;
+    __syncthreads();
+    // (with fewer tokens than adapters, an earlier token of the same adapter does the work)
+    if ((int)blockIdx.z * NT >= total || (by_token && mine[0] != blockIdx.x)) return;
     const int j0 = blockIdx.y * JR;
     const uint4* ar[JR];
 #pragma unroll
     for (int j = 0; j < JR; ++j) ar[j] = reinterpret_cast<const uint4*>(m + ((size_t)id * r + j0 + j) * C);
     const float scale = scaling ? scaling[id] : 1.0f;
-    while (m0 | m1) {
-        int tok[NT], n = 0;
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-            tok[q] = 0;
-            if (m0) {
-                tok[q] = __ffs(m0) - 1;
-                m0 &= m0 - 1;
-                ++n;
-            } else if (m1) {
-                tok[q] = 31 + __ffs(m1);
-                m1 &= m1 - 1;
-                ++n;
-            }
-        }
+    for (int q0 = blockIdx.z * NT; q0 < total; q0 += gridDim.z * NT) {
+        const int n = min(NT, total - q0);
         const uint4* xr[NT];
 #pragma unroll
-        for (int q = 0; q < NT; ++q) xr[q] = reinterpret_cast<const uint4*>(x + (size_t)tok[q] * C);
+        for (int q = 0; q < NT; ++q) xr[q] = reinterpret_cast<const uint4*>(x + (size_t)mine[q0 + min(q, n - 1)] * C);
         float acc[NT][JR] = {};
         if (n == 1) few_dots<1>(xr, ar, C / 8, tid, acc);
         else if (n == 2) few_dots<2>(xr, ar, C / 8, tid, acc);
@@ -1036,10 +1035,7 @@ __global__ void __launch_bounds__(256) shrink_few_kernel(const uint16_t* x, cons
             float f = 0.0f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) f += part[w][q][j];
-            int t = tok[0];
-#pragma unroll
-            for (int u = 1; u < NT; ++u) t = q == u ? tok[u] : t;
-            v[(size_t)t * r + j0 + j] = to_bf(f * scale);
+            v[(size_t)mine[q0 + q] * r + j0 + j] = to_bf(f * scale);
         }
     }
 }
@@ -1059,6 +1055,7 @@ struct ShrinkArgs {
     int cols;        // columns of one adapter: r rounded up to 16 (forward) or 64 (backward)
     int per_pass;    // 256 / cols
     int splits, passes;  // CTAs per cluster; passes that run at the same time
+    int ring;        // bytes of the stages
     uint16_t* v;     // [T][r]
     DevStatus st;
 };
@@ -1066,19 +1063,19 @@ struct ShrinkArgs {
 constexpr int kShrinkRing = 192 * 1024;
 constexpr int kShrinkStages = 12;
 constexpr int kShrinkThreads = 192;
-constexpr int kShrinkSmem = 1024 + kShrinkRing + 256 + 128 * 8 + kMaxAdapters / 8;
+constexpr int kShrinkExtra = 1024 + 256 + 128 * 8 + kMaxAdapters / 8;
 
 template <bool BWD>
 __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_constant__ ShrinkArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kShrinkRing);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.ring);
     uint64_t* empty = full + kShrinkStages;
     uint64_t* tfull = empty + kShrinkStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* count = reinterpret_cast<int*>(tmem_slot + 2);
-    int* ids = reinterpret_cast<int*>(smem + kShrinkRing + 256);
+    int* ids = reinterpret_cast<int*>(smem + a.ring + 256);
     int* list = ids + 128;
     uint32_t* bits = reinterpret_cast<uint32_t*>(list + 128);
 
@@ -1127,7 +1124,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
         const int cnt = min(a.per_pass, n_list - pass * a.per_pass);
         const int* mine = list + pass * a.per_pass;
         const int stage_bytes = 16384 + cnt * a.cols * 128;
-        const int stages = min(kShrinkStages, kShrinkRing / stage_bytes);
+        const int stages = min(kShrinkStages, a.ring / stage_bytes);
         int stage = 0;
         if (warp == 0) {
             const uint64_t pol = policy_evict_normal();
@@ -1274,7 +1271,6 @@ struct GradCfg {
 template <int RB>
 __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_constant__ GradArgs a) {
     using C = GradCfg<RB>;
-    pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* landed = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
@@ -1322,6 +1318,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_cons
     const uint32_t tbase = *tmem_slot;
     const uint32_t landed_u = smem_u32(landed), full_u = smem_u32(full), empty_u = smem_u32(empty), stage_u = smem_u32(smem);
     pdl_wait();
+    pdl_launch_dependents();  // (dx's projection, which needs nothing of this kernel)
 
     int stage = 0;
     uint32_t phase = 0, accum = 0, armed = 0, armed_phase = 0;
@@ -1603,7 +1600,7 @@ ProjPlan project_plan(int T, int O, int C) {
         return p;
     }
     p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-    p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : p.cap;
+    p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : (T + 15) / 16 * 16;
     const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
     const int resident = p.cap <= 64 ? 2 : 1;
     // few tiles: clusters share a tile's contraction, four chunks of it per CTA at least
@@ -1615,7 +1612,7 @@ ProjPlan project_plan(int T, int O, int C) {
 // tokens [T][C] times W (and each token's low-rank matrix times v) into out [T][O]
 template <bool BWD>
 int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, const void* lr, const int32_t* adapter_of,
-            const void* v, void* out, int out_fp32, const DevStatus& st, cudaStream_t stream) {
+            const void* v, bool v_ready, void* out, int out_fp32, const DevStatus& st, cudaStream_t stream) {
     const uint64_t K = p->in_features, N = p->out_features, r = p->rank, n = p->n_adapters;
     ProjArgs a;
     a.T = T;
@@ -1626,6 +1623,7 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     const ProjPlan plan = project_plan(T, a.O, a.C);
     a.bn = plan.bn;
     a.splits = plan.splits;
+    a.v_ready = v_ready;
     int rc = make_tmap_3d(&a.w, w, K, N, 1, K * 2, K * N * 2, 64, BWD ? 64 : 128, 1);
     if (rc) return rc;
     if (BWD) rc = make_tmap_3d(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, 64, 1);
@@ -1654,9 +1652,9 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
            const int32_t* adapter_of, void* v, const DevStatus& st, cudaStream_t stream) {
     const int C = BWD ? p->out_features : p->in_features;
     cudaError_t e;
-    // Up to 64 tokens the adapters' rows are what is read, and no tile of 128 tokens fills.
-    if (!BWD && T <= kFewTokens) {
-        e = launch_pdl(shrink_few_kernel, dim3(std::min(T, p->n_adapters), p->rank / JR), dim3(256), 0, stream,
+    if (!BWD && T <= kFewTokens && (long)T * p->rank <= kFewProducts) {
+        e = launch_pdl(shrink_few_kernel, dim3(std::min(T, p->n_adapters), p->rank / JR, T <= 64 ? 1 : kFewShares), dim3(256),
+                       0, stream,
                        static_cast<const uint16_t*>(tokens), static_cast<const uint16_t*>(m), scaling, adapter_of, T, C,
                        (int)p->rank, (int)p->n_adapters, static_cast<uint16_t*>(v), st);
     } else {
@@ -1684,13 +1682,18 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
         while (a.splits < 8 && tiles * (a.splits + 1) <= sms && (a.splits + 1) * 4 <= kc) ++a.splits;
         const int most = (std::min(std::min(T, 128), p->n_adapters) + a.per_pass - 1) / a.per_pass;
         a.passes = std::max(1, std::min(most, sms / (tiles * a.splits)));
+        // a stage per chunk of the CTA's share at most (and room for its sums): a short one leaves
+        // the SM room for the next kernel's start
+        const int pass_cols = std::min(a.per_pass, p->n_adapters) * a.cols, share = (kc + a.splits - 1) / a.splits;
+        a.ring = std::min(kShrinkRing, std::max(share * (16384 + pass_cols * 128), (p->rank + 15) / 16 * 16 * 512));
+        a.ring = (a.ring + 1023) / 1024 * 1024;
         auto kern = shrink_kernel<BWD>;
         static std::atomic<uint64_t> configured{0};
         e = configure_once(configured, [&] {
-            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkSmem);
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkRing + kShrinkExtra);
         });
         if (e == cudaSuccess)
-            e = launch_pdl_cluster(kern, dim3(tiles * a.passes * a.splits), dim3(kShrinkThreads), kShrinkSmem, stream,
+            e = launch_pdl_cluster(kern, dim3(tiles * a.passes * a.splits), dim3(kShrinkThreads), a.ring + kShrinkExtra, stream,
                                    a.splits, a);
     }
     if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "adapter rank-product launch: %s", cudaGetErrorString(e));
@@ -1775,7 +1778,7 @@ int moe_adapter_project(const moe_adapter_t* adapter, int T, const void* x, cons
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint16_t* v = static_cast<uint16_t*>(v_out ? v_out : ws);
     if ((rc = shrink<false>(adapter, T, x, a, scaling, adapter_of, v, st, s))) return rc;
-    return project<false>(adapter, T, x, w, b, adapter_of, v, out, out_fp32, st, s);
+    return project<false>(adapter, T, x, w, b, adapter_of, v, false, out, out_fp32, st, s);
 }
 
 int moe_adapter_project_backward(const moe_adapter_t* adapter, int T, const void* dy, const void* x, const void* w,
@@ -1806,8 +1809,10 @@ int moe_adapter_project_backward(const moe_adapter_t* adapter, int T, const void
     if ((rc = api_device_status(&st))) return rc;
     void* dv = ws;
     if ((rc = shrink<true>(adapter, T, dy, b, scaling, adapter_of, dv, st, s))) return rc;
-    if (dx && (rc = project<true>(adapter, T, dy, w, a, adapter_of, dv, dx, 0, st, s))) return rc;
-    if (da) return gradients(adapter, T, dy, x, dv, v, adapter_of, da, db, st, s);
+    // the gradients first: the projection starts while they end (it waits for no predecessor
+    // before it reads dv, and each of them started after dv's kernel had ended)
+    if (da && (rc = gradients(adapter, T, dy, x, dv, v, adapter_of, da, db, st, s))) return rc;
+    if (dx) return project<true>(adapter, T, dy, w, a, adapter_of, dv, da != nullptr, dx, 0, st, s);
     return MOE_OK;
 }
 

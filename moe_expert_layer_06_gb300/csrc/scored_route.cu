@@ -415,15 +415,6 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int e0 = group * lay.gs + in_group;
     const bool grouped = a.topk_groups < a.n_groups;
     const bool stats = KIND == kKeySoftmax || (!a.sigmoid && !a.renormalize);
-    float bmax = -INFINITY;
-    if (KIND != kKeyLogit) {
-        if (warp == 0 && lane < LPT)
-            for (int i = 0; i < PER; ++i) bias[sub * ROW + i] = a.bias && i < n_mine ? a.bias[e0 + i] : 0.0f;
-        __syncthreads();
-        for (int i = 0; i < n_mine; ++i) bmax = fmaxf(bmax, bias[sub * ROW + i]);
-        bmax = token_max<LPT>(bmax);
-    }
-
     auto bias_of = [&](int e) { return a.bias ? __ldg(a.bias + e) : 0.0f; };
 
     float c[PER];  // logits, then values
@@ -479,6 +470,14 @@ __global__ void __launch_bounds__(kWarps * 32)
     int tw = (blockIdx.x * kWarps + warp) * TPW;  // the warp's first token
     int buf = 0;
     if (PER >= 4 && vec && tw < a.T) prefetch(tw, 0);
+    float bmax = -INFINITY;
+    if (KIND != kKeyLogit) {
+        if (warp == 0 && lane < LPT)
+            for (int i = 0; i < PER; ++i) bias[sub * ROW + i] = a.bias && i < n_mine ? a.bias[e0 + i] : 0.0f;
+        __syncthreads();
+        for (int i = 0; i < n_mine; ++i) bmax = fmaxf(bmax, bias[sub * ROW + i]);
+        bmax = token_max<LPT>(bmax);
+    }
     for (; tw < a.T; tw += stride) {
         const int t = tw + slot;
         if (PER >= 4 && vec) {
