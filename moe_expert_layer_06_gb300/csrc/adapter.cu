@@ -941,8 +941,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
 // x rank is small (32 tokens, rank 16: 4 against 13 us; 192 tokens, rank 32: 5 against 12).
 constexpr int kFewTokens = 256;
 constexpr int kFewProducts = 8192;  // tokens x rank
-constexpr int kFewShares = 4;       // of an adapter's tokens, from 64 tokens
-constexpr int JR = 2, NT = 4;
+constexpr int kFewShares = 4;       // of an adapter's tokens at most, one for 16 tokens of the batch
+constexpr int JR = 2, NT = 8;
 
 __device__ __forceinline__ void dot8(float& acc, const uint4& p, const uint4& q) {
     const uint32_t* x = &p.x;
@@ -1016,6 +1016,7 @@ __global__ void __launch_bounds__(256) shrink_few_kernel(const uint16_t* x, cons
         float acc[NT][JR] = {};
         if (n == 1) few_dots<1>(xr, ar, C / 8, tid, acc);
         else if (n == 2) few_dots<2>(xr, ar, C / 8, tid, acc);
+        else if (n <= 4) few_dots<4>(xr, ar, C / 8, tid, acc);
         else few_dots<NT>(xr, ar, C / 8, tid, acc);
         __syncthreads();  // part is free
 #pragma unroll
@@ -1564,6 +1565,52 @@ cudaError_t launch_project_pair(const ProjArgs& a, int grid, cudaStream_t stream
     return launch_project(project_pair_kernel<BWD>, configured, kPairSmem, grid, 2, stream, a);
 }
 
+// Clusters of `size` CTAs that are resident at a time, where a CTA fills an SM (or `two` fit
+// one): processors come in groups that a cluster does not cross (15 clusters of 8 and 36 of 4
+// of 152 SMs).  Asked once per device.
+int active_clusters(int size, bool two) {
+    if (size == 1) return num_sms() * (two ? 2 : 1);
+    static std::atomic<int> known[64][2][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / (2 * size);
+    int n = known[dev][two][size].load(std::memory_order_relaxed);
+    if (n) return n;
+    auto kern = two ? project_kernel<false, 32> : project_kernel<false, 256>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = two ? ProjCfg<32>::kSmemBytes : ProjCfg<256>::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = std::max(1, num_sms() / (2 * size));
+    }
+    known[dev][two][size].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs per cluster, up to `most`, that share `chunks` of contraction of each of `tiles`: the
+// least of rounds x (a CTA's chunks + 8 for its start and end), at least four chunks each.
+int split_of(long tiles, int chunks, int most, bool two) {
+    int at = 1;
+    long best = -1;
+    for (int s = 1; s <= most && (s == 1 || s * 4 <= chunks); ++s) {
+        const long slots = active_clusters(s, two);
+        const long cost = (tiles + slots - 1) / slots * ((chunks + s - 1) / s + 8 + (s > 1 ? 1 : 0));
+        if (best < 0 || cost < best) {
+            best = cost;
+            at = s;
+        }
+    }
+    return at;
+}
+
 // How a projection of T tokens to O features is cut: token capacity and tokens per tile,
 // CTAs that share a tile's contraction, or pairs of CTAs; grid.
 struct ProjPlan {
@@ -1602,9 +1649,7 @@ ProjPlan project_plan(int T, int O, int C) {
     p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
     p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : (T + 15) / 16 * 16;
     const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
-    const int resident = p.cap <= 64 ? 2 : 1;
-    // few tiles: clusters share a tile's contraction, four chunks of it per CTA at least
-    while (p.splits < 8 && tiles * (p.splits + 1) <= (long)sms * resident && (p.splits + 1) * 4 <= kc) ++p.splits;
+    p.splits = tiles < 2 * sms ? split_of(tiles, kc, 8, p.cap <= 64) : 1;
     p.grid = p.splits > 1 ? (int)tiles * p.splits : (int)std::min<long>(tiles, sms);
     return p;
 }
@@ -1653,7 +1698,7 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
     const int C = BWD ? p->out_features : p->in_features;
     cudaError_t e;
     if (!BWD && T <= kFewTokens && (long)T * p->rank <= kFewProducts) {
-        e = launch_pdl(shrink_few_kernel, dim3(std::min(T, p->n_adapters), p->rank / JR, T <= 64 ? 1 : kFewShares), dim3(256),
+        e = launch_pdl(shrink_few_kernel, dim3(std::min(T, p->n_adapters), p->rank / JR, std::min((T + 15) / 16, kFewShares)), dim3(256),
                        0, stream,
                        static_cast<const uint16_t*>(tokens), static_cast<const uint16_t*>(m), scaling, adapter_of, T, C,
                        (int)p->rank, (int)p->n_adapters, static_cast<uint16_t*>(v), st);
@@ -1675,11 +1720,9 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
         a.n_adapters = p->n_adapters;
         a.v = static_cast<uint16_t*>(v);
         a.st = st;
-        // clusters share the contraction (four chunks per CTA at least) and a tile's passes run
-        // side by side as far as there are SMs
+        // clusters share the contraction, and a tile's passes run side by side as far as there are SMs
         const int sms = num_sms(), tiles = (T + 127) / 128, kc = (C + 63) / 64;
-        a.splits = 1;
-        while (a.splits < 8 && tiles * (a.splits + 1) <= sms && (a.splits + 1) * 4 <= kc) ++a.splits;
+        a.splits = split_of(tiles, kc, 8, false);
         const int most = (std::min(std::min(T, 128), p->n_adapters) + a.per_pass - 1) / a.per_pass;
         a.passes = std::max(1, std::min(most, sms / (tiles * a.splits)));
         // a stage per chunk of the CTA's share at most (and room for its sums): a short one leaves
@@ -1733,8 +1776,7 @@ int gradients(const moe_adapter_t* p, int T, const void* dy, const void* x, cons
     const int rb = (p->rank + 63) / 64;
     // few adapters: clusters split the tokens (the shares of ranks above 128 do not fit shared memory)
     const int ctas = ((a.F[0] + 255) / 256 + (a.F[1] + 255) / 256) * p->n_adapters;
-    a.splits = 1;
-    while (a.splits < 4 && rb <= 2 && ctas * (a.splits + 1) <= num_sms() && (T + 63) / 64 >= 4 * (a.splits + 1)) ++a.splits;
+    a.splits = rb <= 2 ? split_of(ctas, (T + 63) / 64 / p->n_adapters, 4, false) : 1;
     const cudaError_t e = rb == 1   ? launch_grad_rb<1>(a, p->n_adapters, stream)
                           : rb == 2 ? launch_grad_rb<2>(a, p->n_adapters, stream)
                                     : launch_grad_rb<4>(a, p->n_adapters, stream);
