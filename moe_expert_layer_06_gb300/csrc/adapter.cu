@@ -30,11 +30,7 @@ __device__ __forceinline__ float bf(uint16_t u) { return __uint_as_float((uint32
 
 __device__ __forceinline__ uint16_t to_bf(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-// Two bf16 in a word: is either an infinity or NaN; the word with such elements zero.
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
+// Two bf16 in a word, infinities and NaN among them set to zero.
 __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
     if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
     if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
@@ -266,21 +262,24 @@ struct VRows {
 // elements leave its tile here (true: there were some) and are added to their own tokens
 // in the epilogue.
 __device__ __forceinline__ bool take_odd(uint8_t* st_a, int tid) {
-    bool hit = false;
+    uint4* at = reinterpret_cast<uint4*>(st_a) + tid;
+    uint32_t most = 0;  // largest magnitudes, as pairs of 16-bit numbers
 #pragma unroll
     for (int q = 0; q < kABytes / 16 / 128; ++q) {
-        uint4* at = reinterpret_cast<uint4*>(st_a) + q * 128 + tid;
-        uint4 val = *at;
-        if (not_finite(val.x) | not_finite(val.y) | not_finite(val.z) | not_finite(val.w)) {
-            val.x = finite_part(val.x);
-            val.y = finite_part(val.y);
-            val.z = finite_part(val.z);
-            val.w = finite_part(val.w);
-            *at = val;
-            hit = true;
-        }
+        const uint4 val = at[q * 128];
+        most = __vmaxu2(__vmaxu2(most, val.x & 0x7fff7fffu), val.y & 0x7fff7fffu);
+        most = __vmaxu2(__vmaxu2(most, val.z & 0x7fff7fffu), val.w & 0x7fff7fffu);
     }
-    return hit;
+    if ((most & 0xffffu) < 0x7f80u && (most >> 16) < 0x7f80u) return false;
+    for (int q = 0; q < kABytes / 16 / 128; ++q) {
+        uint4 val = at[q * 128];
+        val.x = finite_part(val.x);
+        val.y = finite_part(val.y);
+        val.z = finite_part(val.z);
+        val.w = finite_part(val.w);
+        at[q * 128] = val;
+    }
+    return true;
 }
 
 __device__ __forceinline__ bool has_odd(const TileList& tl, int n_ext) {
@@ -971,7 +970,7 @@ __device__ __forceinline__ void few_dots(const uint4* const (&xr)[NT], const uin
     }
 }
 
-__global__ void __launch_bounds__(256) shrink_few_kernel(const uint16_t* x, const uint16_t* m, const float* scaling,
+__global__ void __launch_bounds__(256, 3) shrink_few_kernel(const uint16_t* x, const uint16_t* m, const float* scaling,
                                                          const int32_t* adapter_of, int T, int C, int r, int n_adapters,
                                                          uint16_t* v, DevStatus st) {
     pdl_wait();
@@ -1633,7 +1632,7 @@ int tile_height(int T, int units, int slots, int by) {
     return at;
 }
 
-ProjPlan project_plan(int T, int O, int C) {
+ProjPlan project_plan(int T, int O, int C, int r, int n_adapters) {
     ProjPlan p;
     const int sms = num_sms(), m_tiles = (O + 127) / 128, kc = (C + 63) / 64;
     p.splits = 1;
@@ -1649,7 +1648,9 @@ ProjPlan project_plan(int T, int O, int C) {
     p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
     p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : (T + 15) / 16 * 16;
     const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
-    p.splits = tiles < 2 * sms ? split_of(tiles, kc, 8, p.cap <= 64) : 1;
+    // (a small batch may hold as many adapters as tokens, and each adds a chunk per 64 of its rank)
+    const int extra = (T <= 256 ? std::min(T, n_adapters) : 2) * ((r + 63) / 64);
+    p.splits = tiles < 2 * sms ? split_of(tiles, kc + extra, 8, p.cap <= 64) : 1;
     p.grid = p.splits > 1 ? (int)tiles * p.splits : (int)std::min<long>(tiles, sms);
     return p;
 }
@@ -1665,7 +1666,7 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     a.C = BWD ? p->out_features : p->in_features;
     a.r = p->rank;
     a.n_adapters = p->n_adapters;
-    const ProjPlan plan = project_plan(T, a.O, a.C);
+    const ProjPlan plan = project_plan(T, a.O, a.C, a.r, a.n_adapters);
     a.bn = plan.bn;
     a.splits = plan.splits;
     a.v_ready = v_ready;
