@@ -215,6 +215,25 @@ struct ProjArgs {
     DevStatus st;
 };
 
+// How adapters fill the 64-wide chunks: small ranks share one, `per` adapters of `seg`
+// columns each (a rank up to 16 four, up to 32 two), larger ones take several.
+struct Packing {
+    int r, per, seg;
+    __device__ __forceinline__ explicit Packing(int rank)
+        : r(rank), per(rank <= 16 ? 4 : rank <= 32 ? 2 : 1), seg(64 / per) {}
+    __device__ __forceinline__ int chunks(int count) const {
+        return per > 1 ? (count + per - 1) / per : count * ((r + 63) / 64);
+    }
+    // adapters of chunk e: list[first .. first + n)
+    __device__ __forceinline__ int first(int e, int count) const { return per > 1 ? e * per : e % count; }
+    __device__ __forceinline__ int n(int e, int count) const { return per > 1 ? min(per, count - e * per) : 1; }
+    __device__ __forceinline__ int j0(int e, int count) const { return per > 1 ? 0 : e / count * 64; }
+    // 16-wide steps of chunk e, of which step q is used if it lies in an adapter's rank
+    __device__ __forceinline__ bool step(int q, int e, int count) const {
+        return per > 1 ? q * 16 / seg < n(e, count) && q * 16 % seg < r : j0(e, count) + q * 16 < r;
+    }
+};
+
 // What a tile's workers know of its adapters.
 struct TileList {
     int count;
@@ -228,11 +247,21 @@ struct TileList {
 template <int RPT>
 struct VRows {
     int id[RPT];
+    int pos[RPT];  // of its adapter in the list
     uint4 v[RPT][8];
 
-    __device__ __forceinline__ void ids(const int* of, int n, int tid) {
+    __device__ __forceinline__ void ids(const int* of, int n, const int* list, int count, int tid) {
 #pragma unroll
-        for (int q = 0; q < RPT; ++q) id[q] = tid + q * 128 < n ? of[tid + q * 128] : -1;
+        for (int q = 0; q < RPT; ++q) {
+            id[q] = tid + q * 128 < n ? of[tid + q * 128] : -1;
+            int lo = 0, hi = count - 1;  // the list ascends
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (list[mid] < id[q]) lo = mid + 1;
+                else hi = mid;
+            }
+            pos[q] = id[q] >= 0 ? lo : -1;
+        }
     }
     __device__ __forceinline__ void load(const ProjArgs& a, int row0, int j0, int tid) {
 #pragma unroll
@@ -244,19 +273,61 @@ struct VRows {
                     v[q][g] = *reinterpret_cast<const uint4*>(a.v + (size_t)(row0 + tid + q * 128) * a.r + j0 + g * 8);
             }
     }
-    // sb: the rows of adapter `of`, zeros elsewhere (n rows, swizzled as TMA would)
-    __device__ __forceinline__ void store(uint8_t* sb, int n, int of, int tid) const {
+    // sb: the rows of the PER adapters from `first` of the list, each in its own columns,
+    // zeros elsewhere (n rows, swizzled as TMA would)
+    template <int PER>
+    __device__ __forceinline__ void store_per(uint8_t* sb, int n, int first, int tid) const {
 #pragma unroll
         for (int q = 0; q < RPT; ++q) {
             const int row = tid + q * 128;
             if (row >= n) continue;
+            const int p = pos[q] < 0 ? -1 : pos[q] - first;
 #pragma unroll
             for (int g = 0; g < 8; ++g)
                 *reinterpret_cast<uint4*>(sb + row * 128 + ((g ^ (row & 7)) << 4)) =
-                    id[q] == of ? v[q][g] : make_uint4(0, 0, 0, 0);
+                    p == g / (8 / PER) ? v[q][g % (8 / PER)] : make_uint4(0, 0, 0, 0);
         }
     }
+    __device__ __forceinline__ void store(uint8_t* sb, int n, int first, int per, int tid) const {
+        if (per == 4) store_per<4>(sb, n, first, tid);
+        else if (per == 2) store_per<2>(sb, n, first, tid);
+        else store_per<1>(sb, n, first, tid);
+    }
 };
+
+// The copies of adapter chunk e: rows of B_i (features, then rank) or A_i (rank, then
+// features) of each of its adapters.
+template <bool BWD>
+__device__ __forceinline__ void load_adapters(const ProjArgs& a, const Packing& pk, const TileList& tl, int e, uint32_t sa,
+                                              uint32_t bar, int m0, uint64_t pol) {
+    const int first = pk.first(e, tl.count), n = pk.n(e, tl.count), j0 = pk.j0(e, tl.count);
+    mbar_arrive_expect_tx(bar, n * pk.seg * 256);
+    for (int p = 0; p < n; ++p) {
+        const int id = tl.list[first + p];
+        if (BWD) {
+            tma_load_3d(sa + p * pk.seg * 128, &a.lr, bar, m0, j0, id, pol);
+            tma_load_3d(sa + kABytes / 2 + p * pk.seg * 128, &a.lr, bar, m0 + 64, j0, id, pol);
+        } else {
+            tma_load_3d(sa + p * pk.seg * 256, &a.lr, bar, j0, m0, id, pol);
+        }
+    }
+}
+
+// The A operand of adapter chunks (forward): each adapter's 128 rows of `seg` columns, swizzled
+// over their own width (layout codes 2, 4, 6: 128, 64, 32 bytes).
+__device__ __forceinline__ uint64_t adapter_desc(uint32_t smem_addr, const Packing& pk) {
+    uint64_t d = (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;
+    d |= (uint64_t)(pk.seg * 16 >> 4) << 32;  // 8 rows
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)(pk.per == 1 ? 2u : pk.per == 2 ? 4u : 6u) << 61;
+    return d;
+}
+
+// Offset of step q in it, in 16 bytes.
+__device__ __forceinline__ int adapter_step(int q, const Packing& pk) {
+    return pk.per == 4 ? q * 256 : pk.per == 2 ? (q >> 1) * 512 + (q & 1) * 2 : q * 2;
+}
 
 // Zero times an infinity or NaN of an adapter would reach the other adapters' tokens: such
 // elements leave its tile here (true: there were some) and are added to their own tokens
@@ -294,12 +365,14 @@ template <bool BWD>
 __device__ __noinline__ void add_odd(const ProjArgs& a, const TileList& tl, int n_ext, int t0, int at, int feat,
                                      float (&y)[16]) {
     pdl_wait();  // v
+    const Packing pk(a.r);
     for (int w = 0; w * 32 < n_ext; ++w) {
         for (uint32_t b = tl.odd[w]; b; b &= b - 1) {
             const int e = w * 32 + __ffs(b) - 1;
-            const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
+            const int first = pk.first(e, tl.count), last = first + pk.n(e, tl.count) - 1, j0 = pk.j0(e, tl.count);
             for (int j = 0; j < 16; ++j) {
-                if (tl.ids[at + j] != id) continue;
+                const int id = tl.ids[at + j];
+                if (id < tl.list[first] || id > tl.list[last]) continue;  // (the list ascends)
                 for (int l = j0; l < min(a.r, j0 + 64); ++l) {
                     const size_t el = BWD ? ((size_t)id * a.r + l) * a.O + feat : ((size_t)id * a.O + feat) * a.r + l;
                     const float u = bf(a.lr_ptr[el]);
@@ -383,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     const int m_tiles = (a.O + 127) / 128;
     const int n_tiles = m_tiles * ((a.T + a.bn - 1) / a.bn);
     const int first = blockIdx.x / S, step = gridDim.x / S;
-    const int kc = (a.C + 63) / 64, rc = (a.r + 63) / 64;
+    const int kc = (a.C + 63) / 64;
+    const Packing pk(a.r);
     const int c0 = (int)((long)kc * rank / S), c1 = (int)((long)kc * (rank + 1) / S);
 
     if (warp == 0 && lane == 0) {
@@ -457,19 +531,11 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             }
             if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
             const TileList& tl = lists[n & 1];
-            for (int e = rank; e < tl.count * rc; e += S) {
+            const int n_ext = pk.chunks(tl.count);
+            for (int e = rank; e < n_ext; e += S) {
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
-                if (elect_one()) {
-                    const uint32_t sa = stage_u + stage * C::kStageBytes, lb = landed_u + stage * 8;
-                    const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
-                    mbar_arrive_expect_tx(lb, kABytes);
-                    if (BWD) {
-                        tma_load_3d(sa, &a.lr, lb, m0, j0, id, pol);
-                        tma_load_3d(sa + kABytes / 2, &a.lr, lb, m0 + 64, j0, id, pol);
-                    } else {
-                        tma_load_3d(sa, &a.lr, lb, j0, m0, id, pol);
-                    }
-                }
+                if (elect_one())
+                    load_adapters<BWD>(a, pk, tl, e, stage_u + stage * C::kStageBytes, landed_u + stage * 8, m0, pol);
                 __syncwarp();
                 advance(true);
             }
@@ -491,17 +557,26 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             if (!(ok = warp_wait(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, limit))) break;
             tc_fence_after();
             uint32_t accum = 0;
-            auto chunk = [&](int left) {
+            // 64 of the contraction (`left` of them), or adapter chunk e >= 0
+            auto chunk = [&](int left, int e, int count) {
                 if (!(ok = warp_wait(full_u + stage * 8, phase, abort_flag, limit))) return;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t ad = ad0 + stage * (C::kStageBytes >> 4), bd = bd0 + stage * (C::kStageBytes >> 4);
                     // 16 of the contraction per instruction: 32 bytes along K, or 16 K rows
                     constexpr int kAStep = BWD ? 128 : 2;
-                    umma_bf16(d, ad, bd, idesc, accum);
-                    if (left > 16) umma_bf16(d, ad + kAStep, bd + 2, idesc, 1);
-                    if (left > 32) umma_bf16(d, ad + 2 * kAStep, bd + 4, idesc, 1);
-                    if (left > 48) umma_bf16(d, ad + 3 * kAStep, bd + 6, idesc, 1);
+                    if (e < 0) {
+                        umma_bf16(d, ad, bd, idesc, accum);
+                        if (left > 16) umma_bf16(d, ad + kAStep, bd + 2, idesc, 1);
+                        if (left > 32) umma_bf16(d, ad + 2 * kAStep, bd + 4, idesc, 1);
+                        if (left > 48) umma_bf16(d, ad + 3 * kAStep, bd + 6, idesc, 1);
+                    } else {
+                        const uint64_t ed = BWD ? ad : adapter_desc(stage_u, pk) + stage * (C::kStageBytes >> 4);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (pk.step(q, e, count))
+                                umma_bf16(d, ed + (BWD ? kAStep * q : adapter_step(q, pk)), bd + 2 * q, idesc, accum || q > 0);
+                    }
                     umma_commit(empty_u + stage * 8);
                 }
                 __syncwarp();
@@ -511,10 +586,10 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                     phase ^= 1;
                 }
             };
-            for (int c = c0; c < c1 && ok; ++c) chunk(a.C - c * 64);
+            for (int c = c0; c < c1 && ok; ++c) chunk(a.C - c * 64, -1, 0);
             if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
-            const int n_ext = lists[n & 1].count * rc;
-            for (int e = rank; e < n_ext && ok; e += S) chunk(a.r - e / lists[n & 1].count * 64);
+            const int count = lists[n & 1].count, n_ext = pk.chunks(count);
+            for (int e = rank; e < n_ext && ok; e += S) chunk(0, e, count);
             if (elect_one()) umma_commit(smem_u32(&tfull[n & 1]));
             __syncwarp();
         }
@@ -540,13 +615,13 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st, tid, 128, 1);
             if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
             stage = (stage + c1 - c0) % stages;
-            const int n_ext = tl.count * rc;
+            const int n_ext = pk.chunks(tl.count);
             if (rank < n_ext && !a.v_ready) pdl_wait();
             VRows<BN == 256 ? 2 : 1> vr;
-            vr.ids(tl.ids, a.bn, tid);
+            vr.ids(tl.ids, a.bn, tl.list, tl.count, tid);
             int held = -1;
             for (int e = rank; e < n_ext; e += S) {
-                const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
+                const int first_of = pk.first(e, tl.count), j0 = pk.j0(e, tl.count);
                 if (j0 != held) vr.load(a, row0, held = j0, tid);
                 // the adapter tile has landed: the stage is free of its last use, too
                 if (*abort_flag || !mbar_wait(smem_u32(&landed[stage]), (land_phase >> stage) & 1u, limit)) {
@@ -556,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 land_phase ^= 1u << stage;
                 uint8_t* st_a = smem + stage * C::kStageBytes;
                 uint8_t* sb = st_a + kABytes;
-                vr.store(sb, a.bn, id, tid);
+                vr.store(sb, a.bn, first_of, pk.per, tid);
                 if (take_odd(st_a, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
@@ -579,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             tc_fence_after();
             // (the MMA warp read the list before its last commit)
             const int feat = m0 + q * 32 + lane;
-            const int n_ext = tl.count * rc;
+            const int n_ext = pk.chunks(tl.count);
             const uint32_t tmem = tbase + (n & 1) * BN + ((uint32_t)(q * 32) << 16);
             const bool any_odd = has_odd(tl, n_ext);
             for (int g = 0; g * 16 < rows; ++g) {
@@ -686,7 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
     const int m_tiles = (a.O + 255) / 256;
     const int n_tiles = m_tiles * ((a.T + a.bn - 1) / a.bn);
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
-    const int kc = (a.C + 63) / 64, rc = (a.r + 63) / 64;
+    const int kc = (a.C + 63) / 64;
+    const Packing pk(a.r);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kPairStages; ++s) {
@@ -759,19 +835,11 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             }
             if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
             const TileList& tl = lists[n & 1];
-            for (int e = 0; e < tl.count * rc; ++e) {
+            const int n_ext = pk.chunks(tl.count);
+            for (int e = 0; e < n_ext; ++e) {
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
-                if (elect_one()) {
-                    const uint32_t sa = stage_u + stage * kPairStageBytes, lb = landed_u + stage * 8;
-                    const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
-                    mbar_arrive_expect_tx(lb, kABytes);
-                    if (BWD) {
-                        tma_load_3d(sa, &a.lr, lb, m0, j0, id, pol);
-                        tma_load_3d(sa + kABytes / 2, &a.lr, lb, m0 + 64, j0, id, pol);
-                    } else {
-                        tma_load_3d(sa, &a.lr, lb, j0, m0, id, pol);
-                    }
-                }
+                if (elect_one())
+                    load_adapters<BWD>(a, pk, tl, e, stage_u + stage * kPairStageBytes, landed_u + stage * 8, m0, pol);
                 __syncwarp();
                 advance(true);
             }
@@ -812,9 +880,9 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 if (!(ok = wait_cluster(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
                 uint32_t accum = 0;
-                auto chunk = [&](int left, bool ext) {
+                auto chunk = [&](int left, int e, int count) {
                     if (!(ok = wait_cluster(full_u + stage * 8, phase))) return;
-                    if (ext) {
+                    if (e >= 0) {
                         if (!(ok = wait_cluster(smem_u32(&other[stage]), (other_phase >> stage) & 1u))) return;
                         other_phase ^= 1u << stage;
                     }
@@ -822,10 +890,19 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                     if (elect_one()) {
                         const uint64_t ad = ad0 + stage * (kPairStageBytes >> 4), bd = bd0 + stage * (kPairStageBytes >> 4);
                         constexpr int kAStep = BWD ? 128 : 2;
-                        umma_bf16_pair(d, ad, bd, idesc, accum);
-                        if (left > 16) umma_bf16_pair(d, ad + kAStep, bd + 2, idesc, 1);
-                        if (left > 32) umma_bf16_pair(d, ad + 2 * kAStep, bd + 4, idesc, 1);
-                        if (left > 48) umma_bf16_pair(d, ad + 3 * kAStep, bd + 6, idesc, 1);
+                        if (e < 0) {
+                            umma_bf16_pair(d, ad, bd, idesc, accum);
+                            if (left > 16) umma_bf16_pair(d, ad + kAStep, bd + 2, idesc, 1);
+                            if (left > 32) umma_bf16_pair(d, ad + 2 * kAStep, bd + 4, idesc, 1);
+                            if (left > 48) umma_bf16_pair(d, ad + 3 * kAStep, bd + 6, idesc, 1);
+                        } else {
+                            const uint64_t ed = BWD ? ad : adapter_desc(stage_u, pk) + stage * (kPairStageBytes >> 4);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (pk.step(q, e, count))
+                                    umma_bf16_pair(d, ed + (BWD ? kAStep * q : adapter_step(q, pk)), bd + 2 * q, idesc,
+                                                   accum || q > 0);
+                        }
                         umma_commit_pair(empty_u + stage * 8);
                     }
                     __syncwarp();
@@ -835,10 +912,10 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                         phase ^= 1;
                     }
                 };
-                for (int c = 0; c < kc && ok; ++c) chunk(a.C - c * 64, false);
+                for (int c = 0; c < kc && ok; ++c) chunk(a.C - c * 64, -1, 0);
                 if (!ok || !(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
-                const int n_ext = lists[n & 1].count * rc;
-                for (int e = 0; e < n_ext && ok; ++e) chunk(a.r - e / lists[n & 1].count * 64, true);
+                const int count = lists[n & 1].count, n_ext = pk.chunks(count);
+                for (int e = 0; e < n_ext && ok; ++e) chunk(0, e, count);
                 if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]));
                 __syncwarp();
             }
@@ -864,13 +941,13 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st, tid, 128, 1);
             if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
             stage = (stage + kc) % kPairStages;
-            const int n_ext = tl.count * rc;
+            const int n_ext = pk.chunks(tl.count);
             if (n_ext && !a.v_ready) pdl_wait();
             VRows<1> vr;
-            vr.ids(tl.ids + rank * half, half, tid);
+            vr.ids(tl.ids + rank * half, half, tl.list, tl.count, tid);
             int held = -1;
             for (int e = 0; e < n_ext; ++e) {
-                const int id = tl.list[e % tl.count], j0 = e / tl.count * 64;
+                const int first_of = pk.first(e, tl.count), j0 = pk.j0(e, tl.count);
                 if (j0 != held) vr.load(a, row0 + rank * half, held = j0, tid);
                 if (*abort_flag || !mbar_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, limit)) {
                     ok = false;
@@ -878,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 }
                 land_phase ^= 1u << stage;
                 uint8_t* st_a = smem + stage * kPairStageBytes;
-                vr.store(st_a + kABytes, half, id, tid);
+                vr.store(st_a + kABytes, half, first_of, pk.per, tid);
                 if (take_odd(st_a, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
@@ -902,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 break;
             tc_fence_after();
             const int feat = m0 + q * 32 + lane;
-            const int n_ext = tl.count * rc;
+            const int n_ext = pk.chunks(tl.count);
             const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
             const bool any_odd = has_odd(tl, n_ext);
             for (int g = 0; g * 16 < rows; ++g) {
@@ -938,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
 // read, so many small CTAs keep them coming.  It ends sooner than the tensor-core kernel,
 // whose 128-token tiles multiply every token with every adapter of the tile, while tokens
 // x rank is small (32 tokens, rank 16: 4 against 13 us; 192 tokens, rank 32: 5 against 12).
-constexpr int kFewTokens = 256;
+constexpr int kFewTokens = 64;
 constexpr int kFewProducts = 8192;  // tokens x rank
 constexpr int kFewShares = 4;       // of an adapter's tokens at most, one for 16 tokens of the batch
 constexpr int JR = 2, NT = 8;
@@ -1649,7 +1726,8 @@ ProjPlan project_plan(int T, int O, int C, int r, int n_adapters) {
     p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : (T + 15) / 16 * 16;
     const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
     // (a small batch may hold as many adapters as tokens, and each adds a chunk per 64 of its rank)
-    const int extra = (T <= 256 ? std::min(T, n_adapters) : 2) * ((r + 63) / 64);
+    const int held = T <= 256 ? std::min(T, n_adapters) : 2;
+    const int extra = r <= 16 ? (held + 3) / 4 : r <= 32 ? (held + 1) / 2 : held * ((r + 63) / 64);
     p.splits = tiles < 2 * sms ? split_of(tiles, kc + extra, 8, p.cap <= 64) : 1;
     p.grid = p.splits > 1 ? (int)tiles * p.splits : (int)std::min<long>(tiles, sms);
     return p;
@@ -1672,8 +1750,9 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     a.v_ready = v_ready;
     int rc = make_tmap_3d(&a.w, w, K, N, 1, K * 2, K * N * 2, 64, BWD ? 64 : 128, 1);
     if (rc) return rc;
-    if (BWD) rc = make_tmap_3d(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, 64, 1);
-    else rc = make_tmap_3d(&a.lr, lr, r, N, n, r * 2, r * N * 2, 64, 128, 1);
+    const uint32_t seg = a.r <= 16 ? 16 : a.r <= 32 ? 32 : 64;  // (as Packing)
+    if (BWD) rc = make_tmap_3d(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, seg, 1);
+    else rc = make_tmap_3d(&a.lr, lr, r, N, n, r * 2, r * N * 2, seg, 128, 1, false, seg * 2);
     if (rc) return rc;
     const uint64_t C = a.C;
     if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.pair ? plan.bn / 2 : plan.bn))) return rc;

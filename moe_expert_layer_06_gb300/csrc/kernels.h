@@ -174,10 +174,11 @@ cudaError_t launch_gemm(GemmMode mode, int bn, const GemmArgs& args, int grid, c
 int gemm_max_slots();  // slots the GEMM's shared-memory item table holds
 
 // ---------------------------------------------------------------- TMA tensor maps
-// 3-D bf16 tensor map, dims innermost first (elements), strides of dims 1,2 in bytes.
+// 3-D bf16 tensor map, dims innermost first (elements), strides of dims 1,2 in bytes; the
+// swizzle (128, 64 or 32 bytes) is the box's inner extent at least.
 int make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                  uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
-                 uint32_t box2, bool fp8 = false);
+                 uint32_t box2, bool fp8 = false, int swizzle_bytes = 128);
 
 // ---------------------------------------------------------------- FP8 (E4M3) quantisation
 // codes[r][c] = e4m3(x[r][c] / scale[r]), scale[r] = amax(|x[r]|) / 448 (1 for a zero row),
