@@ -1130,7 +1130,7 @@ struct ShrinkArgs {
     const int32_t* adapter_of;
     int T, C, r, n_adapters;
     int cols;        // columns of one adapter: r rounded up to 16 (forward) or 64 (backward)
-    int per_pass;    // 256 / cols
+    int per_pass;    // adapters of a pass: 256 / cols at most
     int splits, passes;  // CTAs per cluster; passes that run at the same time
     int ring;        // bytes of the stages
     uint16_t* v;     // [T][r]
@@ -1800,11 +1800,14 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
         a.n_adapters = p->n_adapters;
         a.v = static_cast<uint16_t*>(v);
         a.st = st;
-        // clusters share the contraction, and a tile's passes run side by side as far as there are SMs
-        const int sms = num_sms(), tiles = (T + 127) / 128, kc = (C + 63) / 64;
+        // clusters share the contraction
+        const int tiles = (T + 127) / 128, kc = (C + 63) / 64;
         a.splits = split_of(tiles, kc, 8, false);
-        const int most = (std::min(std::min(T, 128), p->n_adapters) + a.per_pass - 1) / a.per_pass;
-        a.passes = std::max(1, std::min(most, sms / (tiles * a.splits)));
+        // A tile's adapters in as many passes side by side as clusters are resident, so narrower
+        // ones than 256 columns where there are few tiles.
+        const int most = std::min(std::min(T, 128), p->n_adapters), beside = std::max(1, active_clusters(a.splits, false) / tiles);
+        a.per_pass = std::min(a.per_pass, (most + beside - 1) / beside);
+        a.passes = std::min((most + a.per_pass - 1) / a.per_pass, beside);
         // a stage per chunk of the CTA's share at most (and room for its sums): a short one leaves
         // the SM room for the next kernel's start
         const int pass_cols = std::min(a.per_pass, p->n_adapters) * a.cols, share = (kc + a.splits - 1) / a.splits;
