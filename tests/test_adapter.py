@@ -151,6 +151,33 @@ def test_more_tiles_than_processors_and_many_adapters_per_tile(T, K, N, r, n):
 
 
 @pytest.mark.gpu
+def test_very_long_batches():
+    """More 64-token chunks than the gradient kernel lists at a time (262144 tokens)."""
+    c = Case(270001, 16, 24, 8, 3, "runs")
+    y, v = c.forward()
+    dx, da, db = c.backward(v)
+    assert m.moe_check_status() == 0
+    ref = c.reference()
+    for name, got in (("y", y), ("dx", dx), ("da", da), ("db", db)):
+        close(got, *ref[name], name=name)
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """An output of more than 2^31 elements: its last rows are those of the last tokens alone."""
+    T, K, N, r, n, tail = 270000, 8, 8200, 8, 2, 100
+    c = Case(tail, K, N, r, n, "each")
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    of = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    x[-tail:], of[-tail:] = c.x.cuda(), c.of.cuda()
+    out = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    m.moe_adapter_project(c.p, T, x, c.w.cuda(), c.a.cuda(), c.b.cuda(), c.s.cuda(), of, out, None, scratch(c.p, T))
+    assert m.moe_check_status() == 0
+    close(out[-tail:], *c.reference()["y"])
+    assert not bool(out[:-tail].any())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_no_adapters_no_scaling_and_fp32_output(T):
     c = Case(T, 264, 392, 16, 4, "none", scaled=False)

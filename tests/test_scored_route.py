@@ -277,6 +277,44 @@ def test_from_hidden_states(tokens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [2431, 2432, 5003])
+@pytest.mark.parametrize("E,k,r", ROUTERS)
+def test_large_batches_match_small_ones(E, k, r, T):
+    """Row by row the same whatever the batch (which chooses how many tokens a warp takes)."""
+    g = torch.Generator().manual_seed(T + E)
+    l = torch.randn(T, E, generator=g) * 1.7
+    l[torch.rand(T, E, generator=g) < 0.02] = -INF
+    l[::7] = torch.randint(-1, 2, (len(l[::7]), E), generator=g).float()  # ties
+    l = l.cuda()
+    bias = (torch.randn(E, generator=g) * 0.05).cuda()
+    for b in (bias, None):
+        idx, w = call(l, b, r, k)
+        for a in range(0, T, 600):
+            i2, w2 = call(l[a:a + 600].contiguous(), b, r, k)
+            assert torch.equal(idx[a:a + 600], i2)
+            # a softmax's sum may be added in another order: log2(E) roundings
+            assert bool(((w[a:a + 600] - w2).abs() <= 40 * 2.0 ** -24 * w2).all())
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    T, E, k = 2_200_000, 1024, 8
+    r = m.Router(m.MOE_SCORE_SOFTMAX, 1, 1, m.MOE_GROUP_MAX, 0, 1.0)
+    l = torch.zeros(T, E, device="cuda")
+    l[-50:] = torch.randn(50, E, generator=torch.Generator().manual_seed(1)).cuda()
+    idx, w = call(l, None, r, k)
+    i2, w2 = call(l[-50:].contiguous(), None, r, k)
+    assert torch.equal(idx[-50:], i2) and bool(((w[-50:] - w2).abs() <= 40 * 2.0 ** -24 * w2).all())
+    assert bool((idx[:-50] == torch.arange(k, device="cuda")).all())
+    d = torch.full((T, E), float("nan"), device="cuda")
+    dw = torch.ones(T, k, device="cuda")
+    m.moe_route_scored_backward(shape_of(E, k), r, T, l, idx, dw, d)
+    d2 = torch.empty(50, E, device="cuda")
+    m.moe_route_scored_backward(shape_of(E, k), r, 50, l[-50:].contiguous(), i2, dw[:50], d2)
+    assert torch.equal(d[-50:], d2) and bool(torch.isfinite(d).all())
+
+
+@pytest.mark.gpu
 def test_out_of_range_ids_in_the_backward_pass_set_the_status():
     r = m.Router(m.MOE_SCORE_SIGMOID, 1, 1, m.MOE_GROUP_MAX, 1, 1.0)
     l = torch.zeros(3, 16, device="cuda")
