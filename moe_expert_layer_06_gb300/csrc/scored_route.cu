@@ -228,9 +228,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Reductions over the LPT consecutive lanes of one token (every lane gets the result).
 template <int LPT>
 __device__ __forceinline__ float token_max(float v) {
+    if constexpr (LPT == 32) {
+        float r;  // one instruction for the warp
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+        return r;
+    } else {
 #pragma unroll
-    for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
+        for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    }
 }
 
 template <int LPT>
