@@ -503,7 +503,9 @@ MOE_API int moe_gather_rows(int n_rows, int row_bytes, const void* src, const in
  * dx [T,K], da [n_adapters,r,K], db [n_adapters,N,r] bf16, written whole (zeros
  * for an adapter without tokens); dx may be NULL, and so may da and db together
  * (x and v are then not read).  T = 0 writes zeros to da and db.  Sums run in an
- * order that the sizes alone fix: results repeat bit for bit.
+ * order that the sizes alone fix: results repeat bit for bit on one GPU model.
+ * An infinity or NaN in one adapter, or in one token, shows in that adapter's or
+ * token's results only.
  * ws: device scratch of moe_adapter_workspace_size() bytes (it serves both
  * directions).  Limits: K, N and r multiples of 8, r <= 256, n_adapters <= 4096. */
 typedef struct {
