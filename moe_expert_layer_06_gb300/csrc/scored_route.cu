@@ -365,8 +365,13 @@ __device__ __noinline__ void resolve_order(const RouteArgs& a, int t, const uint
         bool open = false;
         if (rel > 0.0)
             for (int j = lane; j < min(a.k, n - 1); j += 32) {
-                const int q = sorted[j], r = sorted[j + 1];
-                open |= v[q] - v[r] <= rel * fabs(s[q] - s[r]) + 0x1p-45;
+                const int q = sorted[j];
+                for (int i = j + 1; i < n; ++i) {
+                    const int r = sorted[i];
+                    const double gap = v[q] - v[r];
+                    if (!(gap <= rel + 0x1p-45)) break;  // (scores are at most 1)
+                    open |= gap <= rel * fabs(s[q] - s[r]) + 0x1p-45;
+                }
             }
         again = __any_sync(0xffffffffu, open);
         if (again) {
@@ -722,14 +727,21 @@ __global__ void __launch_bounds__(kWarps * 32)
             // neighbours of the first k + 1 in order, too close for fp32?
             bool close = false;
             for (int j = sub; j < min(a.k, n - 1); j += LPT) {
-                const int q = sorted[j], r = sorted[j + 1];
-                float near = eps;
-                if (KIND == kKeySoftmax) {
-                    // the error is relative to the scores: those of the pair, where the largest is 1 / den
-                    const float pq = cand[q] - bias_of(cand_e[q]), pr = cand[r] - bias_of(cand_e[r]);
-                    near = eps - 2.0f * err + 0x1p-23f * 16.0f * (fabsf(pq) + fabsf(pr));
+                const int q = sorted[j];
+                if (KIND == kKeySigmoid) {
+                    close |= cand[q] - cand[sorted[j + 1]] <= eps;
+                    continue;
                 }
-                close |= cand[q] - cand[r] <= near;
+                // A softmax's error is relative to the scores: the pair's own, where eps takes the
+                // largest of the row (all followers within eps: their scores differ).
+                const float pq = fabsf(cand[q] - bias_of(cand_e[q]));
+                for (int i = j + 1; i < n; ++i) {
+                    const int r = sorted[i];
+                    const float gap = cand[q] - cand[r];
+                    if (!(gap <= eps)) break;
+                    const float pr = fabsf(cand[r] - bias_of(cand_e[r]));
+                    close |= gap <= eps - 2.0f * err + 0x1p-23f * 16.0f * (pq + pr);
+                }
             }
             uint32_t todo = __ballot_sync(0xffffffffu, close);
             dirty = todo != 0;

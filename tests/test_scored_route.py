@@ -197,6 +197,24 @@ def test_masked_experts(E, k, r, biased):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E,k,r", ROUTERS)
+@pytest.mark.parametrize("T", [40, 2500])
+@pytest.mark.parametrize("low", [-INF, float(torch.finfo(torch.float32).min), -1e4])
+def test_biases_that_keep_experts_out(E, k, r, T, low):
+    """A bias of -inf, the lowest value or far below the scores: such experts come last, and count as
+    what they are where too few others remain."""
+    g = torch.Generator().manual_seed(E + T)
+    l = (torch.randn(T, E, generator=g) * 1.7).cuda()
+    bias = torch.randn(E, generator=g) * 0.05
+    bias[torch.rand(E, generator=g) < 0.6] = low
+    check(l[:40].contiguous(), bias.cuda(), r, k)
+    if T > 40:
+        idx, w = call(l, bias.cuda(), r, k)
+        i2, w2 = call(l[-40:].contiguous(), bias.cuda(), r, k)
+        assert torch.equal(idx[-40:], i2) and bool(((w[-40:] - w2).abs() <= 40 * 2.0 ** -24 * w2).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("score", [m.MOE_SCORE_SIGMOID, m.MOE_SCORE_SOFTMAX])
 @pytest.mark.parametrize("renorm", [0, 1])
 def test_large_and_infinite_logits(score, renorm):
