@@ -426,12 +426,15 @@ struct ProjCfg {
 // tokens in turn; the accumulator is double buffered, so a tile's stores run under the
 // next tile's products.  A cluster's CTAs take a share of the contraction each and one
 // tile only; their fp32 sums meet in distributed shared memory, added in rank order.
+// Measured: one token, 7168 to 2048 features, 11 us a call with v's kernel (29 MB of W at
+// 6.5 TB/s in the middle 4.5 us; the rest is the start, the cluster's sum and the launches);
+// 192 tokens, 2048 to 7168, 18 us without adapters (each feature tile reads the tokens
+// again) and 28 with 23 of them.
 // The kernel before this one in the stream writes only v (it waited for its own
 // predecessors before it let this one start), so only the readers of v wait for it.
 template <bool BWD, int BN>
 __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(const __grid_constant__ ProjArgs a) {
     using C = ProjCfg<BN>;
-    pdl_launch_dependents();
     constexpr int stages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -486,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();  // (not before the tensor memory is this CTA's: see shrink_kernel)
     const uint32_t tbase = *tmem_slot;
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -729,6 +733,8 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
 // 32 KB per 64 of the contraction, so six stages (3072 cycles of products) fit where a CTA
 // on its own has four of 48 KB (2048 cycles, less than the round trip of a stage).
 // The leader (rank 0) issues the products; both load, write v and drain their own half.
+// Bound by the tensor cores: 4096 tokens, 7168 to 4096 features, 145 us (1.70 PFLOP/s, 89%
+// of the measured burst; 550 cycles a stage of 512 cycles of products).
 constexpr int kPairStages = 6;
 constexpr int kPairStageBytes = kABytes + 128 * 128;
 constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 512 + 2 * (int)sizeof(TileList) + kMaxAdapters / 8;
@@ -736,7 +742,6 @@ static_assert(kPairSmem <= 227 * 1024, "shared memory overflow");
 
 template <bool BWD>
 __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_constant__ ProjArgs a) {
-    pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);  // (the leader's)
@@ -789,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
     __syncthreads();
     cluster_sync();  // the barriers of both CTAs exist before either is signalled
     tc_fence_after();
+    pdl_launch_dependents();  // (not before the tensor memory is this pair's: see shrink_kernel)
     const uint32_t tbase = *tmem_slot;
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -1120,7 +1126,8 @@ __global__ void __launch_bounds__(256, 3) shrink_few_kernel(const uint16_t* x, c
 // ---------------------------------------------------------------- v and dv, many tokens
 // D[128 tokens][columns] = X tile . [A_i of the tile's adapters, stacked]^T on the tensor
 // cores: every token is multiplied with every adapter of its tile and keeps its own
-// columns, so the tokens are read once whatever their order.  Up to 256 columns at a time
+// columns, so the tokens are read once whatever their order.  Bound by reading them: 4096 x
+// 7168 (58 MB) at rank 64 takes 12 us in a stream of calls.  Up to 256 columns at a time
 // (`per_pass` adapters); clusters share the contraction.  Backward: dY . B_i, with B_i
 // read MN-major.
 struct ShrinkArgs {
@@ -1141,6 +1148,19 @@ constexpr int kShrinkRing = 192 * 1024;
 constexpr int kShrinkStages = 12;
 constexpr int kShrinkThreads = 192;
 constexpr int kShrinkExtra = 1024 + 256 + 128 * 8 + kMaxAdapters / 8;
+// An allocation of tensor memory waits until the columns are free.  It must not wait for a
+// kernel that waits for its own, nor for a CTA that waits for this one's cluster, so
+// whatever shares an SM fits its 512 columns at the same time:
+//  - a kernel lets the next one start only when its CTAs have their columns;
+//  - at most two of these CTAs (256 columns each) are on an SM, none beside one that holds
+//    all 512: a short ring is filled up to a third of an SM's shared memory and more.
+constexpr int kShrinkLeast = 77 * 1024;
+constexpr int kSmShared = 228 * 1024;
+static_assert(3 * kShrinkLeast > kSmShared, "a third CTA would wait for columns");
+static_assert(kShrinkLeast + kPairSmem > kSmShared && kShrinkLeast + ProjCfg<256>::kSmemBytes > kSmShared,
+              "a projection would wait for columns");
+static_assert(2 * kShrinkLeast + ProjCfg<32>::kSmemBytes > kSmShared && ProjCfg<128>::kTmemCols <= 256,
+              "a projection beside one of these CTAs has the columns that it needs");
 
 template <bool BWD>
 __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_constant__ ShrinkArgs a) {
@@ -1181,10 +1201,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
         tmem_relinquish();
     }
     pdl_wait();
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch_dependents();
     const uint32_t tbase = *tmem_slot;
     tile_adapters(a.adapter_of, row0, rows, a.n_adapters, 128, ids, list, bits, count, a.st, threadIdx.x, kShrinkThreads, 1);
     const int n_list = *count;
@@ -1323,7 +1343,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
 // that hold tokens of its adapter, and reads nothing else.  Both operands are MN-major (the
 // contraction runs over tokens).  In a chunk with other tokens too, their rows are set to
 // zero in shared memory, in both operands, so whatever they hold stays out.  What bounds
-// it is reading the tokens: 40 KB a chunk at rank 64, five in flight.
+// it is reading the tokens (40 KB a chunk at rank 64, five in flight) and the adapter with
+// the most of them: 4096 tokens of 4 adapters, 7168 and 2048 features, 25 us, where the 75 MB
+// take 11.
 struct GradArgs {
     CUtensorMap z[2];  // box {64 features, 64 tokens} of x [T][K], dy [T][N]
     CUtensorMap u[2];  // box {64 r, 64 tokens} of dv, v [T][r]
@@ -1340,6 +1362,7 @@ constexpr int kGradSegment = 4096;  // chunks whose list is held at a time
 template <int RB>  // 64-column blocks of the rank
 struct GradCfg {
     static constexpr int kStageBytes = 32768 + RB * 8192;
+    // (two CTAs of two stages on an SM took 37 us where one of five takes 26)
     static constexpr int kStages = RB == 1 ? 5 : RB == 2 ? 4 : 3;
     static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256 + kGradSegment * 2;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory overflow");
@@ -1808,8 +1831,7 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
         const int most = std::min(std::min(T, 128), p->n_adapters), beside = std::max(1, active_clusters(a.splits, false) / tiles);
         a.per_pass = std::min(a.per_pass, (most + beside - 1) / beside);
         a.passes = std::min((most + a.per_pass - 1) / a.per_pass, beside);
-        // a stage per chunk of the CTA's share at most (and room for its sums): a short one leaves
-        // the SM room for the next kernel's start
+        // a stage per chunk of the CTA's share at most (and room for its sums)
         const int pass_cols = std::min(a.per_pass, p->n_adapters) * a.cols, share = (kc + a.splits - 1) / a.splits;
         a.ring = std::min(kShrinkRing, std::max(share * (16384 + pass_cols * 128), (p->rank + 15) / 16 * 16 * 512));
         a.ring = (a.ring + 1023) / 1024 * 1024;
@@ -1819,8 +1841,8 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkRing + kShrinkExtra);
         });
         if (e == cudaSuccess)
-            e = launch_pdl_cluster(kern, dim3(tiles * a.passes * a.splits), dim3(kShrinkThreads), a.ring + kShrinkExtra, stream,
-                                   a.splits, a);
+            e = launch_pdl_cluster(kern, dim3(tiles * a.passes * a.splits), dim3(kShrinkThreads),
+                                   std::max(a.ring + kShrinkExtra, kShrinkLeast), stream, a.splits, a);
     }
     if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "adapter rank-product launch: %s", cudaGetErrorString(e));
     return MOE_OK;

