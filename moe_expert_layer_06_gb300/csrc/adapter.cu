@@ -331,18 +331,24 @@ __device__ __forceinline__ int adapter_step(int q, const Packing& pk) {
 
 // Zero times an infinity or NaN of an adapter would reach the other adapters' tokens: such
 // elements leave its tile here (true: there were some) and are added to their own tokens
-// in the epilogue.
-__device__ __forceinline__ bool take_odd(uint8_t* st_a, int tid) {
+// in the epilogue.  Only the columns that were copied are looked at: the rest of a stage,
+// which no product reads, holds what was there before.
+template <bool BWD>
+__device__ __forceinline__ bool take_odd(uint8_t* st_a, int columns, int tid) {
+    // (backward: features along the rows, in two halves)
+    const int used = columns * (BWD ? 8 : 16);
+    auto in = [&](int q) { return (BWD ? tid + (q & 3) * 128 : tid + q * 128) < used; };
     uint4* at = reinterpret_cast<uint4*>(st_a) + tid;
     uint32_t most = 0;  // largest magnitudes, as pairs of 16-bit numbers
 #pragma unroll
     for (int q = 0; q < kABytes / 16 / 128; ++q) {
-        const uint4 val = at[q * 128];
+        const uint4 val = in(q) ? at[q * 128] : make_uint4(0, 0, 0, 0);
         most = __vmaxu2(__vmaxu2(most, val.x & 0x7fff7fffu), val.y & 0x7fff7fffu);
         most = __vmaxu2(__vmaxu2(most, val.z & 0x7fff7fffu), val.w & 0x7fff7fffu);
     }
     if ((most & 0xffffu) < 0x7f80u && (most >> 16) < 0x7f80u) return false;
     for (int q = 0; q < kABytes / 16 / 128; ++q) {
+        if (!in(q)) continue;
         uint4 val = at[q * 128];
         val.x = finite_part(val.x);
         val.y = finite_part(val.y);
@@ -636,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 uint8_t* st_a = smem + stage * C::kStageBytes;
                 uint8_t* sb = st_a + kABytes;
                 vr.store(sb, a.bn, first_of, pk.per, tid);
-                if (take_odd(st_a, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
+                if (take_odd<BWD>(st_a, pk.n(e, tl.count) * pk.seg, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
                 if (tid == 0) mbar_arrive(smem_u32(&full[stage]));
@@ -962,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 land_phase ^= 1u << stage;
                 uint8_t* st_a = smem + stage * kPairStageBytes;
                 vr.store(st_a + kABytes, half, first_of, pk.per, tid);
-                if (take_odd(st_a, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
+                if (take_odd<BWD>(st_a, pk.n(e, tl.count) * pk.seg, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
                 if (tid == 0) {
