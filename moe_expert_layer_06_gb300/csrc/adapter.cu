@@ -203,6 +203,7 @@ struct ProjArgs {
     CUtensorMap w;      // forward: box {64 k, 128 n} of W [N][K]; backward: box {64 k, 64 n}
     CUtensorMap lr;     // forward: box {64 r, 128 n} of B [n][N][r]; backward: box {64 k, 64 r} of A [n][r][K]
     CUtensorMap x;      // tokens: box {64, 1, tokens of one CTA} of x [T][K] | dy [T][N]
+    CUtensorMap y;      // box {64, 1, 16} of a bf16 output
     const int32_t* adapter_of;
     const uint16_t* v;  // [T][r] v | dv
     const uint16_t* lr_ptr;  // what `lr` maps
@@ -414,6 +415,79 @@ __device__ __forceinline__ void store_group(const ProjArgs& a, int t0, int n, in
     }
 }
 
+// ---- a tile's bf16 outputs through shared memory
+// A lane that holds one feature of 16 tokens writes 64 bytes of a row with its warp: 450 ns
+// for 16 tokens, 7 us for the 256 of a tile, more than its products take below 1700 of the
+// contraction.  Here the accumulator comes as 8 x 8 fragments, which stmatrix turns to rows
+// of features, and copies of 16 tokens x 64 features take them out.
+constexpr int kOutBlock = 4096;           // 32 tokens x 64 features
+constexpr int kOutBytes = 2 * 2 * kOutBlock;  // two of each pair of warps
+
+// 16 lanes x 32 columns: r[4 i + 0, 1] columns 8 i + 2 (lane % 4) + 0, 1 of row lane / 4, r[4 i + 2, 3] of row lane / 4 + 8
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ uint32_t pack_bf(uint32_t lo, uint32_t hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Warp q's quarter of the accumulator at `tmem`: `rows` tokens from row0, of the 128
+// features from m0.  Warps 2 p and 2 p + 1 share 64 features, two blocks at `out` and the
+// copies, which the first one's lane 0 issues; `blocks` counts the blocks so far.
+__device__ __forceinline__ void drain_tile(const ProjArgs& a, uint32_t tmem, uint32_t out, int row0, int rows, int m0, int q,
+                                           int lane, int& blocks) {
+    const int pair = q >> 1, f0 = m0 + pair * 64;
+    const bool issuer = !(q & 1) && lane == 0;
+    // this lane's address of a row of 8 features: token lane % 8, features 8 (lane / 8) of the warp's 32 (swizzled as the copy reads)
+    const uint32_t at = (lane & 7) * 128 + ((((q & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+    for (int t = 0; t < rows; t += 32, ++blocks) {
+        uint32_t lo[16], hi[16];
+        tmem_ld_16x256(tmem + t, lo);
+        tmem_ld_16x256(tmem + t + (16u << 16), hi);
+        tmem_ld_wait();
+        const uint32_t block = out + (pair * 2 + (blocks & 1)) * kOutBlock;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            stmatrix_trans(block + i * 1024 + at, pack_bf(lo[4 * i], lo[4 * i + 1]), pack_bf(lo[4 * i + 2], lo[4 * i + 3]),
+                           pack_bf(hi[4 * i], hi[4 * i + 1]), pack_bf(hi[4 * i + 2], hi[4 * i + 3]));
+        fence_async_smem();
+        if (issuer) bulk_wait_read();  // the other block is free, which the next round writes
+        __syncwarp();
+        named_sync(2 + pair, 64);
+        if (issuer) {
+            // (a tile's tokens are a multiple of 16 but at the end of the batch, where the copy ends too)
+            if (f0 < a.O) {
+                tma_store_3d(&a.y, block, f0, 0, row0 + t);
+                if (t + 16 < rows) tma_store_3d(&a.y, block + kOutBlock / 2, f0, 0, row0 + t + 16);
+            }
+            bulk_commit();
+        }
+        __syncwarp();
+    }
+}
+
 // BN: capacity of the token operand.  Up to 64 tokens two CTAs share an SM.
 template <int BN>
 struct ProjCfg {
@@ -423,7 +497,9 @@ struct ProjCfg {
     static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 4 : 5;
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
     static constexpr int kBarBytes = 512;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + 2 * (int)sizeof(TileList) + kMaxAdapters / 8;
+    static constexpr bool kCopyOut = BN > 64;  // (the shared memory of two CTAs has no room for it)
+    static constexpr int kRingBytes = kStages * kStageBytes + (kCopyOut ? kOutBytes : 0);
+    static constexpr int kSmemBytes = 1024 + kRingBytes + kBarBytes + 2 * (int)sizeof(TileList) + kMaxAdapters / 8;
     static_assert(kSmemBytes <= (BN <= 64 ? 113 : 227) * 1024, "shared memory overflow");
     static_assert(kStages * kStageBytes >= BN * 128 * 4, "the split sums fit the stages");
 };
@@ -444,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     constexpr int stages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + stages * C::kStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRingBytes);
     uint64_t* empty = full + stages;
     uint64_t* landed = empty + stages;  // the adapter tile of a stage, before the v writers are done with it
     uint64_t* tfull = landed + stages;  // accumulator complete / drained
@@ -455,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert((3 * C::kStages + 9) * 8 + 8 <= C::kBarBytes, "barriers");
-    TileList* lists = reinterpret_cast<TileList*>(smem + stages * C::kStageBytes + C::kBarBytes);
+    TileList* lists = reinterpret_cast<TileList*>(smem + C::kRingBytes + C::kBarBytes);
     uint32_t* bits = reinterpret_cast<uint32_t*>(lists + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -487,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         tma_prefetch_desc(&a.w);
         tma_prefetch_desc(&a.x);
         tma_prefetch_desc(&a.lr);
+        if (!a.out_fp32) tma_prefetch_desc(&a.y);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -654,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         // ---- epilogue: TMEM lane = output feature, column = token
         const int q = warp & 3;
         bool ok = true;
+        int blocks = 0;
         for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
             const int m0 = (i % m_tiles) * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             const TileList& tl = lists[n & 1];
@@ -667,7 +745,9 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             const int n_ext = pk.chunks(tl.count);
             const uint32_t tmem = tbase + (n & 1) * BN + ((uint32_t)(q * 32) << 16);
             const bool any_odd = has_odd(tl, n_ext);
-            for (int g = 0; g * 16 < rows; ++g) {
+            const bool copy_out = C::kCopyOut && S == 1 && !a.out_fp32 && !any_odd;
+            if (copy_out) drain_tile(a, tmem, stage_u + stages * C::kStageBytes, row0, rows, m0, q, lane, blocks);
+            for (int g = 0; g * 16 < rows && !copy_out; ++g) {
                 float v[16];
                 tmem_ld16(tmem + g * 16, v);
                 tmem_ld_wait();
@@ -690,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             }
         }
         if (!ok && lane == 0) give_up();
+        if (C::kCopyOut && lane == 0) bulk_wait();
     }
     if (S > 1) {
         // every share is in its CTA's shared memory; each CTA adds up a part of the tile
@@ -743,14 +824,15 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
 // of the measured burst; 550 cycles a stage of 512 cycles of products).
 constexpr int kPairStages = 6;
 constexpr int kPairStageBytes = kABytes + 128 * 128;
-constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 512 + 2 * (int)sizeof(TileList) + kMaxAdapters / 8;
+constexpr int kPairRing = kPairStages * kPairStageBytes + kOutBytes;
+constexpr int kPairSmem = 1024 + kPairRing + 512 + 2 * (int)sizeof(TileList) + kMaxAdapters / 8;
 static_assert(kPairSmem <= 227 * 1024, "shared memory overflow");
 
 template <bool BWD>
 __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_constant__ ProjArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);  // (the leader's)
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairRing);  // (the leader's)
     uint64_t* empty = full + kPairStages;
     uint64_t* landed = empty + kPairStages;
     uint64_t* other = landed + kPairStages;  // (the leader's) the other CTA's half of an adapter chunk is in place
@@ -762,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert((4 * kPairStages + 9) * 8 + 8 <= 512, "barriers");
-    TileList* lists = reinterpret_cast<TileList*>(smem + kPairStages * kPairStageBytes + 512);
+    TileList* lists = reinterpret_cast<TileList*>(smem + kPairRing + 512);
     uint32_t* bits = reinterpret_cast<uint32_t*>(lists + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -794,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
         tma_prefetch_desc(&a.w);
         tma_prefetch_desc(&a.x);
         tma_prefetch_desc(&a.lr);
+        if (!a.out_fp32) tma_prefetch_desc(&a.y);
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
     tc_fence_before();
@@ -982,6 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
     } else {
         const int q = warp & 3;
         bool ok = true;
+        int blocks = 0;
         for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
             const int m0 = (i % m_tiles) * 256 + rank * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             const TileList& tl = lists[n & 1];
@@ -994,7 +1078,9 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             const int n_ext = pk.chunks(tl.count);
             const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
             const bool any_odd = has_odd(tl, n_ext);
-            for (int g = 0; g * 16 < rows; ++g) {
+            const bool copy_out = !a.out_fp32 && !any_odd;
+            if (copy_out) drain_tile(a, tmem, stage_u + kPairStages * kPairStageBytes, row0, rows, m0, q, lane, blocks);
+            for (int g = 0; g * 16 < rows && !copy_out; ++g) {
                 float v[16];
                 tmem_ld16(tmem + g * 16, v);
                 tmem_ld_wait();
@@ -1010,6 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             }
         }
         if (!ok && lane == 0) give_up();
+        if (lane == 0) bulk_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -1785,6 +1872,8 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     if (rc) return rc;
     const uint64_t C = a.C;
     if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.pair ? plan.bn / 2 : plan.bn))) return rc;
+    const uint64_t O = a.O;
+    if (!out_fp32 && (rc = make_tmap_3d(&a.y, out, O, 1, (uint64_t)T, O * 2, O * 2, 64, 1, 16))) return rc;
     a.lr_ptr = static_cast<const uint16_t*>(lr);
     a.adapter_of = adapter_of;
     a.v = static_cast<const uint16_t*>(v);
