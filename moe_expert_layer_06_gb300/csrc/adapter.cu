@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             mbar_init(smem_u32(&tfull[s]), 1);
             mbar_init(smem_u32(&tempty[s]), 4);
             mbar_init(smem_u32(&listed[s]), 1);
-            mbar_init(smem_u32(&lfree[s]), 4);
+            mbar_init(smem_u32(&lfree[s]), 5);  // the epilogue and the loads
         }
         mbar_init(smem_u32(done), 1);
         *abort_flag = 0;
@@ -626,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 __syncwarp();
                 advance(true);
             }
+            if (lane == 0) mbar_arrive(smem_u32(&lfree[n & 1]));  // the list has been read
         }
         if (!ok && lane == 0) give_up();
         // every copy has landed before the CTA exits
@@ -832,7 +833,7 @@ template <bool BWD>
 __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_constant__ ProjArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairRing);  // (the leader's)
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairRing);  // (beside the leader: of adapter chunks only)
     uint64_t* empty = full + kPairStages;
     uint64_t* landed = empty + kPairStages;
     uint64_t* other = landed + kPairStages;  // (the leader's) the other CTA's half of an adapter chunk is in place
@@ -868,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             mbar_init(smem_u32(&tfull[s]), 1);
             mbar_init(smem_u32(&tempty[s]), 8);
             mbar_init(smem_u32(&listed[s]), 1);
-            mbar_init(smem_u32(&lfree[s]), 4);
+            mbar_init(smem_u32(&lfree[s]), 5 + rank);  // the epilogue, the loads and, beside the leader, the signals
         }
         mbar_init(smem_u32(done), 1);
         *abort_flag = 0;
@@ -938,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 __syncwarp();
                 advance(true);
             }
+            if (lane == 0) mbar_arrive(smem_u32(&lfree[n & 1]));  // the list has been read
         }
         if (!ok && lane == 0) give_up();
         // every stage's last products are done, so its copies have landed
@@ -1018,6 +1020,27 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             // all products are complete before TMEM is freed
             if (elect_one()) umma_commit_pair(smem_u32(done));
             __syncwarp();
+        } else {
+            // the other CTA's workers signal here, and the leader hears of it from this warp: the
+            // arrival there takes 500 cycles, which kept them from their next chunk
+            bool ok = true;
+            int at = 0;
+            uint32_t ext_phase = 0;
+            for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
+                if (!(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
+                const int n_ext = pk.chunks(lists[n & 1].count);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&lfree[n & 1]));
+                at += kc;
+                for (int e = 0; e < n_ext; ++e, ++at) {
+                    const int stage = at % kPairStages;
+                    if (!(ok = warp_wait(full_u + stage * 8, (ext_phase >> stage) & 1u, abort_flag, limit))) break;
+                    ext_phase ^= 1u << stage;
+                    if (lane == 0) mbar_arrive_cluster(lead_other + stage * 8);
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) give_up();
         }
         mbar_wait(smem_u32(done), 0, limit);
     } else if (warp < 6) {
@@ -1054,10 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
                 if (take_odd<BWD>(st_a, pk.n(e, tl.count) * pk.seg, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
                 fence_async_smem();
                 named_sync(1, 128);
-                if (tid == 0) {
-                    if (rank == 0) mbar_arrive(full_u + stage * 8);
-                    else mbar_arrive_cluster(lead_other + stage * 8);
-                }
+                if (tid == 0) mbar_arrive(full_u + stage * 8);
                 if (++stage == kPairStages) stage = 0;
             }
         }
@@ -1069,7 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
         for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
             const int m0 = (i % m_tiles) * 256 + rank * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             const TileList& tl = lists[n & 1];
-            // (the list is read here and, in the leader, by the product warp: both before lfree)
+            // (in the leader the product warp has read the list before its last commit)
             if (!(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit)) ||
                 !(ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit)))
                 break;
