@@ -1856,9 +1856,19 @@ int tile_height(int T, int units, int slots, int by) {
 ProjPlan project_plan(int T, int O, int C, int r, int n_adapters) {
     ProjPlan p;
     const int sms = num_sms(), m_tiles = (O + 127) / 128, kc = (C + 63) / 64;
-    p.splits = 1;
-    // as many tiles as SMs: pairs of CTAs
-    p.pair = T > 128 && (long)m_tiles * ((T + 255) / 256) >= sms;
+    p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+    p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : (T + 15) / 16 * 16;
+    const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
+    // (a small batch may hold as many adapters as tokens, and each adds a chunk per 64 of its rank)
+    const int held = T <= 256 ? std::min(T, n_adapters) : 2;
+    const int extra = r <= 16 ? (held + 3) / 4 : r <= 32 ? (held + 1) / 2 : held * ((r + 63) / 64);
+    const bool many = T > 128 && (long)m_tiles * ((T + 255) / 256) >= sms;
+    p.splits = !many && tiles < 2 * sms ? split_of(tiles, kc + extra, 8, p.cap <= 64) : 1;
+    // As many tiles as SMs, or a long contraction that no cluster shares: pairs of CTAs.  (4096
+    // tokens, 4608 to 1024 features, a backward pass without gradients: 64 pairs 39 us, 128 CTAs
+    // on their own 44; 2933 tokens, 1992 to 400: 25 and 27.  A pair begins later: 2048 tokens,
+    // 1024 to 1024, 16 and 15 us.)
+    p.pair = many || (T > 128 && p.splits == 1 && kc >= 31);
     if (p.pair) {
         const int units = (O + 255) / 256, slots = sms / 2;
         p.cap = 256;
@@ -1866,13 +1876,6 @@ ProjPlan project_plan(int T, int O, int C, int r, int n_adapters) {
         p.grid = 2 * (int)std::min<long>((long)units * ((T + p.bn - 1) / p.bn), slots);
         return p;
     }
-    p.cap = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-    p.bn = T > 256 ? tile_height(T, m_tiles, sms, 16) : (T + 15) / 16 * 16;
-    const long tiles = (long)m_tiles * ((T + p.bn - 1) / p.bn);
-    // (a small batch may hold as many adapters as tokens, and each adds a chunk per 64 of its rank)
-    const int held = T <= 256 ? std::min(T, n_adapters) : 2;
-    const int extra = r <= 16 ? (held + 3) / 4 : r <= 32 ? (held + 1) / 2 : held * ((r + 63) / 64);
-    p.splits = tiles < 2 * sms ? split_of(tiles, kc + extra, 8, p.cap <= 64) : 1;
     p.grid = p.splits > 1 ? (int)tiles * p.splits : (int)std::min<long>(tiles, sms);
     return p;
 }
