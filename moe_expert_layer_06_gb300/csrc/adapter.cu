@@ -14,7 +14,7 @@
 // MN-major (the contraction runs over their rows).
 #include <algorithm>
 
-#include "kernels.h"
+#include "operators.cuh"
 
 namespace moe {
 namespace {
@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
 // 32 KB per 64 of the contraction, so six stages (3072 cycles of products) fit where a CTA
 // on its own has four of 48 KB (2048 cycles, less than the round trip of a stage).
 // The leader (rank 0) issues the products; both load, write v and drain their own half.
-// Bound by the tensor cores: 4096 tokens, 7168 to 4096 features, 145 us (1.70 PFLOP/s, 89%
+// Bound by the tensor cores: 4096 tokens, 7168 to 4096 features, 140 us (1.71 PFLOP/s, 89%
 // of the measured burst; 550 cycles a stage of 512 cycles of products).
 constexpr int kPairStages = 6;
 constexpr int kPairStageBytes = kABytes + 128 * 128;
@@ -1899,7 +1899,7 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     if (rc) return rc;
     const uint32_t seg = a.r <= 16 ? 16 : a.r <= 32 ? 32 : 64;  // (as Packing)
     if (BWD) rc = make_tmap_3d(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, seg, 1);
-    else rc = make_tmap_3d(&a.lr, lr, r, N, n, r * 2, r * N * 2, seg, 128, 1, false, seg * 2);
+    else rc = make_tmap_3d_swizzled(&a.lr, lr, r, N, n, r * 2, r * N * 2, seg, 128, 1, seg * 2);
     if (rc) return rc;
     const uint64_t C = a.C;
     if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.pair ? plan.bn / 2 : plan.bn))) return rc;

@@ -238,9 +238,6 @@ __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Order this thread's shared-memory writes before later reads by the async proxy (TMA, UMMA).
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 // Shared-memory matrix descriptor of a K-major operand tile written by TMA with
 // 128-byte swizzle: rows of 128 B (64 bf16), 8-row groups 1024 B apart.
 __device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t smem_addr) {
@@ -252,21 +249,6 @@ __device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t smem_addr) {
     d |= (uint64_t)2u << 61;                        // 128-byte swizzle
     return d;
 }
-
-// Shared-memory matrix descriptor of an MN-major operand tile written by TMA with
-// 128-byte swizzle: K rows of 128 B (64 bf16 of M or N), 8-row groups 1024 B apart,
-// blocks of 64 of M or N `block_bytes` apart.
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint32_t block_bytes) {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(block_bytes >> 4) << 16;        // leading byte offset: next 64 of M or N
-    d |= (uint64_t)(1024u >> 4) << 32;              // stride byte offset: next 8 of K
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
-}
-constexpr uint32_t kIdescAMnMajor = 1u << 15;  // A / B transposed (MN-major) in an instruction descriptor
-constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // Instruction descriptor, kind::f16: bf16 A and B (both K-major), fp32 D, M x N.
 __host__ __device__ __forceinline__ uint32_t umma_idesc_bf16(int M, int N) {

@@ -49,32 +49,6 @@ inline cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, si
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-// The same in clusters of `cluster` CTAs along x (1: none).
-template <typename... Params, typename... Args>
-inline cudaError_t launch_pdl_cluster(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                      int cluster, Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (pdl_enabled()) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = cluster;
-        attr[n].val.clusterDim.y = 1;
-        attr[n++].val.clusterDim.z = 1;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
-
 // Run `configure` (a kernel attribute such as its dynamic shared memory) the
 // first time the calling thread's device needs it, from any number of host
 // threads: `done` holds one bit per configured device (ordinals 0..63; others
@@ -174,11 +148,10 @@ cudaError_t launch_gemm(GemmMode mode, int bn, const GemmArgs& args, int grid, c
 int gemm_max_slots();  // slots the GEMM's shared-memory item table holds
 
 // ---------------------------------------------------------------- TMA tensor maps
-// 3-D bf16 tensor map, dims innermost first (elements), strides of dims 1,2 in bytes; the
-// swizzle (128, 64 or 32 bytes) is the box's inner extent at least.
+// 3-D bf16 tensor map, dims innermost first (elements), strides of dims 1,2 in bytes.
 int make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                  uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
-                 uint32_t box2, bool fp8 = false, int swizzle_bytes = 128);
+                 uint32_t box2, bool fp8 = false);
 
 // ---------------------------------------------------------------- FP8 (E4M3) quantisation
 // codes[r][c] = e4m3(x[r][c] / scale[r]), scale[r] = amax(|x[r]|) / 448 (1 for a zero row),
@@ -236,12 +209,5 @@ int num_sms();
 // outside moe_api.cu.
 int api_fail(int code, const char* fmt, ...);
 int api_check_shape(const moe_shape_t* shape, int T);
-int api_device_status(DevStatus* st);
-// The router GEMM into ws (checked against moe_route_workspace_size): *ksplit partial
-// logits [ksplit][T][E], to be added in order.
-int api_router_gemm(const moe_shape_t* shape, int T, const void* x, const void* w_router, void* ws, size_t ws_bytes,
-                    int* ksplit, cudaStream_t stream);
-// Pointer checks: 0, or the error code with its text set.
-int api_need(const void* p, const char* name, unsigned align = 16);
 
 }  // namespace moe

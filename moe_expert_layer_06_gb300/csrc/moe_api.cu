@@ -10,7 +10,7 @@
 #include <vector>
 
 #include "moe.h"
-#include "kernels.h"
+#include "operators.cuh"
 
 namespace moe {
 
@@ -97,8 +97,8 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
-int make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-                 uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8, int swizzle_bytes) {
+static int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                          uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8, int swizzle_bytes) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     const cuuint64_t dims[3] = {d0, d1, d2};
@@ -116,6 +116,16 @@ int make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, u
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return MOE_OK;
+}
+
+int make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                 uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8) {
+    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, fp8, 128);
+}
+
+int make_tmap_3d_swizzled(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                          uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, int swizzle_bytes) {
+    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, false, swizzle_bytes);
 }
 
 // weight stack [n][rows][K] -> dims {K, rows, n}, box {64, 128, 1}

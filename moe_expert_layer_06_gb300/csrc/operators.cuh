@@ -1,0 +1,67 @@
+// What the operators around the layer (scored_route.cu, adapter.cu) share.
+#pragma once
+
+#include "kernels.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------- launches
+// launch_pdl in clusters of `cluster` CTAs along x (1: none).
+template <typename... Params, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                      int cluster, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl_enabled()) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// ---------------------------------------------------------------- device
+// Order this thread's shared-memory writes before later reads by the async proxy (TMA, UMMA).
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory matrix descriptor of an MN-major operand tile written by TMA with
+// 128-byte swizzle: K rows of 128 B (64 bf16 of M or N), 8-row groups 1024 B apart,
+// blocks of 64 of M or N `block_bytes` apart.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(block_bytes >> 4) << 16;        // leading byte offset: next 64 of M or N
+    d |= (uint64_t)(1024u >> 4) << 32;              // stride byte offset: next 8 of K
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+constexpr uint32_t kIdescAMnMajor = 1u << 15;  // A / B transposed (MN-major) in an instruction descriptor
+constexpr uint32_t kIdescBMnMajor = 1u << 16;
+
+// ---------------------------------------------------------------- moe_api.cu
+// make_tmap_3d for bf16 with a swizzle of 128, 64 or 32 bytes, the box's inner extent at least.
+int make_tmap_3d_swizzled(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                          uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1,
+                          uint32_t box2, int swizzle_bytes);
+int api_device_status(DevStatus* st);
+// The router GEMM into ws (checked against moe_route_workspace_size): *ksplit partial
+// logits [ksplit][T][E], to be added in order.
+int api_router_gemm(const moe_shape_t* shape, int T, const void* x, const void* w_router, void* ws, size_t ws_bytes,
+                    int* ksplit, cudaStream_t stream);
+// Pointer checks: 0, or the error code with its text set.
+int api_need(const void* p, const char* name, unsigned align = 16);
+
+}  // namespace moe

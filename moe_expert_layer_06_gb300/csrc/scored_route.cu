@@ -14,7 +14,7 @@
 
 #include <algorithm>
 
-#include "kernels.h"
+#include "operators.cuh"
 
 namespace moe {
 namespace {
