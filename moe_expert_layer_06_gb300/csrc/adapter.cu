@@ -825,8 +825,8 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
 
 // Many tiles: a pair of CTAs computes 256 features x bn tokens with one product per 16 of
 // the contraction (cta_group::2).  Each CTA holds 128 rows of W and half of the tokens,
-// 32 KB per 64 of the contraction, so six stages (3072 cycles of products) fit where a CTA
-// on its own has four of 48 KB (2048 cycles, less than the round trip of a stage).
+// 32 KB per 64 of the contraction, so six stages (6 x 512 cycles of products) fit where a CTA
+// on its own has four of 48 KB (4 x 512, less than the round trip of a stage).
 // The leader (rank 0) issues the products; both load, write v and drain their own half.
 // Bound by the tensor cores: 4096 tokens, 7168 to 4096 features, 140 us (1.71 PFLOP/s, 89%
 // of the measured burst; 550 cycles a stage of 512 cycles of products).

@@ -151,6 +151,20 @@ def test_more_tiles_than_processors_and_many_adapters_per_tile(T, K, N, r, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r,n", [(100, 264, 24008, 24, 3), (200, 24008, 136, 8, 5), (2040, 264, 1000, 16, 9),
+                                       (1100, 2104, 1000, 32, 2), (300, 72, 5000, 64, 4)])
+def test_tiles_that_no_cluster_shares(T, K, N, r, n):
+    """Outputs through shared memory, at every tile height, feature and token edge."""
+    c = Case(T, K, N, r, n, "each")
+    ref = c.reference()
+    y, v = c.forward()
+    close(y, *ref["y"], name="y")
+    dx, da, db = c.backward(v)
+    for got, name in ((dx, "dx"), (da, "da"), (db, "db")):
+        close(got, *ref[name], name=name)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,long,short,n", [(956, 7720, 216, 5), (2048, 9000, 136, 6), (300, 2048, 72, 40), (9000, 520, 200, 3)])
 def test_calls_one_after_another_over_a_short_contraction(T, long, short, n):
     """A short rank product may start while the projection of the call before it runs."""
