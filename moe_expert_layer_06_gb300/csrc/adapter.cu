@@ -514,7 +514,9 @@ struct ProjCfg {
 // One persistent CTA (or cluster of `splits`) takes tiles of 128 output features x bn
 // tokens in turn; the accumulator is double buffered, so a tile's stores run under the
 // next tile's products.  A cluster's CTAs take a share of the contraction each and one
-// tile only; their fp32 sums meet in distributed shared memory, added in rank order.
+// tile only; their fp32 sums meet in distributed shared memory, added in rank order.  (The
+// plan counts the chunks of as many adapters as the tile may hold, so a short contraction
+// may have more CTAs than chunks: a CTA without any adds zeros.)
 // Measured: one token, 7168 to 2048 features, 11 us a call with v's kernel (29 MB of W at
 // 6.5 TB/s in the middle 4.5 us; the rest is the start, the cluster's sum and the launches);
 // 192 tokens, 2048 to 7168, 18 us without adapters (each feature tile reads the tokens
@@ -754,11 +756,18 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
             const uint32_t tmem = tbase + (n & 1) * BN + ((uint32_t)(q * 32) << 16);
             const bool any_odd = has_odd(tl, n_ext);
             const bool copy_out = C::kCopyOut && S == 1 && !a.out_fp32 && !any_odd;
+            // A short contraction may leave a CTA of the cluster without a chunk of it, and the tile
+            // without an adapter chunk for it: its accumulator was never written.
+            const bool no_share = c0 == c1 && rank >= n_ext;
             if (copy_out) drain_tile(a, tmem, stage_u + stages * C::kStageBytes, row0, rows, m0, q, lane, blocks);
             for (int g = 0; g * 16 < rows && !copy_out; ++g) {
                 float v[16];
                 tmem_ld16(tmem + g * 16, v);
                 tmem_ld_wait();
+                if (no_share) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+                }
                 if (any_odd && feat < a.O) add_odd<BWD>(a, tl, n_ext, row0 + g * 16, g * 16, feat, v);
                 __syncwarp();
                 if (S > 1) {

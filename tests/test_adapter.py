@@ -187,6 +187,31 @@ def test_calls_one_after_another_over_a_short_contraction(T, long, short, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [64, 192, 256, 448])
+@pytest.mark.parametrize("T,r,n", [(1, 64, 16), (16, 64, 16), (64, 64, 64), (200, 72, 64), (300, 256, 16)])
+@pytest.mark.parametrize("ids", ["none", "one", "two"])
+def test_short_contractions_with_few_of_many_adapters(T, C, r, n, ids):
+    """Fewer chunks of contraction than the clusters that the configured adapters call for have CTAs, and
+    a batch that uses none, one or two of those: some CTAs have nothing to multiply."""
+    loud = Case(256, 512, 4096, 8, 1, "none")  # leaves large sums in the tensor memory
+    loud.x *= 1000
+    for K, N in ((C, 1024), (1024, C)):
+        c = Case(T, K, N, r, n, "none" if ids == "none" else "one")
+        if ids == "two":
+            c.of[::2] = 0
+        ref = c.reference()
+        loud.forward()
+        y, v = c.forward()
+        y32, _ = c.forward(fp32=True)
+        loud.forward()
+        dx, da, db = c.backward(v)
+        assert m.moe_check_status() == 0
+        close(y32, *ref["y"], bf16=False, name="y fp32")
+        for name, got in (("y", y), ("dx", dx), ("da", da), ("db", db)):
+            close(got, *ref[name], name=name)
+
+
+@pytest.mark.gpu
 def test_very_long_batches():
     """More 64-token chunks than the gradient kernel lists at a time (262144 tokens)."""
     c = Case(270001, 16, 24, 8, 3, "runs")
