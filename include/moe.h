@@ -178,7 +178,9 @@ MOE_API int moe_route_grouped(const moe_shape_t* shape, int T, int n_groups, int
  *              tiny scores keeps its ratios).
  * A logit of -inf or NaN masks its expert: score 0, selected only when fewer
  * than k others remain in the kept groups (then the lowest masked experts of
- * those groups), weight 0.  A row with no unmasked expert gets weights 0.
+ * those groups), weight 0.  A row with no unmasked expert gets weights 0.  A
+ * select_bias of -inf or NaN keeps its expert out of the selection in the same way,
+ * but leaves its score as it is: selected for want of others, it has its weight.
  * x, w_router, logits_in, logits_out, outputs and workspace as moe_route (there
  * is no bias on the logits).  Limits: those of moe_route_grouped. */
 #define MOE_SCORE_SOFTMAX 0

@@ -134,7 +134,7 @@ __device__ __noinline__ void select_fp64(const RouteArgs& a, int t, double* c) {
         if (l == -INFINITY) continue;
         double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : (l == mx ? 1.0 : exp(l - (double)mx)) / den;
         if (a.bias) s += a.bias[e];
-        c[e] = s;
+        c[e] = s == s ? s : -INFINITY;  // (a NaN bias keeps its expert out as one of -inf does)
     }
     __syncwarp();
     uint32_t kept = 0xffffffffu;
@@ -161,7 +161,8 @@ __device__ __noinline__ void select_fp64(const RouteArgs& a, int t, double* c) {
             kept |= 1u << i;
         }
     }
-    // lane j keeps the j-th selected expert; taken experts are marked NaN
+    // Lane j keeps the j-th selected expert; taken experts are marked NaN, which nothing else is.
+    // The kept groups hold k experts at least (check_router), so each round finds one.
     int mine = -1;
     for (int j = 0; j < a.k; ++j) {
         double v = 0.0;
@@ -175,6 +176,7 @@ __device__ __noinline__ void select_fp64(const RouteArgs& a, int t, double* c) {
             }
         }
         warp_best(v, i);
+        i = min(i, a.E - 1);  // (whatever the values: an index of the row)
         if ((i & 31) == lane) c[i] = NAN;
         if (lane == j) mine = i;
     }

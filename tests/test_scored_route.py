@@ -215,6 +215,26 @@ def test_biases_that_keep_experts_out(E, k, r, T, low):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E,k,r", ROUTERS)
+@pytest.mark.parametrize("T", [40, 2500])
+@pytest.mark.parametrize("share", [0.05, 0.6, 0.97, 1.0])
+def test_nan_biases_keep_experts_out(E, k, r, T, share):
+    """Some or all entries of the bias are NaN (a balance update that diverged): as a bias of -inf."""
+    g = torch.Generator().manual_seed(E + T)
+    l = torch.randn(T, E, generator=g) * 1.7
+    l[torch.rand(T, E, generator=g) < 0.1] = -INF
+    l = l.cuda()
+    bias = torch.randn(E, generator=g) * 0.05
+    out = torch.rand(E, generator=g) < share
+    low, nan = bias.clone(), bias.clone()
+    low[out], nan[out] = -INF, float("nan")
+    check(l[:40].contiguous(), low.cuda(), r, k)
+    idx, w = call(l, nan.cuda(), r, k)
+    i2, w2 = call(l, low.cuda(), r, k)
+    assert torch.equal(idx, i2) and torch.equal(w, w2)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("score", [m.MOE_SCORE_SIGMOID, m.MOE_SCORE_SOFTMAX])
 @pytest.mark.parametrize("renorm", [0, 1])
 def test_large_and_infinite_logits(score, renorm):
