@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                 }
 #pragma unroll
                 for (int u = 0; u < (PER >= 4 ? 4 : 1); ++u) {
-                    // 2^-149 l: nothing beside the bias, but for -inf, which stays -inf
+                    // 2^-149 l: nothing beside the bias, but for -inf, which stays -inf (and +inf: see below)
                     const float base = fmaf(c[i + u], 0x1p-149f, b4[u]);
                     if (KIND == kKeySigmoid) c[i + u] = base + fast_rcp(1.0f + fast_exp2(c[i + u] * -kLog2e));
                     else c[i + u] = fmaf(e[(i + u) % (KIND == kKeySoftmax ? PER : 1)], inv_den, base);
@@ -576,6 +576,13 @@ __global__ void __launch_bounds__(kWarps * 32)
         float m[NB];
 #pragma unroll
         for (int q = 0; q < NB; ++q) m[q] = max_of<BLK>(c + q * BLK);
+        // Values of +inf are not what they stand for (an infinite logit's score is 1), and their
+        // differences are NaN; so are sums beyond the largest float: such a row goes to select_fp64.
+        auto any_lane = [&](bool p) {
+            const uint32_t b = __ballot_sync(0xffffffffu, p);
+            return LPT == 32 ? b != 0 : ((b >> (slot * LPT)) & ((1u << (LPT & 31)) - 1u)) != 0;
+        };
+        if (KIND != kKeyLogit) unsure |= any_lane(max_of<NB>(m) == INFINITY);
         auto write_rows = [&]() {
             float* r = rows + lane * ROW;
             if constexpr (PER >= 4) {
@@ -613,6 +620,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                 k0 = fmaxf(k0, o0);
             }
             const float g = KIND != kKeyLogit && a.top2 && k1 != -INFINITY ? k0 + k1 : k0;
+            if (KIND != kKeyLogit && a.top2) unsure |= any_lane(fabsf(g) == INFINITY && k0 != -INFINITY);
             int rank = 0;
             for (int o = 0; o < a.n_groups; ++o) {
                 const float v = __shfl_sync(0xffffffffu, g, o * lpg, LPT);

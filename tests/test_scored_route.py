@@ -252,6 +252,61 @@ def test_large_and_infinite_logits(score, renorm):
         assert bool(((w.double().sum(1) - 1).abs() < 1e-6).all())
 
 
+def few_and_many(l, bias, r, k, T):
+    """check() on the first 48 rows, and row by row the same in a batch of T."""
+    rows = len(l)
+    check(l, bias, r, k)
+    big = l.repeat((T + rows - 1) // rows, 1)[:T].contiguous()
+    idx, w = call(big, bias, r, k)
+    i2, w2 = call(l, bias, r, k)
+    at = torch.arange(T, device="cuda") % rows
+    assert torch.equal(idx, i2[at])
+    assert bool(((w - w2[at]).abs() <= 40 * 2.0 ** -24 * w2[at]).all())
+
+
+@pytest.mark.gpu
+def test_an_infinite_logit_keeps_its_group():
+    """sigmoid(inf) = 1 and no more: its group has the best expert, and is the one kept."""
+    r = m.Router(m.MOE_SCORE_SIGMOID, 8, 1, m.MOE_GROUP_MAX, 1, 1.0)
+    l = torch.zeros(5, 64)
+    for t, e in enumerate((0, 7, 20, 41, 63)):
+        l[t, e] = INF
+    for bias in (torch.zeros(64), None):
+        idx, _ = call(l.cuda(), None if bias is None else bias.cuda(), r, 3)
+        assert idx[:, 0].tolist() == [0, 7, 20, 41, 63]
+    # beside a low bias it is one expert among others
+    bias = torch.zeros(64)
+    bias[20] = -2.0
+    check(l.cuda(), bias.cuda(), r, 3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k,r", ROUTERS)
+@pytest.mark.parametrize("low", [0.0, -3.0, INF])
+def test_infinite_logits_beside_biases(E, k, r, low):
+    """Infinite logits among others, beside biases of which some are zero, far down or +inf."""
+    g = torch.Generator().manual_seed(E + k)
+    l = torch.randn(48, E, generator=g) * 1.7
+    l[torch.rand(48, E, generator=g) < 0.03] = INF
+    l[torch.rand(48, E, generator=g) < 0.1] = -INF
+    bias = torch.randn(E, generator=g) * 0.1
+    bias[torch.rand(E, generator=g) < 0.4] = low
+    few_and_many(l.cuda(), bias.cuda(), r, k, 2500)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k,r", ROUTERS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_biases_whose_sums_pass_the_largest_float(E, k, r, sign):
+    """Two biases of a group add up to more than fp32 holds, and such groups still differ."""
+    g = torch.Generator().manual_seed(E + k)
+    l = torch.randn(48, E, generator=g) * 1.7
+    bias = sign * (1.0 + 2.4 * torch.rand(E, generator=g)) * 1e38
+    few_and_many(l.cuda(), bias.cuda(), r, k, 2500)
+    bias[torch.rand(E, generator=g) < 0.5] = 0.0
+    few_and_many(l.cuda(), bias.cuda(), r, k, 2500)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("score", [m.MOE_SCORE_SIGMOID, m.MOE_SCORE_SOFTMAX])
 @pytest.mark.parametrize("renorm", [0, 1])
