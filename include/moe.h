@@ -170,9 +170,10 @@ MOE_API int moe_route_grouped(const moe_shape_t* shape, int T, int n_groups, int
  *              missing or masked); the best topk_groups groups are kept (ties ->
  *              lower group).  topk_idx[t,0..k-1]: the k largest c of the kept
  *              groups, descending, ties -> lower expert.  The bias moves the
- *              selection and never the weights.  Orders are those of the exact
- *              values: where fp32 cannot tell two c apart they are compared in
- *              fp64.
+ *              selection and never the weights.  Orders are those of c in fp64
+ *              (where two sigmoids above a logit of 37 are equal, say: lower
+ *              expert); with neither a bias nor sums of two, when c orders as the
+ *              logits do, those of the logits, which do not saturate.
  *   weight     topk_w[t,j] = scale * s_j, or with renormalize scale * s_j / sum_i s_i
  *              over the selected (computed relative to the largest, so a row of
  *              tiny scores keeps its ratios).

@@ -113,7 +113,9 @@ __device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int e) {
 }
 
 // One row in fp64 from its logits, k arg-max rounds: rows that fp32 cannot decide, and
-// shapes outside the fast kernel's layout.  c: E doubles of this warp's shared memory.
+// shapes outside the fast kernel's layout.  c: E doubles of this warp's shared memory.  Where
+// the scores order as the logits do (no bias, no sums of two) c stays the logits, as in the fast
+// kernel: a sigmoid is 1 in fp64 too from a logit of 37 on, a softmax's small terms are 0.
 __device__ __noinline__ void select_fp64(const RouteArgs& a, int t, double* c) {
     const int lane = threadIdx.x & 31;
     float mx = -INFINITY;
@@ -129,7 +131,9 @@ __device__ __noinline__ void select_fp64(const RouteArgs& a, int t, double* c) {
             if (c[e] != -INFINITY) den += c[e] == mx ? 1.0 : exp(c[e] - (double)mx);
         den = warp_sum(den);
     }
-    for (int e = lane; e < a.E; e += 32) {
+    // (beside an infinite logit every other softmax is 0: they tie)
+    const bool by_logit = !a.bias && !(a.top2 && a.topk_groups < a.n_groups) && (a.sigmoid || mx < INFINITY);
+    for (int e = lane; e < a.E && !by_logit; e += 32) {
         const double l = c[e];
         if (l == -INFINITY) continue;
         double s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : (l == mx ? 1.0 : exp(l - (double)mx)) / den;

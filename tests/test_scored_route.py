@@ -307,6 +307,38 @@ def test_biases_whose_sums_pass_the_largest_float(E, k, r, sign):
     few_and_many(l.cuda(), bias.cuda(), r, k, 2500)
 
 
+SATURATED = [(64, 4, 8, 2), (64, 32, 8, 4), (64, 32, 1, 1), (256, 8, 8, 4), (1024, 8, 1, 1), (1024, 32, 1, 1), (96, 6, 32, 7),
+             (40, 31, 1, 1), (40, 32, 1, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [m.MOE_SCORE_SIGMOID, m.MOE_SCORE_SOFTMAX])
+@pytest.mark.parametrize("E,k,groups,kept", SATURATED)
+@pytest.mark.parametrize("T", [24, 2500])
+def test_scores_that_saturate(score, E, k, groups, kept, T):
+    """Logits whose scores are equal in fp64, in rows that every path decides: without a bias the
+    logits order them, with one its fp64 sum does, and equal ones go to the lower expert."""
+    g = torch.Generator().manual_seed(E + k)
+    values = torch.tensor([40.0, 41.0, 50.0, 60.0, 100.0, 3.0, 2.0, -1.0, -800.0, -900.0])
+    l = values[torch.randint(0, len(values), (24, E), generator=g)]
+    l[8:16] = torch.where(torch.rand(8, E, generator=g) < 0.9, torch.tensor(40.0), l[8:16])  # more equal ones than candidates
+    l[16:] = torch.where(torch.rand(8, E, generator=g) < 0.9, torch.tensor(-INF), l[16:])  # fewer than k unmasked
+    l[17] = torch.where(l[17] == -INF, l[17], torch.tensor(INF))
+    r = m.Router(score, groups, kept, m.MOE_GROUP_MAX, 1, 1.0)
+    gs = E // groups
+    want = torch.zeros(24, k, dtype=torch.int64)
+    for t, row in enumerate(l.tolist()):
+        best = sorted(range(groups), key=lambda i: (-max(row[i * gs:(i + 1) * gs]), i))[:kept]
+        want[t] = torch.tensor(sorted((e for i in best for e in range(i * gs, (i + 1) * gs)), key=lambda e: (-row[e], e))[:k])
+    big = l.repeat((T + 23) // 24, 1)[:T].contiguous().cuda()
+    at = torch.arange(T) % 24
+    idx, _ = call(big, None, r, k)
+    assert torch.equal(idx.cpu().long(), want[at])
+    for bias in (torch.zeros(E), torch.full((E,), 0.25)):
+        idx, _ = call(big, bias.cuda(), r, k)
+        assert torch.equal(idx.cpu().long(), reference(l, bias, r, k)[0][at])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("score", [m.MOE_SCORE_SIGMOID, m.MOE_SCORE_SOFTMAX])
 @pytest.mark.parametrize("renorm", [0, 1])
