@@ -204,7 +204,8 @@ MOE_API int moe_route_scored(const moe_shape_t* shape, const moe_router_t* route
 /* Gradient of topk_w with respect to the logits, the selection held fixed
  * (select_bias has none).  logits [T,E] fp32 as used by moe_route_scored,
  * topk_idx [T,k] its selection, d_topk_w [T,k] fp32; d_logits [T,E] fp32 is
- * written whole (zeros where there is no gradient; masked logits get 0).
+ * written whole (zeros where there is no gradient; masked logits get 0, and the
+ * d_topk_w of a masked expert, an infinity or NaN too, counts nothing).
  *   d_s_j = scale * d_w_j, or scale / S * (d_w_j - sum_i d_w_i s_i / S);
  *   sigmoid: d_l_j = d_s_j s_j (1 - s_j);  softmax: d_l_e = s_e (d_s_e - sum_i d_s_i s_i).
  * An id outside [0, E) sets the device status and contributes nothing. */

@@ -850,9 +850,10 @@ __global__ void __launch_bounds__(kWarps * 32) scored_backward_kernel(const floa
         const int e = lane < k ? topk_idx[(size_t)t * k + lane] : -1;
         const bool in = e >= 0 && e < E;
         if (lane < k && !in) raise_status(st, kStatusInvalidExpert);
-        const float g = in ? dw[(size_t)t * k + lane] : 0.0f;
         const float l = in ? masked_logit(row[e]) : -INFINITY;
         const bool live = l != -INFINITY;
+        // (a masked expert's weight is 0 whatever the logits: what its dw holds stays out of the row's sums)
+        const float g = live ? dw[(size_t)t * k + lane] : 0.0f;
         if (!dense) {
             const float rest = sigmoid && live ? 1.0f / (1.0f + expf(l)) : 1.0f;  // 1 - sigmoid(l)
             float d;

@@ -367,6 +367,30 @@ def test_gradient_against_differences(score, renorm):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", [m.MOE_SCORE_SIGMOID, m.MOE_SCORE_SOFTMAX])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_gradients_of_masked_experts_stay_out(score, renorm):
+    """Masked experts among the selected, with infinities and NaN for their weights' gradients."""
+    E, k, T = 64, 6, 30
+    r = m.Router(score, 1, 1, m.MOE_GROUP_MAX, renorm, 1.5)
+    g = torch.Generator().manual_seed(4)
+    l = torch.randn(T, E, generator=g)
+    for t in range(T):
+        l[t, torch.randperm(E, generator=g)[:E - t % (k + 1)]] = -INF if t % 2 else float("nan")
+    l = l.cuda()
+    idx, _ = call(l, None, r, k)
+    dw = torch.randn(T, k, generator=g).cuda()
+    lk = l.gather(1, idx.long())
+    masked = torch.isnan(lk) | (lk == -INF)
+    assert bool(masked.any()) and not bool(masked.all())
+    want, got = torch.empty(T, E, device="cuda"), torch.empty(T, E, device="cuda")
+    m.moe_route_scored_backward(shape_of(E, k), r, T, l, idx, dw.masked_fill(masked, 0.0), want)
+    for bad in (float("nan"), INF):
+        m.moe_route_scored_backward(shape_of(E, k), r, T, l, idx, dw.masked_fill(masked, bad), got)
+        assert torch.equal(got, want) and bool((got[torch.isnan(l) | (l == -INF)] == 0).all())
+
+
+@pytest.mark.gpu
 def test_no_bias_softmax_agrees_with_moe_route():
     E, k, T = 256, 8, 100
     l = (torch.randn(T, E, generator=torch.Generator().manual_seed(1)) * 2).cuda()
