@@ -72,8 +72,10 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The same where nothing written before it is read after it by another CTA: what it holds
-// back is the reuse or the end of shared memory that has been read.  (A release waits for
-// the stores to global memory, 1.4 us at the end of a rank product.)
+// back is the reuse or the end of shared memory that has been read.  Every load from a peer
+// before it has to be used before it, too (here: stored), as only that says that the load is
+// over: none is issued whose value is then dropped.  (A release waits for the stores to
+// global memory, 1.4 us at the end of a rank product.)
 __device__ __forceinline__ void cluster_sync_read() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -798,6 +800,8 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         const int p0 = (int)((long)quads * rank / S), p1 = (int)((long)quads * (rank + 1) / S);
         if (!*abort_flag)
             for (int p = p0 + threadIdx.x; p < p1; p += kThreads) {
+                const int feat = m0 + (p & 31) * 4;
+                if (feat >= a.O) continue;  // (O % 8 == 0: the four are valid together)
                 const uint32_t addr = stage_u + p * 16;
                 float4 f[8];
 #pragma unroll
@@ -812,8 +816,6 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                         y.z += f[s].z;
                         y.w += f[s].w;
                     }
-                const int feat = m0 + (p & 31) * 4;
-                if (feat >= a.O) continue;  // (O % 8 == 0: the four are valid together)
                 const size_t at = (size_t)(row0 + (p >> 5)) * a.O + feat;
                 if (a.out_fp32) {
                     *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = y;
@@ -1736,9 +1738,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_cons
             float f[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) f[j] = 0.0f;
-            for (int s = 0; s < S; ++s)
+            // (only what is stored is read: see cluster_sync_read)
+            for (int s = 0; s < S && f0 + feat < F; ++s)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] += ld_peer(stage_u + ((g * 16 + j) * 256 + feat) * 4, s);
+                for (int j = 0; j < 16; ++j)
+                    if (g * 16 + j < a.r) f[j] += ld_peer(stage_u + ((g * 16 + j) * 256 + feat) * 4, s);
             store16(f0 + feat, g * 16, f);
         }
         cluster_sync_read();

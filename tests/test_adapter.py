@@ -212,6 +212,28 @@ def test_short_contractions_with_few_of_many_adapters(T, C, r, n, ids):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r,n", [(7, 2056, 136, 8, 2), (150, 1160, 2184, 72, 1), (520, 2312, 264, 24, 1)])
+def test_shared_sums_past_the_last_feature_and_rank(T, K, N, r, n):
+    """Clusters whose CTAs read one another's sums, where tiles reach past the features and the rank:
+    call after call the same."""
+    c = Case(T, K, N, r, n, "one")
+    ref = c.reference()
+    x, w, a, b, s, of, dy = (t.cuda() for t in (c.x, c.w, c.a, c.b, c.s, c.of, c.dy))
+    ws, outs = scratch(c.p, T), []
+    new = lambda *shape: torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    for _ in range(10):
+        y, v, dx, da, db = new(T, N), new(T, r), new(T, K), new(n, r, K), new(n, N, r)
+        m.moe_adapter_project(c.p, T, x, w, a, b, s, of, y, v, ws)
+        m.moe_adapter_project_backward(c.p, T, dy, x, w, a, b, s, of, v, dx, da, db, ws)
+        outs.append((y, v, dx, da, db))
+    assert m.moe_check_status() == 0
+    for out in outs:
+        assert all(torch.equal(p, q) for p, q in zip(out, outs[0]))
+    for name, got in zip(("y", "v", "dx", "da", "db"), outs[0]):
+        close(got, *ref[name], name=name)
+
+
+@pytest.mark.gpu
 def test_very_long_batches():
     """More 64-token chunks than the gradient kernel lists at a time (262144 tokens)."""
     c = Case(270001, 16, 24, 8, 3, "runs")
