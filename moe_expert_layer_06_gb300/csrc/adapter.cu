@@ -37,10 +37,6 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
     return w;
 }
 
-__device__ __forceinline__ void named_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // One lane of the (converged) warp.  TMA and UMMA operands have to sit in uniform
 // registers: where the whole warp runs a loop and only the issue is guarded this way, they
 // stay there (a loop inside `if (lane == 0)` took 540 cycles more per K chunk).
@@ -164,13 +160,13 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t addr, uint32_t rank) {
 
 // The tile's adapter ids (-1: none) and the list of distinct ones, ascending; *count
 // their number.  `n_threads` threads call it (tid 0..), synchronised by barrier `bar`;
-// `bits` holds kMaxAdapters bits.
-__device__ __forceinline__ void tile_adapters(const int32_t* adapter_of, int row0, int rows, int n_adapters, int bn,
+// `bits` holds kMaxAdapters bits.  False on all of them, and nothing written, if one is not `ready`.
+__device__ __forceinline__ bool tile_adapters(const int32_t* adapter_of, int row0, int rows, int n_adapters, int bn,
                                               int* ids, int* list, uint32_t* bits, int* count, const DevStatus& st,
-                                              int tid, int n_threads, int bar) {
+                                              int tid, int n_threads, int bar, bool ready = true) {
     const int words = (n_adapters + 31) / 32;
     for (int i = tid; i < words; i += n_threads) bits[i] = 0;
-    named_sync(bar, n_threads);
+    if (!named_and(bar, n_threads, ready)) return false;
     for (int i = tid; i < bn; i += n_threads) {
         int id = -1;
         if (i < rows) {
@@ -206,6 +202,7 @@ __device__ __forceinline__ void tile_adapters(const int32_t* adapter_of, int row
         if (tid == 0) *count = base;
     }
     named_sync(bar, n_threads);
+    return true;
 }
 
 struct ProjArgs {
@@ -698,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         __syncwarp();
         mbar_wait(smem_u32(done), 0, limit);
     } else if (warp < 6) {
-        // ---- adapter lists and v chunks
+        // ---- adapter lists and v chunks (one verdict on each wait: the four warps leave together)
         const int tid = threadIdx.x - 64;  // 0..127
         bool ok = true;
         int stage = 0;
@@ -706,12 +703,11 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
             const int row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             TileList& tl = lists[n & 1];
-            if (*abort_flag || !mbar_wait(smem_u32(&lfree[n & 1]), ((n >> 1) & 1) ^ 1, limit)) {
-                ok = false;
+            const bool ready = !*abort_flag && mbar_wait(smem_u32(&lfree[n & 1]), ((n >> 1) & 1) ^ 1, limit);
+            for (int q = tid; q < kMaxExtra / 32 && ready; q += 128) tl.odd[q] = 0;
+            if (!(ok = tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st,
+                                     tid, 128, 1, ready)))
                 break;
-            }
-            for (int q = tid; q < kMaxExtra / 32; q += 128) tl.odd[q] = 0;
-            tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st, tid, 128, 1);
             if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
             stage = (stage + c1 - c0) % stages;
             const int n_ext = pk.chunks(tl.count);
@@ -723,17 +719,15 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
                 const int first_of = pk.first(e, tl.count), j0 = pk.j0(e, tl.count);
                 if (j0 != held) vr.load(a, row0, held = j0, tid);
                 // the adapter tile has landed: the stage is free of its last use, too
-                if (*abort_flag || !mbar_wait(smem_u32(&landed[stage]), (land_phase >> stage) & 1u, limit)) {
-                    ok = false;
-                    break;
-                }
+                const bool here = !*abort_flag && mbar_wait(smem_u32(&landed[stage]), (land_phase >> stage) & 1u, limit);
                 land_phase ^= 1u << stage;
-                uint8_t* st_a = smem + stage * C::kStageBytes;
-                uint8_t* sb = st_a + kABytes;
-                vr.store(sb, a.bn, first_of, pk.per, tid);
-                if (take_odd<BWD>(st_a, pk.n(e, tl.count) * pk.seg, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
-                fence_async_smem();
-                named_sync(1, 128);
+                if (here) {
+                    uint8_t* st_a = smem + stage * C::kStageBytes;
+                    vr.store(st_a + kABytes, a.bn, first_of, pk.per, tid);
+                    if (take_odd<BWD>(st_a, pk.n(e, tl.count) * pk.seg, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
+                    fence_async_smem();
+                }
+                if (!(ok = named_and(1, 128, here))) break;
                 if (tid == 0) mbar_arrive(smem_u32(&full[stage]));
                 if (++stage == stages) stage = 0;
             }
@@ -747,10 +741,9 @@ __global__ void __launch_bounds__(kThreads, BN <= 64 ? 2 : 1) project_kernel(con
         for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
             const int m0 = (i % m_tiles) * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             const TileList& tl = lists[n & 1];
-            if (*abort_flag || !mbar_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, limit)) {
-                ok = false;
-                break;
-            }
+            ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit);
+            if (C::kCopyOut) ok = named_and(2 + (q >> 1), 64, ok);  // (the two warps that share drain_tile's barrier)
+            if (!ok) break;
             tc_fence_after();
             // (the MMA warp read the list before its last commit)
             const int feat = m0 + q * 32 + lane;
@@ -1069,12 +1062,11 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
         for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
             const int row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             TileList& tl = lists[n & 1];
-            if (*abort_flag || !mbar_wait(smem_u32(&lfree[n & 1]), ((n >> 1) & 1) ^ 1, limit)) {
-                ok = false;
+            const bool ready = !*abort_flag && mbar_wait(smem_u32(&lfree[n & 1]), ((n >> 1) & 1) ^ 1, limit);
+            for (int q = tid; q < kMaxExtra / 32 && ready; q += 128) tl.odd[q] = 0;
+            if (!(ok = tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st,
+                                     tid, 128, 1, ready)))
                 break;
-            }
-            for (int q = tid; q < kMaxExtra / 32; q += 128) tl.odd[q] = 0;
-            tile_adapters(a.adapter_of, row0, rows, a.n_adapters, a.bn, tl.ids, tl.list, bits, &tl.count, a.st, tid, 128, 1);
             if (tid == 0) mbar_arrive(smem_u32(&listed[n & 1]));
             stage = (stage + kc) % kPairStages;
             const int n_ext = pk.chunks(tl.count);
@@ -1085,16 +1077,15 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             for (int e = 0; e < n_ext; ++e) {
                 const int first_of = pk.first(e, tl.count), j0 = pk.j0(e, tl.count);
                 if (j0 != held) vr.load(a, row0 + rank * half, held = j0, tid);
-                if (*abort_flag || !mbar_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, limit)) {
-                    ok = false;
-                    break;
-                }
+                const bool here = !*abort_flag && mbar_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, limit);
                 land_phase ^= 1u << stage;
-                uint8_t* st_a = smem + stage * kPairStageBytes;
-                vr.store(st_a + kABytes, half, first_of, pk.per, tid);
-                if (take_odd<BWD>(st_a, pk.n(e, tl.count) * pk.seg, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
-                fence_async_smem();
-                named_sync(1, 128);
+                if (here) {
+                    uint8_t* st_a = smem + stage * kPairStageBytes;
+                    vr.store(st_a + kABytes, half, first_of, pk.per, tid);
+                    if (take_odd<BWD>(st_a, pk.n(e, tl.count) * pk.seg, tid)) atomicOr(&tl.odd[e >> 5], 1u << (e & 31));
+                    fence_async_smem();
+                }
+                if (!(ok = named_and(1, 128, here))) break;
                 if (tid == 0) mbar_arrive(full_u + stage * 8);
                 if (++stage == kPairStages) stage = 0;
             }
@@ -1108,9 +1099,9 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
             const int m0 = (i % m_tiles) * 256 + rank * 128, row0 = (i / m_tiles) * a.bn, rows = min(a.bn, a.T - row0);
             const TileList& tl = lists[n & 1];
             // (in the leader the product warp has read the list before its last commit)
-            if (!(ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit)) ||
-                !(ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit)))
-                break;
+            ok = warp_wait(smem_u32(&listed[n & 1]), (n >> 1) & 1, abort_flag, limit) &&
+                 warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit);
+            if (!(ok = named_and(2 + (q >> 1), 64, ok))) break;  // (the two warps that share drain_tile's barrier)
             tc_fence_after();
             const int feat = m0 + q * 32 + lane;
             const int n_ext = pk.chunks(tl.count);
@@ -1401,7 +1392,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
             __syncwarp();
         } else {
             // each token's own columns into this CTA's share, [column][token]
-            if (ok) ok = mbar_wait(smem_u32(tfull), acc_phase, limit) && !*abort_flag;
+            if (ok) ok = __all_sync(0xffffffffu, warp_wait(smem_u32(tfull), acc_phase, abort_flag, limit) && !*abort_flag);
             if (ok) {
                 tc_fence_after();
                 const int q = warp & 3, row = q * 32 + lane;
@@ -1637,13 +1628,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_cons
             }
         } else {
             const int tid = threadIdx.x - 64;
-            for (int q = q0; q < cnt && ok; q += S) {
-                if (!(ok = warp_wait(landed_u + stage * 8, phase, abort_flag, limit))) break;
+            // (to the end of the list whatever happens: the barrier is for all four warps)
+            for (int q = q0; q < cnt; q += S) {
+                if (ok && !(ok = warp_wait(landed_u + stage * 8, phase, abort_flag, limit))) *abort_flag = 1;
                 if (list[q] & 0x8000) {
                     const int t0 = (seg + (list[q] & 0x7fff)) * 64;
                     uint8_t* sz = smem + stage * C::kStageBytes;
                     // 8 threads per token row; the 128-byte rows of all blocks
-                    for (int row = tid >> 3; row < 64; row += 16) {
+                    for (int row = tid >> 3; row < 64 && ok; row += 16) {
                         if (t0 + row < a.T && a.adapter_of[t0 + row] == id) continue;
 #pragma unroll
                         for (int b = 0; b < 4 + RB; ++b)
@@ -1652,7 +1644,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_cons
                     fence_async_smem();
                     named_sync(1, 128);
                 }
-                if (tid == 0) mbar_arrive(full_u + stage * 8);
+                if (tid == 0 && ok) mbar_arrive(full_u + stage * 8);
                 if (++stage == C::kStages) {
                     stage = 0;
                     phase ^= 1;
@@ -1675,7 +1667,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_cons
         __syncwarp();
         mbar_wait(smem_u32(done), 0, limit);
     } else {
-        ok = mbar_wait(smem_u32(done), 0, limit) && !*abort_flag;
+        // (the same for every lane, with its warp's loads and shuffles below)
+        ok = __all_sync(0xffffffffu, warp_wait(smem_u32(done), 0, abort_flag, limit) && !*abort_flag);
     }
     __syncwarp();
     tc_fence_before();

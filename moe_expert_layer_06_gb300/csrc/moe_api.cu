@@ -709,14 +709,23 @@ static int plan_replicas_host(const moe_shape_t* s, const int32_t* counts, int n
 }
 
 // ------------------------------------------------------------------ failure-path probe
-__global__ void expire_wait_kernel(DevStatus st) {
-    __shared__ __align__(8) uint64_t bar;
+// Half of a group of four warps waits for a phase that never completes, half for one that has:
+// they decide together, and the status says so if every one of them gave up.
+__global__ void __launch_bounds__(128) expire_wait_kernel(DevStatus st) {
+    __shared__ __align__(8) uint64_t bar[2];
+    __shared__ int gave_up;
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&bar), 1);
+        mbar_init(smem_u32(&bar[0]), 1);  // nothing arrives on this one
+        mbar_init(smem_u32(&bar[1]), 1);
         fence_mbar_init();
-        // phase 0 never completes: nothing arrives on this barrier
-        if (!mbar_wait(smem_u32(&bar), 0, st.limit_ns)) raise_status(st, kStatusWaitTimeout);
+        gave_up = 0;
+        mbar_arrive(smem_u32(&bar[1]));
     }
+    __syncthreads();
+    const bool here = mbar_wait(smem_u32(&bar[threadIdx.x & 1]), 0, st.limit_ns);
+    if (!named_and(1, 128, here)) atomicAdd(&gave_up, 1);
+    named_sync(1, 128);
+    if (threadIdx.x == 0 && gave_up == 128) raise_status(st, kStatusWaitTimeout);
 }
 
 int api_fail(int code, const char* fmt, ...) {
@@ -781,7 +790,7 @@ int moe_debug_expire_wait(void* stream) {
     DevStatus st;
     int rc = device_status(&st);
     if (rc) return rc;
-    expire_wait_kernel<<<1, 32, 0, as_stream(stream)>>>(st);
+    expire_wait_kernel<<<1, 128, 0, as_stream(stream)>>>(st);
     MOE_CUDA(cudaGetLastError(), "expire-wait launch");
     return MOE_OK;
 }

@@ -36,6 +36,28 @@ inline cudaError_t launch_pdl_cluster(void (*kern)(Params...), dim3 grid, dim3 b
 // Order this thread's shared-memory writes before later reads by the async proxy (TMA, UMMA).
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Barrier `id` of `threads` threads (whole warps).
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The same with a verdict of each thread: true on all of them if it was on every one.  Threads
+// that share a barrier and wait for something with a limit decide this way whether they go on:
+// one that left on its own would keep the others in their next barrier, which has no limit.
+__device__ __forceinline__ bool named_and(int id, int threads, bool ok) {
+    uint32_t all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)ok), "r"(id), "r"(threads)
+        : "memory");
+    return all != 0;
+}
+
 // Shared-memory matrix descriptor of an MN-major operand tile written by TMA with
 // 128-byte swizzle: K rows of 128 B (64 bf16 of M or N), 8-row groups 1024 B apart,
 // blocks of 64 of M or N `block_bytes` apart.
