@@ -1273,7 +1273,9 @@ constexpr int kShrinkExtra = 1024 + 256 + 128 * 8 + kMaxAdapters / 8;
 // An allocation of tensor memory waits until the columns are free.  It must not wait for a
 // kernel that waits for its own, nor for a CTA that waits for this one's cluster, so
 // whatever shares an SM fits its 512 columns at the same time:
-//  - a kernel lets the next one start only when its CTAs have their columns;
+//  - the rank product, the first kernel of a call, takes its columns when the kernel before has
+//    ended, whatever that was (the layer's GEMM starts the next kernel before it has its own);
+//  - the kernels of a call let the next one start only when their CTAs have their columns;
 //  - at most two of these CTAs (256 columns each) are on an SM, none beside one that holds
 //    all 512: a short ring is filled up to a third of an SM's shared memory and more.
 constexpr int kShrinkLeast = 77 * 1024;
@@ -1318,11 +1320,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
         tma_prefetch_desc(&a.x);
         tma_prefetch_desc(&a.m);
     }
+    pdl_wait();
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), 256);
         tmem_relinquish();
     }
-    pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

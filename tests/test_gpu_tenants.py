@@ -107,6 +107,21 @@ def test_replays_from_a_graph_and_changes_tenants():
     assert m.moe_check_status() == 0
 
 
+@pytest.mark.parametrize("T", [70, 300])
+def test_layers_one_after_another(T):
+    """The rank product may start while the layer's GEMM before it runs, and that GEMM while the call
+    before ends: pass after pass the same."""
+    w, ad, t = inputs(T)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    down, buf = shared_down_matrix(d["sd"]), Buffers(w, ad, T)
+    outs = [torch.empty(T, w.hidden, dtype=torch.bfloat16, device=DEV) for _ in range(20)]
+    for out in outs:
+        tenant_forward(w, ROUTER, ad, T, d["x"], d["wr"], d["bias"], d["wg"], d["wu"], d["wd"], d["sg"], d["su"], down,
+                       d["a"], d["b"], d["s"], d["of"], out, buf)
+    assert m.moe_check_status() == 0
+    assert all(torch.equal(o, outs[0]) for o in outs) and bool(torch.isfinite(outs[0].float()).all())
+
+
 def test_sizes_that_do_not_belong_together_are_refused():
     w, ad, t = inputs(4)
     with pytest.raises(ValueError, match="features"):
