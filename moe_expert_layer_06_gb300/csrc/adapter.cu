@@ -1903,16 +1903,16 @@ int project(const moe_adapter_t* p, int T, const void* tokens, const void* w, co
     a.bn = plan.bn;
     a.splits = plan.splits;
     a.v_ready = v_ready;
-    int rc = make_tmap_3d(&a.w, w, K, N, 1, K * 2, K * N * 2, 64, BWD ? 64 : 128, 1);
+    int rc = make_tmap_rows(&a.w, w, K, N, 1, K * 2, K * N * 2, 64, BWD ? 64 : 128, 1);
     if (rc) return rc;
     const uint32_t seg = a.r <= 16 ? 16 : a.r <= 32 ? 32 : 64;  // (as Packing)
-    if (BWD) rc = make_tmap_3d(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, seg, 1);
-    else rc = make_tmap_3d_swizzled(&a.lr, lr, r, N, n, r * 2, r * N * 2, seg, 128, 1, seg * 2);
+    if (BWD) rc = make_tmap_rows(&a.lr, lr, K, r, n, K * 2, K * r * 2, 64, seg, 1);
+    else rc = make_tmap_rows(&a.lr, lr, r, N, n, r * 2, r * N * 2, seg, 128, 1, seg * 2);
     if (rc) return rc;
     const uint64_t C = a.C;
-    if ((rc = make_tmap_3d(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.pair ? plan.bn / 2 : plan.bn))) return rc;
+    if ((rc = make_tmap_rows(&a.x, tokens, C, 1, (uint64_t)T, C * 2, C * 2, 64, 1, plan.pair ? plan.bn / 2 : plan.bn))) return rc;
     const uint64_t O = a.O;
-    if (!out_fp32 && (rc = make_tmap_3d(&a.y, out, O, 1, (uint64_t)T, O * 2, O * 2, 64, 1, 16))) return rc;
+    if (!out_fp32 && (rc = make_tmap_rows(&a.y, out, O, 1, (uint64_t)T, O * 2, O * 2, 64, 1, 16))) return rc;
     a.lr_ptr = static_cast<const uint16_t*>(lr);
     a.adapter_of = adapter_of;
     a.v = static_cast<const uint16_t*>(v);
@@ -1942,12 +1942,12 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
     } else {
         ShrinkArgs a;
         const uint64_t c = C, r = p->rank, n = p->n_adapters;
-        int rc = make_tmap_3d(&a.x, tokens, c, 1, (uint64_t)T, c * 2, c * 2, 64, 1, 128);
+        int rc = make_tmap_rows(&a.x, tokens, c, 1, (uint64_t)T, c * 2, c * 2, 64, 1, 128);
         if (rc) return rc;
         a.cols = BWD ? (p->rank + 63) / 64 * 64 : (p->rank + 15) / 16 * 16;
         a.per_pass = 256 / a.cols;
-        if (BWD) rc = make_tmap_3d(&a.m, m, r, c, n, r * 2, r * c * 2, 64, 64, 1);
-        else rc = make_tmap_3d(&a.m, m, c, r, n, c * 2, c * r * 2, 64, a.cols, 1);
+        if (BWD) rc = make_tmap_rows(&a.m, m, r, c, n, r * 2, r * c * 2, 64, 64, 1);
+        else rc = make_tmap_rows(&a.m, m, c, r, n, c * 2, c * r * 2, 64, a.cols, 1);
         if (rc) return rc;
         a.scaling = scaling;
         a.adapter_of = adapter_of;
@@ -1999,10 +1999,10 @@ int gradients(const moe_adapter_t* p, int T, const void* dy, const void* x, cons
     GradArgs a;
     const uint64_t K = p->in_features, N = p->out_features, r = p->rank, t = T;
     int rc;
-    if ((rc = make_tmap_3d(&a.z[0], x, K, t, 1, K * 2, K * t * 2, 64, 64, 1)) ||
-        (rc = make_tmap_3d(&a.z[1], dy, N, t, 1, N * 2, N * t * 2, 64, 64, 1)) ||
-        (rc = make_tmap_3d(&a.u[0], dv, r, t, 1, r * 2, r * t * 2, 64, 64, 1)) ||
-        (rc = make_tmap_3d(&a.u[1], v, r, t, 1, r * 2, r * t * 2, 64, 64, 1)))
+    if ((rc = make_tmap_rows(&a.z[0], x, K, t, 1, K * 2, K * t * 2, 64, 64, 1)) ||
+        (rc = make_tmap_rows(&a.z[1], dy, N, t, 1, N * 2, N * t * 2, 64, 64, 1)) ||
+        (rc = make_tmap_rows(&a.u[0], dv, r, t, 1, r * 2, r * t * 2, 64, 64, 1)) ||
+        (rc = make_tmap_rows(&a.u[1], v, r, t, 1, r * 2, r * t * 2, 64, 64, 1)))
         return rc;
     a.adapter_of = adapter_of;
     a.T = T;

@@ -98,7 +98,8 @@ static EncodeTiledFn encode_fn() {
 }
 
 static int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-                          uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8, int swizzle_bytes) {
+                          uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8, int swizzle_bytes,
+                          bool narrow) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     const cuuint64_t dims[3] = {d0, d1, d2};
@@ -111,8 +112,7 @@ static int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint6
                     swizzle_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
                     : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                           : CU_TENSOR_MAP_SWIZZLE_128B,
-                    // (rows that do not start on lines: a wider fetch brings in more that the box does not read)
-                    stride2 % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return MOE_OK;
@@ -120,12 +120,14 @@ static int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint6
 
 int make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                  uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8) {
-    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, fp8, 128);
+    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, fp8, 128, false);
 }
 
-int make_tmap_3d_swizzled(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-                          uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, int swizzle_bytes) {
-    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, false, swizzle_bytes);
+int make_tmap_rows(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                   uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, int swizzle_bytes) {
+    const uint64_t pitch = d1 > 1 ? stride1 : stride2;
+    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, false, swizzle_bytes,
+                          pitch % 128 != 0 && d0 > box0);
 }
 
 // weight stack [n][rows][K] -> dims {K, rows, n}, box {64, 128, 1}
