@@ -30,10 +30,11 @@ __device__ __forceinline__ float bf(uint16_t u) { return __uint_as_float((uint32
 
 __device__ __forceinline__ uint16_t to_bf(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-// Two bf16 in a word, infinities and NaN among them set to zero.
+// Two bf16 in a word, infinities and NaN among them replaced by 1 of their sign: beside the
+// infinity that is added later it is lost, and times an infinite v it is that infinity already.
 __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    if ((w & 0x7f80u) == 0x7f80u) w = (w & 0xffff8000u) | 0x3f80u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w = (w & 0x8000ffffu) | 0x3f800000u;
     return w;
 }
 
@@ -336,9 +337,9 @@ __device__ __forceinline__ int adapter_step(int q, const Packing& pk) {
     return pk.per == 4 ? q * 256 : pk.per == 2 ? (q >> 1) * 512 + (q & 1) * 2 : q * 2;
 }
 
-// Zero times an infinity or NaN of an adapter would reach the other adapters' tokens: such
-// elements leave its tile here (true: there were some) and are added to their own tokens
-// in the epilogue.  Only the columns that were copied are looked at: the rest of a stage,
+// Zero times an infinity or NaN of an adapter would reach the other adapters' tokens: ones take
+// the places of such elements in its tile here (true: there were some), and what they are is
+// added to their own tokens in the epilogue.  Only the columns that were copied are looked at: the rest of a stage,
 // which no product reads, holds what was there before.
 template <bool BWD>
 __device__ __forceinline__ bool take_odd(uint8_t* st_a, int columns, int tid) {

@@ -335,6 +335,31 @@ def test_infinities_and_nan_stay_with_their_own_request(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,r", [(5, 16), (64, 72), (300, 72), (2100, 24)])
+def test_infinite_products_of_infinities(T, r):
+    """A rank product beyond the largest float meets an infinity of its adapter: an infinity of the
+    product's sign, and no NaN."""
+    c = Case(T, 264, 4616, r, 4, "each", seed=5)
+    c.of[T // 2] = 1
+    t, l = T // 2, r - 3
+    c.w[:, 0], c.w[0], c.x[:, 0], c.dy[:, 0] = 0, 0, 0, 0
+    c.a[1, :, 0], c.b[1, 0] = 0, 0
+    c.x[t, 0], c.a[1, l, 0] = 1e30, 1e20      # v[t, l] = inf
+    c.dy[t, 0], c.b[1, 0, l] = 1e30, 1e20     # dv[t, l] = inf
+    c.b[1, 5, l], c.b[1, 9, l] = float("inf"), -float("inf")
+    c.a[1, l, 5], c.a[1, l, 9] = float("inf"), -float("inf")
+    for z in (c.x, c.dy):                     # v[l] and dv[l] of all the adapter's tokens are inf, too
+        z[:, 5], z[:, 9] = 1, -1
+    y, v = c.forward()
+    dx, _, _ = c.backward(v)
+    mine = (c.of == 1).cuda()
+    assert bool((v[mine][:, l] == float("inf")).all())
+    for got in (y, dx):
+        assert bool((got[mine][:, 5] == float("inf")).all()) and bool((got[mine][:, 9] == -float("inf")).all())
+        assert bool(torch.isfinite(got[~mine].float()).all())
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences():
     """The function is linear in x, in A (through v) and in B: f(z + h d) - f(z - h d) = 2 h <grad, d>.
     In fp64 from the definition with the kernel's gradients, each off by its tolerance."""
