@@ -1968,7 +1968,7 @@ int shrink(const moe_adapter_t* p, int T, const void* tokens, const void* m, con
         a.passes = std::min((most + a.per_pass - 1) / a.per_pass, beside);
         // a stage per chunk of the CTA's share at most (and room for its sums)
         const int pass_cols = std::min(a.per_pass, p->n_adapters) * a.cols, share = (kc + a.splits - 1) / a.splits;
-        a.ring = std::min(kShrinkRing, std::max(share * (16384 + pass_cols * 128), (p->rank + 15) / 16 * 16 * 512));
+        a.ring = (int)std::min<long>(kShrinkRing, std::max((long)share * (16384 + pass_cols * 128), (p->rank + 15L) / 16 * 16 * 512));
         a.ring = (a.ring + 1023) / 1024 * 1024;
         auto kern = shrink_kernel<BWD>;
         static std::atomic<uint64_t> configured{0};

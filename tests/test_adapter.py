@@ -261,6 +261,24 @@ def test_offsets_beyond_32_bits():
 
 
 @pytest.mark.gpu
+def test_a_contraction_whose_copies_pass_32_bits():
+    """A share of the contraction of more than 2^31 bytes of copies; all but 64 of its features are zero."""
+    T, K, N, r = 65, 59_700_000, 8, 8
+    c = Case(T, 64, N, r, 1, "one")
+    at = torch.cat([torch.arange(32), torch.arange(K - 32, K)])
+    big = []
+    for t in (c.x, c.w, c.a):
+        z = torch.zeros(*t.shape[:-1], K, dtype=torch.bfloat16, device="cuda")
+        z[..., at.cuda()] = t.cuda()
+        big.append(z)
+    p = m.Adapter(K, N, 1, r)
+    y = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    m.moe_adapter_project(p, T, big[0], big[1], big[2], c.b.cuda(), c.s.cuda(), c.of.cuda(), y, None, scratch(p, T))
+    assert m.moe_check_status() == 0
+    close(y, *c.reference()["y"])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_no_adapters_no_scaling_and_fp32_output(T):
     c = Case(T, 264, 392, 16, 4, "none", scaled=False)
