@@ -117,9 +117,10 @@ MOE_API int moe_check_status(void* stream);
  * any device; default 2e9.  Returns MOE_ERR_INVALID_ARG for 0. */
 MOE_API int moe_set_wait_limit_ns(uint64_t ns);
 
-/* Launch one kernel whose bounded wait is on a barrier nothing completes: it
- * gives up after the current wait limit and sets the timeout status, which
- * moe_check_status() then reports.  For tests of the failure path only. */
+/* Launch one kernel half of whose threads wait on a barrier nothing completes:
+ * they give up after the current wait limit, all of them leave together, and the
+ * kernel sets the timeout status, which moe_check_status() then reports.  For
+ * tests of the failure path only. */
 MOE_API int moe_debug_expire_wait(void* stream);
 
 /* ---------------------------------------------------------------- step 1: route

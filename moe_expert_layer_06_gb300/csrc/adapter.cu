@@ -3,6 +3,10 @@
 // and the gradients of x, A and B (W is frozen):
 //   dv_t = s_i B_i^T dy_t,  dx_t = W^T dy_t + A_i^T dv_t,
 //   dA_i = sum dv_t x_t^T,  dB_i = sum dy_t v_t^T.
+// v and dv are summed in fp32 and rounded to bf16 once, as they are tensor-core operands beside
+// bf16 A and B: 2^-8 of a value at most, which takes the error of y against 64 bits from 1.7e-3
+// (its own rounding) to 1.8e-3 - 2.2e-3 where the adapter adds half as much as W does, and that of
+// the gradients to 2.3e-3.
 //
 // The projection is a swap-AB tcgen05 GEMM (weight rows are the 128-row UMMA A
 // operand, tokens the N operand).  The adapters ride along as extra K chunks of
@@ -1241,7 +1245,7 @@ __global__ void __launch_bounds__(256, 3) shrink_few_kernel(const uint16_t* x, c
             float f = 0.0f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) f += part[w][q][j];
-            v[(size_t)mine[q0 + q] * r + j0 + j] = to_bf(f * scale);
+            v[(size_t)mine[q0 + q] * r + j0 + j] = to_bf(f * scale);  // (the one rounding of v)
         }
     }
 }
@@ -1444,7 +1448,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) shrink_kernel(const __grid_
                     f[j] += S > 1 ? ld_peer(addr + j * 512, s) : reinterpret_cast<const float*>(smem)[(j0 + j) * 128 + row];
             uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j)  // (the one rounding of v or dv)
                 w[j] = (uint32_t)to_bf(f[2 * j] * scale) | ((uint32_t)to_bf(f[2 * j + 1] * scale) << 16);
             *reinterpret_cast<uint4*>(a.v + (size_t)(row0 + row) * a.r + j0) = make_uint4(w[0], w[1], w[2], w[3]);
         }

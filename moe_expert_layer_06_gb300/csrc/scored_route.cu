@@ -8,7 +8,7 @@
 // candidates are ranked against one another, so the cost hardly grows with k.
 // The selection is made on fp32 values whose error is bounded; a row where two
 // values that decide the selection or its order lie within that bound of one
-// another is decided again in fp64 (about one row in a thousand).
+// another is decided again in fp64 (about one row in a thousand), as is a row with values of +inf.
 #include <float.h>
 #include <math.h>
 
@@ -394,12 +394,13 @@ __host__ __device__ __forceinline__ int warp_smem(int E, int row) {
     return b > d ? b : d;
 }
 
-// LPT lanes per token, 32 / LPT tokens per warp.  What bounds it is issuing instructions:
-// most of a token's (threshold, ranking, weights) cost the same for one token per warp or
-// four, and the ones per expert are kept to the score and three more: a maximum of
-// blocks, a comparison with the threshold and its bit.  Measured: 65536 x 256 sigmoids in
-// 8 groups 50 us (430 instructions a token, issued in 53% of the cycles; 29 us where the
-// logits decide), 8192 x 1024 softmax with a bias 29 us, one token 4.2 us.
+// LPT lanes per token, 32 / LPT tokens per warp.  Its time is instructions and the latency
+// between them: 430 a token (65536 x 256 sigmoids in 8 groups), 23 us of the 51 if every cycle
+// issued one; 16 warps an SM, all that 128 registers allow, issue in 53% of them.  Most of a
+// token's (threshold, ranking, weights) cost the same for one token per warp or four, and the
+// ones per expert are kept to the score and three more: a maximum of blocks, a comparison with
+// the threshold and its bit.  Measured: 65536 x 256 51 us (29 where the logits decide), 8192 x
+// 1024 softmax with a bias 30 us, one token 4.2 us.
 template <int LPT, int PER, int KIND>
 __global__ void __launch_bounds__(kWarps * 32)
     scored_topk_kernel(const __grid_constant__ RouteArgs a, int lpg, int vec) {
