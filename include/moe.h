@@ -528,6 +528,73 @@ MOE_API int moe_adapter_project_backward(const moe_adapter_t* adapter, int T, co
                                          const int32_t* adapter_of, const void* v, void* dx, void* da, void* db,
                                          void* ws, size_t ws_bytes, void* stream);
 
+/* Gradient of moe_combine (y_shared's is d_out itself):
+ *   dy_disp[inv_perm[t*k+j], :] = bf16( topk_w[t,j] * d_out[t,:] ),
+ *   d_topk_w[t,j] = sum over the columns of d_out[t,:] * y_disp[inv_perm[t*k+j], :]   (fp32).
+ * d_out [T,H], y_disp and dy_disp [T*k,H] bf16; the sums run in a fixed order.  A row index outside
+ * [0, T*k) sets the device status, writes no row and gives the gradient 0. */
+MOE_API int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_out, const void* y_disp,
+                         const int32_t* inv_perm, const float* topk_w, void* dy_disp, float* d_topk_w, void* stream);
+
+/* ---------------------------------------------------------------- training the experts
+ * The expert products by themselves, with their gradients, and the activations
+ * between them kept in 8 bits.  A layer's experts forward: moe_expert_project (gate and
+ * up as two parts), moe_swiglu_checkpoint, moe_expert_down; backward: moe_combine_backward,
+ * moe_expert_project_backward (down), moe_swiglu_backward, moe_expert_project_backward (gate and up);
+ * moe_expert_layer_06_gb300.training runs the whole layer this way.
+ *
+ * Rows of slot s are [offsets[s], offsets[s+1]) (moe_dispatch; offsets [n_slots+1] at least, on the
+ * device).  Offsets outside [0, rows] or running backwards set the device status and are cut to it.
+ * moe_expert_project: for each part p (two: gate and up),
+ *   out[r, p*N + n] = sum over k of x[r,k] * w_p[s,n,k]        (r in slot s)
+ * moe_expert_project_backward:
+ *   dx[r,k] = sum over p and n of dy[r, p*N + n] * w_p[s,n,k],
+ *   dw_p[s,n,k] = sum over the slot's rows r of dy[r, p*N + n] * x[r,k].
+ * x [rows,K], dy and out [rows, n_parts*N], w and w2 [n_slots,N,K] (w2 NULL for one part), dx [rows,K],
+ * dw and dw2 as w and w2; dx may be NULL, and so may dw and dw2.  For dw the rows are given as x
+ * (bf16) or in 8 bits as x8 [rows,K] and x8_scale [rows, ceil(K/128)] (moe_checkpoint_rows; K a
+ * multiple of 16): exactly one of the two.  Products of bf16, sums in fp32, rounded once.
+ * out, dx and dw are written as their type says: MOE_OUT_BF16; MOE_OUT_F32; MOE_OUT_F32_ADD adds to
+ * the fp32 values that they hold (gradients of several batches, or of several paths to one input).
+ * Rows of no slot are neither read nor written; a slot without rows gets dw = 0.  An infinity or
+ * NaN in a row shows in that row's results and its slot's dw only.  Sums run in an order that the
+ * sizes and counts fix: results repeat bit for bit on one GPU model.  rows = 0 writes dw alone.
+ * Limits: K and N multiples of 8 and at most 2^24, n_slots <= 1024. */
+#define MOE_OUT_BF16 0
+#define MOE_OUT_F32 1
+#define MOE_OUT_F32_ADD 2
+typedef struct {
+    int32_t in_features;   /* K */
+    int32_t out_features;  /* N, of one part */
+    int32_t n_slots;       /* S */
+    int32_t n_parts;       /* 1 | 2 */
+} moe_project_t;
+MOE_API int moe_expert_project(const moe_project_t* project, int rows, const void* x, const int32_t* offsets,
+                               const void* w, const void* w2, void* out, int out_type, void* stream);
+MOE_API int moe_expert_project_backward(const moe_project_t* project, int rows, const void* dy, const void* x,
+                                        const uint8_t* x8, const float* x8_scale, const int32_t* offsets, const void* w,
+                                        const void* w2, void* dx, int dx_type, void* dw, void* dw2, int dw_type,
+                                        void* stream);
+
+/* Activations kept in 8 bits: a row is cut into blocks of MOE_PAYLOAD_BLOCK columns (the last one
+ * shorter), and a block stored as E4M3 codes and one fp32 scale, the least power of two from
+ * 2^-117 to 2^119 with amax / scale <= 448 (amax: its largest finite magnitude; 1 for a block of
+ * zeros; 2^119 where none has); code = e4m3(x / scale), rounded to nearest even, saturating.  code * scale is a bf16 value, so the
+ * backward products use the kept values themselves.  Infinities and NaN are kept as NaN.
+ * moe_checkpoint_rows: x [rows,cols] bf16 -> codes [rows,cols], scale [rows, ceil(cols/128)].
+ * moe_swiglu_checkpoint: gate_up [rows, 2*inter] bf16 (gate, then up: moe_expert_project's out) ->
+ *   h [rows,inter] = bf16( silu(gate) * up ), and gate and up kept: codes [rows, 2*inter], scale
+ *   [rows, 2*ceil(inter/128)] (the gate's blocks, then the up's).
+ * moe_swiglu_backward: with g and u the kept values, s = sigmoid(g) and dh [rows,inter] bf16,
+ *   d_gate_up[:, :inter] = dh * u * s * (1 + g * (1 - s)),  d_gate_up[:, inter:] = dh * g * s,
+ *   h [rows,inter] (NULL to skip) = bf16( g * s * u ), what the down projection's dw multiplies.
+ * cols and inter: multiples of 8. */
+MOE_API int moe_checkpoint_rows(int rows, int cols, const void* x, uint8_t* codes, float* scale, void* stream);
+MOE_API int moe_swiglu_checkpoint(int rows, int inter, const void* gate_up, void* h, uint8_t* codes, float* scale,
+                                  void* stream);
+MOE_API int moe_swiglu_backward(int rows, int inter, const uint8_t* codes, const float* scale, const void* dh,
+                                void* d_gate_up, void* h, void* stream);
+
 /* ---------------------------------------------------------------- whole layer
  * moe_route (from x), moe_dispatch, moe_expert_ffn, moe_combine on one stream
  * (7 kernel launches; capturable in a CUDA graph).  Intermediates live in the

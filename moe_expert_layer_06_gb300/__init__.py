@@ -41,7 +41,8 @@ EXPORTS = (
     "moe_workspace_size_fp8", "moe_forward_fp8", "moe_expert_down_fp8", "moe_dispatch_workspace_size",
     "moe_expert_down_fp8_payload", "moe_combine_fp8", "moe_ep_plan", "moe_gather_rows",
     "moe_route_scored", "moe_route_scored_backward", "moe_adapter_workspace_size", "moe_adapter_project",
-    "moe_adapter_project_backward",
+    "moe_adapter_project_backward", "moe_expert_project", "moe_expert_project_backward", "moe_checkpoint_rows",
+    "moe_swiglu_checkpoint", "moe_swiglu_backward", "moe_combine_backward",
 )
 
 # router scores and group scores of moe_route_scored
@@ -50,7 +51,12 @@ MOE_SCORE_SIGMOID = 1
 MOE_GROUP_MAX = 0
 MOE_GROUP_TOP2 = 1
 
-# columns per scale of the E4M3 combine payload (MOE_PAYLOAD_BLOCK in include/moe.h)
+# how moe_expert_project and its backward pass write an output (MOE_OUT_* in include/moe.h)
+MOE_OUT_BF16 = 0
+MOE_OUT_F32 = 1
+MOE_OUT_F32_ADD = 2
+
+# columns per scale of the E4M3 combine payload and of activations kept in 8 bits (MOE_PAYLOAD_BLOCK in include/moe.h)
 MOE_PAYLOAD_BLOCK = 128
 
 # capacity of the fixed scratch of moe_expert_ffn_noalloc (include/moe.h)
@@ -88,6 +94,14 @@ class Adapter(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "n_adapters", "rank")]
 
 
+class Project(ctypes.Structure):
+    """Sizes of matrix products grouped by expert (moe_project_t)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "n_slots", "n_parts")]
+
+    def __init__(self, in_features, out_features, n_slots, n_parts=1):
+        super().__init__(in_features, out_features, n_slots, n_parts)
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
@@ -107,6 +121,12 @@ _SIG = {
     "moe_adapter_workspace_size": (_Z, [_P, _I]),
     "moe_adapter_project": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _Z, _P]),
     "moe_adapter_project_backward": (_I, [_P, _I] + [_P] * 12 + [_Z, _P]),
+    "moe_expert_project": (_I, [_P, _I] + [_P] * 5 + [_I, _P]),
+    "moe_expert_project_backward": (_I, [_P, _I] + [_P] * 8 + [_I, _P, _P, _I, _P]),
+    "moe_checkpoint_rows": (_I, [_I, _I] + [_P] * 4),
+    "moe_swiglu_checkpoint": (_I, [_I, _I] + [_P] * 5),
+    "moe_swiglu_backward": (_I, [_I, _I] + [_P] * 6),
+    "moe_combine_backward": (_I, [_P, _I] + [_P] * 7),
     "moe_expert_histogram": (_I, [_P, _I, _P, _P, _P, _P, _P]),
     "moe_eplb_imbalance": (ctypes.c_double, [_P, _I]),
     "moe_eplb_window_bytes": (_Z, [_P, _I]),
@@ -409,6 +429,81 @@ def moe_expert_ffn_noalloc(shape, T, x, x_disp, offsets, w_gate, w_up, w_down, w
 def moe_combine(shape, T, y_disp, inv_perm, topk_w, y_shared, out, stream=None):
     _check(lib().moe_combine(_shape(shape), T, _ptr(y_disp), _ptr(inv_perm), _ptr(topk_w), _ptr(y_shared),
                              _ptr(out), _stream(stream)))
+
+
+def moe_combine_backward(shape, T, d_out, y_disp, inv_perm, topk_w, dy_disp, d_topk_w, stream=None):
+    """Gradient of moe_combine: of every expert output row and of the routing weights."""
+    n, H, k, bf16 = T * shape.top_k, shape.hidden, shape.top_k, torch.bfloat16
+    _check(lib().moe_combine_backward(
+        _shape(shape), T, _dense(d_out, "d_out", (T, H), bf16), _dense(y_disp, "y_disp", (n, H), bf16),
+        _dense(inv_perm, "inv_perm", (n,), torch.int32), _dense(topk_w, "topk_w", (T, k), torch.float32),
+        _dense(dy_disp, "dy_disp", (n, H), bf16), _dense(d_topk_w, "d_topk_w", (T, k), torch.float32), _stream(stream)))
+
+
+# ------------------------------------------------------------------ training the experts
+
+def _out_type(t, add: bool) -> int:
+    """How an output is written: as its tensor's type, or (fp32) added to what it holds."""
+    if t is None or (t.dtype != torch.float32 and not add):
+        return MOE_OUT_BF16
+    if add and t.dtype != torch.float32:
+        raise ValueError("an output that is added to must be float32")
+    return MOE_OUT_F32_ADD if add else MOE_OUT_F32
+
+
+def _offsets(offsets, n_slots):
+    if offsets is not None and (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] <= n_slots):
+        raise ValueError(f"offsets must be int32, {n_slots + 1} at least")
+    return _ptr(offsets)
+
+
+def moe_expert_project(project, rows, x, offsets, w, w2, out, add=False, stream=None):
+    """out [rows, n_parts * out_features], bf16 or fp32; add: what it holds (fp32) is added to."""
+    K, N, S, P = project.in_features, project.out_features, project.n_slots, project.n_parts
+    bf16, kind = torch.bfloat16, _out_type(out, add)
+    _check(lib().moe_expert_project(
+        ctypes.byref(project), rows, _dense(x, "x", (rows, K), bf16), _offsets(offsets, S), _dense(w, "w", (S, N, K), bf16),
+        _dense(w2, "w2", (S, N, K), bf16), _dense(out, "out", (rows, P * N), torch.float32 if kind else bf16), kind,
+        _stream(stream)))
+
+
+def moe_expert_project_backward(project, rows, dy, x, x8, x8_scale, offsets, w, w2, dx, dw, dw2=None, add_dx=False,
+                                add_dw=False, stream=None):
+    """dx and / or dw (and dw2), each bf16 or fp32; the rows as x (bf16) or as x8 and x8_scale (moe_checkpoint_rows)."""
+    K, N, S, P = project.in_features, project.out_features, project.n_slots, project.n_parts
+    bf16, f32 = torch.bfloat16, torch.float32
+    x_kind, w_kind = _out_type(dx, add_dx), _out_type(dw, add_dw)
+    w_type = f32 if w_kind else bf16
+    _check(lib().moe_expert_project_backward(
+        ctypes.byref(project), rows, _dense(dy, "dy", (rows, P * N), bf16), _dense(x, "x", (rows, K), bf16),
+        _dense(x8, "x8", (rows, K), torch.uint8), _dense(x8_scale, "x8_scale", (rows, -(-K // MOE_PAYLOAD_BLOCK)), f32),
+        _offsets(offsets, S), _dense(w, "w", (S, N, K), bf16), _dense(w2, "w2", (S, N, K), bf16),
+        _dense(dx, "dx", (rows, K), f32 if x_kind else bf16), x_kind, _dense(dw, "dw", (S, N, K), w_type),
+        _dense(dw2, "dw2", (S, N, K), w_type), w_kind, _stream(stream)))
+
+
+def moe_checkpoint_rows(rows, cols, x, codes, scale, stream=None):
+    """Rows kept in 8 bits: codes [rows, cols] uint8 and a power of two for each 128 columns."""
+    _check(lib().moe_checkpoint_rows(
+        rows, cols, _dense(x, "x", (rows, cols), torch.bfloat16), _dense(codes, "codes", (rows, cols), torch.uint8),
+        _dense(scale, "scale", (rows, -(-cols // MOE_PAYLOAD_BLOCK)), torch.float32), _stream(stream)))
+
+
+def moe_swiglu_checkpoint(rows, inter, gate_up, h, codes, scale, stream=None):
+    """h = silu(gate) * up of gate_up [rows, 2 * inter], which is kept in 8 bits (codes, scale)."""
+    _check(lib().moe_swiglu_checkpoint(
+        rows, inter, _dense(gate_up, "gate_up", (rows, 2 * inter), torch.bfloat16),
+        _dense(h, "h", (rows, inter), torch.bfloat16), _dense(codes, "codes", (rows, 2 * inter), torch.uint8),
+        _dense(scale, "scale", (rows, 2 * -(-inter // MOE_PAYLOAD_BLOCK)), torch.float32), _stream(stream)))
+
+
+def moe_swiglu_backward(rows, inter, codes, scale, dh, d_gate_up, h=None, stream=None):
+    """d_gate_up from dh and what moe_swiglu_checkpoint kept; h: the activation again, from the same."""
+    _check(lib().moe_swiglu_backward(
+        rows, inter, _dense(codes, "codes", (rows, 2 * inter), torch.uint8),
+        _dense(scale, "scale", (rows, 2 * -(-inter // MOE_PAYLOAD_BLOCK)), torch.float32),
+        _dense(dh, "dh", (rows, inter), torch.bfloat16), _dense(d_gate_up, "d_gate_up", (rows, 2 * inter), torch.bfloat16),
+        _dense(h, "h", (rows, inter), torch.bfloat16), _stream(stream)))
 
 
 def moe_workspace_size(shape, T: int) -> int:

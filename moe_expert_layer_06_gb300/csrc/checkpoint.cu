@@ -1,0 +1,298 @@
+// Activations kept in 8 bits for the backward pass, and SwiGLU with its gradient on them.
+//
+// Rows are cut into blocks of 128 columns (the last one shorter).  A block's scale is the least
+// power of two, from 2^-117 to 2^119, that brings its largest finite value to 448 at most; a code is
+// e4m3(x / scale), saturating (448 * 2^119 for the few values above it: 2^120 would round them to an
+// infinity).  A power of two divides and multiplies without rounding, so the only error is
+// the code's own (2^-4 of a value at most, above 2^-6 of the scale), and code * scale is a bf16
+// number again: four significant bits, 2^-117 * 2^-9 the smallest.  The backward pass multiplies
+// the very values that were kept.  (A scale of amax / 448 would gain under one bit of range, and
+// its products would round a second time.)  Infinities and NaN are kept as NaN, which E4M3 has.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "operators.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBlock = MOE_PAYLOAD_BLOCK;
+constexpr int kThreads = 256;
+constexpr int kLanes = 16;                    // lanes that share a block, 8 columns each
+constexpr int kGroups = kThreads / kLanes;    // blocks of a CTA side by side
+
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// |x| of two bf16, infinities and NaN as 0
+__device__ __forceinline__ uint32_t finite_abs(uint32_t w) {
+    w &= 0x7fff7fffu;
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+}
+
+// infinities as NaN
+__device__ __forceinline__ uint32_t no_inf(uint32_t w) {
+    if ((w & 0x7fffu) == 0x7f80u) w |= 0x40u;
+    if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x400000u;
+    return w;
+}
+
+// The exponent of a block's scale, from 8 of its values in each of 16 lanes (the whole warp calls).
+// Values whose |x| reaches infinity or NaN leave the maximum, and become NaN.
+__device__ __forceinline__ int block_exponent(uint4& v) {
+    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    if (__any_sync(0xffffffffu, (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u)) {
+        m = __vmaxu2(__vmaxu2(finite_abs(v.x), finite_abs(v.y)), __vmaxu2(finite_abs(v.z), finite_abs(v.w)));
+        v = make_uint4(no_inf(v.x), no_inf(v.y), no_inf(v.z), no_inf(v.w));
+    }
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const uint32_t top = max(m & 0xffffu, m >> 16);  // bf16 bits: exponent, then 7 of the mantissa
+    if (top == 0) return 0;
+    // 448 is 1.75 * 2^8
+    return min(max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0), -117), 119);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ uint32_t encode4(uint32_t a, uint32_t b, float inv) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(lo_of(a) * inv, hi_of(a) * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(lo_of(b) * inv, hi_of(b) * inv), __NV_SATFINITE, __NV_E4M3);
+    return (lo & 0xffffu) | (hi << 16);
+}
+
+__device__ __forceinline__ uint2 encode8(const uint4& v, int e) {
+    const float inv = pow2(-e);
+    return make_uint2(encode4(v.x, v.y, inv), encode4(v.z, v.w, inv));
+}
+
+__device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = (i < 2 ? c.x : c.y) >> (i & 1) * 16;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
+        const float2 p = __half22float2(__half2(h));
+        f[2 * i] = p.x * scale;
+        f[2 * i + 1] = p.y * scale;
+    }
+}
+
+// sigmoid(g) and 1 - sigmoid(g), each as exact as the other: e^-|g| does not overflow, and neither
+// is a difference.
+__device__ __forceinline__ void sigmoids(float g, float& s, float& rest) {
+    const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e);
+    s = g >= 0.0f ? r : e * r;
+    rest = g >= 0.0f ? e * r : r;
+    if (g != g) s = g;
+}
+
+// Block u (of `blocks` a row) of the CTA's: its row and its place in it.
+struct Place {
+    size_t row;
+    int block;
+};
+__device__ __forceinline__ Place place_of(size_t first, int u, int blocks) {
+    const size_t row0 = first / blocks;
+    const unsigned at = (unsigned)(first - row0 * blocks) + u;
+    return {row0 + at / (unsigned)blocks, (int)(at % (unsigned)blocks)};
+}
+
+template <int U>  // blocks of a group of lanes
+__global__ void __launch_bounds__(kThreads) keep_kernel(const uint16_t* __restrict__ x, size_t rows, int cols, int blocks,
+                                                        uint8_t* __restrict__ codes, float* __restrict__ scale) {
+    pdl_begin();
+    const size_t first = (size_t)blockIdx.x * (kGroups * U);
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    uint4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const Place p = place_of(first, i * kGroups + group, blocks);
+        const int c = p.block * kBlock + lane * 8;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (p.row < rows && c < cols) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + p.row * cols + c));
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const Place p = place_of(first, i * kGroups + group, blocks);
+        const int c = p.block * kBlock + lane * 8;
+        const int e = block_exponent(v[i]);
+        if (p.row >= rows) continue;
+        if (c < cols) *reinterpret_cast<uint2*>(codes + p.row * cols + c) = encode8(v[i], e);
+        if (lane == 0) scale[p.row * blocks + p.block] = pow2(e);
+    }
+}
+
+template <int U>
+__global__ void __launch_bounds__(kThreads) swiglu_keep_kernel(const uint16_t* __restrict__ gate_up, size_t rows, int inter,
+                                                               int blocks, uint16_t* __restrict__ h,
+                                                               uint8_t* __restrict__ codes, float* __restrict__ scale) {
+    pdl_begin();
+    const size_t first = (size_t)blockIdx.x * (kGroups * U);
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    uint4 g[U], u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const Place p = place_of(first, i * kGroups + group, blocks);
+        const int c = p.block * kBlock + lane * 8;
+        g[i] = u[i] = make_uint4(0, 0, 0, 0);
+        if (p.row < rows && c < inter) {
+            const uint16_t* at = gate_up + p.row * 2 * inter + c;
+            g[i] = __ldcs(reinterpret_cast<const uint4*>(at));
+            u[i] = __ldcs(reinterpret_cast<const uint4*>(at + inter));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const Place p = place_of(first, i * kGroups + group, blocks);
+        const int c = p.block * kBlock + lane * 8;
+        uint32_t out[4];
+        const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w}, uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b, rest;
+            sigmoids(lo_of(gw[j]), a, rest);
+            sigmoids(hi_of(gw[j]), b, rest);
+            out[j] = pack_bf(lo_of(gw[j]) * a * lo_of(uw[j]), hi_of(gw[j]) * b * hi_of(uw[j]));
+        }
+        const int eg = block_exponent(g[i]), eu = block_exponent(u[i]);
+        if (p.row >= rows) continue;
+        if (c < inter) {
+            *reinterpret_cast<uint4*>(h + p.row * inter + c) = make_uint4(out[0], out[1], out[2], out[3]);
+            uint8_t* at = codes + p.row * 2 * inter + c;
+            *reinterpret_cast<uint2*>(at) = encode8(g[i], eg);
+            *reinterpret_cast<uint2*>(at + inter) = encode8(u[i], eu);
+        }
+        if (lane == 0) {
+            scale[p.row * 2 * blocks + p.block] = pow2(eg);
+            scale[(p.row * 2 + 1) * blocks + p.block] = pow2(eu);
+        }
+    }
+}
+
+template <int U>
+__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t* __restrict__ codes,
+                                                                   const float* __restrict__ scale,
+                                                                   const uint16_t* __restrict__ dh, size_t rows, int inter,
+                                                                   int blocks, uint16_t* __restrict__ d_gate_up,
+                                                                   uint16_t* __restrict__ h) {
+    pdl_begin();
+    const size_t first = (size_t)blockIdx.x * (kGroups * U);
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    uint2 cg[U], cu[U];
+    uint4 d[U];
+    float sg[U], su[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const Place p = place_of(first, i * kGroups + group, blocks);
+        const int c = p.block * kBlock + lane * 8;
+        if (p.row < rows && c < inter) {
+            const uint8_t* at = codes + p.row * 2 * inter + c;
+            cg[i] = __ldcs(reinterpret_cast<const uint2*>(at));
+            cu[i] = __ldcs(reinterpret_cast<const uint2*>(at + inter));
+            d[i] = __ldcs(reinterpret_cast<const uint4*>(dh + p.row * inter + c));
+            sg[i] = __ldg(scale + p.row * 2 * blocks + p.block);
+            su[i] = __ldg(scale + (p.row * 2 + 1) * blocks + p.block);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const Place p = place_of(first, i * kGroups + group, blocks);
+        const int c = p.block * kBlock + lane * 8;
+        if (p.row >= rows || c >= inter) continue;
+        float g[8], u[8], act[8], dg[8], du[8];
+        decode8(cg[i], sg[i], g);
+        decode8(cu[i], su[i], u);
+        const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float up = j & 1 ? hi_of(dw[j >> 1]) : lo_of(dw[j >> 1]);
+            float s, rest;
+            sigmoids(g[j], s, rest);
+            const float silu = g[j] * s;
+            act[j] = silu * u[j];
+            du[j] = up * silu;
+            dg[j] = up * u[j] * (s * fmaf(g[j], rest, 1.0f));
+        }
+        uint16_t* out = d_gate_up + p.row * 2 * inter + c;
+        *reinterpret_cast<uint4*>(out) =
+            make_uint4(pack_bf(dg[0], dg[1]), pack_bf(dg[2], dg[3]), pack_bf(dg[4], dg[5]), pack_bf(dg[6], dg[7]));
+        *reinterpret_cast<uint4*>(out + inter) =
+            make_uint4(pack_bf(du[0], du[1]), pack_bf(du[2], du[3]), pack_bf(du[4], du[5]), pack_bf(du[6], du[7]));
+        if (h)
+            *reinterpret_cast<uint4*>(h + p.row * inter + c) =
+                make_uint4(pack_bf(act[0], act[1]), pack_bf(act[2], act[3]), pack_bf(act[4], act[5]), pack_bf(act[6], act[7]));
+    }
+}
+
+int check_rows(int rows, int cols, const char* name) {
+    if (rows < 0 || cols <= 0 || cols % 8) return api_fail(MOE_ERR_INVALID_ARG, "rows >= 0 and %s > 0, a multiple of 8, required", name);
+    if (cols > 1 << 24) return api_fail(MOE_ERR_UNSUPPORTED, "%s %d > %d", name, cols, 1 << 24);
+    if ((long long)rows * ((cols + kBlock - 1) / kBlock) / kGroups >= INT32_MAX)
+        return api_fail(MOE_ERR_UNSUPPORTED, "too many rows");
+    return MOE_OK;
+}
+
+template <int U>
+dim3 grid_of(int rows, int blocks) {
+    return dim3((unsigned)(((size_t)rows * blocks + kGroups * U - 1) / (kGroups * U)));
+}
+
+int launched(cudaError_t e, const char* what) {
+    return e == cudaSuccess ? MOE_OK : api_fail(MOE_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_checkpoint_rows(int rows, int cols, const void* x, uint8_t* codes, float* scale, void* stream) {
+    int rc = check_rows(rows, cols, "cols");
+    if (rc || rows == 0) return rc;
+    if ((rc = api_need(x, "x")) || (rc = api_need(codes, "codes")) || (rc = api_need(scale, "scale", 4))) return rc;
+    PdlScope pdl(rows);
+    const int blocks = (cols + kBlock - 1) / kBlock;
+    return launched(launch_pdl(keep_kernel<4>, grid_of<4>(rows, blocks), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                               static_cast<const uint16_t*>(x), (size_t)rows, cols, blocks, codes, scale),
+                    "checkpoint");
+}
+
+int moe_swiglu_checkpoint(int rows, int inter, const void* gate_up, void* h, uint8_t* codes, float* scale, void* stream) {
+    int rc = check_rows(rows, inter, "inter");
+    if (rc || rows == 0) return rc;
+    if ((rc = api_need(gate_up, "gate_up")) || (rc = api_need(h, "h")) || (rc = api_need(codes, "codes")) ||
+        (rc = api_need(scale, "scale", 4)))
+        return rc;
+    PdlScope pdl(rows);
+    const int blocks = (inter + kBlock - 1) / kBlock;
+    return launched(launch_pdl(swiglu_keep_kernel<2>, grid_of<2>(rows, blocks), dim3(kThreads), 0,
+                               reinterpret_cast<cudaStream_t>(stream), static_cast<const uint16_t*>(gate_up), (size_t)rows, inter,
+                               blocks, static_cast<uint16_t*>(h), codes, scale),
+                    "SwiGLU");
+}
+
+int moe_swiglu_backward(int rows, int inter, const uint8_t* codes, const float* scale, const void* dh, void* d_gate_up, void* h,
+                        void* stream) {
+    int rc = check_rows(rows, inter, "inter");
+    if (rc || rows == 0) return rc;
+    if ((rc = api_need(codes, "codes")) || (rc = api_need(scale, "scale", 4)) || (rc = api_need(dh, "dh")) ||
+        (rc = api_need(d_gate_up, "d_gate_up")))
+        return rc;
+    if (h && (rc = api_need(h, "h"))) return rc;
+    PdlScope pdl(rows);
+    const int blocks = (inter + kBlock - 1) / kBlock;
+    return launched(launch_pdl(swiglu_backward_kernel<2>, grid_of<2>(rows, blocks), dim3(kThreads), 0,
+                               reinterpret_cast<cudaStream_t>(stream), codes, scale, static_cast<const uint16_t*>(dh), (size_t)rows,
+                               inter, blocks, static_cast<uint16_t*>(d_gate_up), static_cast<uint16_t*>(h)),
+                    "SwiGLU gradient");
+}
+
+}  // extern "C"

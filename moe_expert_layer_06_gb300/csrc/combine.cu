@@ -168,7 +168,76 @@ __global__ void __launch_bounds__(256, 2) combine_fp8_kernel(const uint4* __rest
     }
 }
 
+// Gradient of the combine: dy[row] = w * dout[t] and dw = <dout[t], y[row]> of each assignment
+// a = (t, j), row = inv_perm[a].  `tpr` threads (whole warps) per assignment, kCombineVec vectors
+// of 8 columns of each in flight.
+constexpr int kCombineVec = 4;
+__global__ void __launch_bounds__(256) combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ y,
+                                                               const int32_t* __restrict__ inv_perm,
+                                                               const float* __restrict__ topk_w, int n, int k, int vpr, int tpr,
+                                                               uint4* __restrict__ dy, float* __restrict__ dw, DevStatus st) {
+    pdl_begin();
+    __shared__ float part[8];
+    const int sub = threadIdx.x / tpr, at = threadIdx.x - sub * tpr, lane = threadIdx.x & 31;
+    const int a = blockIdx.x * (256 / tpr) + sub;
+    const int row = a < n ? __ldg(inv_perm + a) : -1;
+    const bool live = row >= 0 && row < n;
+    float sum = 0.0f;
+    if (live) {
+        const float w = __ldg(topk_w + a);
+        const uint4* d = dout + (size_t)(a / k) * vpr;
+        const uint4* yr = y + (size_t)row * vpr;
+        uint4* out = dy + (size_t)row * vpr;
+        for (int c0 = at; c0 < vpr; c0 += tpr * kCombineVec) {
+            uint4 dv[kCombineVec], yv[kCombineVec];
+#pragma unroll
+            for (int i = 0; i < kCombineVec; ++i) {
+                const int c = c0 + i * tpr;
+                if (c < vpr) {
+                    dv[i] = __ldg(d + c);
+                    yv[i] = __ldcs(yr + c);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kCombineVec; ++i) {
+                const int c = c0 + i * tpr;
+                if (c < vpr) {
+                    float df[8], yf[8];
+                    unpack8(dv[i], df);
+                    unpack8(yv[i], yf);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) sum = fmaf(df[q], yf[q], sum);
+                    out[c] = make_uint4(pack2(w * df[0], w * df[1]), pack2(w * df[2], w * df[3]), pack2(w * df[4], w * df[5]),
+                                        pack2(w * df[6], w * df[7]));
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (lane == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (at == 0 && a < n) {
+        sum = 0.0f;
+        for (int i = 0; i < tpr / 32; ++i) sum += part[(threadIdx.x >> 5) + i];
+        dw[a] = sum;
+        if (!live) raise_status(st, kStatusBadShape);
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_combine_backward(const uint16_t* dout, const uint16_t* y_disp, const int32_t* inv_perm, const float* topk_w,
+                                    int T, int k, int hidden, uint16_t* dy_disp, float* d_topk_w, const DevStatus& st,
+                                    cudaStream_t stream) {
+    const int vpr = hidden / 8, n = T * k;
+    int tpr = 32;
+    while (tpr < 256 && tpr * kCombineVec < vpr) tpr *= 2;
+    const int per = 256 / tpr;
+    return launch_pdl(combine_backward_kernel, dim3((n + per - 1) / per), dim3(256), 0, stream,
+                      reinterpret_cast<const uint4*>(dout), reinterpret_cast<const uint4*>(y_disp), inv_perm, topk_w, n, k, vpr, tpr,
+                      reinterpret_cast<uint4*>(dy_disp), d_topk_w, st);
+}
 
 cudaError_t launch_combine_fp8(const uint8_t* y8, const float* y_scale, const int32_t* inv_perm, const float* topk_w,
                                const float* y_shared, int T, int k, int hidden, uint16_t* out, cudaStream_t stream) {

@@ -203,6 +203,11 @@ cudaError_t launch_combine(const uint16_t* y_disp, const int32_t* inv_perm, cons
 cudaError_t launch_combine_fp8(const uint8_t* y8, const float* y_scale, const int32_t* inv_perm, const float* topk_w,
                                const float* y_shared, int T, int k, int hidden, uint16_t* out, cudaStream_t stream);
 
+// dy_disp[inv_perm[a]] = topk_w[a] * dout[a / k], d_topk_w[a] = <dout[a / k], y_disp[inv_perm[a]]>.
+cudaError_t launch_combine_backward(const uint16_t* dout, const uint16_t* y_disp, const int32_t* inv_perm, const float* topk_w,
+                                    int T, int k, int hidden, uint16_t* dy_disp, float* d_topk_w, const DevStatus& st,
+                                    cudaStream_t stream);
+
 int num_sms();
 
 // Error reporting and shape validation of the C ABI, for entry points defined

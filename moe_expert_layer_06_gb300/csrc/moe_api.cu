@@ -973,6 +973,26 @@ int moe_combine(const moe_shape_t* shape, int T, const void* y_disp, const int32
     return MOE_OK;
 }
 
+int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_out, const void* y_disp, const int32_t* inv_perm,
+                         const float* topk_w, void* dy_disp, float* d_topk_w, void* stream) {
+    PdlScope pdl((long)T * (shape ? shape->top_k : 0));
+    int rc = check_shape(shape, T);
+    if (rc) return rc;
+    if (T == 0) return MOE_OK;
+    NEED(d_out, "d_out");
+    NEED(y_disp, "y_disp");
+    NEED4(inv_perm, "inv_perm");
+    NEED4(topk_w, "topk_w");
+    NEED(dy_disp, "dy_disp");
+    NEED4(d_topk_w, "d_topk_w");
+    DevStatus st;
+    if ((rc = device_status(&st))) return rc;
+    MOE_CUDA(launch_combine_backward(static_cast<const uint16_t*>(d_out), static_cast<const uint16_t*>(y_disp), inv_perm, topk_w, T,
+                                     shape->top_k, shape->hidden, static_cast<uint16_t*>(dy_disp), d_topk_w, st, as_stream(stream)),
+             "combine gradient launch");
+    return MOE_OK;
+}
+
 size_t moe_workspace_size(const moe_shape_t* shape, int T) {
     if (check_shape(shape, T)) return 0;
     return fwd_layout(shape, T).total;

@@ -73,6 +73,15 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint3
 constexpr uint32_t kIdescAMnMajor = 1u << 15;  // A / B transposed (MN-major) in an instruction descriptor
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
+// The rows of slot s: offsets[s] to offsets[s + 1], within [0, rows] whatever they hold (false: they
+// did not lie there, or ran backwards).
+__device__ __forceinline__ bool slot_rows(const int32_t* offsets, int s, int rows, int& lo, int& hi) {
+    const int a = __ldg(offsets + s), b = __ldg(offsets + s + 1);
+    lo = min(max(a, 0), rows);
+    hi = min(max(b, lo), rows);
+    return a == lo && b == hi;
+}
+
 // ---------------------------------------------------------------- moe_api.cu
 // make_tmap_3d for bf16 rows along dimension 1 (or 2 where dimension 1 is 1), with a swizzle of 128,
 // 64 or 32 bytes, the box's inner extent at least.  Parts of rows that do not start on 128-byte lines
