@@ -2,9 +2,16 @@
 //   y[r]  = W_p[s] x[r]                    for the rows r of slot s, parts p side by side (gate, up)
 //   dx[r] = sum_p W_p[s]^T dy_p[r],  dW_p[s] = sum over s's rows of dy_p[r] x[r]^T.
 // The rows of a slot are consecutive (a dispatch's order), their counts ragged.
+//
+// All three are tcgen05 products of CTA pairs (cta_group::2), 256 outputs of one operand times up to
+// 256 of the other, fp32 sums in tensor memory, double buffered so that a tile's stores run under the
+// next tile's products.  Persistent pairs take tiles in turn; what there is of them follows from the
+// offsets on the device.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "e4m3.cuh"
+#include <algorithm>
+
 #include "operators.cuh"
 
 namespace moe {
@@ -12,108 +19,734 @@ namespace {
 
 constexpr int kMaxSlots = 1024;
 constexpr int kMaxFeatures = 1 << 24;
+constexpr int kHalf = 128 * 64 * 2;          // one CTA's 128 rows or features of an operand's 64-wide chunk
+constexpr int kStageBytes = 2 * kHalf;
+constexpr int kStages = 6;
+constexpr int kRing = kStages * kStageBytes;
 
-struct Args {
-    const uint16_t* rows_in;  // x [R][K] | dy [R][P][N]
-    const uint16_t* x;
-    const uint8_t* x8;
-    const float* x8_scale;
-    const uint16_t* w[2];
-    void* out[2];
+__device__ __forceinline__ uint32_t to_u(float f) { return __float_as_uint(f); }
+
+__device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// A block of outputs in shared memory into (or added to) the tensor.
+__device__ __forceinline__ void put(const CUtensorMap* map, int type, uint32_t src, int c0, int c1, int c2) {
+    if (type == MOE_OUT_F32_ADD) tma_reduce_add_3d(map, src, c0, c1, c2);
+    else tma_store_3d(map, src, c0, c1, c2);
+}
+
+template <int N>
+__device__ __forceinline__ void bulk_wait_read_but() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
+__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// A wait for what the other CTA of the pair wrote and signalled: acquires for the cluster.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const volatile int* abort_flag, unsigned long long limit) {
+    bool done = mbar_try_wait_cluster(bar, parity);
+    if (!__all_sync(0xffffffffu, done)) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!done && !*abort_flag && globaltimer_ns() - t0 <= limit) done = mbar_try_wait_cluster(bar, parity);
+        done = __all_sync(0xffffffffu, done);
+    }
+    return done;
+}
+
+// ---------------------------------------------------------------- y and dx
+// One pair's tile: 256 outputs (128 rows of W, or for dx 128 columns, in each CTA) times the rows of
+// a slot in chunks of equal height, a multiple of 32 up to 256 (half of them in each CTA).
+// dx's W is read MN-major, as its contraction runs over W's rows.
+struct RowsArgs {
+    CUtensorMap w[2];  // box {64, 128} of [S][N][K], dx: {64, 64}
+    CUtensorMap in[4]; // box {64, 1, 16 << j} of x [R][1][K], dx: dy [R][P][N]
+    CUtensorMap out;   // box {64, 1, 16} bf16, {32, 1, 16} fp32 of y [R][P][N], dx: [R][1][K]
     const int32_t* offsets;
+    void* out_ptr;
     int R, K, N, P, S, type;
     DevStatus st;
 };
+constexpr int kRowsThreads = 192;  // copies, products, four warps that drain accumulators
+constexpr int kOutBytes = 16384;   // bf16: 2 x 2 blocks of 32 rows x 64 features; fp32: 4 x 2 of 16 rows x 32
+constexpr int kRowsSmem = 1024 + kRing + kOutBytes + 256 + (kMaxSlots + 1) * 4;
+static_assert(kRowsSmem <= 227 * 1024, "shared memory overflow");
 
-__device__ __forceinline__ float bf(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+__device__ __forceinline__ int chunks_of(int count) { return (count + 255) / 256; }
 
-__device__ __forceinline__ void store(void* out, size_t at, float v, int type) {
-    if (type == MOE_OUT_BF16) static_cast<uint16_t*>(out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    else if (type == MOE_OUT_F32) static_cast<float*>(out)[at] = v;
-    else static_cast<float*>(out)[at] += v;
-}
+struct RowsTile {
+    int s, part, m0;   // slot; part and first output of it
+    int row0, rows, bn;
+    bool shared_w;     // other tiles read the same of W
+};
 
-__device__ __forceinline__ float kept(const Args& a, int r, int c) {
-    const int nb = (a.K + MOE_PAYLOAD_BLOCK - 1) / MOE_PAYLOAD_BLOCK;
-    __nv_fp8_e4m3 v;
-    v.__x = a.x8[(size_t)r * a.K + c];
-    return (float)v * a.x8_scale[(size_t)r * nb + c / MOE_PAYLOAD_BLOCK];
-}
-
-// C [64][64] = sum over l of A(i, l) B(j, l), 256 threads with 4 x 4 each, 16 of l at a time.
-template <typename FA, typename FB>
-__device__ __forceinline__ void product(int L, FA&& fa, FB&& fb, float (&c)[4][4]) {
-    __shared__ float sa[16][65], sb[16][65];
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
-    for (int l0 = 0; l0 < L; l0 += 16) {
-        for (int q = threadIdx.x; q < 1024; q += 256) {
-            const int l = q & 15, i = q >> 4;
-            sa[l][i] = l0 + l < L ? fa(i, l0 + l) : 0.0f;
-            sb[l][i] = l0 + l < L ? fb(i, l0 + l) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int l = 0; l < 16; ++l)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[i][j] = fmaf(sa[l][ti * 4 + i], sb[l][tj * 4 + j], c[i][j]);
-        __syncthreads();
-    }
-}
-
-// 64 rows of one slot times 64 of the outputs: y, or (DX) dx.
 template <bool DX>
-__global__ void __launch_bounds__(256) rows_kernel(const Args a) {
-    pdl_begin();
-    int chunk = blockIdx.y, lo = 0, hi = 0, s = 0;
-    for (; s < a.S; ++s) {
-        if (!slot_rows(a.offsets, s, a.R, lo, hi) && threadIdx.x == 0) raise_status(a.st, kStatusBadShape);
-        const int n = (hi - lo + 63) / 64;
-        if (chunk < n) break;
-        chunk -= n;
+__device__ __forceinline__ RowsTile rows_tile(const RowsArgs& a, const int* pre, int i) {
+    int lo = 0, hi = a.S - 1;  // the last slot with pre[s] <= i
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= i) lo = mid;
+        else hi = mid - 1;
     }
-    if (s == a.S) return;
-    const int r0 = lo + chunk * 64, O = DX ? a.K : a.P * a.N, o0 = blockIdx.x * 64;
-    float c[4][4];
-    product(
-        DX ? a.P * a.N : a.K,
-        [&](int i, int l) { return r0 + i < hi ? bf(a.rows_in[(size_t)(r0 + i) * (DX ? a.P * a.N : a.K) + l]) : 0.0f; },
-        [&](int j, int l) {
-            if (o0 + j >= O) return 0.0f;
-            const int n = DX ? l : o0 + j, k = DX ? o0 + j : l;
-            return bf(a.w[n / a.N][((size_t)s * a.N + n % a.N) * a.K + k]);
-        },
-        c);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = r0 + threadIdx.x / 16 * 4 + i, o = o0 + threadIdx.x % 16 * 4 + j;
-            if (r < hi && o < O) store(a.out[0], (size_t)r * O + o, c[i][j], a.type);
-        }
+    RowsTile t;
+    t.s = lo;
+    int r0, r1;
+    slot_rows(a.offsets, t.s, a.R, r0, r1);
+    const int n = chunks_of(r1 - r0), l = i - pre[t.s], c = l % n, m = l / n;
+    // (equal heights: a chunk of few rows reads as much of W as a high one.  The last of n chunks of
+    // this height is never empty: n - 1 roundings of under 32 rows are less than a chunk, up to n = 7,
+    // and from n = 8 on the height is 256)
+    const int h = ((r1 - r0 + n - 1) / n + 31) & ~31;
+    const int tiles = ((DX ? a.K : a.N) + 255) / 256;
+    t.part = m / tiles;
+    t.m0 = (m - t.part * tiles) * 256;
+    t.row0 = r0 + c * h;
+    t.rows = min(h, r1 - t.row0);
+    t.bn = (t.rows + 31) & ~31;
+    t.shared_w = n > 1;
+    return t;
 }
 
-// 64 x 64 of a slot's dW.
-__global__ void __launch_bounds__(256) weights_kernel(const Args a) {
-    pdl_begin();
-    const int s = blockIdx.z, nt = (a.N + 63) / 64, p = blockIdx.y / nt, n0 = blockIdx.y % nt * 64, k0 = blockIdx.x * 64;
-    int lo, hi;
-    if (!slot_rows(a.offsets, s, a.R, lo, hi) && threadIdx.x == 0) raise_status(a.st, kStatusBadShape);
-    float c[4][4];
-    product(
-        hi - lo, [&](int i, int l) { return n0 + i < a.N ? bf(a.rows_in[((size_t)(lo + l) * a.P + p) * a.N + n0 + i]) : 0.0f; },
-        [&](int j, int l) {
-            if (k0 + j >= a.K) return 0.0f;
-            return a.x ? bf(a.x[(size_t)(lo + l) * a.K + k0 + j]) : kept(a, lo + l, k0 + j);
-        },
-        c);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + threadIdx.x / 16 * 4 + i, k = k0 + threadIdx.x % 16 * 4 + j;
-            if (n < a.N && k < a.K) store(a.out[p], ((size_t)s * a.N + n) * a.K + k, c[i][j], a.type);
+// Warps 2 p and 2 p + 1 share 64 features and two blocks at `out` (as bf16), the copies of which the
+// first one's lane 0 issues.  Copies take 16 rows at a time; the rows after a slot's last full 16 are
+// stored by the threads, as what follows belongs to another slot.
+__device__ __forceinline__ void drain_bf16(const RowsArgs& a, const RowsTile& t, int O, int P, uint32_t tmem, uint32_t out, int m0,
+                                           int q, int lane, int& blocks) {
+    const int pair = q >> 1, f0 = m0 + pair * 64;
+    const bool issuer = !(q & 1) && lane == 0;
+    const uint32_t at = (lane & 7) * 128 + ((((q & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+    for (int r = 0; r < t.rows; r += 32, ++blocks) {
+        uint32_t lo[16], hi[16];
+        tmem_ld_16x256(tmem + r, lo);
+        tmem_ld_16x256(tmem + r + (16u << 16), hi);
+        tmem_ld_wait();
+        const uint32_t block = out + (pair * 2 + (blocks & 1)) * 4096;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            stmatrix_trans(block + i * 1024 + at, pack_bf(lo[4 * i], lo[4 * i + 1]), pack_bf(lo[4 * i + 2], lo[4 * i + 3]),
+                           pack_bf(hi[4 * i], hi[4 * i + 1]), pack_bf(hi[4 * i + 2], hi[4 * i + 3]));
+        fence_async_smem();
+        if (issuer) bulk_wait_read();  // the other block is free, which the next round writes
+        __syncwarp();
+        named_sync(2 + pair, 64);
+        if (issuer) {
+            if (f0 < O) {
+                if (r + 16 <= t.rows) tma_store_3d(&a.out, block, f0, t.part, t.row0 + r);
+                if (r + 32 <= t.rows) tma_store_3d(&a.out, block + 2048, f0, t.part, t.row0 + r + 16);
+            }
+            bulk_commit();
         }
+        __syncwarp();
+        // the rest: 8 rows at a time, 8 threads a row
+        const int piece = lane & 7;
+        for (int k = max(r, t.rows & ~15) - r + (q & 1) * 4 + (lane >> 3); k < min(32, t.rows - r); k += 8)
+            if (f0 + piece * 8 < O)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_ptr) + ((size_t)(t.row0 + r + k) * P + t.part) * O + f0 + piece * 8) =
+                    ld_shared4(block + k * 128 + ((piece ^ (k & 7)) << 4));
+        __syncwarp();
+    }
+}
+
+// fp32: a warp's 32 features of 16 rows at a time.
+__device__ __forceinline__ void drain_f32(const RowsArgs& a, const RowsTile& t, int O, int P, uint32_t tmem, uint32_t out, int m0,
+                                          int q, int lane, int& blocks) {
+    const int f0 = m0 + q * 32;
+    for (int r = 0; r < t.rows; r += 16, ++blocks) {
+        float v[16];
+        tmem_ld16(tmem + r, v);
+        tmem_ld_wait();
+        if (r + 16 > t.rows) {
+            float* dst = static_cast<float*>(a.out_ptr) + ((size_t)(t.row0 + r) * P + t.part) * O + f0 + lane;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (r + k < t.rows && f0 + lane < O) {
+                    float* d = dst + (size_t)k * P * O;
+                    *d = a.type == MOE_OUT_F32_ADD ? *d + v[k] : v[k];
+                }
+            __syncwarp();
+            break;
+        }
+        const uint32_t block = out + (q * 2 + (blocks & 1)) * 2048;
+        if (lane == 0) bulk_wait_read_but<1>();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) st_shared(block + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) + (lane & 3) * 4, to_u(v[k]));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (f0 < O) put(&a.out, a.type, block, f0, t.part, t.row0 + r);
+            bulk_commit();
+        }
+        __syncwarp();
+    }
+}
+
+template <bool DX>
+__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ RowsArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kOutBytes);  // (the leader's)
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 2;  // (the leader's)
+    uint64_t* done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barriers");
+    int* pre = reinterpret_cast<int*>(smem + kRing + kOutBytes + 256);  // tiles before each slot
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned long long limit = a.st.limit_ns;
+    const int rank = (int)cluster_rank();
+    const int O = DX ? a.K : a.N, out_parts = DX ? 1 : a.P;
+    const int m_tiles = (O + 255) / 256 * out_parts;
+    const int kc1 = ((DX ? a.N : a.K) + 63) / 64, kc = kc1 * (DX ? a.P : 1);  // chunks of a part, of a tile
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&tfull[s]), 1);
+            mbar_init(smem_u32(&tempty[s]), 8);
+        }
+        mbar_init(smem_u32(done), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.w[0]);
+        tma_prefetch_desc(&a.in[3]);
+        tma_prefetch_desc(&a.out);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    pdl_wait();
+    if (warp == 0) {
+        const int per = (a.S + 31) / 32, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
+        int sum = 0;
+        bool fits = true;
+        for (int s = s0; s < s1; ++s) {
+            int r0, r1;
+            fits &= slot_rows(a.offsets, s, a.R, r0, r1);
+            sum += chunks_of(r1 - r0) * m_tiles;
+        }
+        if (!fits && blockIdx.x == 0) raise_status(a.st, kStatusBadShape);
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        int run = incl - sum;
+        for (int s = s0; s < s1; ++s) {
+            int r0, r1;
+            slot_rows(a.offsets, s, a.R, r0, r1);
+            pre[s] = run;
+            run += chunks_of(r1 - r0) * m_tiles;
+        }
+        if (lane == 31) pre[a.S] = incl;
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the barriers of both CTAs exist before either is signalled
+    tc_fence_after();
+    pdl_launch_dependents();  // (not before the tensor memory is this pair's: the next kernel takes its own)
+    const uint32_t tbase = *tmem_slot;
+    const int n_tiles = pre[a.S], first = blockIdx.x / 2, step = gridDim.x / 2;
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        raise_status(a.st, kStatusWaitTimeout);
+    };
+    const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), stage_u = smem_u32(smem);
+    const uint32_t lead_full = leader_addr(full_u), lead_tempty = leader_addr(smem_u32(tempty));
+
+    if (warp == 0) {
+        const uint64_t pol_once = policy_evict_first(), pol = policy_evict_normal();
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0, used = 0;
+        for (int i = first; i < n_tiles && ok; i += step) {
+            const RowsTile t = rows_tile<DX>(a, pre, i);
+            const int m0 = t.m0 + rank * 128, n16 = t.bn / 32, row0 = t.row0 + rank * n16 * 16;
+            const uint64_t pol_w = t.shared_w ? pol : pol_once;
+            for (int c = 0; c < kc; ++c) {
+                if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
+                const int part = DX ? (c >= kc1) : t.part, at = (DX && part ? c - kc1 : c) * 64;
+                if (elect_one()) {
+                    const uint32_t sa = stage_u + stage * kStageBytes, fb = lead_full + stage * 8;
+                    // the leader expects the bytes of both
+                    if (rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * kHalf + t.bn * 128);
+                    if (DX) {
+                        tma_load_3d_pair(sa, &a.w[part], fb, m0, at, t.s, pol_w);
+                        tma_load_3d_pair(sa + kHalf / 2, &a.w[part], fb, m0 + 64, at, t.s, pol_w);
+                    } else {
+                        tma_load_3d_pair(sa, &a.w[part], fb, at, m0, t.s, pol_w);
+                    }
+                    for (int bit = 3, off = 0; bit >= 0; --bit)
+                        if (n16 & (1 << bit)) {
+                            tma_load_3d_pair(sa + kHalf + off * 2048, &a.in[bit], fb, at, DX ? part : 0, row0 + off * 16, pol);
+                            off += 1 << bit;
+                        }
+                }
+                __syncwarp();
+                used |= 1u << stage;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        // every stage's last products are done, so its copies have landed
+        for (int s = 0; s < kStages; ++s) {
+            if ((used >> stage) & 1u) mbar_wait(empty_u + stage * 8, phase ^ 1, limit);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint64_t ad0 = DX ? umma_desc_mn_sw128(stage_u, kHalf / 2) : umma_desc_sw128(stage_u);
+            const uint64_t bd0 = umma_desc_sw128(stage_u + kHalf);
+            constexpr int kAStep = DX ? 128 : 2;  // 16 of the contraction, in 16 bytes
+            const int last = (DX ? a.N : a.K) - (kc1 - 1) * 64;  // width of a part's last chunk
+            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
+                const RowsTile t = rows_tile<DX>(a, pre, i);
+                const uint32_t idesc = umma_idesc_bf16(256, t.bn) | (DX ? kIdescAMnMajor : 0u);
+                const uint32_t d = tbase + (n & 1) * 256;
+                if (!(ok = wait_cluster(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, limit))) break;
+                tc_fence_after();
+                for (int c = 0; c < kc; ++c) {
+                    if (!(ok = wait_cluster(full_u + stage * 8, phase, abort_flag, limit))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t ad = ad0 + stage * (kStageBytes >> 4), bd = bd0 + stage * (kStageBytes >> 4);
+                        const int left = c == kc1 - 1 || c == kc - 1 ? last : 64;
+                        umma_bf16_pair(d, ad, bd, idesc, c > 0);
+                        if (left > 16) umma_bf16_pair(d, ad + kAStep, bd + 2, idesc, 1);
+                        if (left > 32) umma_bf16_pair(d, ad + 2 * kAStep, bd + 4, idesc, 1);
+                        if (left > 48) umma_bf16_pair(d, ad + 3 * kAStep, bd + 6, idesc, 1);
+                        umma_commit_pair(empty_u + stage * 8);
+                    }
+                    __syncwarp();
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]));
+                __syncwarp();
+            }
+            if (!ok && lane == 0) give_up();
+            // all products are complete before the tensor memory is freed
+            if (elect_one()) umma_commit_pair(smem_u32(done));
+            __syncwarp();
+        }
+        mbar_wait(smem_u32(done), 0, limit);
+    } else {
+        const int q = warp & 3;
+        bool ok = true;
+        int blocks = 0;
+        for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
+            const RowsTile t = rows_tile<DX>(a, pre, i);
+            ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit);
+            if (!(ok = named_and(2 + (q >> 1), 64, ok))) break;  // (the two warps that share drain_bf16's barrier)
+            tc_fence_after();
+            const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16), out = stage_u + kRing;
+            if (a.type == MOE_OUT_BF16) drain_bf16(a, t, O, out_parts, tmem, out, t.m0 + rank * 128, q, lane, blocks);
+            else drain_f32(a, t, O, out_parts, tmem, out, t.m0 + rank * 128, q, lane, blocks);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_tempty + (n & 1) * 8);
+        }
+        if (!ok && lane == 0) give_up();
+        if (lane == 0) bulk_wait();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may signal it or read its memory
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tbase, 512);
+}
+
+// ---------------------------------------------------------------- dW
+// One pair's tile: 256 of N (128 of dy's columns in each CTA) times 256 of K (128 of x's columns in
+// each), summed over the slot's rows, 64 at a time; both operands are MN-major.  Of a slot's last
+// chunk as many 16 rows are copied and multiplied as it has; the rows of the next slot among them are
+// set to zero in shared memory, in both operands, so whatever they hold stays out.
+// Rows in 8 bits are copied as codes into the lower half of their operand's place, taken from there
+// into registers and written back as bf16 over the whole of it.
+struct WeightArgs {
+    CUtensorMap dy[3];   // box {64, 1, 16 << j} of dy [R][P][N]
+    CUtensorMap x[3];    // of x [R][1][K]; codes: box {128, 1, 16 << j}
+    CUtensorMap out[2];  // box {64, 32, 1} bf16, {32, 32, 1} fp32 of dw [S][N][K]
+    const float* scale;  // [R][n_blk]
+    const int32_t* offsets;
+    int R, K, N, P, S, type, n_blk, n_tiles;
+    DevStatus st;
+};
+constexpr int kWeightThreads = 320;  // copies, products, four warps on the rows, four that drain accumulators
+constexpr int kWeightOut = 4 * 2 * 4096;  // two blocks of 32 x 128 bytes of each draining warp
+constexpr int kWeightSmem = 1024 + kRing + kWeightOut + 512;
+static_assert(kWeightSmem <= 227 * 1024, "shared memory overflow");
+
+struct WeightTile {
+    int s, part, n0, k0;
+    int row0, rows;
+};
+
+__device__ __forceinline__ WeightTile weight_tile(const WeightArgs& a, int i) {
+    const int kt = (a.K + 255) / 256, nt = (a.N + 255) / 256;
+    WeightTile t;
+    t.k0 = i % kt * 256;
+    i /= kt;
+    t.n0 = i % nt * 256;
+    i /= nt;
+    t.part = i % a.P;
+    t.s = i / a.P;
+    int r1;
+    slot_rows(a.offsets, t.s, a.R, t.row0, r1);
+    t.rows = r1 - t.row0;
+    return t;
+}
+
+// 16 codes times their scale as bf16.
+__device__ __forceinline__ void decode16(const uint4& c, float scale, uint32_t (&w)[8]) {
+    const uint32_t v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((v[i >> 1] >> (i & 1) * 16) & 0xffffu), __NV_E4M3);
+        const float2 p = __half22float2(__half2(h));
+        w[i] = pack_bf(to_u(p.x * scale), to_u(p.y * scale));
+    }
+}
+
+template <bool X8>
+__global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kWeightOut);  // (the leader's) copies that need no work, of both
+    uint64_t* empty = full + kStages;
+    uint64_t* landed = empty + kStages;  // this CTA's copies that need work
+    uint64_t* ready = landed + kStages;  // ... and have had it
+    uint64_t* other = ready + kStages;   // (the leader's) the same in the other CTA
+    uint64_t* tfull = other + kStages;
+    uint64_t* tempty = tfull + 2;        // (the leader's)
+    uint64_t* done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((5 * kStages + 5) * 8 + 8 <= 512, "barriers");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned long long limit = a.st.limit_ns;
+    const int rank = (int)cluster_rank();
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&landed[s]), 1);
+            mbar_init(smem_u32(&ready[s]), 4);
+            mbar_init(smem_u32(&other[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&tfull[s]), 1);
+            mbar_init(smem_u32(&tempty[s]), 8);
+        }
+        mbar_init(smem_u32(done), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.dy[2]);
+        tma_prefetch_desc(&a.x[2]);
+        tma_prefetch_desc(&a.out[0]);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    pdl_wait();
+    if (warp == 0 && blockIdx.x == 0)
+        for (int s = lane; s < a.S; s += 32) {
+            int r0, r1;
+            if (!slot_rows(a.offsets, s, a.R, r0, r1)) raise_status(a.st, kStatusBadShape);
+        }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the barriers of both CTAs exist before either is signalled
+    tc_fence_after();
+    pdl_launch_dependents();  // (not before the tensor memory is this pair's)
+    const uint32_t tbase = *tmem_slot;
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        raise_status(a.st, kStatusWaitTimeout);
+    };
+    const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed), ready_u = smem_u32(ready);
+    const uint32_t other_u = smem_u32(other), stage_u = smem_u32(smem);
+    const uint32_t lead_full = leader_addr(full_u), lead_tempty = leader_addr(smem_u32(tempty)), lead_other = leader_addr(other_u);
+
+    if (warp == 0) {
+        const uint64_t pol = policy_evict_normal();
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0, used = 0, used_land = 0, land_phase = 0;
+        for (int i = first; i < a.n_tiles && ok; i += step) {
+            const WeightTile t = weight_tile(a, i);
+            const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 128;
+            for (int r = 0; r < t.rows; r += 64) {
+                const int left = min(64, t.rows - r), n16 = (left + 15) / 16;
+                const bool odd = left & 15, work = X8 || odd;
+                if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
+                if (elect_one()) {
+                    const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kHalf;
+                    const uint32_t fb = lead_full + stage * 8, lb = landed_u + stage * 8;
+                    const uint32_t dy_bytes = n16 * 4096, x_bytes = X8 ? n16 * 2048 : n16 * 4096;
+                    if (!odd && rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * (dy_bytes + (X8 ? 0 : x_bytes)));
+                    if (work) mbar_arrive_expect_tx(lb, X8 && !odd ? x_bytes : dy_bytes + x_bytes);
+                    for (int bit = 2, off = 0; bit >= 0; --bit)
+                        if (n16 & (1 << bit)) {
+                            const int row = t.row0 + r + off * 16;
+                            const uint32_t o = off * 2048;
+                            if (odd) {
+                                tma_load_3d(sa + o, &a.dy[bit], lb, n0, t.part, row, pol);
+                                tma_load_3d(sa + o + kHalf / 2, &a.dy[bit], lb, n0 + 64, t.part, row, pol);
+                            } else {
+                                tma_load_3d_pair(sa + o, &a.dy[bit], fb, n0, t.part, row, pol);
+                                tma_load_3d_pair(sa + o + kHalf / 2, &a.dy[bit], fb, n0 + 64, t.part, row, pol);
+                            }
+                            if (X8) {
+                                tma_load_3d(sb + o, &a.x[bit], lb, k0, 0, row, pol);
+                            } else if (odd) {
+                                tma_load_3d(sb + o, &a.x[bit], lb, k0, 0, row, pol);
+                                tma_load_3d(sb + o + kHalf / 2, &a.x[bit], lb, k0 + 64, 0, row, pol);
+                            } else {
+                                tma_load_3d_pair(sb + o, &a.x[bit], fb, k0, 0, row, pol);
+                                tma_load_3d_pair(sb + o + kHalf / 2, &a.x[bit], fb, k0 + 64, 0, row, pol);
+                            }
+                            off += 1 << bit;
+                        }
+                }
+                __syncwarp();
+                used |= 1u << stage;
+                used_land = work ? used_land | 1u << stage : used_land & ~(1u << stage);
+                if (work) land_phase ^= 1u << stage;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        // every stage's last products are done, so its copies have landed
+        for (int s = 0; s < kStages; ++s) {
+            if ((used >> stage) & 1u) {
+                if (!ok && ((used_land >> stage) & 1u)) mbar_wait(landed_u + stage * 8, ((land_phase >> stage) & 1u) ^ 1, limit);
+                mbar_wait(empty_u + stage * 8, phase ^ 1, limit);
+            }
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        bool ok = true;
+        int stage = 0, n = 0;
+        uint32_t full_phase = 0, work_phase = 0;  // (of each stage: not every chunk uses both)
+        if (rank == 0) {
+            const uint32_t idesc = umma_idesc_bf16(256, 256) | kIdescAMnMajor | kIdescBMnMajor;
+            const uint64_t ad0 = umma_desc_mn_sw128(stage_u, kHalf / 2), bd0 = umma_desc_mn_sw128(stage_u + kHalf, kHalf / 2);
+            for (int i = first; i < a.n_tiles && ok; i += step) {
+                const WeightTile t = weight_tile(a, i);
+                if (t.rows == 0) continue;
+                const uint32_t d = tbase + (n & 1) * 256;
+                if (!(ok = wait_cluster(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, limit))) break;
+                tc_fence_after();
+                for (int r = 0; r < t.rows; r += 64) {
+                    const int left = min(64, t.rows - r);
+                    if (!(left & 15)) {
+                        if (!(ok = wait_cluster(full_u + stage * 8, (full_phase >> stage) & 1u, abort_flag, limit))) break;
+                        full_phase ^= 1u << stage;
+                    }
+                    if (X8 || (left & 15)) {
+                        if (!(ok = wait_cluster(ready_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit) &&
+                                   wait_cluster(other_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit)))
+                            break;
+                        work_phase ^= 1u << stage;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t ad = ad0 + stage * (kStageBytes >> 4), bd = bd0 + stage * (kStageBytes >> 4);
+                        umma_bf16_pair(d, ad, bd, idesc, r > 0);
+                        if (left > 16) umma_bf16_pair(d, ad + 128, bd + 128, idesc, 1);
+                        if (left > 32) umma_bf16_pair(d, ad + 256, bd + 256, idesc, 1);
+                        if (left > 48) umma_bf16_pair(d, ad + 384, bd + 384, idesc, 1);
+                        umma_commit_pair(empty_u + stage * 8);
+                    }
+                    __syncwarp();
+                    if (++stage == kStages) stage = 0;
+                }
+                if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]));
+                __syncwarp();
+                ++n;
+            }
+            if (!ok && lane == 0) give_up();
+            // all products are complete before the tensor memory is freed
+            if (elect_one()) umma_commit_pair(smem_u32(done));
+            __syncwarp();
+        } else {
+            // the other CTA's rows are ready: the leader hears of it from this warp, as the arrival
+            // there takes 500 cycles
+            for (int i = first; i < a.n_tiles && ok; i += step) {
+                const WeightTile t = weight_tile(a, i);
+                for (int r = 0; r < t.rows; r += 64) {
+                    if (X8 || (min(64, t.rows - r) & 15)) {
+                        if (!(ok = warp_wait(ready_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit))) break;
+                        work_phase ^= 1u << stage;
+                        if (lane == 0) mbar_arrive_cluster(lead_other + stage * 8);
+                        __syncwarp();
+                    }
+                    if (++stage == kStages) stage = 0;
+                }
+            }
+            if (!ok && lane == 0) give_up();
+        }
+        mbar_wait(smem_u32(done), 0, limit);
+    } else if (warp < 6) {
+        const int tid = threadIdx.x - 64;
+        bool ok = true;
+        int stage = 0;
+        uint32_t land_phase = 0;
+        for (int i = first; i < a.n_tiles && ok; i += step) {
+            const WeightTile t = weight_tile(a, i);
+            const int blk = (t.k0 + rank * 128) / MOE_PAYLOAD_BLOCK;
+            for (int r = 0; r < t.rows; r += 64) {
+                const int left = min(64, t.rows - r), rows16 = (left + 15) & ~15;
+                if (X8 || (left & 15)) {
+                    const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kHalf;
+                    float scale = 0.0f;
+                    if (X8 && (tid >> 1) < left && blk < a.n_blk) scale = __ldg(a.scale + (size_t)(t.row0 + r + (tid >> 1)) * a.n_blk + blk);
+                    ok = warp_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, abort_flag, limit);
+                    land_phase ^= 1u << stage;
+                    if (X8) {
+                        // two threads a row, 64 columns each (pieces of 16 bytes in the order of the
+                        // swizzle, the second thread's in another, so that both find their banks free)
+                        const int row = tid >> 1, half = tid & 1;
+                        uint4 c[4];
+                        if (ok && row < left)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                c[k] = ld_shared4(sb + row * 128 + (((half * 4 + (k ^ half * 2)) ^ (row & 7)) << 4));
+                        if (!(ok = named_and(1, 128, ok))) break;
+                        if (row < rows16) {
+                            const uint32_t to = sb + half * (kHalf / 2) + row * 128;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                                if (row < left) decode16(c[k], scale, w);
+                                const int piece = (k ^ half * 2) * 2;
+                                st_shared4(to + ((piece ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                                st_shared4(to + (((piece + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
+                            }
+                        }
+                    } else if (!ok) {
+                        break;
+                    }
+                    if (left & 15) {
+                        // the rows of the last 16 that are not the slot's, 8 threads a row
+                        const int row = rows16 - 16 + (tid >> 3);
+                        if (row >= left) {
+                            const uint32_t o = row * 128 + (tid & 7) * 16;
+                            st_shared4(sa + o, 0, 0, 0, 0);
+                            st_shared4(sa + o + kHalf / 2, 0, 0, 0, 0);
+                            if (!X8) {
+                                st_shared4(sb + o, 0, 0, 0, 0);
+                                st_shared4(sb + o + kHalf / 2, 0, 0, 0, 0);
+                            }
+                        }
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ready_u + stage * 8);
+                }
+                if (++stage == kStages) stage = 0;
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    } else {
+        const int q = warp & 3;
+        const uint32_t out = stage_u + kRing + q * 2 * 4096;
+        bool ok = true;
+        int blocks = 0, n = 0;
+        for (int i = first; i < a.n_tiles; i += step) {
+            const WeightTile t = weight_tile(a, i);
+            if (t.rows == 0 && a.type == MOE_OUT_F32_ADD) continue;
+            if (t.rows) {
+                if (!(ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
+                tc_fence_after();
+            }
+            const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
+            const int row = t.n0 + rank * 128 + q * 32;
+            const int cols = min(256, a.K - t.k0), by = a.type == MOE_OUT_BF16 ? 64 : 32;  // 128 bytes
+            for (int c = 0; c < cols; c += by, ++blocks) {
+                const uint32_t block = out + (blocks & 1) * 4096, to = block + lane * 128;
+                if (lane == 0) bulk_wait_read_but<1>();
+                __syncwarp();
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {  // 32 bytes of each row at a time
+                    float v[16];
+                    uint32_t w[8];
+                    if (a.type == MOE_OUT_BF16) {
+                        if (t.rows) {
+                            tmem_ld16(tmem + c + h * 16, v);
+                            tmem_ld_wait();
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = t.rows ? pack_bf(to_u(v[2 * k]), to_u(v[2 * k + 1])) : 0u;
+                    } else {
+                        if (t.rows) {
+                            tmem_ld16(tmem + c + (h >> 1) * 16, v);
+                            tmem_ld_wait();
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = t.rows ? to_u(h & 1 ? v[8 + k] : v[k]) : 0u;
+                    }
+                    st_shared4(to + (((2 * h) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                    st_shared4(to + (((2 * h + 1) ^ (lane & 7)) << 4), w[4], w[5], w[6], w[7]);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (row < a.N) put(&a.out[t.part], a.type, block, t.k0 + c, row, t.s);
+                    bulk_commit();
+                }
+                __syncwarp();
+            }
+            if (t.rows) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(lead_tempty + (n & 1) * 8);
+                ++n;
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        if (lane == 0) bulk_wait();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may signal it or read its memory
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tbase, 512);
 }
 
 int check_project(const moe_project_t* p, int rows) {
@@ -127,6 +760,8 @@ int check_project(const moe_project_t* p, int rows) {
     if (p->n_slots > kMaxSlots) return api_fail(MOE_ERR_UNSUPPORTED, "n_slots %d > %d", p->n_slots, kMaxSlots);
     if (p->in_features > kMaxFeatures || p->out_features > kMaxFeatures)
         return api_fail(MOE_ERR_UNSUPPORTED, "more than %d features", kMaxFeatures);
+    if ((double)p->in_features * p->out_features * p->n_slots * p->n_parts > 0x1p46)
+        return api_fail(MOE_ERR_UNSUPPORTED, "weights of more than 2^46 elements");
     if (rows > INT32_MAX / 2) return api_fail(MOE_ERR_UNSUPPORTED, "too many rows");
     return MOE_OK;
 }
@@ -144,21 +779,83 @@ int need_parts(const moe_project_t* p, const void* a, const void* b, const char*
     return b ? api_fail(MOE_ERR_INVALID_ARG, "%s is given, but n_parts is 1", name2) : MOE_OK;
 }
 
-Args make_args(const moe_project_t* p, int rows, const int32_t* offsets, const void* w, const void* w2) {
-    Args a = {};
+int launched(cudaError_t e, const char* what) {
+    return e == cudaSuccess ? MOE_OK : api_fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+template <typename Kern, typename A>
+int launch_pairs(Kern kern, std::atomic<uint64_t>& configured, int threads, int smem, long tiles, cudaStream_t stream, const A& a,
+                 const char* what) {
+    const int rc = launched(configure_once(configured,
+                                           [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); }),
+                            what);
+    if (rc) return rc;
+    const int pairs = (int)std::min<long>(tiles, std::max(1, num_sms() / 2));
+    return launched(launch_pdl_cluster(kern, dim3(2 * pairs), dim3(threads), smem, stream, 2, a), what);
+}
+
+// A tensor that is written: box of 128 bytes.
+int out_map(CUtensorMap* map, void* out, uint64_t d0, uint64_t d1, uint64_t d2, int type, uint32_t box1, uint32_t box2) {
+    const uint64_t size = type == MOE_OUT_BF16 ? 2 : 4;
+    return type == MOE_OUT_BF16 ? make_tmap_3d(map, out, d0, d1, d2, d0 * size, d0 * d1 * size, 64, box1, box2)
+                                : make_tmap_f32(map, out, d0, d1, d2, 32, box1, box2);
+}
+
+template <bool DX>
+int rows_product(const moe_project_t* p, int rows, const void* in, const int32_t* offsets, const void* w, const void* w2, void* out,
+                 int type, const DevStatus& st, cudaStream_t stream) {
+    RowsArgs a;
+    const uint64_t K = p->in_features, N = p->out_features, S = p->n_slots, P = p->n_parts, R = rows;
+    int rc = make_tmap_3d(&a.w[0], w, K, N, S, K * 2, K * N * 2, 64, DX ? 64 : 128, 1);
+    if (rc) return rc;
+    a.w[1] = a.w[0];
+    if (w2 && (rc = make_tmap_3d(&a.w[1], w2, K, N, S, K * 2, K * N * 2, 64, DX ? 64 : 128, 1))) return rc;
+    const uint64_t C = DX ? N : K, CP = DX ? P : 1, O = DX ? K : N, OP = DX ? 1 : P;
+    for (int j = 0; j < 4; ++j)
+        if ((rc = make_tmap_3d(&a.in[j], in, C, CP, R, C * 2, C * CP * 2, 64, 1, 16u << j))) return rc;
+    if ((rc = out_map(&a.out, out, O, OP, R, type, 1, 16))) return rc;
+    a.offsets = offsets;
+    a.out_ptr = out;
     a.R = rows;
     a.K = p->in_features;
     a.N = p->out_features;
     a.P = p->n_parts;
     a.S = p->n_slots;
-    a.w[0] = static_cast<const uint16_t*>(w);
-    a.w[1] = static_cast<const uint16_t*>(w2);
-    a.offsets = offsets;
-    return a;
+    a.type = type;
+    a.st = st;
+    static std::atomic<uint64_t> configured{0};
+    const long tiles = (long)((O + 255) / 256 * OP) * (rows / 256 + std::min(rows, p->n_slots));  // (as many as there may be)
+    return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, tiles, stream, a, DX ? "expert gradient" : "expert projection");
 }
 
-int launched(cudaError_t e, const char* what) {
-    return e == cudaSuccess ? MOE_OK : api_fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+template <bool X8>
+int weights_product(const moe_project_t* p, int rows, const void* dy, const void* x, const float* scale, const int32_t* offsets, void* dw,
+                    void* dw2, int type, const DevStatus& st, cudaStream_t stream) {
+    WeightArgs a;
+    const uint64_t K = p->in_features, N = p->out_features, S = p->n_slots, P = p->n_parts, R = rows;
+    int rc;
+    for (int j = 0; j < 3; ++j)
+        if ((rc = make_tmap_3d(&a.dy[j], dy, N, P, R, N * 2, N * P * 2, 64, 1, 16u << j)) ||
+            (rc = X8 ? make_tmap_3d(&a.x[j], x, K, 1, R, K, K, 128, 1, 16u << j, true)
+                     : make_tmap_3d(&a.x[j], x, K, 1, R, K * 2, K * 2, 64, 1, 16u << j)))
+            return rc;
+    if ((rc = out_map(&a.out[0], dw, K, N, S, type, 32, 1))) return rc;
+    a.out[1] = a.out[0];
+    if (dw2 && (rc = out_map(&a.out[1], dw2, K, N, S, type, 32, 1))) return rc;
+    a.scale = scale;
+    a.offsets = offsets;
+    a.R = rows;
+    a.K = p->in_features;
+    a.N = p->out_features;
+    a.P = p->n_parts;
+    a.S = p->n_slots;
+    a.type = type;
+    a.n_blk = (p->in_features + MOE_PAYLOAD_BLOCK - 1) / MOE_PAYLOAD_BLOCK;
+    a.st = st;
+    const uint64_t tiles = (K + 255) / 256 * ((N + 255) / 256) * P * S;
+    a.n_tiles = (int)tiles;
+    static std::atomic<uint64_t> configured{0};
+    return launch_pairs(weights_kernel<X8>, configured, kWeightThreads, kWeightSmem, (long)tiles, stream, a, "expert weight gradient");
 }
 
 }  // namespace
@@ -177,14 +874,9 @@ int moe_expert_project(const moe_project_t* project, int rows, const void* x, co
         (rc = api_need(out, "out")))
         return rc;
     PdlScope pdl(rows);
-    Args a = make_args(project, rows, offsets, w, w2);
-    if ((rc = api_device_status(&a.st))) return rc;
-    a.rows_in = static_cast<const uint16_t*>(x);
-    a.out[0] = out;
-    a.type = out_type;
-    return launched(launch_pdl(rows_kernel<false>, dim3((a.P * a.N + 63) / 64, (rows + 63) / 64 + a.S), dim3(256), 0,
-                               reinterpret_cast<cudaStream_t>(stream), a),
-                    "expert projection launch");
+    DevStatus st;
+    if ((rc = api_device_status(&st))) return rc;
+    return rows_product<false>(project, rows, x, offsets, w, w2, out, out_type, st, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int moe_expert_project_backward(const moe_project_t* project, int rows, const void* dy, const void* x, const uint8_t* x8,
@@ -211,25 +903,12 @@ int moe_expert_project_backward(const moe_project_t* project, int rows, const vo
         if (x8 && project->in_features % 16) return api_fail(MOE_ERR_INVALID_ARG, "x8 needs in_features %% 16 == 0");
     }
     PdlScope pdl(rows);
-    Args a = make_args(project, rows, offsets, w, w2);
-    if ((rc = api_device_status(&a.st))) return rc;
-    a.rows_in = static_cast<const uint16_t*>(dy);
-    a.x = static_cast<const uint16_t*>(x);
-    a.x8 = x8;
-    a.x8_scale = x8_scale;
-    if (dx) {
-        a.out[0] = dx;
-        a.type = dx_type;
-        if ((rc = launched(launch_pdl(rows_kernel<true>, dim3((a.K + 63) / 64, (rows + 63) / 64 + a.S), dim3(256), 0, s, a),
-                           "expert gradient launch")))
-            return rc;
-    }
+    DevStatus st;
+    if ((rc = api_device_status(&st))) return rc;
+    if (dx && (rc = rows_product<true>(project, rows, dy, offsets, w, w2, dx, dx_type, st, s))) return rc;
     if (!dw) return MOE_OK;
-    a.out[0] = dw;
-    a.out[1] = dw2;
-    a.type = dw_type;
-    return launched(launch_pdl(weights_kernel, dim3((a.K + 63) / 64, (a.N + 63) / 64 * a.P, a.S), dim3(256), 0, s, a),
-                    "expert weight gradient launch");
+    return x8 ? weights_product<true>(project, rows, dy, x8, x8_scale, offsets, dw, dw2, dw_type, st, s)
+              : weights_product<false>(project, rows, dy, x, nullptr, offsets, dw, dw2, dw_type, st, s);
 }
 
 }  // extern "C"

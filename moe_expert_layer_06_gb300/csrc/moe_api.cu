@@ -98,16 +98,15 @@ static EncodeTiledFn encode_fn() {
 }
 
 static int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-                          uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8, int swizzle_bytes,
-                          bool narrow) {
+                          uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, CUtensorMapDataType type,
+                          int swizzle_bytes, bool narrow) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     const cuuint64_t dims[3] = {d0, d1, d2};
     const cuuint64_t strides[2] = {stride1, stride2};
     const cuuint32_t box[3] = {box0, box1, box2};
     const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                    const_cast<void*>(base), dims, strides, box, estr,
+    CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE,
                     swizzle_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
                     : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
@@ -120,14 +119,20 @@ static int encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint6
 
 int make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                  uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, bool fp8) {
-    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, fp8, 128, false);
+    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2,
+                          fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 128, false);
+}
+
+int make_tmap_f32(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0, uint32_t box1,
+                  uint32_t box2) {
+    return encode_tmap_3d(map, base, d0, d1, d2, d0 * 4, d0 * d1 * 4, box0, box1, box2, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 128, false);
 }
 
 int make_tmap_rows(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                    uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2, int swizzle_bytes) {
     const uint64_t pitch = d1 > 1 ? stride1 : stride2;
-    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, false, swizzle_bytes,
-                          pitch % 128 != 0 && d0 > box0);
+    return encode_tmap_3d(map, base, d0, d1, d2, stride1, stride2, box0, box1, box2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          swizzle_bytes, pitch % 128 != 0 && d0 > box0);
 }
 
 // weight stack [n][rows][K] -> dims {K, rows, n}, box {64, 128, 1}
