@@ -92,65 +92,86 @@ __device__ __forceinline__ void sigmoids(float g, float& s, float& rest) {
     if (g != g) s = g;
 }
 
-// Block u (of `blocks` a row) of the CTA's: its row and its place in it.
+// Block u of the CTA's, of `n` a row.  Its row without a division where there are few of them: below
+// 4096, at < n + 64 and at * n < 2^32, for which the rounded-up reciprocal gives at / n exactly;
+// above, at / n is 0 or 1.
+struct Blocks {
+    int n;
+    uint32_t reciprocal;  // 2^32 / n + 1, 0 from 4096 on
+};
 struct Place {
     size_t row;
     int block;
 };
-__device__ __forceinline__ Place place_of(size_t first, int u, int blocks) {
-    const size_t row0 = first / blocks;
-    const unsigned at = (unsigned)(first - row0 * blocks) + u;
-    return {row0 + at / (unsigned)blocks, (int)(at % (unsigned)blocks)};
+constexpr int kMostUnits = 64;  // of a CTA
+__device__ __forceinline__ Place place_of(size_t first, int u, Blocks b) {
+    const size_t row0 = first >> 32 ? first / b.n : (uint32_t)first / (uint32_t)b.n;
+    const uint32_t at = (uint32_t)(first - row0 * b.n) + u;
+    const uint32_t q = b.reciprocal ? (b.n == 1 ? at : __umulhi(at, b.reciprocal)) : at >= (uint32_t)b.n;
+    return {row0 + q, (int)(at - q * b.n)};
 }
 
-template <int U>  // blocks of a group of lanes
-__global__ void __launch_bounds__(kThreads) keep_kernel(const uint16_t* __restrict__ x, size_t rows, int cols, int blocks,
+// EVEN: rows are whole blocks, which then follow one another whatever the row.
+template <int U, bool EVEN>  // U: blocks of a group of lanes
+__global__ void __launch_bounds__(kThreads) keep_kernel(const uint16_t* __restrict__ x, size_t rows, int cols, Blocks blocks,
                                                         uint8_t* __restrict__ codes, float* __restrict__ scale) {
     pdl_begin();
-    const size_t first = (size_t)blockIdx.x * (kGroups * U);
+    const size_t first = (size_t)blockIdx.x * (kGroups * U), total = rows * blocks.n;
     const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     uint4 v[U];
+    size_t at[U];  // of the lane's columns; ~0: none
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const Place p = place_of(first, i * kGroups + group, blocks);
-        const int c = p.block * kBlock + lane * 8;
+        const size_t b = first + i * kGroups + group;
+        if (EVEN) {
+            at[i] = b < total ? b * kBlock + lane * 8 : ~size_t(0);
+        } else {
+            const Place p = place_of(first, i * kGroups + group, blocks);
+            const int c = p.block * kBlock + lane * 8;
+            at[i] = b < total && c < cols ? p.row * cols + c : ~size_t(0);
+        }
         v[i] = make_uint4(0, 0, 0, 0);
-        if (p.row < rows && c < cols) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + p.row * cols + c));
+        if (at[i] != ~size_t(0)) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + at[i]));
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const Place p = place_of(first, i * kGroups + group, blocks);
-        const int c = p.block * kBlock + lane * 8;
         const int e = block_exponent(v[i]);
-        if (p.row >= rows) continue;
-        if (c < cols) *reinterpret_cast<uint2*>(codes + p.row * cols + c) = encode8(v[i], e);
-        if (lane == 0) scale[p.row * blocks + p.block] = pow2(e);
+        if (at[i] != ~size_t(0)) *reinterpret_cast<uint2*>(codes + at[i]) = encode8(v[i], e);
+        if (lane == 0 && at[i] != ~size_t(0)) scale[first + i * kGroups + group] = pow2(e);
     }
+}
+
+// Where a lane's gate lies in gate_up and codes (the up `inter` further on), and in h; ~0: none.
+struct GatePlace {
+    size_t gate, h, scale;
+};
+__device__ __forceinline__ GatePlace gate_place(size_t first, int u, int lane, size_t rows, int inter, Blocks blocks) {
+    const Place p = place_of(first, u, blocks);
+    const int c = p.block * kBlock + lane * 8;
+    if (p.row >= rows || c >= inter) return {~size_t(0), 0, 0};
+    return {p.row * 2 * inter + c, p.row * inter + c, p.row * 2 * blocks.n + p.block};
 }
 
 template <int U>
 __global__ void __launch_bounds__(kThreads) swiglu_keep_kernel(const uint16_t* __restrict__ gate_up, size_t rows, int inter,
-                                                               int blocks, uint16_t* __restrict__ h,
+                                                               Blocks blocks, uint16_t* __restrict__ h,
                                                                uint8_t* __restrict__ codes, float* __restrict__ scale) {
     pdl_begin();
     const size_t first = (size_t)blockIdx.x * (kGroups * U);
     const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     uint4 g[U], u[U];
+    GatePlace p[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const Place p = place_of(first, i * kGroups + group, blocks);
-        const int c = p.block * kBlock + lane * 8;
+        p[i] = gate_place(first, i * kGroups + group, lane, rows, inter, blocks);
         g[i] = u[i] = make_uint4(0, 0, 0, 0);
-        if (p.row < rows && c < inter) {
-            const uint16_t* at = gate_up + p.row * 2 * inter + c;
-            g[i] = __ldcs(reinterpret_cast<const uint4*>(at));
-            u[i] = __ldcs(reinterpret_cast<const uint4*>(at + inter));
+        if (p[i].gate != ~size_t(0)) {
+            g[i] = __ldcs(reinterpret_cast<const uint4*>(gate_up + p[i].gate));
+            u[i] = __ldcs(reinterpret_cast<const uint4*>(gate_up + p[i].gate + inter));
         }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const Place p = place_of(first, i * kGroups + group, blocks);
-        const int c = p.block * kBlock + lane * 8;
         uint32_t out[4];
         const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w}, uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
@@ -161,16 +182,13 @@ __global__ void __launch_bounds__(kThreads) swiglu_keep_kernel(const uint16_t* _
             out[j] = pack_bf(lo_of(gw[j]) * a * lo_of(uw[j]), hi_of(gw[j]) * b * hi_of(uw[j]));
         }
         const int eg = block_exponent(g[i]), eu = block_exponent(u[i]);
-        if (p.row >= rows) continue;
-        if (c < inter) {
-            *reinterpret_cast<uint4*>(h + p.row * inter + c) = make_uint4(out[0], out[1], out[2], out[3]);
-            uint8_t* at = codes + p.row * 2 * inter + c;
-            *reinterpret_cast<uint2*>(at) = encode8(g[i], eg);
-            *reinterpret_cast<uint2*>(at + inter) = encode8(u[i], eu);
-        }
+        if (p[i].gate == ~size_t(0)) continue;
+        *reinterpret_cast<uint4*>(h + p[i].h) = make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint2*>(codes + p[i].gate) = encode8(g[i], eg);
+        *reinterpret_cast<uint2*>(codes + p[i].gate + inter) = encode8(u[i], eu);
         if (lane == 0) {
-            scale[p.row * 2 * blocks + p.block] = pow2(eg);
-            scale[(p.row * 2 + 1) * blocks + p.block] = pow2(eu);
+            scale[p[i].scale] = pow2(eg);
+            scale[p[i].scale + blocks.n] = pow2(eu);
         }
     }
 }
@@ -179,7 +197,7 @@ template <int U>
 __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t* __restrict__ codes,
                                                                    const float* __restrict__ scale,
                                                                    const uint16_t* __restrict__ dh, size_t rows, int inter,
-                                                                   int blocks, uint16_t* __restrict__ d_gate_up,
+                                                                   Blocks blocks, uint16_t* __restrict__ d_gate_up,
                                                                    uint16_t* __restrict__ h) {
     pdl_begin();
     const size_t first = (size_t)blockIdx.x * (kGroups * U);
@@ -187,24 +205,21 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t
     uint2 cg[U], cu[U];
     uint4 d[U];
     float sg[U], su[U];
+    GatePlace p[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const Place p = place_of(first, i * kGroups + group, blocks);
-        const int c = p.block * kBlock + lane * 8;
-        if (p.row < rows && c < inter) {
-            const uint8_t* at = codes + p.row * 2 * inter + c;
-            cg[i] = __ldcs(reinterpret_cast<const uint2*>(at));
-            cu[i] = __ldcs(reinterpret_cast<const uint2*>(at + inter));
-            d[i] = __ldcs(reinterpret_cast<const uint4*>(dh + p.row * inter + c));
-            sg[i] = __ldg(scale + p.row * 2 * blocks + p.block);
-            su[i] = __ldg(scale + (p.row * 2 + 1) * blocks + p.block);
+        p[i] = gate_place(first, i * kGroups + group, lane, rows, inter, blocks);
+        if (p[i].gate != ~size_t(0)) {
+            cg[i] = __ldcs(reinterpret_cast<const uint2*>(codes + p[i].gate));
+            cu[i] = __ldcs(reinterpret_cast<const uint2*>(codes + p[i].gate + inter));
+            d[i] = __ldcs(reinterpret_cast<const uint4*>(dh + p[i].h));
+            sg[i] = __ldg(scale + p[i].scale);
+            su[i] = __ldg(scale + p[i].scale + blocks.n);
         }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const Place p = place_of(first, i * kGroups + group, blocks);
-        const int c = p.block * kBlock + lane * 8;
-        if (p.row >= rows || c >= inter) continue;
+        if (p[i].gate == ~size_t(0)) continue;
         float g[8], u[8], act[8], dg[8], du[8];
         decode8(cg[i], sg[i], g);
         decode8(cu[i], su[i], u);
@@ -219,13 +234,13 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t
             du[j] = up * silu;
             dg[j] = up * u[j] * (s * fmaf(g[j], rest, 1.0f));
         }
-        uint16_t* out = d_gate_up + p.row * 2 * inter + c;
+        uint16_t* out = d_gate_up + p[i].gate;
         *reinterpret_cast<uint4*>(out) =
             make_uint4(pack_bf(dg[0], dg[1]), pack_bf(dg[2], dg[3]), pack_bf(dg[4], dg[5]), pack_bf(dg[6], dg[7]));
         *reinterpret_cast<uint4*>(out + inter) =
             make_uint4(pack_bf(du[0], du[1]), pack_bf(du[2], du[3]), pack_bf(du[4], du[5]), pack_bf(du[6], du[7]));
         if (h)
-            *reinterpret_cast<uint4*>(h + p.row * inter + c) =
+            *reinterpret_cast<uint4*>(h + p[i].h) =
                 make_uint4(pack_bf(act[0], act[1]), pack_bf(act[2], act[3]), pack_bf(act[4], act[5]), pack_bf(act[6], act[7]));
     }
 }
@@ -238,9 +253,15 @@ int check_rows(int rows, int cols, const char* name) {
     return MOE_OK;
 }
 
+Blocks blocks_of(int cols) {
+    const int n = (cols + kBlock - 1) / kBlock;
+    return {n, n < 4096 ? (uint32_t)((1ull << 32) / n + 1) : 0u};
+}
+
 template <int U>
-dim3 grid_of(int rows, int blocks) {
-    return dim3((unsigned)(((size_t)rows * blocks + kGroups * U - 1) / (kGroups * U)));
+dim3 grid_of(int rows, Blocks blocks) {
+    static_assert(kGroups * U <= kMostUnits, "place_of's bound");
+    return dim3((unsigned)(((size_t)rows * blocks.n + kGroups * U - 1) / (kGroups * U)));
 }
 
 int launched(cudaError_t e, const char* what) {
@@ -259,8 +280,8 @@ int moe_checkpoint_rows(int rows, int cols, const void* x, uint8_t* codes, float
     if (rc || rows == 0) return rc;
     if ((rc = api_need(x, "x")) || (rc = api_need(codes, "codes")) || (rc = api_need(scale, "scale", 4))) return rc;
     PdlScope pdl(rows);
-    const int blocks = (cols + kBlock - 1) / kBlock;
-    return launched(launch_pdl(keep_kernel<4>, grid_of<4>(rows, blocks), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+    const Blocks blocks = blocks_of(cols);
+    return launched(launch_pdl(cols % kBlock ? keep_kernel<4, false> : keep_kernel<4, true>, grid_of<4>(rows, blocks), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream),
                                static_cast<const uint16_t*>(x), (size_t)rows, cols, blocks, codes, scale),
                     "checkpoint");
 }
@@ -272,7 +293,7 @@ int moe_swiglu_checkpoint(int rows, int inter, const void* gate_up, void* h, uin
         (rc = api_need(scale, "scale", 4)))
         return rc;
     PdlScope pdl(rows);
-    const int blocks = (inter + kBlock - 1) / kBlock;
+    const Blocks blocks = blocks_of(inter);
     return launched(launch_pdl(swiglu_keep_kernel<2>, grid_of<2>(rows, blocks), dim3(kThreads), 0,
                                reinterpret_cast<cudaStream_t>(stream), static_cast<const uint16_t*>(gate_up), (size_t)rows, inter,
                                blocks, static_cast<uint16_t*>(h), codes, scale),
@@ -288,7 +309,7 @@ int moe_swiglu_backward(int rows, int inter, const uint8_t* codes, const float* 
         return rc;
     if (h && (rc = api_need(h, "h"))) return rc;
     PdlScope pdl(rows);
-    const int blocks = (inter + kBlock - 1) / kBlock;
+    const Blocks blocks = blocks_of(inter);
     return launched(launch_pdl(swiglu_backward_kernel<2>, grid_of<2>(rows, blocks), dim3(kThreads), 0,
                                reinterpret_cast<cudaStream_t>(stream), codes, scale, static_cast<const uint16_t*>(dh), (size_t)rows,
                                inter, blocks, static_cast<uint16_t*>(d_gate_up), static_cast<uint16_t*>(h)),

@@ -10,6 +10,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace moe {
@@ -168,60 +170,80 @@ __global__ void __launch_bounds__(256, 2) combine_fp8_kernel(const uint4* __rest
     }
 }
 
-// Gradient of the combine: dy[row] = w * dout[t] and dw = <dout[t], y[row]> of each assignment
-// a = (t, j), row = inv_perm[a].  `tpr` threads (whole warps) per assignment, kCombineVec vectors
-// of 8 columns of each in flight.
+// Gradient of the combine: dy[row] = w * dout[t] and dw = <dout[t], y[row]> of each assignment (t, j),
+// row = inv_perm[t * k + j].  `tpr` threads (whole warps) hold up to kCombineVec vectors of 8 columns
+// of dout[t] each and go through `per` of the token's assignments, the next one's row of y on its way
+// meanwhile; longer rows (LONG) are read in turns for each assignment.
 constexpr int kCombineVec = 4;
+template <bool LONG>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ y,
                                                                const int32_t* __restrict__ inv_perm,
-                                                               const float* __restrict__ topk_w, int n, int k, int vpr, int tpr,
-                                                               uint4* __restrict__ dy, float* __restrict__ dw, DevStatus st) {
+                                                               const float* __restrict__ topk_w, int T, int k, int per, int vpr,
+                                                               int tpr, uint4* __restrict__ dy, float* __restrict__ dw,
+                                                               DevStatus st) {
     pdl_begin();
-    __shared__ float part[8];
-    const int sub = threadIdx.x / tpr, at = threadIdx.x - sub * tpr, lane = threadIdx.x & 31;
-    const int a = blockIdx.x * (256 / tpr) + sub;
-    const int row = a < n ? __ldg(inv_perm + a) : -1;
-    const bool live = row >= 0 && row < n;
-    float sum = 0.0f;
-    if (live) {
-        const float w = __ldg(topk_w + a);
-        const uint4* d = dout + (size_t)(a / k) * vpr;
-        const uint4* yr = y + (size_t)row * vpr;
-        uint4* out = dy + (size_t)row * vpr;
-        for (int c0 = at; c0 < vpr; c0 += tpr * kCombineVec) {
-            uint4 dv[kCombineVec], yv[kCombineVec];
+    __shared__ float part[32][8];  // of each assignment and warp
+    const int sub = threadIdx.x / tpr, at = threadIdx.x - sub * tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (256 / tpr) + sub, j0 = blockIdx.y * per, n = min(per, k - j0);
+    const int32_t* rows = inv_perm + (size_t)t * k + j0;
+    uint4 dv[kCombineVec], yv[kCombineVec];
+    auto load_d = [&](int c0) {
 #pragma unroll
-            for (int i = 0; i < kCombineVec; ++i) {
-                const int c = c0 + i * tpr;
-                if (c < vpr) {
-                    dv[i] = __ldg(d + c);
-                    yv[i] = __ldcs(yr + c);
+        for (int i = 0; i < kCombineVec; ++i)
+            if (c0 + i * tpr < vpr) dv[i] = __ldg(dout + (size_t)t * vpr + c0 + i * tpr);
+    };
+    auto load_y = [&](int row, int c0) {
+        if ((unsigned)row >= (unsigned)(T * k)) return;
+#pragma unroll
+        for (int i = 0; i < kCombineVec; ++i)
+            if (c0 + i * tpr < vpr) yv[i] = __ldcs(y + (size_t)row * vpr + c0 + i * tpr);
+    };
+    if (t < T) {
+        int row = __ldg(rows);
+        if (!LONG) {
+            load_d(at);
+            load_y(row, at);
+        }
+        for (int j = 0; j < n; ++j) {
+            const int next = j + 1 < n ? __ldg(rows + j + 1) : -1;
+            const float w = __ldg(topk_w + (size_t)t * k + j0 + j);
+            const bool live = (unsigned)row < (unsigned)(T * k);
+            float sum = 0.0f;
+            for (int c0 = at; c0 < (LONG ? vpr : at + 1); c0 += tpr * kCombineVec) {
+                if (LONG) {
+                    load_d(c0);
+                    load_y(row, c0);
                 }
-            }
+                uint4 now[kCombineVec];
 #pragma unroll
-            for (int i = 0; i < kCombineVec; ++i) {
-                const int c = c0 + i * tpr;
-                if (c < vpr) {
+                for (int i = 0; i < kCombineVec; ++i) now[i] = yv[i];
+                if (!LONG) load_y(next, at);
+                if (!live) continue;
+#pragma unroll
+                for (int i = 0; i < kCombineVec; ++i) {
+                    const int c = c0 + i * tpr;
+                    if (c >= vpr) continue;
                     float df[8], yf[8];
                     unpack8(dv[i], df);
-                    unpack8(yv[i], yf);
+                    unpack8(now[i], yf);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) sum = fmaf(df[q], yf[q], sum);
-                    out[c] = make_uint4(pack2(w * df[0], w * df[1]), pack2(w * df[2], w * df[3]), pack2(w * df[4], w * df[5]),
-                                        pack2(w * df[6], w * df[7]));
+                    __stcs(dy + (size_t)row * vpr + c, make_uint4(pack2(w * df[0], w * df[1]), pack2(w * df[2], w * df[3]),
+                                                                  pack2(w * df[4], w * df[5]), pack2(w * df[6], w * df[7])));
                 }
             }
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            if (lane == 0) part[j][warp] = sum;
+            if (!live && at == 0) raise_status(st, kStatusBadShape);
+            row = next;
         }
     }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (lane == 0) part[threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (at == 0 && a < n) {
-        sum = 0.0f;
-        for (int i = 0; i < tpr / 32; ++i) sum += part[(threadIdx.x >> 5) + i];
-        dw[a] = sum;
-        if (!live) raise_status(st, kStatusBadShape);
+    for (int j = at; j < n && t < T; j += tpr) {
+        float sum = 0.0f;
+        for (int i = 0; i < tpr / 32; ++i) sum += part[j][sub * (tpr / 32) + i];
+        dw[(size_t)t * k + j0 + j] = sum;
     }
 }
 
@@ -230,12 +252,15 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const uint4* __re
 cudaError_t launch_combine_backward(const uint16_t* dout, const uint16_t* y_disp, const int32_t* inv_perm, const float* topk_w,
                                     int T, int k, int hidden, uint16_t* dy_disp, float* d_topk_w, const DevStatus& st,
                                     cudaStream_t stream) {
-    const int vpr = hidden / 8, n = T * k;
+    const int vpr = hidden / 8;
     int tpr = 32;
     while (tpr < 256 && tpr * kCombineVec < vpr) tpr *= 2;
-    const int per = 256 / tpr;
-    return launch_pdl(combine_backward_kernel, dim3((n + per - 1) / per), dim3(256), 0, stream,
-                      reinterpret_cast<const uint4*>(dout), reinterpret_cast<const uint4*>(y_disp), inv_perm, topk_w, n, k, vpr, tpr,
+    const int tokens = 256 / tpr, groups = (T + tokens - 1) / tokens;
+    // a token's assignments in one go, or shared out until two CTAs an SM have some
+    const int shares = std::min(k, std::max(1, 2 * num_sms() / groups)), per = (k + shares - 1) / shares;
+    auto kern = tpr * kCombineVec < vpr ? combine_backward_kernel<true> : combine_backward_kernel<false>;
+    return launch_pdl(kern, dim3(groups, (k + per - 1) / per), dim3(256), 0, stream, reinterpret_cast<const uint4*>(dout),
+                      reinterpret_cast<const uint4*>(y_disp), inv_perm, topk_w, T, k, per, vpr, tpr,
                       reinterpret_cast<uint4*>(dy_disp), d_topk_w, st);
 }
 

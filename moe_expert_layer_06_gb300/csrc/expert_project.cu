@@ -52,6 +52,18 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
     return v;
 }
 
+// 32 lanes x 32 bits, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
 // A wait for what the other CTA of the pair wrote and signalled: acquires for the cluster.
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const volatile int* abort_flag, unsigned long long limit) {
     bool done = mbar_try_wait_cluster(bar, parity);
@@ -398,8 +410,12 @@ struct WeightArgs {
     int R, K, N, P, S, type, n_blk, n_tiles;
     DevStatus st;
 };
-constexpr int kWeightThreads = 320;  // copies, products, four warps on the rows, four that drain accumulators
-constexpr int kWeightOut = 4 * 2 * 4096;  // two blocks of 32 x 128 bytes of each draining warp
+// Four warps work on the rows of a chunk; codes take them four times as long as the chunk's products,
+// so four such groups take chunks in turn.
+constexpr int kDrainWarps = 8;
+constexpr int kWeightOut = kDrainWarps * 4096;  // a block of 32 x 128 bytes of each draining warp
+constexpr int work_groups(bool x8) { return x8 ? 4 : 1; }
+constexpr int weight_threads(bool x8) { return 64 + 128 * work_groups(x8) + 32 * kDrainWarps; }
 constexpr int kWeightSmem = 1024 + kRing + kWeightOut + 512;
 static_assert(kWeightSmem <= 227 * 1024, "shared memory overflow");
 
@@ -435,7 +451,7 @@ __device__ __forceinline__ void decode16(const uint4& c, float scale, uint32_t (
 }
 
 template <bool X8>
-__global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+__global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __grid_constant__ WeightArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kWeightOut);  // (the leader's) copies that need no work, of both
@@ -453,6 +469,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
     const int rank = (int)cluster_rank();
+    constexpr int kGroups = work_groups(X8);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&tfull[s]), 1);
-            mbar_init(smem_u32(&tempty[s]), 8);
+            mbar_init(smem_u32(&tempty[s]), 2 * kDrainWarps);
         }
         mbar_init(smem_u32(done), 1);
         *abort_flag = 0;
@@ -621,22 +638,23 @@ __global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid
             if (!ok && lane == 0) give_up();
         }
         mbar_wait(smem_u32(done), 0, limit);
-    } else if (warp < 6) {
-        const int tid = threadIdx.x - 64;
+    } else if (warp < 2 + 4 * kGroups) {
+        const int tid = (threadIdx.x - 64) & 127, group = (warp - 2) >> 2;
         bool ok = true;
-        int stage = 0;
+        int stage = 0, turn = 0;  // of the chunks that need work
         uint32_t land_phase = 0;
         for (int i = first; i < a.n_tiles && ok; i += step) {
             const WeightTile t = weight_tile(a, i);
             const int blk = (t.k0 + rank * 128) / MOE_PAYLOAD_BLOCK;
             for (int r = 0; r < t.rows; r += 64) {
                 const int left = min(64, t.rows - r), rows16 = (left + 15) & ~15;
-                if (X8 || (left & 15)) {
+                const bool work = X8 || (left & 15), mine = work && turn == group;
+                if (work && ++turn == kGroups) turn = 0;
+                if (mine) {
                     const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kHalf;
                     float scale = 0.0f;
                     if (X8 && (tid >> 1) < left && blk < a.n_blk) scale = __ldg(a.scale + (size_t)(t.row0 + r + (tid >> 1)) * a.n_blk + blk);
                     ok = warp_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, abort_flag, limit);
-                    land_phase ^= 1u << stage;
                     if (X8) {
                         // two threads a row, 64 columns each (pieces of 16 bytes in the order of the
                         // swizzle, the second thread's in another, so that both find their banks free)
@@ -646,7 +664,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 c[k] = ld_shared4(sb + row * 128 + (((half * 4 + (k ^ half * 2)) ^ (row & 7)) << 4));
-                        if (!(ok = named_and(1, 128, ok))) break;
+                        if (!(ok = named_and(1 + group, 128, ok))) break;
                         if (row < rows16) {
                             const uint32_t to = sb + half * (kHalf / 2) + row * 128;
 #pragma unroll
@@ -678,15 +696,17 @@ __global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ready_u + stage * 8);
                 }
+                if (work) land_phase ^= 1u << stage;
                 if (++stage == kStages) stage = 0;
             }
         }
         if (!ok && lane == 0) give_up();
     } else {
-        const int q = warp & 3;
-        const uint32_t out = stage_u + kRing + q * 2 * 4096;
+        // two warps for each quarter of the accumulators, half of the columns each
+        const int q = warp & 3, part = (warp - 2 - 4 * kGroups) >> 2;
+        const uint32_t block = stage_u + kRing + (part * 4 + q) * 4096, to = block + lane * 128;
         bool ok = true;
-        int blocks = 0, n = 0;
+        int n = 0;
         for (int i = first; i < a.n_tiles; i += step) {
             const WeightTile t = weight_tile(a, i);
             if (t.rows == 0 && a.type == MOE_OUT_F32_ADD) continue;
@@ -696,32 +716,31 @@ __global__ void __launch_bounds__(kWeightThreads, 1) weights_kernel(const __grid
             }
             const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
             const int row = t.n0 + rank * 128 + q * 32;
-            const int cols = min(256, a.K - t.k0), by = a.type == MOE_OUT_BF16 ? 64 : 32;  // 128 bytes
-            for (int c = 0; c < cols; c += by, ++blocks) {
-                const uint32_t block = out + (blocks & 1) * 4096, to = block + lane * 128;
-                if (lane == 0) bulk_wait_read_but<1>();
+            const bool bf16 = a.type == MOE_OUT_BF16;
+            const int by = bf16 ? 64 : 32;  // 128 bytes
+            for (int c = part * 128; c < min(part * 128 + 128, a.K - t.k0); c += by) {
+                if (lane == 0) bulk_wait_read();  // the block's last copy has read it
                 __syncwarp();
 #pragma unroll 1
-                for (int h = 0; h < 4; ++h) {  // 32 bytes of each row at a time
-                    float v[16];
-                    uint32_t w[8];
-                    if (a.type == MOE_OUT_BF16) {
-                        if (t.rows) {
-                            tmem_ld16(tmem + c + h * 16, v);
-                            tmem_ld_wait();
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) w[k] = t.rows ? pack_bf(to_u(v[2 * k]), to_u(v[2 * k + 1])) : 0u;
+                for (int h = 0; h < by; h += 32) {
+                    uint32_t v[32];
+                    if (t.rows) {
+                        tmem_ld32(tmem + c + h, v);
+                        tmem_ld_wait();
                     } else {
-                        if (t.rows) {
-                            tmem_ld16(tmem + c + (h >> 1) * 16, v);
-                            tmem_ld_wait();
-                        }
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) w[k] = t.rows ? to_u(h & 1 ? v[8 + k] : v[k]) : 0u;
+                        for (int k = 0; k < 32; ++k) v[k] = 0;
                     }
-                    st_shared4(to + (((2 * h) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-                    st_shared4(to + (((2 * h + 1) ^ (lane & 7)) << 4), w[4], w[5], w[6], w[7]);
+                    if (bf16) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_shared4(to + (((h / 8 + k) ^ (lane & 7)) << 4), pack_bf(v[8 * k], v[8 * k + 1]), pack_bf(v[8 * k + 2], v[8 * k + 3]),
+                                       pack_bf(v[8 * k + 4], v[8 * k + 5]), pack_bf(v[8 * k + 6], v[8 * k + 7]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            st_shared4(to + ((k ^ (lane & 7)) << 4), v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -855,7 +874,7 @@ int weights_product(const moe_project_t* p, int rows, const void* dy, const void
     const uint64_t tiles = (K + 255) / 256 * ((N + 255) / 256) * P * S;
     a.n_tiles = (int)tiles;
     static std::atomic<uint64_t> configured{0};
-    return launch_pairs(weights_kernel<X8>, configured, kWeightThreads, kWeightSmem, (long)tiles, stream, a, "expert weight gradient");
+    return launch_pairs(weights_kernel<X8>, configured, weight_threads(X8), kWeightSmem, (long)tiles, stream, a, "expert weight gradient");
 }
 
 }  // namespace
