@@ -52,6 +52,14 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
     return v;
 }
 
+// 16 bytes of this CTA's shared memory to another CTA's, which a barrier there hears of: a signal that
+// nobody waits for here, and that is sent when what the thread did before is done.
+__device__ __forceinline__ void signal_by_copy(uint32_t dst, uint32_t src, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst), "r"(src),
+                 "r"(bar)
+                 : "memory");
+}
+
 // 32 lanes x 32 bits, 32 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -410,13 +418,16 @@ struct WeightArgs {
     int R, K, N, P, S, type, n_blk, n_tiles;
     DevStatus st;
 };
-// Four warps work on the rows of a chunk; codes take them four times as long as the chunk's products,
-// so four such groups take chunks in turn.
+// Four warps work on the rows of a chunk, where the last one of a slot needs it.  Codes, which all need
+// it, take eight warps 400 cycles of a chunk's 512, and the way there and back more: two groups take
+// chunks in turn.
 constexpr int kDrainWarps = 8;
 constexpr int kWeightOut = kDrainWarps * 4096;  // a block of 32 x 128 bytes of each draining warp
-constexpr int work_groups(bool x8) { return x8 ? 4 : 1; }
-constexpr int weight_threads(bool x8) { return 64 + 128 * work_groups(x8) + 32 * kDrainWarps; }
+constexpr int work_groups(bool x8) { return x8 ? 2 : 1; }
+constexpr int work_warps(bool x8) { return x8 ? 8 : 4; }  // of a group
+constexpr int weight_threads(bool x8) { return 64 + 32 * work_warps(x8) * work_groups(x8) + 32 * kDrainWarps; }
 constexpr int kWeightSmem = 1024 + kRing + kWeightOut + 512;
+constexpr int kSignals = 384;  // of those 512 bytes: 16 for each stage, and 16 to send
 static_assert(kWeightSmem <= 227 * 1024, "shared memory overflow");
 
 struct WeightTile {
@@ -464,19 +475,19 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
     uint64_t* done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((5 * kStages + 5) * 8 + 8 <= 512, "barriers");
+    static_assert((5 * kStages + 5) * 8 + 8 <= kSignals && kSignals + 16 * (kStages + 1) <= 512, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
     const int rank = (int)cluster_rank();
-    constexpr int kGroups = work_groups(X8);
+    constexpr int kGroups = work_groups(X8), kWork = work_warps(X8);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
-            mbar_init(smem_u32(&ready[s]), 4);
+            mbar_init(smem_u32(&ready[s]), kWork);
             mbar_init(smem_u32(&other[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -529,6 +540,7 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                     const uint32_t fb = lead_full + stage * 8, lb = landed_u + stage * 8;
                     const uint32_t dy_bytes = n16 * 4096, x_bytes = X8 ? n16 * 2048 : n16 * 4096;
                     if (!odd && rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * (dy_bytes + (X8 ? 0 : x_bytes)));
+                    if (work && rank == 0) mbar_arrive_expect_tx(other_u + stage * 8, 16);
                     if (work) mbar_arrive_expect_tx(lb, X8 && !odd ? x_bytes : dy_bytes + x_bytes);
                     for (int bit = 2, off = 0; bit >= 0; --bit)
                         if (n16 & (1 << bit)) {
@@ -621,25 +633,31 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
             if (elect_one()) umma_commit_pair(smem_u32(done));
             __syncwarp();
         } else {
-            // the other CTA's rows are ready: the leader hears of it from this warp, as the arrival
-            // there takes 500 cycles
+            // The other CTA's rows are ready: the leader hears of it by a copy.  (An arrival there
+            // holds its thread for 1400 to 2000 cycles, until its release is seen by the cluster: codes
+            // took 3087 us of 4096 tokens, 8 experts each, gate and up, where rows in bf16 took 1170.)
+            const uint32_t signals = smem_u32(full) + kSignals, lead_signals = leader_addr(signals);
             for (int i = first; i < a.n_tiles && ok; i += step) {
                 const WeightTile t = weight_tile(a, i);
                 for (int r = 0; r < t.rows; r += 64) {
                     if (X8 || (min(64, t.rows - r) & 15)) {
                         if (!(ok = warp_wait(ready_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit))) break;
                         work_phase ^= 1u << stage;
-                        if (lane == 0) mbar_arrive_cluster(lead_other + stage * 8);
+                        if (lane == 0) signal_by_copy(lead_signals + stage * 16, signals + kStages * 16, lead_other + stage * 8);
                         __syncwarp();
                     }
                     if (++stage == kStages) stage = 0;
                 }
             }
-            if (!ok && lane == 0) give_up();
+            if (!ok) {
+                if (lane == 0) give_up();
+                // (the last signals are on their way: time enough for them to arrive)
+                for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;) {}
+            }
         }
         mbar_wait(smem_u32(done), 0, limit);
-    } else if (warp < 2 + 4 * kGroups) {
-        const int tid = (threadIdx.x - 64) & 127, group = (warp - 2) >> 2;
+    } else if (warp < 2 + kWork * kGroups) {
+        const int tid = (threadIdx.x - 64) & (kWork * 32 - 1), group = (warp - 2) / kWork;
         bool ok = true;
         int stage = 0, turn = 0;  // of the chunks that need work
         uint32_t land_phase = 0;
@@ -653,25 +671,24 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                 if (mine) {
                     const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kHalf;
                     float scale = 0.0f;
-                    if (X8 && (tid >> 1) < left && blk < a.n_blk) scale = __ldg(a.scale + (size_t)(t.row0 + r + (tid >> 1)) * a.n_blk + blk);
+                    if (X8 && (tid >> 2) < left && blk < a.n_blk) scale = __ldg(a.scale + (size_t)(t.row0 + r + (tid >> 2)) * a.n_blk + blk);
                     ok = warp_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, abort_flag, limit);
                     if (X8) {
-                        // two threads a row, 64 columns each (pieces of 16 bytes in the order of the
-                        // swizzle, the second thread's in another, so that both find their banks free)
-                        const int row = tid >> 1, half = tid & 1;
-                        uint4 c[4];
+                        // four threads a row, 32 columns each (pieces of 16 bytes in the order of the
+                        // swizzle, those of the second 64 columns in another, so that all find their banks free)
+                        const int row = tid >> 2, part = tid & 3, flip = part >> 1;
+                        uint4 c[2];
                         if (ok && row < left)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                c[k] = ld_shared4(sb + row * 128 + (((half * 4 + (k ^ half * 2)) ^ (row & 7)) << 4));
-                        if (!(ok = named_and(1 + group, 128, ok))) break;
+                            for (int k = 0; k < 2; ++k) c[k] = ld_shared4(sb + row * 128 + (((part * 2 + (k ^ flip)) ^ (row & 7)) << 4));
+                        if (!(ok = named_and(1 + group, kWork * 32, ok))) break;
                         if (row < rows16) {
-                            const uint32_t to = sb + half * (kHalf / 2) + row * 128;
+                            const uint32_t to = sb + flip * (kHalf / 2) + row * 128;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < 2; ++k) {
                                 uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                                 if (row < left) decode16(c[k], scale, w);
-                                const int piece = (k ^ half * 2) * 2;
+                                const int piece = (part & 1) * 4 + (k ^ flip) * 2;
                                 st_shared4(to + ((piece ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
                                 st_shared4(to + (((piece + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
                             }
@@ -679,7 +696,7 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                     } else if (!ok) {
                         break;
                     }
-                    if (left & 15) {
+                    if ((left & 15) && tid < 128) {
                         // the rows of the last 16 that are not the slot's, 8 threads a row
                         const int row = rows16 - 16 + (tid >> 3);
                         if (row >= left) {
@@ -703,7 +720,7 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
         if (!ok && lane == 0) give_up();
     } else {
         // two warps for each quarter of the accumulators, half of the columns each
-        const int q = warp & 3, part = (warp - 2 - 4 * kGroups) >> 2;
+        const int q = warp & 3, part = (warp - 2 - kWork * kGroups) >> 2;
         const uint32_t block = stage_u + kRing + (part * 4 + q) * 4096, to = block + lane * 128;
         bool ok = true;
         int n = 0;
