@@ -427,14 +427,13 @@ struct WeightArgs {
     int R, K, N, P, S, type, n_blk, n_tiles;
     DevStatus st;
 };
-// Four warps work on the rows of a chunk, where the last one of a slot needs it.  Codes, which all need
-// it, take eight warps 400 cycles of a chunk's 512, and the way there and back more: two groups take
-// chunks in turn.
+// Four warps work on the rows of a chunk, 16 rows each, where the last one of a slot needs it.  Codes
+// all need it, and take them longer than the chunk's products: three such groups take chunks in turn.
+constexpr int kWork = 4;
 constexpr int kDrainWarps = 8;
 constexpr int kWeightOut = kDrainWarps * 4096;  // a block of 32 x 128 bytes of each draining warp
-constexpr int work_groups(bool x8) { return x8 ? 2 : 1; }
-constexpr int work_warps(bool x8) { return x8 ? 8 : 4; }  // of a group
-constexpr int weight_threads(bool x8) { return 64 + 32 * work_warps(x8) * work_groups(x8) + 32 * kDrainWarps; }
+constexpr int work_groups(bool x8) { return x8 ? 3 : 1; }
+constexpr int weight_threads(bool x8) { return 64 + 32 * kWork * work_groups(x8) + 32 * kDrainWarps; }
 constexpr int kWeightSmem = 1024 + kRing + kWeightOut + 512;
 constexpr int kSignals = 384;  // of those 512 bytes: 16 for each stage, and 16 to send
 static_assert(kWeightSmem <= 227 * 1024, "shared memory overflow");
@@ -459,14 +458,15 @@ __device__ __forceinline__ WeightTile weight_tile(const WeightArgs& a, int i) {
     return t;
 }
 
-// 16 codes times their scale as bf16.
+// 16 codes times their scale as bf16: both steps are exact (the header of checkpoint.cu says why).
 __device__ __forceinline__ void decode16(const uint4& c, float scale, uint32_t (&w)[8]) {
     const uint32_t v[4] = {c.x, c.y, c.z, c.w};
+    const __nv_bfloat162 by = __float2bfloat162_rn(scale);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((v[i >> 1] >> (i & 1) * 16) & 0xffffu), __NV_E4M3);
-        const float2 p = __half22float2(__half2(h));
-        w[i] = pack_bf(to_u(p.x * scale), to_u(p.y * scale));
+        const __nv_bfloat162 p = __hmul2(__float22bfloat162_rn(__half22float2(__half2(h))), by);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
 }
 
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kWeightOut);  // (the leader's) copies that need no work, of both
     uint64_t* empty = full + kStages;
     uint64_t* landed = empty + kStages;  // this CTA's copies that need work
-    uint64_t* ready = landed + kStages;  // ... and have had it
+    uint64_t* ready = landed + kStages;  // (the leader's) ... and have had it
     uint64_t* other = ready + kStages;   // (the leader's) the same in the other CTA
     uint64_t* tfull = other + kStages;
     uint64_t* tempty = tfull + 2;        // (the leader's)
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
     const int rank = (int)cluster_rank();
-    constexpr int kGroups = work_groups(X8), kWork = work_warps(X8);
+    constexpr int kGroups = work_groups(X8);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                     const uint32_t fb = lead_full + stage * 8, lb = landed_u + stage * 8;
                     const uint32_t dy_bytes = n16 * 4096, x_bytes = X8 ? n16 * 2048 : n16 * 4096;
                     if (!odd && rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * (dy_bytes + (X8 ? 0 : x_bytes)));
-                    if (work && rank == 0) mbar_arrive_expect_tx(other_u + stage * 8, 16);
+                    if (work && rank == 0) mbar_arrive_expect_tx(other_u + stage * 8, kWork * 16);
                     if (work) mbar_arrive_expect_tx(lb, X8 && !odd ? x_bytes : dy_bytes + x_bytes);
                     for (int bit = 2, off = 0; bit >= 0; --bit)
                         if (n16 & (1 << bit)) {
@@ -641,32 +641,14 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
             // all products are complete before the tensor memory is freed
             if (elect_one()) umma_commit_pair(smem_u32(done));
             __syncwarp();
-        } else {
-            // The other CTA's rows are ready: the leader hears of it by a copy.  (An arrival there
-            // holds its thread for 1400 to 2000 cycles, until its release is seen by the cluster: codes
-            // took 3087 us of 4096 tokens, 8 experts each, gate and up, where rows in bf16 took 1170.)
-            const uint32_t signals = smem_u32(full) + kSignals, lead_signals = leader_addr(signals);
-            for (int i = first; i < a.n_tiles && ok; i += step) {
-                const WeightTile t = weight_tile(a, i);
-                for (int r = 0; r < t.rows; r += 64) {
-                    if (X8 || (min(64, t.rows - r) & 15)) {
-                        if (!(ok = warp_wait(ready_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit))) break;
-                        work_phase ^= 1u << stage;
-                        if (lane == 0) signal_by_copy(lead_signals + stage * 16, signals + kStages * 16, lead_other + stage * 8);
-                        __syncwarp();
-                    }
-                    if (++stage == kStages) stage = 0;
-                }
-            }
-            if (!ok) {
-                if (lane == 0) give_up();
-                // (the last signals are on their way: time enough for them to arrive)
-                for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;) {}
-            }
         }
         mbar_wait(smem_u32(done), 0, limit);
     } else if (warp < 2 + kWork * kGroups) {
-        const int tid = (threadIdx.x - 64) & (kWork * 32 - 1), group = (warp - 2) / kWork;
+        const int group = (warp - 2) / kWork, sub = (warp - 2) % kWork;
+        // The leader hears of the other CTA's rows by copies.  (An arrival there holds its thread for
+        // 1400 to 2000 cycles, until its release is seen by the cluster: one for each chunk, and codes
+        // took 3087 us of 4096 tokens, 8 experts each, gate and up, where rows in bf16 took 1170.)
+        const uint32_t signals = smem_u32(full) + kSignals, lead_signals = leader_addr(signals);
         bool ok = true;
         int stage = 0, turn = 0;  // of the chunks that need work
         uint32_t land_phase = 0;
@@ -679,37 +661,45 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                 if (work && ++turn == kGroups) turn = 0;
                 if (mine) {
                     const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kHalf;
-                    float scale = 0.0f;
-                    if (X8 && (tid >> 2) < left && blk < a.n_blk) scale = __ldg(a.scale + (size_t)(t.row0 + r + (tid >> 2)) * a.n_blk + blk);
-                    ok = warp_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, abort_flag, limit);
-                    if (X8) {
-                        // four threads a row, 32 columns each (pieces of 16 bytes in the order of the
-                        // swizzle, those of the second 64 columns in another, so that all find their banks free)
-                        const int row = tid >> 2, part = tid & 3, flip = part >> 1;
-                        uint4 c[2];
-                        if (ok && row < left)
+                    // codes: four threads a row, 32 columns each, 8 rows at a time
+                    const int row0 = sub * 16 + (lane >> 2), part = lane & 3, flip = part >> 1;
+                    float scale[2] = {0.0f, 0.0f};
+                    if (X8 && blk < a.n_blk)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) c[k] = ld_shared4(sb + row * 128 + (((part * 2 + (k ^ flip)) ^ (row & 7)) << 4));
-                        if (!(ok = named_and(1 + group, kWork * 32, ok))) break;
-                        if (row < rows16) {
-                            const uint32_t to = sb + flip * (kHalf / 2) + row * 128;
+                        for (int k = 0; k < 2; ++k)
+                            if (row0 + k * 8 < left) scale[k] = __ldg(a.scale + (size_t)(t.row0 + r + row0 + k * 8) * a.n_blk + blk);
+                    if (!(ok = warp_wait(landed_u + stage * 8, (land_phase >> stage) & 1u, abort_flag, limit))) break;
+                    if (X8 && sub * 16 < rows16) {
+                        // pieces of 16 bytes in the order of the swizzle, those of the second 64 columns
+                        // in another, so that all find their banks free.  A row's codes lie where the
+                        // first 64 columns of the same row go: its four threads are of one warp.
+                        uint4 c[2][2];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                                if (row < left) decode16(c[k], scale, w);
-                                const int piece = (part & 1) * 4 + (k ^ flip) * 2;
-                                st_shared4(to + ((piece ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-                                st_shared4(to + (((piece + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                c[k][i] = ld_shared4(sb + (row0 + k * 8) * 128 + (((part * 2 + (i ^ flip)) ^ (row0 & 7)) << 4));
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t to = sb + flip * (kHalf / 2) + (row0 + k * 8) * 128;
+                            const bool live = row0 + k * 8 < left;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t w[8];
+                                decode16(c[k][i], scale[k], w);
+                                const int piece = (part & 1) * 4 + (i ^ flip) * 2;
+                                st_shared4(to + ((piece ^ (row0 & 7)) << 4), live ? w[0] : 0u, live ? w[1] : 0u, live ? w[2] : 0u, live ? w[3] : 0u);
+                                st_shared4(to + (((piece + 1) ^ (row0 & 7)) << 4), live ? w[4] : 0u, live ? w[5] : 0u, live ? w[6] : 0u,
+                                           live ? w[7] : 0u);
                             }
                         }
-                    } else if (!ok) {
-                        break;
                     }
-                    if ((left & 15) && tid < 128) {
+                    if (left & 15) {
                         // the rows of the last 16 that are not the slot's, 8 threads a row
-                        const int row = rows16 - 16 + (tid >> 3);
+                        const int row = rows16 - 16 + sub * 4 + (lane >> 3);
                         if (row >= left) {
-                            const uint32_t o = row * 128 + (tid & 7) * 16;
+                            const uint32_t o = row * 128 + (lane & 7) * 16;
                             st_shared4(sa + o, 0, 0, 0, 0);
                             st_shared4(sa + o + kHalf / 2, 0, 0, 0, 0);
                             if (!X8) {
@@ -720,13 +710,21 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(ready_u + stage * 8);
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(ready_u + stage * 8);
+                        else signal_by_copy(lead_signals + stage * 16, signals + kStages * 16, lead_other + stage * 8);
+                    }
+                    __syncwarp();
                 }
                 if (work) land_phase ^= 1u << stage;
                 if (++stage == kStages) stage = 0;
             }
         }
-        if (!ok && lane == 0) give_up();
+        if (!ok) {
+            if (lane == 0) give_up();
+            // (the last signals are on their way: time enough for them to arrive)
+            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;) {}
+        }
     } else {
         // two warps for each quarter of the accumulators, half of the columns each
         const int q = warp & 3, part = (warp - 2 - kWork * kGroups) >> 2;
