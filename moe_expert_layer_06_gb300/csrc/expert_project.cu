@@ -79,19 +79,6 @@ __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// A wait for what the other CTA of the pair wrote and signalled: acquires for the cluster, which costs
-// 100 to 150 ns where it is waited for, so what copies and this CTA's own warps signal is not waited for
-// this way.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const volatile int* abort_flag, unsigned long long limit) {
-    bool done = mbar_try_wait_cluster(bar, parity);
-    if (!__all_sync(0xffffffffu, done)) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!done && !*abort_flag && globaltimer_ns() - t0 <= limit) done = mbar_try_wait_cluster(bar, parity);
-        done = __all_sync(0xffffffffu, done);
-    }
-    return done;
-}
-
 // ---------------------------------------------------------------- y and dx
 // One pair's tile: 256 outputs (128 rows of W, or for dx 128 columns, in each CTA) times the rows of
 // a slot in chunks of equal height, a multiple of 32 up to 256 (half of them in each CTA).
@@ -597,6 +584,9 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
             }
         }
     } else if (warp == 1) {
+        // What it waits for is read by the tensor cores alone, each CTA's half in its own shared
+        // memory: the waits do not acquire for the cluster (100 to 200 ns each; three of them held the
+        // products of codes up).
         bool ok = true;
         int stage = 0, n = 0;
         uint32_t full_phase = 0, work_phase = 0;  // (of each stage: not every chunk uses both)
@@ -617,7 +607,7 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                     }
                     if (X8 || (left & 15)) {
                         if (!(ok = warp_wait(ready_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit) &&
-                                   wait_cluster(other_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit)))
+                                   warp_wait(other_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit)))
                             break;
                         work_phase ^= 1u << stage;
                     }
