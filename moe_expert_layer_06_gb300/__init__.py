@@ -263,10 +263,10 @@ def _dense(t, name, shape, dtype):
     """Pointer of a device tensor whose sizes and type are checked (None passes)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():  # the common case first: these calls take microseconds
+        return t.data_ptr()
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if t.is_cuda and t.is_contiguous():  # the common case first: these calls take microseconds
-        return t.data_ptr()
     return _ptr(t)
 
 
@@ -452,9 +452,11 @@ def _out_type(t, add: bool) -> int:
 
 
 def _offsets(offsets, n_slots):
-    if offsets is not None and (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] <= n_slots):
+    if offsets is None:
+        return None
+    if offsets.dtype is not torch.int32 or offsets.dim() != 1 or offsets.numel() <= n_slots:
         raise ValueError(f"offsets must be int32, {n_slots + 1} at least")
-    return _ptr(offsets)
+    return offsets.data_ptr() if offsets.is_cuda and offsets.is_contiguous() else _ptr(offsets)
 
 
 def moe_expert_project(project, rows, x, offsets, w, w2, out, add=False, stream=None):
