@@ -19,9 +19,9 @@ namespace {
 
 constexpr int kMaxSlots = 1024;
 constexpr int kMaxFeatures = 1 << 24;
-constexpr int kHalf = 128 * 64 * 2;          // one CTA's 128 rows or features of an operand's 64-wide chunk
-constexpr int kStageBytes = 2 * kHalf;
+constexpr int kHalf = 128 * 64 * 2;  // one CTA's 128 rows or features of an operand's 64-wide chunk
 constexpr int kStages = 6;
+constexpr int kStageBytes = 2 * kHalf;
 constexpr int kRing = kStages * kStageBytes;
 
 __device__ __forceinline__ uint32_t to_u(float f) { return __float_as_uint(f); }
@@ -60,6 +60,23 @@ __device__ __forceinline__ void signal_by_copy(uint32_t dst, uint32_t src, uint3
                  : "memory");
 }
 
+// 16 lanes x 64 columns: as tmem_ld_16x256, i up to 7
+__device__ __forceinline__ void tmem_ld_16x256_64(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void stmatrix(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 // 32 lanes x 32 bits, 32 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -80,7 +97,7 @@ __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar) {
 }
 
 // ---------------------------------------------------------------- y and dx
-// One pair's tile: 256 outputs (128 rows of W, or for dx 128 columns, in each CTA) times the rows of
+// One pair's tile: 256 outputs (128 rows of W, or for dx columns, in each CTA) times the rows of
 // a slot in chunks of equal height, a multiple of 32 up to 256 (half of them in each CTA).
 // dx's W is read MN-major, as its contraction runs over W's rows.
 struct RowsArgs {
@@ -93,7 +110,8 @@ struct RowsArgs {
     DevStatus st;
 };
 constexpr int kRowsThreads = 192;  // copies, products, four warps that drain accumulators
-constexpr int kOutBytes = 16384;   // bf16: 2 x 2 blocks of 32 rows x 64 features; fp32: 4 x 2 of 16 rows x 32
+constexpr int kOutBlocks = 3;
+constexpr int kOutBytes = 2 * kOutBlocks * 4096;  // of 32 rows x 64 features each, for two pairs of warps
 constexpr int kRowsSmem = 1024 + kRing + kOutBytes + 256 + (kMaxSlots + 1) * 4;
 static_assert(kRowsSmem <= 227 * 1024, "shared memory overflow");
 
@@ -118,22 +136,20 @@ __device__ __forceinline__ RowsTile rows_tile(const RowsArgs& a, const int* pre,
     int r0, r1;
     slot_rows(a.offsets, t.s, a.R, r0, r1);
     const int n = chunks_of(r1 - r0), l = i - pre[t.s], c = l % n, m = l / n;
-    // (equal heights: a chunk of few rows reads as much of W as a high one.  The last of n chunks of
-    // this height is never empty: n - 1 roundings of under 32 rows are less than a chunk, up to n = 7,
-    // and from n = 8 on the height is 256)
-    const int h = ((r1 - r0 + n - 1) / n + 31) & ~31;
+    // (heights within 32 of each other: a chunk of few rows reads as much of W as a high one)
+    const int units = (r1 - r0 + 31) / 32, h = units / n, more = units - h * n;
     const int tiles = ((DX ? a.K : a.N) + 255) / 256;
     t.part = m / tiles;
     t.m0 = (m - t.part * tiles) * 256;
-    t.row0 = r0 + c * h;
-    t.rows = min(h, r1 - t.row0);
-    t.bn = (t.rows + 31) & ~31;
+    t.row0 = r0 + 32 * (c * h + min(c, more));
+    t.bn = 32 * (h + (c < more ? 1 : 0));
+    t.rows = min(t.bn, r1 - t.row0);
     t.shared_w = n > 1;
     return t;
 }
 
-// Warps 2 p and 2 p + 1 share 64 features and two blocks at `out` (as bf16), the copies of which the
-// first one's lane 0 issues.  Copies take 16 rows at a time; the rows after a slot's last full 16 are
+// Warps 2 p and 2 p + 1 share 64 features and three blocks at `out`, the copies of which the first
+// one's lane 0 issues (with two, the drain waited for its copies: 640 cycles for 32 rows).  Copies take 16 rows at a time; the rows after a slot's last full 16 are
 // stored by the threads, as what follows belongs to another slot.
 __device__ __forceinline__ void drain_bf16(const RowsArgs& a, const RowsTile& t, int O, int P, uint32_t tmem, uint32_t out, int m0,
                                            int q, int lane, int& blocks) {
@@ -145,13 +161,13 @@ __device__ __forceinline__ void drain_bf16(const RowsArgs& a, const RowsTile& t,
         tmem_ld_16x256(tmem + r, lo);
         tmem_ld_16x256(tmem + r + (16u << 16), hi);
         tmem_ld_wait();
-        const uint32_t block = out + (pair * 2 + (blocks & 1)) * 4096;
+        const uint32_t block = out + (pair * kOutBlocks + blocks % kOutBlocks) * 4096;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             stmatrix_trans(block + i * 1024 + at, pack_bf(lo[4 * i], lo[4 * i + 1]), pack_bf(lo[4 * i + 2], lo[4 * i + 3]),
                            pack_bf(hi[4 * i], hi[4 * i + 1]), pack_bf(hi[4 * i + 2], hi[4 * i + 3]));
         fence_async_smem();
-        if (issuer) bulk_wait_read();  // the other block is free, which the next round writes
+        if (issuer) bulk_wait_read_but<kOutBlocks - 2>();  // the block is free that the next round writes
         __syncwarp();
         named_sync(2 + pair, 64);
         if (issuer) {
@@ -399,7 +415,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- dW
-// One pair's tile: 256 of N (128 of dy's columns in each CTA) times 256 of K (128 of x's columns in
+// One pair's tile: 256 of N, or twice that (128 of dy's columns in each CTA), times 256 of K (128 of x's columns in
 // each), summed over the slot's rows, 64 at a time; both operands are MN-major.  Of a slot's last
 // chunk as many 16 rows are copied and multiplied as it has; the rows of the next slot among them are
 // set to zero in shared memory, in both operands, so whatever they hold stays out.
@@ -408,34 +424,94 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 struct WeightArgs {
     CUtensorMap dy[3];   // box {64, 1, 16 << j} of dy [R][P][N]
     CUtensorMap x[3];    // of x [R][1][K]; codes: box {128, 1, 16 << j}
-    CUtensorMap out[2];  // box {64, 32, 1} bf16, {32, 32, 1} fp32 of dw [S][N][K]
+    CUtensorMap out[2];  // box {64, 16, 1} bf16, {32, 32, 1} fp32 of dw [S][N][K]
     const float* scale;  // [R][n_blk]
     const int32_t* offsets;
     int R, K, N, P, S, type, n_blk, n_tiles;
     DevStatus st;
 };
+template <bool M2>
+struct WeightRing {
+    static constexpr int kA = M2 ? 2 * kHalf : kHalf;  // dy's; then x's
+    static constexpr int kStageBytes = kA + kHalf;
+    static constexpr int kStages = M2 ? 4 : 6;
+};
+static_assert(kRing == WeightRing<false>::kStages * WeightRing<false>::kStageBytes &&
+                  kRing == WeightRing<true>::kStages * WeightRing<true>::kStageBytes,
+              "rings of one size");
+
+// The products of one tile's chunks, issued by a warp that waits for chunk c by `ready(c)` and for an
+// accumulator by `free(slot, phase)`; `issue(half, stage, c, slot)` multiplies, and `release(stage)`
+// and `full(slot)` commit.  `u` counts accumulators.  With two halves the first runs ahead over the
+// stages in flight until the second one's accumulator is free; a stage is released by the second.
+template <int STAGES, typename Ready, typename Free, typename TestFree, typename Issue, typename Release, typename Full>
+__device__ __forceinline__ bool tile_products(bool two, int chunks, int& stage, int& u, Ready&& ready, Free&& free, TestFree&& test_free,
+                                              Issue&& issue, Release&& release, Full&& full) {
+    const int u0 = u;
+    u += two ? 2 : 1;
+    if (!free(u0)) return false;
+    if (!two) {
+        for (int c = 0; c < chunks; ++c) {
+            if (!ready(c)) return false;
+            issue(0, stage, c, u0);
+            release(stage);
+            if (++stage == STAGES) stage = 0;
+        }
+        full(u0);
+        return true;
+    }
+    int k0 = 0, k1 = 0, st1 = stage;
+    bool second = false;
+    while (k1 < chunks) {
+        if (!second) second = test_free(u0 + 1);
+        if (second && k1 < k0) {
+            issue(1, st1, k1, u0 + 1);
+            release(st1);
+            if (++st1 == STAGES) st1 = 0;
+            ++k1;
+        } else if (k0 < chunks && k0 - k1 < STAGES) {
+            if (!ready(k0)) return false;
+            issue(0, stage, k0, u0);
+            if (++stage == STAGES) stage = 0;
+            if (++k0 == chunks) full(u0);
+        } else {
+            if (!free(u0 + 1)) return false;
+            second = true;
+        }
+    }
+    full(u0 + 1);
+    return true;
+}
+
 // Four warps work on the rows of a chunk, 16 rows each, where the last one of a slot needs it.  Codes
-// all need it, and take them longer than the chunk's products: three such groups take chunks in turn.
+// all need it, and take them longer than the chunk's products: several such groups take chunks in turn.
+// A stage's chunks are all one group's (the groups divide the stages): a group that waited for a chunk
+// of a stage whose last chunk another group had not seen land would take that one's phase for its own.
 constexpr int kWork = 4;
 constexpr int kDrainWarps = 8;
 constexpr int kWeightOut = kDrainWarps * 4096;  // a block of 32 x 128 bytes of each draining warp
-constexpr int work_groups(bool x8) { return x8 ? 3 : 1; }
-constexpr int weight_threads(bool x8) { return 64 + 32 * kWork * work_groups(x8) + 32 * kDrainWarps; }
+constexpr int work_groups(bool x8, bool m2) { return !x8 ? 1 : m2 ? 2 : 3; }
+constexpr int weight_threads(bool x8, bool m2) { return 64 + 32 * kWork * work_groups(x8, m2) + 32 * kDrainWarps; }
 constexpr int kWeightSmem = 1024 + kRing + kWeightOut + 512;
 constexpr int kSignals = 384;  // of those 512 bytes: 16 for each stage, and 16 to send
+static_assert(kSignals + 16 * (WeightRing<false>::kStages + 1) <= 512, "signals");
 static_assert(kWeightSmem <= 227 * 1024, "shared memory overflow");
 
 struct WeightTile {
     int s, part, n0, k0;
     int row0, rows;
+    bool two;  // halves (M2)
 };
 
+template <bool M2>
 __device__ __forceinline__ WeightTile weight_tile(const WeightArgs& a, int i) {
-    const int kt = (a.K + 255) / 256, nt = (a.N + 255) / 256;
+    constexpr int kM = M2 ? 512 : 256;
+    const int kt = (a.K + 255) / 256, nt = (a.N + kM - 1) / kM;
     WeightTile t;
     t.k0 = i % kt * 256;
     i /= kt;
-    t.n0 = i % nt * 256;
+    t.n0 = i % nt * kM;
+    t.two = M2 && t.n0 + 256 < a.N;
     i /= nt;
     t.part = i % a.P;
     t.s = i / a.P;
@@ -457,8 +533,9 @@ __device__ __forceinline__ void decode16(const uint4& c, float scale, uint32_t (
     }
 }
 
-template <bool X8>
-__global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+template <bool X8, bool M2>
+__global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+    constexpr int kStages = WeightRing<M2>::kStages, kStageBytes = WeightRing<M2>::kStageBytes, kA = WeightRing<M2>::kA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kWeightOut);  // (the leader's) copies that need no work, of both
@@ -471,12 +548,13 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
     uint64_t* done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((5 * kStages + 5) * 8 + 8 <= kSignals && kSignals + 16 * (kStages + 1) <= 512, "barriers");
+    static_assert((5 * kStages + 5) * 8 + 8 <= kSignals, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
     const int rank = (int)cluster_rank();
-    constexpr int kGroups = work_groups(X8);
+    constexpr int kGroups = work_groups(X8, M2);
+    static_assert(kStages % kGroups == 0, "a stage is one group's");
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -525,16 +603,16 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
         int stage = 0;
         uint32_t phase = 0, used = 0, used_land = 0, land_phase = 0;
         for (int i = first; i < a.n_tiles && ok; i += step) {
-            const WeightTile t = weight_tile(a, i);
+            const WeightTile t = weight_tile<M2>(a, i);
             const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 128;
             for (int r = 0; r < t.rows; r += 64) {
                 const int left = min(64, t.rows - r), n16 = (left + 15) / 16;
                 const bool odd = left & 15, work = X8 || odd;
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 if (elect_one()) {
-                    const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kHalf;
+                    const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kA;
                     const uint32_t fb = lead_full + stage * 8, lb = landed_u + stage * 8;
-                    const uint32_t dy_bytes = n16 * 4096, x_bytes = X8 ? n16 * 2048 : n16 * 4096;
+                    const uint32_t dy_bytes = (t.two ? 2 : 1) * n16 * 4096, x_bytes = X8 ? n16 * 2048 : n16 * 4096;
                     if (!odd && rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * (dy_bytes + (X8 ? 0 : x_bytes)));
                     if (work && rank == 0) mbar_arrive_expect_tx(other_u + stage * 8, kWork * 16);
                     if (work) mbar_arrive_expect_tx(lb, X8 && !odd ? x_bytes : dy_bytes + x_bytes);
@@ -542,12 +620,18 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                         if (n16 & (1 << bit)) {
                             const int row = t.row0 + r + off * 16;
                             const uint32_t o = off * 2048;
-                            if (odd) {
-                                tma_load_3d(sa + o, &a.dy[bit], lb, n0, t.part, row, pol);
-                                tma_load_3d(sa + o + kHalf / 2, &a.dy[bit], lb, n0 + 64, t.part, row, pol);
-                            } else {
-                                tma_load_3d_pair(sa + o, &a.dy[bit], fb, n0, t.part, row, pol);
-                                tma_load_3d_pair(sa + o + kHalf / 2, &a.dy[bit], fb, n0 + 64, t.part, row, pol);
+#pragma unroll
+                            for (int h = 0; h < (M2 ? 2 : 1); ++h) {
+                                if (h && !t.two) break;
+                                const uint32_t to = sa + h * kHalf + o;
+                                const int n = n0 + h * 256;
+                                if (odd) {
+                                    tma_load_3d(to, &a.dy[bit], lb, n, t.part, row, pol);
+                                    tma_load_3d(to + kHalf / 2, &a.dy[bit], lb, n + 64, t.part, row, pol);
+                                } else {
+                                    tma_load_3d_pair(to, &a.dy[bit], fb, n, t.part, row, pol);
+                                    tma_load_3d_pair(to + kHalf / 2, &a.dy[bit], fb, n + 64, t.part, row, pol);
+                                }
                             }
                             if (X8) {
                                 tma_load_3d(sb + o, &a.x[bit], lb, k0, 0, row, pol);
@@ -588,44 +672,62 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
         // memory: the waits do not acquire for the cluster (100 to 200 ns each; three of them held the
         // products of codes up).
         bool ok = true;
-        int stage = 0, n = 0;
+        int stage = 0, at = 0, u = 0;
         uint32_t full_phase = 0, work_phase = 0;  // (of each stage: not every chunk uses both)
         if (rank == 0) {
             const uint32_t idesc = umma_idesc_bf16(256, 256) | kIdescAMnMajor | kIdescBMnMajor;
-            const uint64_t ad0 = umma_desc_mn_sw128(stage_u, kHalf / 2), bd0 = umma_desc_mn_sw128(stage_u + kHalf, kHalf / 2);
+            const uint64_t ad0 = umma_desc_mn_sw128(stage_u, kHalf / 2), bd0 = umma_desc_mn_sw128(stage_u + kA, kHalf / 2);
             for (int i = first; i < a.n_tiles && ok; i += step) {
-                const WeightTile t = weight_tile(a, i);
+                const WeightTile t = weight_tile<M2>(a, i);
                 if (t.rows == 0) continue;
-                const uint32_t d = tbase + (n & 1) * 256;
-                if (!(ok = warp_wait(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, limit))) break;
-                tc_fence_after();
-                for (int r = 0; r < t.rows; r += 64) {
-                    const int left = min(64, t.rows - r);
-                    if (!(left & 15)) {
-                        if (!(ok = warp_wait(full_u + stage * 8, (full_phase >> stage) & 1u, abort_flag, limit))) break;
-                        full_phase ^= 1u << stage;
-                    }
-                    if (X8 || (left & 15)) {
-                        if (!(ok = warp_wait(ready_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit) &&
-                                   warp_wait(other_u + stage * 8, (work_phase >> stage) & 1u, abort_flag, limit)))
-                            break;
-                        work_phase ^= 1u << stage;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t ad = ad0 + stage * (kStageBytes >> 4), bd = bd0 + stage * (kStageBytes >> 4);
-                        umma_bf16_pair(d, ad, bd, idesc, r > 0);
-                        if (left > 16) umma_bf16_pair(d, ad + 128, bd + 128, idesc, 1);
-                        if (left > 32) umma_bf16_pair(d, ad + 256, bd + 256, idesc, 1);
-                        if (left > 48) umma_bf16_pair(d, ad + 384, bd + 384, idesc, 1);
-                        umma_commit_pair(empty_u + stage * 8);
-                    }
-                    __syncwarp();
-                    if (++stage == kStages) stage = 0;
-                }
-                if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]));
-                __syncwarp();
-                ++n;
+                ok = tile_products<kStages>(
+                    t.two, (t.rows + 63) / 64, stage, u,
+                    [&](int c) {
+                        const int left = min(64, t.rows - c * 64);
+                        bool got = true;
+                        if (!(left & 15)) {
+                            got = warp_wait(full_u + at * 8, (full_phase >> at) & 1u, abort_flag, limit);
+                            full_phase ^= 1u << at;
+                        }
+                        if (X8 || (left & 15)) {
+                            got = got && warp_wait(ready_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit) &&
+                                  warp_wait(other_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit);
+                            work_phase ^= 1u << at;
+                        }
+                        if (++at == kStages) at = 0;
+                        tc_fence_after();
+                        return got;
+                    },
+                    [&](int v) {
+                        const bool got = warp_wait(smem_u32(&tempty[v & 1]), ((v >> 1) & 1) ^ 1, abort_flag, limit);
+                        tc_fence_after();
+                        return got;
+                    },
+                    [&](int v) {
+                        const bool got = __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&tempty[v & 1]), ((v >> 1) & 1) ^ 1));
+                        tc_fence_after();
+                        return got;
+                    },
+                    [&](int half, int st, int c, int v) {
+                        if (elect_one()) {
+                            const uint64_t ad = ad0 + st * (kStageBytes >> 4) + half * (kHalf >> 4), bd = bd0 + st * (kStageBytes >> 4);
+                            const uint32_t d = tbase + (v & 1) * 256;
+                            const int left = min(64, t.rows - c * 64);
+                            umma_bf16_pair(d, ad, bd, idesc, c > 0);
+                            if (left > 16) umma_bf16_pair(d, ad + 128, bd + 128, idesc, 1);
+                            if (left > 32) umma_bf16_pair(d, ad + 256, bd + 256, idesc, 1);
+                            if (left > 48) umma_bf16_pair(d, ad + 384, bd + 384, idesc, 1);
+                        }
+                        __syncwarp();
+                    },
+                    [&](int st) {
+                        if (elect_one()) umma_commit_pair(empty_u + st * 8);
+                        __syncwarp();
+                    },
+                    [&](int v) {
+                        if (elect_one()) umma_commit_pair(smem_u32(&tfull[v & 1]));
+                        __syncwarp();
+                    });
             }
             if (!ok && lane == 0) give_up();
             // all products are complete before the tensor memory is freed
@@ -643,14 +745,14 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
         int stage = 0, turn = 0;  // of the chunks that need work
         uint32_t land_phase = 0;
         for (int i = first; i < a.n_tiles && ok; i += step) {
-            const WeightTile t = weight_tile(a, i);
+            const WeightTile t = weight_tile<M2>(a, i);
             const int blk = (t.k0 + rank * 128) / MOE_PAYLOAD_BLOCK;
             for (int r = 0; r < t.rows; r += 64) {
                 const int left = min(64, t.rows - r), rows16 = (left + 15) & ~15;
                 const bool work = X8 || (left & 15), mine = work && turn == group;
                 if (work && ++turn == kGroups) turn = 0;
                 if (mine) {
-                    const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kHalf;
+                    const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kA;
                     // codes: four threads a row, 32 columns each, 8 rows at a time
                     const int row0 = sub * 16 + (lane >> 2), part = lane & 3, flip = part >> 1;
                     float scale[2] = {0.0f, 0.0f};
@@ -692,6 +794,10 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
                             const uint32_t o = row * 128 + (lane & 7) * 16;
                             st_shared4(sa + o, 0, 0, 0, 0);
                             st_shared4(sa + o + kHalf / 2, 0, 0, 0, 0);
+                            if (t.two) {
+                                st_shared4(sa + o + kHalf, 0, 0, 0, 0);
+                                st_shared4(sa + o + kHalf + kHalf / 2, 0, 0, 0, 0);
+                            }
                             if (!X8) {
                                 st_shared4(sb + o, 0, 0, 0, 0);
                                 st_shared4(sb + o + kHalf / 2, 0, 0, 0, 0);
@@ -718,57 +824,81 @@ __global__ void __launch_bounds__(weight_threads(X8), 1) weights_kernel(const __
     } else {
         // two warps for each quarter of the accumulators, half of the columns each
         const int q = warp & 3, part = (warp - 2 - kWork * kGroups) >> 2;
-        const uint32_t block = stage_u + kRing + (part * 4 + q) * 4096, to = block + lane * 128;
+        const uint32_t block = stage_u + kRing + (part * 4 + q) * 4096;
         bool ok = true;
-        int n = 0;
-        for (int i = first; i < a.n_tiles; i += step) {
-            const WeightTile t = weight_tile(a, i);
+        int u = 0;
+        for (int i = first; i < a.n_tiles && ok; i += step) {
+            const WeightTile t = weight_tile<M2>(a, i);
             if (t.rows == 0 && a.type == MOE_OUT_F32_ADD) continue;
-            if (t.rows) {
-                if (!(ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit))) break;
-                tc_fence_after();
-            }
-            const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
-            const int row = t.n0 + rank * 128 + q * 32;
-            const bool bf16 = a.type == MOE_OUT_BF16;
-            const int by = bf16 ? 64 : 32;  // 128 bytes
-            for (int c = part * 128; c < min(part * 128 + 128, a.K - t.k0); c += by) {
-                if (lane == 0) bulk_wait_read();  // the block's last copy has read it
-                __syncwarp();
+            for (int half = 0; half < (t.two ? 2 : 1); ++half) {
+                if (t.rows) {
+                    if (!(ok = warp_wait(smem_u32(&tfull[u & 1]), (u >> 1) & 1, abort_flag, limit))) break;
+                    tc_fence_after();
+                }
+                const uint32_t tmem = tbase + (u & 1) * 256 + ((uint32_t)(q * 32) << 16);
+                const int row = t.n0 + half * 256 + rank * 128 + q * 32;
+                const int c_end = min(part * 128 + 128, a.K - t.k0);
+                if (a.type == MOE_OUT_BF16) {
+                    // 16 rows x 64 columns at a time, as 8 x 8 fragments that stmatrix puts in rows, in two
+                    // blocks in turn (32 rows in one waited for each copy: 2200 cycles an accumulator)
+                    for (int c = part * 128; c < c_end; c += 64)
 #pragma unroll 1
-                for (int h = 0; h < by; h += 32) {
-                    uint32_t v[32];
-                    if (t.rows) {
-                        tmem_ld32(tmem + c + h, v);
-                        tmem_ld_wait();
-                    } else {
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t v[32];
+                            if (t.rows) {
+                                tmem_ld_16x256_64(tmem + c + ((uint32_t)(h * 16) << 16), v);
+                                tmem_ld_wait();
+                            } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0;
-                    }
-                    if (bf16) {
+                                for (int k = 0; k < 32; ++k) v[k] = 0;
+                            }
+                            if (lane == 0) bulk_wait_read_but<1>();  // the copy before the last has read this block
+                            __syncwarp();
+                            // this lane's address of 8 columns of a row: matrix lane / 8 is columns 8 (lane / 16), rows 8 (lane / 8 % 2)
+                            const int row8 = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            st_shared4(to + (((h / 8 + k) ^ (lane & 7)) << 4), pack_bf(v[8 * k], v[8 * k + 1]), pack_bf(v[8 * k + 2], v[8 * k + 3]),
-                                       pack_bf(v[8 * k + 4], v[8 * k + 5]), pack_bf(v[8 * k + 6], v[8 * k + 7]));
-                    } else {
+                            for (int k = 0; k < 8; k += 2)
+                                stmatrix(block + h * 2048 + row8 * 128 + (((k + (lane >> 4)) ^ (lane & 7)) << 4), pack_bf(v[4 * k], v[4 * k + 1]),
+                                         pack_bf(v[4 * k + 2], v[4 * k + 3]), pack_bf(v[4 * k + 4], v[4 * k + 5]),
+                                         pack_bf(v[4 * k + 6], v[4 * k + 7]));
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (row + h * 16 < a.N) tma_store_3d(&a.out[t.part], block + h * 2048, t.k0 + c, row + h * 16, t.s);
+                                bulk_commit();
+                            }
+                            __syncwarp();
+                        }
+                } else {
+                    for (int c = part * 128; c < c_end; c += 32) {
+                        uint32_t v[32];
+                        if (t.rows) {
+                            tmem_ld32(tmem + c, v);
+                            tmem_ld_wait();
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = 0;
+                        }
+                        if (lane == 0) bulk_wait_read();  // the block's last copy has read it
+                        __syncwarp();
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            st_shared4(to + ((k ^ (lane & 7)) << 4), v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                            st_shared4(block + lane * 128 + ((k ^ (lane & 7)) << 4), v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (row < a.N) put(&a.out[t.part], a.type, block, t.k0 + c, row, t.s);
+                            bulk_commit();
+                        }
+                        __syncwarp();
                     }
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (row < a.N) put(&a.out[t.part], a.type, block, t.k0 + c, row, t.s);
-                    bulk_commit();
+                if (t.rows) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed_cluster(lead_tempty + (u & 1) * 8);
+                    ++u;
                 }
-                __syncwarp();
-            }
-            if (t.rows) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed_cluster(lead_tempty + (n & 1) * 8);
-                ++n;
             }
         }
         if (!ok && lane == 0) give_up();
@@ -834,6 +964,14 @@ int out_map(CUtensorMap* map, void* out, uint64_t d0, uint64_t d1, uint64_t d2, 
                                 : make_tmap_f32(map, out, d0, d1, d2, 32, box1, box2);
 }
 
+template <bool X8, bool M2>
+int launch_weights(WeightArgs& a, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    const long tiles = (long)((a.K + 255) / 256) * (M2 ? (a.N + 511) / 512 : (a.N + 255) / 256) * a.P * a.S;
+    a.n_tiles = (int)tiles;
+    return launch_pairs(weights_kernel<X8, M2>, configured, weight_threads(X8, M2), kWeightSmem, tiles, stream, a, "expert weight gradient");
+}
+
 template <bool DX>
 int rows_product(const moe_project_t* p, int rows, const void* in, const int32_t* offsets, const void* w, const void* w2, void* out,
                  int type, const DevStatus& st, cudaStream_t stream) {
@@ -872,9 +1010,10 @@ int weights_product(const moe_project_t* p, int rows, const void* dy, const void
             (rc = X8 ? make_tmap_3d(&a.x[j], x, K, 1, R, K, K, 128, 1, 16u << j, true)
                      : make_tmap_3d(&a.x[j], x, K, 1, R, K * 2, K * 2, 64, 1, 16u << j)))
             return rc;
-    if ((rc = out_map(&a.out[0], dw, K, N, S, type, 32, 1))) return rc;
+    const uint32_t box = type == MOE_OUT_BF16 ? 16 : 32;
+    if ((rc = out_map(&a.out[0], dw, K, N, S, type, box, 1))) return rc;
     a.out[1] = a.out[0];
-    if (dw2 && (rc = out_map(&a.out[1], dw2, K, N, S, type, 32, 1))) return rc;
+    if (dw2 && (rc = out_map(&a.out[1], dw2, K, N, S, type, box, 1))) return rc;
     a.scale = scale;
     a.offsets = offsets;
     a.R = rows;
@@ -885,10 +1024,14 @@ int weights_product(const moe_project_t* p, int rows, const void* dy, const void
     a.type = type;
     a.n_blk = (p->in_features + MOE_PAYLOAD_BLOCK - 1) / MOE_PAYLOAD_BLOCK;
     a.st = st;
-    const uint64_t tiles = (K + 255) / 256 * ((N + 255) / 256) * P * S;
-    a.n_tiles = (int)tiles;
-    static std::atomic<uint64_t> configured{0};
-    return launch_pairs(weights_kernel<X8>, configured, weight_threads(X8), kWeightSmem, (long)tiles, stream, a, "expert weight gradient");
+    // Twice 256 of N where that leaves every pair several tiles and, rows in bf16, where a slot has many
+    // rows: the products of a tile hide the drain of one accumulator, not of the first of two (16 slots,
+    // gate and up of 7168 to 2048: 128 rows a slot 163 us with 256 and 167 with twice that, 256 both 226,
+    // 512 396 and 329; codes, which are turned half as often, 187 and 171, 266 and 244, 447 and 428.  16
+    // slots of 1024 to 1024, 512 rows each: 19.1 and 21.1).
+    const long tiles = (long)((K + 255) / 256 * ((N + 511) / 512) * P * S);
+    const bool m2 = tiles >= 2L * num_sms() && (X8 || rows >= 384L * p->n_slots);
+    return m2 ? launch_weights<X8, true>(a, stream) : launch_weights<X8, false>(a, stream);
 }
 
 }  // namespace

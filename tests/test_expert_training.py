@@ -150,6 +150,54 @@ def test_every_count_of_rows(P):
         close(got[1][p], dw[0][p], dw[1][p], name=f"dw{p}")
 
 
+# many rows a slot; with 48 slots so many tiles too that those of dw are twice as high, with heights that
+# end in either half of one
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N,P,times", [(136, 200, 1, 1), (1288, 776, 2, 1), (264, 520, 2, 4), (520, 1032, 1, 4), (776, 264, 2, 4)])
+def test_slots_of_many_rows(K, N, P, times):
+    counts = [0, 1, 31, 300, 513, 1025, 0, 576, 97, 2000, 16, 250] * times
+    off = np.concatenate([[0], np.cumsum(counts)])
+    c = Case(int(off[-1]) + 5, K, N, len(counts), P, off, seed=12)
+    y, dx, dw = c.reference()
+    close(c.forward(), *y, name="y")
+    got = c.backward()
+    close(got[0], *dx, name="dx")
+    for p in range(P):
+        close(got[1][p], dw[0][p], dw[1][p], name=f"dw{p}")
+    wide = c.backward(dx_type=F32, dw_type=F32)
+    close(wide[0], *dx, name="dx fp32")
+    added = c.backward(dx=False, dw_type=F32, add_dw=True, fill=1.0)
+    for p in range(P):
+        close(wide[1][p], dw[0][p], dw[1][p], name=f"dw{p} fp32")
+        close(added[1][p], dw[0][p] + 1.0, dw[1][p] + STEP * (dw[0][p].abs() + 1.0), name=f"dw{p} added")
+    assert m.moe_check_status() == 0
+    # the first row of a slot is not its neighbour's, whatever it holds
+    for r in (int(off[4]), int(off[5]), int(off[8]), int(off[10]), c.R - 1):
+        c.x[r, 3], c.dy[r, 5] = float("inf"), float("nan")
+    got = c.backward()
+    for s in (1, 2, 3, 9, 11):
+        close(got[1][0][s], dw[0][0][s], dw[1][0][s], name="dw beside infinities")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N,P,times", [(144, 200, 2, 1), (784, 1032, 1, 1), (272, 520, 2, 8), (528, 1032, 1, 8), (784, 264, 2, 8)])
+def test_weight_gradient_of_many_rows_kept_in_8_bits(K, N, P, times):
+    counts = [700, 0, 1, 513, 1030, 97] if times == 1 else [170, 0, 1, 129, 64, 95] * times
+    off = np.concatenate([[0], np.cumsum(counts)])
+    c = Case(int(off[-1]) + 5, K, N, len(counts), P, off, seed=13)
+    g = torch.Generator().manual_seed(K)
+    # (codes and scales by themselves: every code is a value, the scale of a row any power of two)
+    codes = torch.randint(0, 256, (c.R, K), generator=g).to(torch.uint8)
+    codes = torch.where((codes & 0x7F) == 0x7F, codes - 1, codes)
+    scales = torch.exp2(torch.randint(-12, 4, (c.R, -(-K // 128)), generator=g).float())
+    values = (codes.view(torch.float8_e4m3fn).double() * scales.double().repeat_interleave(128, 1)[:, :K]).to(BF)
+    _, got = c.backward(dx=False, eight=(codes, scales))
+    assert m.moe_check_status() == 0
+    _, _, dw = c.reference(values)
+    for p in range(P):
+        close(got[p], dw[0][p], dw[1][p], name=f"dw{p}")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("R,K,N,S,P", [(100, 72, 136, 5, 2), (700, 600, 328, 3, 1), (45, 264, 512, 9, 2)])
 def test_fp32_outputs_written_and_added(R, K, N, S, P):
