@@ -43,20 +43,36 @@ __device__ __forceinline__ uint32_t no_inf(uint32_t w) {
     return w;
 }
 
-// The exponent of a block's scale, from 8 of its values in each of 16 lanes (the whole warp calls).
-// Values whose |x| reaches infinity or NaN leave the maximum, and become NaN.
-__device__ __forceinline__ int block_exponent(uint4& v) {
-    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-    if (__any_sync(0xffffffffu, (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u)) {
-        m = __vmaxu2(__vmaxu2(finite_abs(v.x), finite_abs(v.y)), __vmaxu2(finite_abs(v.z), finite_abs(v.w)));
-        v = make_uint4(no_inf(v.x), no_inf(v.y), no_inf(v.z), no_inf(v.w));
-    }
+// The largest of 8 bf16 (no signs), as their bits in the lower half.
+__device__ __forceinline__ uint32_t top8(uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    const uint32_t m = __vmaxu2(__vmaxu2(x, y), __vmaxu2(z, w));
+    return max(m & 0xffffu, m >> 16);
+}
+
+// The exponent of a block's scale, from the bits of its largest value: 448 is 1.75 * 2^8.
+__device__ __forceinline__ int exponent_of(uint32_t top) {
+    return top ? min(max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0), -117), 119) : 0;
+}
+
+// The exponents of two blocks' scales, from 8 values of each in each of 16 lanes (the whole warp calls):
+// their maxima go through the lanes together.  Values that are no numbers leave them, and become NaN.
+__device__ __forceinline__ void block_exponents(uint4& v, uint4& w, int& ev, int& ew) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    auto reduce = [](uint32_t m) {
 #pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const uint32_t top = max(m & 0xffffu, m >> 16);  // bf16 bits: exponent, then 7 of the mantissa
-    if (top == 0) return 0;
-    // 448 is 1.75 * 2^8
-    return min(max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0), -117), 119);
+        for (int d = kLanes / 2; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+        return m;
+    };
+    uint32_t m = reduce(top8(v.x & kAbs, v.y & kAbs, v.z & kAbs, v.w & kAbs) |
+                        (top8(w.x & kAbs, w.y & kAbs, w.z & kAbs, w.w & kAbs) << 16));
+    if (__any_sync(0xffffffffu, (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u)) {
+        m = reduce(top8(finite_abs(v.x), finite_abs(v.y), finite_abs(v.z), finite_abs(v.w)) |
+                   (top8(finite_abs(w.x), finite_abs(w.y), finite_abs(w.z), finite_abs(w.w)) << 16));
+        v = make_uint4(no_inf(v.x), no_inf(v.y), no_inf(v.z), no_inf(v.w));
+        w = make_uint4(no_inf(w.x), no_inf(w.y), no_inf(w.z), no_inf(w.w));
+    }
+    ev = exponent_of(m & 0xffffu);
+    ew = exponent_of(m >> 16);
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -83,13 +99,14 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
     }
 }
 
-// sigmoid(g) and 1 - sigmoid(g), each as exact as the other: e^-|g| does not overflow, and neither
-// is a difference.
-__device__ __forceinline__ void sigmoids(float g, float& s, float& rest) {
-    const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e);
-    s = g >= 0.0f ? r : e * r;
-    rest = g >= 0.0f ? e * r : r;
-    if (g != g) s = g;
+// 1 / (1 + e^-g).  e^-g overflows below -88, where the result is 0 instead of e^g (under 2^-126).
+// 1 - sigmoid is taken as a difference: what it loses (2^-24) counts beside 1 where it is used, times g,
+// and is 0 from g = 17 on, where the sigmoid is 1.
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
 }
 
 // Block u of the CTA's, of `n` a row.  Its row without a division where there are few of them: below
@@ -133,11 +150,14 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const uint16_t* __restri
         v[i] = make_uint4(0, 0, 0, 0);
         if (at[i] != ~size_t(0)) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + at[i]));
     }
+    static_assert(U % 2 == 0, "blocks in pairs");
+    int e[U];
+#pragma unroll
+    for (int i = 0; i < U; i += 2) block_exponents(v[i], v[i + 1], e[i], e[i + 1]);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int e = block_exponent(v[i]);
-        if (at[i] != ~size_t(0)) *reinterpret_cast<uint2*>(codes + at[i]) = encode8(v[i], e);
-        if (lane == 0 && at[i] != ~size_t(0)) scale[first + i * kGroups + group] = pow2(e);
+        if (at[i] != ~size_t(0)) *reinterpret_cast<uint2*>(codes + at[i]) = encode8(v[i], e[i]);
+        if (lane == 0 && at[i] != ~size_t(0)) scale[first + i * kGroups + group] = pow2(e[i]);
     }
 }
 
@@ -176,12 +196,11 @@ __global__ void __launch_bounds__(kThreads) swiglu_keep_kernel(const uint16_t* _
         const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w}, uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float a, b, rest;
-            sigmoids(lo_of(gw[j]), a, rest);
-            sigmoids(hi_of(gw[j]), b, rest);
-            out[j] = pack_bf(lo_of(gw[j]) * a * lo_of(uw[j]), hi_of(gw[j]) * b * hi_of(uw[j]));
+            const float a = lo_of(gw[j]), b = hi_of(gw[j]);
+            out[j] = pack_bf(a * sigmoid(a) * lo_of(uw[j]), b * sigmoid(b) * hi_of(uw[j]));
         }
-        const int eg = block_exponent(g[i]), eu = block_exponent(u[i]);
+        int eg, eu;
+        block_exponents(g[i], u[i], eg, eu);
         if (p[i].gate == ~size_t(0)) continue;
         *reinterpret_cast<uint4*>(h + p[i].h) = make_uint4(out[0], out[1], out[2], out[3]);
         *reinterpret_cast<uint2*>(codes + p[i].gate) = encode8(g[i], eg);
@@ -227,12 +246,10 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float up = j & 1 ? hi_of(dw[j >> 1]) : lo_of(dw[j >> 1]);
-            float s, rest;
-            sigmoids(g[j], s, rest);
-            const float silu = g[j] * s;
+            const float s = sigmoid(g[j]), silu = g[j] * s;
             act[j] = silu * u[j];
             du[j] = up * silu;
-            dg[j] = up * u[j] * (s * fmaf(g[j], rest, 1.0f));
+            dg[j] = up * u[j] * (s * fmaf(g[j], 1.0f - s, 1.0f));
         }
         uint16_t* out = d_gate_up + p[i].gate;
         *reinterpret_cast<uint4*>(out) =
