@@ -20,9 +20,7 @@ namespace {
 constexpr int kMaxSlots = 1024;
 constexpr int kMaxFeatures = 1 << 24;
 constexpr int kHalf = 128 * 64 * 2;  // one CTA's 128 rows or features of an operand's 64-wide chunk
-constexpr int kStages = 6;
-constexpr int kStageBytes = 2 * kHalf;
-constexpr int kRing = kStages * kStageBytes;
+constexpr int kRing = 12 * kHalf;
 
 __device__ __forceinline__ uint32_t to_u(float f) { return __float_as_uint(f); }
 
@@ -96,9 +94,26 @@ __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// How the pair's kernels end.  On the way out nobody signals the other CTA any more (who waits for
+// signals has waited for all of them), so the barrier need not see them through; after a wait that
+// expired it does.
+__device__ __forceinline__ void leave_pair(const volatile int* abort_flag, bool owner, uint32_t tmem) {
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        cluster_sync();
+    } else {
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
+    tc_fence_after();
+    if (owner) tmem_dealloc_pair(tmem, 512);
+}
+
 // ---------------------------------------------------------------- y and dx
 // One pair's tile: 256 outputs (128 rows of W, or for dx columns, in each CTA) times the rows of
-// a slot in chunks of equal height, a multiple of 32 up to 256 (half of them in each CTA).
+// a slot in chunks of equal height, a multiple of 32 up to `cap` (half of them in each CTA).
 // dx's W is read MN-major, as its contraction runs over W's rows.
 struct RowsArgs {
     CUtensorMap w[2];  // box {64, 128} of [S][N][K], dx: {64, 64}
@@ -107,15 +122,20 @@ struct RowsArgs {
     const int32_t* offsets;
     void* out_ptr;
     int R, K, N, P, S, type;
+    int cap, stages;   // rows of a chunk at most (64, 128, 256); stages of the ring that then fit
     DevStatus st;
 };
+constexpr int kMostStages = 9;
+__host__ __device__ constexpr int stage_bytes(int cap) { return kHalf + cap / 2 * 128; }
+static_assert(kMostStages * stage_bytes(64) <= kRing && 8 * stage_bytes(128) <= kRing && 6 * stage_bytes(256) <= kRing, "rings");
 constexpr int kRowsThreads = 192;  // copies, products, four warps that drain accumulators
 constexpr int kOutBlocks = 3;
 constexpr int kOutBytes = 2 * kOutBlocks * 4096;  // of 32 rows x 64 features each, for two pairs of warps
-constexpr int kRowsSmem = 1024 + kRing + kOutBytes + 256 + (kMaxSlots + 1) * 4;
+constexpr int kRowsSmem = 1024 + kRing + kOutBytes + 256 + 2 * (kMaxSlots + 1) * 4;
 static_assert(kRowsSmem <= 227 * 1024, "shared memory overflow");
 
-__device__ __forceinline__ int chunks_of(int count) { return (count + 255) / 256; }
+// cap is a power of two
+__device__ __forceinline__ int chunks_of(int count, int cap) { return (int)((unsigned)(count + cap - 1) / (unsigned)cap); }
 
 struct RowsTile {
     int s, part, m0;   // slot; part and first output of it
@@ -124,7 +144,7 @@ struct RowsTile {
 };
 
 template <bool DX>
-__device__ __forceinline__ RowsTile rows_tile(const RowsArgs& a, const int* pre, int i) {
+__device__ __forceinline__ RowsTile rows_tile(const RowsArgs& a, const int* pre, const int* start, int i) {
     int lo = 0, hi = a.S - 1;  // the last slot with pre[s] <= i
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -133,13 +153,12 @@ __device__ __forceinline__ RowsTile rows_tile(const RowsArgs& a, const int* pre,
     }
     RowsTile t;
     t.s = lo;
-    int r0, r1;
-    slot_rows(a.offsets, t.s, a.R, r0, r1);
-    const int n = chunks_of(r1 - r0), l = i - pre[t.s], c = l % n, m = l / n;
+    const int r0 = start[t.s], r1 = max(r0, start[t.s + 1]);
+    const int n = chunks_of(r1 - r0, a.cap), l = i - pre[t.s], m = l / n, c = l - m * n;
     // (heights within 32 of each other: a chunk of few rows reads as much of W as a high one)
     const int units = (r1 - r0 + 31) / 32, h = units / n, more = units - h * n;
     const int tiles = ((DX ? a.K : a.N) + 255) / 256;
-    t.part = m / tiles;
+    t.part = m >= tiles;
     t.m0 = (m - t.part * tiles) * 256;
     t.row0 = r0 + 32 * (c * h + min(c, more));
     t.bn = 32 * (h + (c < more ? 1 : 0));
@@ -149,8 +168,9 @@ __device__ __forceinline__ RowsTile rows_tile(const RowsArgs& a, const int* pre,
 }
 
 // Warps 2 p and 2 p + 1 share 64 features and three blocks at `out`, the copies of which the first
-// one's lane 0 issues (with two, the drain waited for its copies: 640 cycles for 32 rows).  Copies take 16 rows at a time; the rows after a slot's last full 16 are
-// stored by the threads, as what follows belongs to another slot.
+// one's lane 0 issues (with two, the drain waited for its copies: 640 cycles for 32 rows).  Copies take
+// 16 rows at a time; the rows after a slot's last full 16 are stored by the threads, as what follows
+// belongs to another slot.
 __device__ __forceinline__ void drain_bf16(const RowsArgs& a, const RowsTile& t, int O, int P, uint32_t tmem, uint32_t out, int m0,
                                            int q, int lane, int& blocks) {
     const int pair = q >> 1, f0 = m0 + pair * 64;
@@ -227,14 +247,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kOutBytes);  // (the leader's)
-    uint64_t* empty = full + kStages;
-    uint64_t* tfull = empty + kStages;
+    uint64_t* empty = full + kMostStages;
+    uint64_t* tfull = empty + kMostStages;
     uint64_t* tempty = tfull + 2;  // (the leader's)
     uint64_t* done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barriers");
+    static_assert((2 * kMostStages + 5) * 8 + 8 <= 256, "barriers");
     int* pre = reinterpret_cast<int*>(smem + kRing + kOutBytes + 256);  // tiles before each slot
+    int* start = pre + kMaxSlots + 1;                                   // its first row
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
@@ -242,6 +263,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     const int O = DX ? a.K : a.N, out_parts = DX ? 1 : a.P;
     const int m_tiles = (O + 255) / 256 * out_parts;
     const int kc1 = ((DX ? a.N : a.K) + 63) / 64, kc = kc1 * (DX ? a.P : 1);  // chunks of a part, of a tile
+    const int kStages = a.stages, kStageBytes = stage_bytes(a.cap);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -260,6 +282,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         tma_prefetch_desc(&a.out);
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    __syncwarp();
+    cluster_arrive_relaxed();
     pdl_wait();
     if (warp == 0) {
         const int per = (a.S + 31) / 32, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
@@ -268,7 +292,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         for (int s = s0; s < s1; ++s) {
             int r0, r1;
             fits &= slot_rows(a.offsets, s, a.R, r0, r1);
-            sum += chunks_of(r1 - r0) * m_tiles;
+            start[s] = r0;
+            if (s == a.S - 1) start[a.S] = r1;
+            pre[s] = sum;
+            sum += chunks_of(r1 - r0, a.cap) * m_tiles;
         }
         if (!fits && blockIdx.x == 0) raise_status(a.st, kStatusBadShape);
         int incl = sum;
@@ -277,22 +304,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             const int v = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += v;
         }
-        int run = incl - sum;
-        for (int s = s0; s < s1; ++s) {
-            int r0, r1;
-            slot_rows(a.offsets, s, a.R, r0, r1);
-            pre[s] = run;
-            run += chunks_of(r1 - r0) * m_tiles;
-        }
+        for (int s = s0; s < s1; ++s) pre[s] += incl - sum;
         if (lane == 31) pre[a.S] = incl;
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // the barriers of both CTAs exist before either is signalled
     tc_fence_after();
-    pdl_launch_dependents();  // (not before the tensor memory is this pair's: the next kernel takes its own)
     const uint32_t tbase = *tmem_slot;
     const int n_tiles = pre[a.S], first = blockIdx.x / 2, step = gridDim.x / 2;
+    RowsTile t = {};
+    if (first < n_tiles) t = rows_tile<DX>(a, pre, start, first);
+    auto next_tile = [&](int i) {
+        if (i + step < n_tiles) t = rows_tile<DX>(a, pre, start, i + step);
+    };
+    cluster_wait();  // the barriers and tensor memory of both CTAs are there before either is used
+    pdl_launch_dependents();  // (not before the tensor memory is this pair's: the next kernel takes its own)
     auto give_up = [&]() {
         *abort_flag = 1;
         raise_status(a.st, kStatusWaitTimeout);
@@ -305,8 +331,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         bool ok = true;
         int stage = 0;
         uint32_t phase = 0, used = 0;
-        for (int i = first; i < n_tiles && ok; i += step) {
-            const RowsTile t = rows_tile<DX>(a, pre, i);
+        for (int i = first; i < n_tiles && ok; next_tile(i), i += step) {
             const int m0 = t.m0 + rank * 128, n16 = t.bn / 32, row0 = t.row0 + rank * n16 * 16;
             const uint64_t pol_w = t.shared_w ? pol : pol_once;
             for (int c = 0; c < kc; ++c) {
@@ -354,8 +379,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             bool ok = true;
             int stage = 0;
             uint32_t phase = 0;
-            for (int i = first, n = 0; i < n_tiles && ok; i += step, ++n) {
-                const RowsTile t = rows_tile<DX>(a, pre, i);
+            for (int i = first, n = 0; i < n_tiles && ok; next_tile(i), i += step, ++n) {
                 const uint32_t idesc = umma_idesc_bf16(256, t.bn) | (DX ? kIdescAMnMajor : 0u);
                 const uint32_t d = tbase + (n & 1) * 256;
                 if (!(ok = warp_wait(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, limit))) break;
@@ -391,8 +415,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         const int q = warp & 3;
         bool ok = true;
         int blocks = 0;
-        for (int i = first, n = 0; i < n_tiles; i += step, ++n) {
-            const RowsTile t = rows_tile<DX>(a, pre, i);
+        for (int i = first, n = 0; i < n_tiles; next_tile(i), i += step, ++n) {
             ok = warp_wait(smem_u32(&tfull[n & 1]), (n >> 1) & 1, abort_flag, limit);
             if (!(ok = named_and(2 + (q >> 1), 64, ok))) break;  // (the two warps that share drain_bf16's barrier)
             tc_fence_after();
@@ -401,17 +424,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             else drain_f32(a, t, O, out_parts, tmem, out, t.m0 + rank * 128, q, lane, blocks);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_relaxed_cluster(lead_tempty + (n & 1) * 8);
+            // (not where nobody waits for it any more: no signal is on its way at the end)
+            if (lane == 0 && i + 2 * step < n_tiles) mbar_arrive_relaxed_cluster(lead_tempty + (n & 1) * 8);
         }
         if (!ok && lane == 0) give_up();
         if (lane == 0) bulk_wait();
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // neither CTA leaves while the other may signal it or read its memory
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc_pair(tbase, 512);
+    leave_pair(abort_flag, warp == 1, tbase);
 }
 
 // ---------------------------------------------------------------- dW
@@ -576,7 +595,14 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
         tma_prefetch_desc(&a.out[0]);
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    __syncwarp();
+    cluster_arrive_relaxed();
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
     pdl_wait();
+    WeightTile t = weight_tile<M2>(a, first);  // (there are as many tiles as pairs at least)
+    auto next_tile = [&](int i) {
+        if (i + step < a.n_tiles) t = weight_tile<M2>(a, i + step);
+    };
     if (warp == 0 && blockIdx.x == 0)
         for (int s = lane; s < a.S; s += 32) {
             int r0, r1;
@@ -584,11 +610,10 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
         }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // the barriers of both CTAs exist before either is signalled
     tc_fence_after();
+    cluster_wait();  // the barriers and tensor memory of both CTAs are there before either is used
     pdl_launch_dependents();  // (not before the tensor memory is this pair's)
     const uint32_t tbase = *tmem_slot;
-    const int first = blockIdx.x / 2, step = gridDim.x / 2;
     auto give_up = [&]() {
         *abort_flag = 1;
         raise_status(a.st, kStatusWaitTimeout);
@@ -602,8 +627,7 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
         bool ok = true;
         int stage = 0;
         uint32_t phase = 0, used = 0, used_land = 0, land_phase = 0;
-        for (int i = first; i < a.n_tiles && ok; i += step) {
-            const WeightTile t = weight_tile<M2>(a, i);
+        for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
             const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 128;
             for (int r = 0; r < t.rows; r += 64) {
                 const int left = min(64, t.rows - r), n16 = (left + 15) / 16;
@@ -677,8 +701,7 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
         if (rank == 0) {
             const uint32_t idesc = umma_idesc_bf16(256, 256) | kIdescAMnMajor | kIdescBMnMajor;
             const uint64_t ad0 = umma_desc_mn_sw128(stage_u, kHalf / 2), bd0 = umma_desc_mn_sw128(stage_u + kA, kHalf / 2);
-            for (int i = first; i < a.n_tiles && ok; i += step) {
-                const WeightTile t = weight_tile<M2>(a, i);
+            for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
                 if (t.rows == 0) continue;
                 ok = tile_products<kStages>(
                     t.two, (t.rows + 63) / 64, stage, u,
@@ -729,6 +752,8 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
                         __syncwarp();
                     });
             }
+            // (the last accumulators have been handed back: no signal is on its way at the end)
+            for (int v = max(0, u - 2); v < u && ok; ++v) ok = warp_wait(smem_u32(&tempty[v & 1]), (v >> 1) & 1, abort_flag, limit);
             if (!ok && lane == 0) give_up();
             // all products are complete before the tensor memory is freed
             if (elect_one()) umma_commit_pair(smem_u32(done));
@@ -744,8 +769,7 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
         bool ok = true;
         int stage = 0, turn = 0;  // of the chunks that need work
         uint32_t land_phase = 0;
-        for (int i = first; i < a.n_tiles && ok; i += step) {
-            const WeightTile t = weight_tile<M2>(a, i);
+        for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
             const int blk = (t.k0 + rank * 128) / MOE_PAYLOAD_BLOCK;
             for (int r = 0; r < t.rows; r += 64) {
                 const int left = min(64, t.rows - r), rows16 = (left + 15) & ~15;
@@ -827,8 +851,7 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
         const uint32_t block = stage_u + kRing + (part * 4 + q) * 4096;
         bool ok = true;
         int u = 0;
-        for (int i = first; i < a.n_tiles && ok; i += step) {
-            const WeightTile t = weight_tile<M2>(a, i);
+        for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
             if (t.rows == 0 && a.type == MOE_OUT_F32_ADD) continue;
             for (int half = 0; half < (t.two ? 2 : 1); ++half) {
                 if (t.rows) {
@@ -904,12 +927,7 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
         if (!ok && lane == 0) give_up();
         if (lane == 0) bulk_wait();
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // neither CTA leaves while the other may signal it or read its memory
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc_pair(tbase, 512);
+    leave_pair(abort_flag, warp == 1, tbase);
 }
 
 int check_project(const moe_project_t* p, int rows) {
@@ -994,8 +1012,15 @@ int rows_product(const moe_project_t* p, int rows, const void* in, const int32_t
     a.S = p->n_slots;
     a.type = type;
     a.st = st;
+    // Where there is about a tile for each pair, what counts is how soon its chunks are there: lower ones,
+    // of which more fit the ring, where slots have few rows (400 rows of 16 slots, gate and up of 600 to
+    // 328: XX us with 256 rows, YY with 64).
+    const long m_tiles = (long)((O + 255) / 256 * OP);
+    a.cap = 256;
+    if (m_tiles * std::min(rows, p->n_slots) <= num_sms() / 2) a.cap = rows <= 48L * p->n_slots ? 64 : rows <= 96L * p->n_slots ? 128 : 256;
+    a.stages = a.cap == 64 ? kMostStages : a.cap == 128 ? 8 : 6;
     static std::atomic<uint64_t> configured{0};
-    const long tiles = (long)((O + 255) / 256 * OP) * (rows / 256 + std::min(rows, p->n_slots));  // (as many as there may be)
+    const long tiles = m_tiles * (rows / a.cap + std::min(rows, p->n_slots));  // (as many as there may be)
     return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, tiles, stream, a, DX ? "expert gradient" : "expert projection");
 }
 

@@ -112,6 +112,11 @@ __device__ __forceinline__ void cluster_sync_read() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// The two halves of a cluster's barrier, releasing nothing: barriers initialised before it (and
+// fenced) are there for the others after it.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // ---- CTA pairs (cta_group::2): one product over the shared memory and tensor memory of both
 // The address of `addr` in the pair's leader.
 __device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
