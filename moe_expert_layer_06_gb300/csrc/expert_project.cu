@@ -145,18 +145,16 @@ struct RowsTile {
 
 template <bool DX>
 __device__ __forceinline__ RowsTile rows_tile(const RowsArgs& a, const int* pre, const int* start, int i) {
-    int lo = 0, hi = a.S - 1;  // the last slot with pre[s] <= i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= i) lo = mid;
-        else hi = mid - 1;
-    }
+    // the last slot with pre[s] <= i, which the warp looks for together: among the first slots of 32
+    // stretches, then in one of them
+    const int lane = threadIdx.x & 31, per = (a.S + 31) / 32;
+    const int at = (__popc(__ballot_sync(0xffffffffu, lane * per < a.S && pre[min(lane * per, a.S)] <= i)) - 1) * per;
     RowsTile t;
-    t.s = lo;
+    t.s = per == 1 ? at : at + __popc(__ballot_sync(0xffffffffu, lane < per && at + lane < a.S && pre[min(at + lane, a.S)] <= i)) - 1;
     const int r0 = start[t.s], r1 = max(r0, start[t.s + 1]);
-    const int n = chunks_of(r1 - r0, a.cap), l = i - pre[t.s], m = l / n, c = l - m * n;
+    const int n = chunks_of(r1 - r0, a.cap), l = i - pre[t.s], m = n > 1 ? l / n : l, c = l - m * n;
     // (heights within 32 of each other: a chunk of few rows reads as much of W as a high one)
-    const int units = (r1 - r0 + 31) / 32, h = units / n, more = units - h * n;
+    const int units = (r1 - r0 + 31) / 32, h = n > 1 ? units / n : units, more = units - h * n;
     const int tiles = ((DX ? a.K : a.N) + 255) / 256;
     t.part = m >= tiles;
     t.m0 = (m - t.part * tiles) * 256;
