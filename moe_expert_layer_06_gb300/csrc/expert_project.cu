@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "operators.cuh"
 
@@ -240,8 +241,9 @@ __device__ __forceinline__ void drain_f32(const RowsArgs& a, const RowsTile& t, 
     }
 }
 
+// The pair `first` of `step`, which share the tiles.
 template <bool DX>
-__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ RowsArgs a) {
+__device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, const int step) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kOutBytes);  // (the leader's)
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             pre[s] = sum;
             sum += chunks_of(r1 - r0, a.cap) * m_tiles;
         }
-        if (!fits && blockIdx.x == 0) raise_status(a.st, kStatusBadShape);
+        if (!fits && first == 0) raise_status(a.st, kStatusBadShape);
         int incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    const int n_tiles = pre[a.S], first = blockIdx.x / 2, step = gridDim.x / 2;
+    const int n_tiles = pre[a.S];
     RowsTile t = {};
     if (first < n_tiles) t = rows_tile<DX>(a, pre, start, first);
     auto next_tile = [&](int i) {
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             __syncwarp();
         }
         mbar_wait(smem_u32(done), 0, limit);
-    } else {
+    } else if (warp < 6) {  // (a launch for dW too has more)
         const int q = warp & 3;
         bool ok = true;
         int blocks = 0;
@@ -429,6 +431,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         if (lane == 0) bulk_wait();
     }
     leave_pair(abort_flag, warp == 1, tbase);
+}
+
+template <bool DX>
+__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ RowsArgs a) {
+    rows_pair<DX>(a, blockIdx.x / 2, gridDim.x / 2);
 }
 
 // ---------------------------------------------------------------- dW
@@ -551,7 +558,7 @@ __device__ __forceinline__ void decode16(const uint4& c, float scale, uint32_t (
 }
 
 template <bool X8, bool M2>
-__global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+__device__ __forceinline__ void weights_pair(const WeightArgs& a, const int first, const int step) {
     constexpr int kStages = WeightRing<M2>::kStages, kStageBytes = WeightRing<M2>::kStageBytes, kA = WeightRing<M2>::kA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -595,13 +602,12 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
     __syncwarp();
     cluster_arrive_relaxed();
-    const int first = blockIdx.x / 2, step = gridDim.x / 2;
     pdl_wait();
     WeightTile t = weight_tile<M2>(a, first);  // (there are as many tiles as pairs at least)
     auto next_tile = [&](int i) {
         if (i + step < a.n_tiles) t = weight_tile<M2>(a, i + step);
     };
-    if (warp == 0 && blockIdx.x == 0)
+    if (warp == 0 && first == 0)
         for (int s = lane; s < a.S; s += 32) {
             int r0, r1;
             if (!slot_rows(a.offsets, s, a.R, r0, r1)) raise_status(a.st, kStatusBadShape);
@@ -928,6 +934,26 @@ __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(cons
     leave_pair(abort_flag, warp == 1, tbase);
 }
 
+template <bool X8, bool M2>
+__global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(const __grid_constant__ WeightArgs a) {
+    weights_pair<X8, M2>(a, blockIdx.x / 2, gridDim.x / 2);
+}
+
+// dx and dW in one launch, `dx_pairs` of its pairs for dx: where neither fills the device for long, one
+// runs beside the other instead of after it.
+struct BothArgs {
+    RowsArgs dx;
+    WeightArgs dw;
+    int dx_pairs;
+};
+constexpr int kBothSmem = kRowsSmem > kWeightSmem ? kRowsSmem : kWeightSmem;
+template <bool X8>
+__global__ void __launch_bounds__(weight_threads(X8, false), 1) gradients_kernel(const __grid_constant__ BothArgs a) {
+    const int pair = blockIdx.x / 2;
+    if (pair < a.dx_pairs) rows_pair<true>(a.dx, pair, a.dx_pairs);
+    else weights_pair<X8, false>(a.dw, pair - a.dx_pairs, gridDim.x / 2 - a.dx_pairs);
+}
+
 int check_project(const moe_project_t* p, int rows) {
     if (!p) return api_fail(MOE_ERR_INVALID_ARG, "project is NULL");
     if (rows < 0) return api_fail(MOE_ERR_INVALID_ARG, "rows = %d < 0", rows);
@@ -963,15 +989,16 @@ int launched(cudaError_t e, const char* what) {
 }
 
 template <typename Kern, typename A>
-int launch_pairs(Kern kern, std::atomic<uint64_t>& configured, int threads, int smem, long tiles, cudaStream_t stream, const A& a,
+int launch_pairs(Kern kern, std::atomic<uint64_t>& configured, int threads, int smem, long pairs, cudaStream_t stream, const A& a,
                  const char* what) {
     const int rc = launched(configure_once(configured,
                                            [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); }),
                             what);
-    if (rc) return rc;
-    const int pairs = (int)std::min<long>(tiles, std::max(1, num_sms() / 2));
-    return launched(launch_pdl_cluster(kern, dim3(2 * pairs), dim3(threads), smem, stream, 2, a), what);
+    return rc ? rc : launched(launch_pdl_cluster(kern, dim3(2 * (unsigned)pairs), dim3(threads), smem, stream, 2, a), what);
 }
+
+constexpr long kBothTiles = 4;  // of a pair
+long most_pairs() { return std::max(1, num_sms() / 2); }
 
 // A tensor that is written: box of 128 bytes.
 int out_map(CUtensorMap* map, void* out, uint64_t d0, uint64_t d1, uint64_t d2, int type, uint32_t box1, uint32_t box2) {
@@ -980,18 +1007,10 @@ int out_map(CUtensorMap* map, void* out, uint64_t d0, uint64_t d1, uint64_t d2, 
                                 : make_tmap_f32(map, out, d0, d1, d2, 32, box1, box2);
 }
 
-template <bool X8, bool M2>
-int launch_weights(WeightArgs& a, cudaStream_t stream) {
-    static std::atomic<uint64_t> configured{0};
-    const long tiles = (long)((a.K + 255) / 256) * (M2 ? (a.N + 511) / 512 : (a.N + 255) / 256) * a.P * a.S;
-    a.n_tiles = (int)tiles;
-    return launch_pairs(weights_kernel<X8, M2>, configured, weight_threads(X8, M2), kWeightSmem, tiles, stream, a, "expert weight gradient");
-}
-
+// y or dx; *tiles: as many as there may be
 template <bool DX>
-int rows_product(const moe_project_t* p, int rows, const void* in, const int32_t* offsets, const void* w, const void* w2, void* out,
-                 int type, const DevStatus& st, cudaStream_t stream) {
-    RowsArgs a;
+int rows_args(const moe_project_t* p, int rows, const void* in, const int32_t* offsets, const void* w, const void* w2, void* out, int type,
+              const DevStatus& st, RowsArgs& a, long* tiles) {
     const uint64_t K = p->in_features, N = p->out_features, S = p->n_slots, P = p->n_parts, R = rows;
     int rc = make_tmap_3d(&a.w[0], w, K, N, S, K * 2, K * N * 2, 64, DX ? 64 : 128, 1);
     if (rc) return rc;
@@ -1012,20 +1031,24 @@ int rows_product(const moe_project_t* p, int rows, const void* in, const int32_t
     a.st = st;
     // Where there is about a tile for each pair, what counts is how soon its chunks are there: lower ones,
     // of which more fit the ring, where slots have few rows (400 rows of 16 slots, gate and up of 600 to
-    // 328: XX us with 256 rows, YY with 64).
-    const long m_tiles = (long)((O + 255) / 256 * OP);
-    a.cap = 256;
-    if (m_tiles * std::min(rows, p->n_slots) <= num_sms() / 2) a.cap = rows <= 48L * p->n_slots ? 64 : rows <= 96L * p->n_slots ? 128 : 256;
+    // 328: 6.8 us with 256 rows, 6.5 with 64).
+    const long m_tiles = (long)((O + 255) / 256 * OP), used = std::min(rows, p->n_slots);
+    a.cap = m_tiles * used > most_pairs() ? 256 : rows <= 48 * used ? 64 : rows <= 96 * used ? 128 : 256;
     a.stages = a.cap == 64 ? kMostStages : a.cap == 128 ? 8 : 6;
+    *tiles = m_tiles * (rows / a.cap + used);
+    return MOE_OK;
+}
+
+template <bool DX>
+int launch_rows(const RowsArgs& a, long tiles, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
-    const long tiles = m_tiles * (rows / a.cap + std::min(rows, p->n_slots));  // (as many as there may be)
-    return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, tiles, stream, a, DX ? "expert gradient" : "expert projection");
+    return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, std::min(tiles, most_pairs()), stream, a,
+                        DX ? "expert gradient" : "expert projection");
 }
 
 template <bool X8>
-int weights_product(const moe_project_t* p, int rows, const void* dy, const void* x, const float* scale, const int32_t* offsets, void* dw,
-                    void* dw2, int type, const DevStatus& st, cudaStream_t stream) {
-    WeightArgs a;
+int weight_args(const moe_project_t* p, int rows, const void* dy, const void* x, const float* scale, const int32_t* offsets, void* dw,
+                void* dw2, int type, const DevStatus& st, WeightArgs& a) {
     const uint64_t K = p->in_features, N = p->out_features, S = p->n_slots, P = p->n_parts, R = rows;
     int rc;
     for (int j = 0; j < 3; ++j)
@@ -1047,14 +1070,52 @@ int weights_product(const moe_project_t* p, int rows, const void* dy, const void
     a.type = type;
     a.n_blk = (p->in_features + MOE_PAYLOAD_BLOCK - 1) / MOE_PAYLOAD_BLOCK;
     a.st = st;
+    a.n_tiles = (int)((K + 255) / 256 * ((N + 255) / 256) * P * S);
+    return MOE_OK;
+}
+
+template <bool X8, bool M2>
+int launch_weights(WeightArgs& a, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    return launch_pairs(weights_kernel<X8, M2>, configured, weight_threads(X8, M2), kWeightSmem, std::min<long>(a.n_tiles, most_pairs()),
+                        stream, a, "expert weight gradient");
+}
+
+template <bool X8>
+int launch_weights(WeightArgs& a, cudaStream_t stream) {
     // Twice 256 of N where that leaves every pair several tiles and, rows in bf16, where a slot has many
     // rows: the products of a tile hide the drain of one accumulator, not of the first of two (16 slots,
     // gate and up of 7168 to 2048: 128 rows a slot 163 us with 256 and 167 with twice that, 256 both 226,
     // 512 396 and 329; codes, which are turned half as often, 187 and 171, 266 and 244, 447 and 428.  16
     // slots of 1024 to 1024, 512 rows each: 19.1 and 21.1).
-    const long tiles = (long)((K + 255) / 256 * ((N + 511) / 512) * P * S);
-    const bool m2 = tiles >= 2L * num_sms() && (X8 || rows >= 384L * p->n_slots);
-    return m2 ? launch_weights<X8, true>(a, stream) : launch_weights<X8, false>(a, stream);
+    const long tiles = (long)((a.K + 255) / 256) * ((a.N + 511) / 512) * a.P * a.S;
+    if (tiles < 4 * most_pairs() || !(X8 || a.R >= 384L * a.S)) return launch_weights<X8, false>(a, stream);
+    a.n_tiles = (int)tiles;
+    return launch_weights<X8, true>(a, stream);
+}
+
+template <bool X8>
+int gradients(const moe_project_t* p, int rows, const void* dy, const void* x, const float* scale, const int32_t* offsets, const void* w,
+              const void* w2, void* dx, int dx_type, void* dw, void* dw2, int dw_type, const DevStatus& st, cudaStream_t stream) {
+    BothArgs a;
+    long dx_tiles = 0;
+    int rc;
+    if (dx && (rc = rows_args<true>(p, rows, dy, offsets, w, w2, dx, dx_type, st, a.dx, &dx_tiles))) return rc;
+    if (dw && (rc = weight_args<X8>(p, rows, dy, x, scale, offsets, dw, dw2, dw_type, st, a.dw))) return rc;
+    // Both in one launch up to a few tiles a pair, the pairs shared by the tiles' chunks of 64 (and ten
+    // for a tile's beginning and end).
+    if (dx && dw && dx_tiles + a.dw.n_tiles <= kBothTiles * most_pairs() && most_pairs() > 1) {
+        const double dx_cost = (double)dx_tiles * (10 + (long)a.dx.P * ((a.dx.N + 63) / 64));
+        const double dw_cost = (double)a.dw.n_tiles * (10 + (rows / p->n_slots + 63) / 64);
+        const long dx_pairs = std::lround(most_pairs() * dx_cost / (dx_cost + dw_cost));
+        a.dx_pairs = (int)std::min(dx_tiles, std::max(1L, std::min(most_pairs() - 1, dx_pairs)));
+        const long dw_pairs = std::min<long>(a.dw.n_tiles, most_pairs() - a.dx_pairs);
+        static std::atomic<uint64_t> configured{0};
+        return launch_pairs(gradients_kernel<X8>, configured, weight_threads(X8, false), kBothSmem, a.dx_pairs + dw_pairs, stream, a,
+                            "expert gradients");
+    }
+    if (dx && (rc = launch_rows<true>(a.dx, dx_tiles, stream))) return rc;
+    return dw ? launch_weights<X8>(a.dw, stream) : MOE_OK;
 }
 
 }  // namespace
@@ -1075,7 +1136,10 @@ int moe_expert_project(const moe_project_t* project, int rows, const void* x, co
     PdlScope pdl(rows);
     DevStatus st;
     if ((rc = api_device_status(&st))) return rc;
-    return rows_product<false>(project, rows, x, offsets, w, w2, out, out_type, st, reinterpret_cast<cudaStream_t>(stream));
+    RowsArgs a;
+    long tiles;
+    if ((rc = rows_args<false>(project, rows, x, offsets, w, w2, out, out_type, st, a, &tiles))) return rc;
+    return launch_rows<false>(a, tiles, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int moe_expert_project_backward(const moe_project_t* project, int rows, const void* dy, const void* x, const uint8_t* x8,
@@ -1104,10 +1168,8 @@ int moe_expert_project_backward(const moe_project_t* project, int rows, const vo
     PdlScope pdl(rows);
     DevStatus st;
     if ((rc = api_device_status(&st))) return rc;
-    if (dx && (rc = rows_product<true>(project, rows, dy, offsets, w, w2, dx, dx_type, st, s))) return rc;
-    if (!dw) return MOE_OK;
-    return x8 ? weights_product<true>(project, rows, dy, x8, x8_scale, offsets, dw, dw2, dw_type, st, s)
-              : weights_product<false>(project, rows, dy, x, nullptr, offsets, dw, dw2, dw_type, st, s);
+    return x8 ? gradients<true>(project, rows, dy, x8, x8_scale, offsets, w, w2, dx, dx_type, dw, dw2, dw_type, st, s)
+              : gradients<false>(project, rows, dy, x, nullptr, offsets, w, w2, dx, dx_type, dw, dw2, dw_type, st, s);
 }
 
 }  // extern "C"
