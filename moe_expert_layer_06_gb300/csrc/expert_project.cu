@@ -997,7 +997,7 @@ int launch_pairs(Kern kern, std::atomic<uint64_t>& configured, int threads, int 
     return rc ? rc : launched(launch_pdl_cluster(kern, dim3(2 * (unsigned)pairs), dim3(threads), smem, stream, 2, a), what);
 }
 
-constexpr long kBothTiles = 4;  // of a pair
+constexpr long kBothTiles = 16;  // of a pair
 long most_pairs() { return std::max(1, num_sms() / 2); }
 
 // A tensor that is written: box of 128 bytes.
@@ -1102,11 +1102,18 @@ int gradients(const moe_project_t* p, int rows, const void* dy, const void* x, c
     int rc;
     if (dx && (rc = rows_args<true>(p, rows, dy, offsets, w, w2, dx, dx_type, st, a.dx, &dx_tiles))) return rc;
     if (dw && (rc = weight_args<X8>(p, rows, dy, x, scale, offsets, dw, dw2, dw_type, st, a.dw))) return rc;
-    // Both in one launch up to a few tiles a pair, the pairs shared by the tiles' chunks of 64 (and ten
-    // for a tile's beginning and end).
+    // Both in one launch up to a few tiles a pair, the pairs shared by what the tiles cost, in cycles: a
+    // chunk of dx 2 for each row and 400 at least, a chunk of dW 512, or turning its codes, and a tile of
+    // dW its drain at least.  (100 rows, 328 to 600 features of 16 slots, a tile or two a pair, 12.2 us
+    // one after the other and 8.3 beside each other; 8000 rows, 2048 to 1024 of 16 slots, 12 tiles, 65 and
+    // 55; 4096 rows, 2048 to 7168 of 32 slots, a hundred, 332 and 383: there one reads memory and the
+    // other writes it, and each takes all the pairs.)
     if (dx && dw && dx_tiles + a.dw.n_tiles <= kBothTiles * most_pairs() && most_pairs() > 1) {
-        const double dx_cost = (double)dx_tiles * (10 + (long)a.dx.P * ((a.dx.N + 63) / 64));
-        const double dw_cost = (double)a.dw.n_tiles * (10 + (rows / p->n_slots + 63) / 64);
+        const long used = std::min(rows, p->n_slots), each = (rows + used - 1) / used;
+        const long height = std::max(200L, std::min<long>(a.dx.cap, each)), chunks = (each + 63) / 64;
+        const double dx_cost = (double)((a.dx.K + 255) / 256) * used * ((each + a.dx.cap - 1) / a.dx.cap) *
+                               (600.0 + 2.0 * height * a.dx.P * ((a.dx.N + 63) / 64));
+        const double dw_cost = (double)a.dw.n_tiles * (600.0 + std::max(2400L, chunks * (X8 ? 900 : 512)));
         const long dx_pairs = std::lround(most_pairs() * dx_cost / (dx_cost + dw_cost));
         a.dx_pairs = (int)std::min(dx_tiles, std::max(1L, std::min(most_pairs() - 1, dx_pairs)));
         const long dw_pairs = std::min<long>(a.dw.n_tiles, most_pairs() - a.dx_pairs);
