@@ -565,14 +565,13 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kWeightOut);  // (the leader's) copies that need no work, of both
     uint64_t* empty = full + kStages;
     uint64_t* landed = empty + kStages;  // this CTA's copies that need work
-    uint64_t* ready = landed + kStages;  // (the leader's) ... and have had it
-    uint64_t* other = ready + kStages;   // (the leader's) the same in the other CTA
-    uint64_t* tfull = other + kStages;
+    uint64_t* ready = landed + kStages;  // (the leader's) ... which have had it, in both
+    uint64_t* tfull = ready + kStages;
     uint64_t* tempty = tfull + 2;        // (the leader's)
     uint64_t* done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((5 * kStages + 5) * 8 + 8 <= kSignals, "barriers");
+    static_assert((4 * kStages + 5) * 8 + 8 <= kSignals, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
@@ -585,8 +584,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
-            mbar_init(smem_u32(&ready[s]), kWork);
-            mbar_init(smem_u32(&other[s]), 1);
+            mbar_init(smem_u32(&ready[s]), kWork + 1);  // the leader's workers and its wait for the others' copies
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&tfull[s]), 1);
@@ -623,8 +621,8 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
         raise_status(a.st, kStatusWaitTimeout);
     };
     const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed), ready_u = smem_u32(ready);
-    const uint32_t other_u = smem_u32(other), stage_u = smem_u32(smem);
-    const uint32_t lead_full = leader_addr(full_u), lead_tempty = leader_addr(smem_u32(tempty)), lead_other = leader_addr(other_u);
+    const uint32_t stage_u = smem_u32(smem);
+    const uint32_t lead_full = leader_addr(full_u), lead_tempty = leader_addr(smem_u32(tempty)), lead_ready = leader_addr(ready_u);
 
     if (warp == 0) {
         const uint64_t pol = policy_evict_normal();
@@ -635,15 +633,15 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
             const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 128;
             for (int r = 0; r < t.rows; r += 64) {
                 const int left = min(64, t.rows - r), n16 = (left + 15) / 16;
-                const bool odd = left & 15, work = X8 || odd;
+                const bool work = X8 || (left & 15);
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 if (elect_one()) {
                     const uint32_t sa = stage_u + stage * kStageBytes, sb = sa + kA;
                     const uint32_t fb = lead_full + stage * 8, lb = landed_u + stage * 8;
                     const uint32_t dy_bytes = (t.two ? 2 : 1) * n16 * 4096, x_bytes = X8 ? n16 * 2048 : n16 * 4096;
-                    if (!odd && rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * (dy_bytes + (X8 ? 0 : x_bytes)));
-                    if (work && rank == 0) mbar_arrive_expect_tx(other_u + stage * 8, kWork * 16);
-                    if (work) mbar_arrive_expect_tx(lb, X8 && !odd ? x_bytes : dy_bytes + x_bytes);
+                    if (!work && rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * (dy_bytes + x_bytes));
+                    if (work && rank == 0) mbar_arrive_expect_tx(ready_u + stage * 8, kWork * 16);
+                    if (work) mbar_arrive_expect_tx(lb, dy_bytes + x_bytes);
                     for (int bit = 2, off = 0; bit >= 0; --bit)
                         if (n16 & (1 << bit)) {
                             const int row = t.row0 + r + off * 16;
@@ -653,7 +651,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                                 if (h && !t.two) break;
                                 const uint32_t to = sa + h * kHalf + o;
                                 const int n = n0 + h * 256;
-                                if (odd) {
+                                if (work) {
                                     tma_load_3d(to, &a.dy[bit], lb, n, t.part, row, pol);
                                     tma_load_3d(to + kHalf / 2, &a.dy[bit], lb, n + 64, t.part, row, pol);
                                 } else {
@@ -663,7 +661,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                             }
                             if (X8) {
                                 tma_load_3d(sb + o, &a.x[bit], lb, k0, 0, row, pol);
-                            } else if (odd) {
+                            } else if (work) {
                                 tma_load_3d(sb + o, &a.x[bit], lb, k0, 0, row, pol);
                                 tma_load_3d(sb + o + kHalf / 2, &a.x[bit], lb, k0 + 64, 0, row, pol);
                             } else {
@@ -710,16 +708,14 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                 ok = tile_products<kStages>(
                     t.two, (t.rows + 63) / 64, stage, u,
                     [&](int c) {
-                        const int left = min(64, t.rows - c * 64);
-                        bool got = true;
-                        if (!(left & 15)) {
+                        // one wait a chunk: two or three of 180 cycles each held up the products of codes
+                        bool got;
+                        if (X8 || (min(64, t.rows - c * 64) & 15)) {
+                            got = warp_wait(ready_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit);
+                            work_phase ^= 1u << at;
+                        } else {
                             got = warp_wait(full_u + at * 8, (full_phase >> at) & 1u, abort_flag, limit);
                             full_phase ^= 1u << at;
-                        }
-                        if (X8 || (left & 15)) {
-                            got = got && warp_wait(ready_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit) &&
-                                  warp_wait(other_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit);
-                            work_phase ^= 1u << at;
                         }
                         if (++at == kStages) at = 0;
                         tc_fence_after();
@@ -836,7 +832,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                     __syncwarp();
                     if (lane == 0) {
                         if (rank == 0) mbar_arrive(ready_u + stage * 8);
-                        else signal_by_copy(lead_signals + stage * 16, signals + kStages * 16, lead_other + stage * 8);
+                        else signal_by_copy(lead_signals + stage * 16, signals + kStages * 16, lead_ready + stage * 8);
                     }
                     __syncwarp();
                 }
