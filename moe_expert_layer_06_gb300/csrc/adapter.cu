@@ -51,17 +51,6 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
     return v;
 }
 
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr, uint32_t rank) {
-    uint32_t a;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-
 // The tile's adapter ids (-1: none) and the list of distinct ones, ascending; *count
 // their number.  `n_threads` threads call it (tid 0..), synchronised by barrier `bar`;
 // `bits` holds kMaxAdapters bits.  False on all of them, and nothing written, if one is not `ready`.

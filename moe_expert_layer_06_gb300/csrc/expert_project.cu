@@ -116,6 +116,8 @@ __device__ __forceinline__ void leave_pair(const volatile int* abort_flag, bool 
 // One pair's tile: 256 outputs (128 rows of W, or for dx columns, in each CTA) times the rows of
 // a slot in chunks of equal height, a multiple of 32 up to `cap` (half of them in each CTA).
 // dx's W is read MN-major, as its contraction runs over W's rows.
+// Few tiles with a long contraction: the pairs of a cluster take a share of it each, and their sums meet
+// in distributed shared memory, added in the pairs' order.
 struct RowsArgs {
     CUtensorMap w[2];  // box {64, 128} of [S][N][K], dx: {64, 64}
     CUtensorMap in[4]; // box {64, 1, 16 << j} of x [R][1][K], dx: dy [R][P][N]
@@ -124,6 +126,7 @@ struct RowsArgs {
     void* out_ptr;
     int R, K, N, P, S, type;
     int cap, stages;   // rows of a chunk at most (64, 128, 256); stages of the ring that then fit
+    int splits;        // pairs of a cluster, which share a tile's contraction; above 1, one tile each
     DevStatus st;
 };
 constexpr int kMostStages = 9;
@@ -243,7 +246,7 @@ __device__ __forceinline__ void drain_f32(const RowsArgs& a, const RowsTile& t, 
 
 // The pair `first` of `step`, which share the tiles.
 template <bool DX>
-__device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, const int step) {
+__device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, const int pairs) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing + kOutBytes);  // (the leader's)
@@ -259,10 +262,13 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
-    const int rank = (int)cluster_rank();
+    const int place = (int)cluster_rank(), rank = place & 1, share = place >> 1;  // (the share of the contraction: 0 without splits)
+    const uint32_t lead = place & ~1, both = 3u << lead;
+    const int first = pair / a.splits;
     const int O = DX ? a.K : a.N, out_parts = DX ? 1 : a.P;
     const int m_tiles = (O + 255) / 256 * out_parts;
     const int kc1 = ((DX ? a.N : a.K) + 63) / 64, kc = kc1 * (DX ? a.P : 1);  // chunks of a part, of a tile
+    const int c0 = a.splits > 1 ? kc * share / a.splits : 0, c1 = a.splits > 1 ? kc * (share + 1) / a.splits : kc;  // this pair's
     const int kStages = a.stages, kStageBytes = stage_bytes(a.cap);
 
     if (warp == 0 && lane == 0) {
@@ -311,7 +317,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    const int n_tiles = pre[a.S];
+    const int n_tiles = pre[a.S], step = a.splits > 1 ? max(1, n_tiles) : pairs;
     RowsTile t = {};
     if (first < n_tiles) t = rows_tile<DX>(a, pre, start, first);
     auto next_tile = [&](int i) {
@@ -324,7 +330,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
         raise_status(a.st, kStatusWaitTimeout);
     };
     const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), stage_u = smem_u32(smem);
-    const uint32_t lead_full = leader_addr(full_u), lead_tempty = leader_addr(smem_u32(tempty));
+    const uint32_t lead_full = leader_addr(full_u, lead), lead_tempty = leader_addr(smem_u32(tempty), lead);
 
     if (warp == 0) {
         const uint64_t pol_once = policy_evict_first(), pol = policy_evict_normal();
@@ -334,7 +340,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
         for (int i = first; i < n_tiles && ok; next_tile(i), i += step) {
             const int m0 = t.m0 + rank * 128, n16 = t.bn / 32, row0 = t.row0 + rank * n16 * 16;
             const uint64_t pol_w = t.shared_w ? pol : pol_once;
-            for (int c = 0; c < kc; ++c) {
+            for (int c = c0; c < c1; ++c) {
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 const int part = DX ? (c >= kc1) : t.part, at = (DX && part ? c - kc1 : c) * 64;
                 if (elect_one()) {
@@ -384,17 +390,17 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
                 const uint32_t d = tbase + (n & 1) * 256;
                 if (!(ok = warp_wait(smem_u32(&tempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, limit))) break;
                 tc_fence_after();
-                for (int c = 0; c < kc; ++c) {
+                for (int c = c0; c < c1; ++c) {
                     if (!(ok = warp_wait(full_u + stage * 8, phase, abort_flag, limit))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t ad = ad0 + stage * (kStageBytes >> 4), bd = bd0 + stage * (kStageBytes >> 4);
                         const int left = c == kc1 - 1 || c == kc - 1 ? last : 64;
-                        umma_bf16_pair(d, ad, bd, idesc, c > 0);
+                        umma_bf16_pair(d, ad, bd, idesc, c > c0);
                         if (left > 16) umma_bf16_pair(d, ad + kAStep, bd + 2, idesc, 1);
                         if (left > 32) umma_bf16_pair(d, ad + 2 * kAStep, bd + 4, idesc, 1);
                         if (left > 48) umma_bf16_pair(d, ad + 3 * kAStep, bd + 6, idesc, 1);
-                        umma_commit_pair(empty_u + stage * 8);
+                        umma_commit_pair(empty_u + stage * 8, both);
                     }
                     __syncwarp();
                     if (++stage == kStages) {
@@ -402,12 +408,12 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
                         phase ^= 1;
                     }
                 }
-                if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]));
+                if (elect_one()) umma_commit_pair(smem_u32(&tfull[n & 1]), both);
                 __syncwarp();
             }
             if (!ok && lane == 0) give_up();
             // all products are complete before the tensor memory is freed
-            if (elect_one()) umma_commit_pair(smem_u32(done));
+            if (elect_one()) umma_commit_pair(smem_u32(done), both);
             __syncwarp();
         }
         mbar_wait(smem_u32(done), 0, limit);
@@ -420,7 +426,16 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
             if (!(ok = named_and(2 + (q >> 1), 64, ok))) break;  // (the two warps that share drain_bf16's barrier)
             tc_fence_after();
             const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16), out = stage_u + kRing;
-            if (a.type == MOE_OUT_BF16) drain_bf16(a, t, O, out_parts, tmem, out, t.m0 + rank * 128, q, lane, blocks);
+            if (a.splits > 1) {
+                // [row][128 outputs] where the ring was: all its products are done
+                for (int r = 0; r < t.rows; r += 16) {
+                    float v[16];
+                    tmem_ld16(tmem + r, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) st_shared(stage_u + ((r + k) * 128 + q * 32 + lane) * 4, to_u(v[k]));
+                }
+            } else if (a.type == MOE_OUT_BF16) drain_bf16(a, t, O, out_parts, tmem, out, t.m0 + rank * 128, q, lane, blocks);
             else drain_f32(a, t, O, out_parts, tmem, out, t.m0 + rank * 128, q, lane, blocks);
             tc_fence_before();
             __syncwarp();
@@ -429,6 +444,33 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int first, co
         }
         if (!ok && lane == 0) give_up();
         if (lane == 0) bulk_wait();
+    }
+    if (a.splits > 1) {
+        __syncwarp();
+        tc_fence_before();
+        cluster_sync();
+        // every pair's CTA of this rank holds the same 128 outputs: the rows in turn, 4 outputs a lane
+        const int f = t.m0 + rank * 128 + lane * 4;
+        if (first < n_tiles && f < O && !*abort_flag)
+            for (int r = share + a.splits * warp; r < t.rows; r += a.splits * (blockDim.x / 32)) {
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int s = 0; s < a.splits; ++s) {
+                    const float4 v = ld_peer4(stage_u + (r * 128 + lane * 4) * 4, 2 * s + rank);
+                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                }
+                const size_t at = ((size_t)(t.row0 + r) * out_parts + t.part) * O + f;
+                if (a.type == MOE_OUT_BF16) {
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out_ptr) + at) =
+                        make_uint2(pack_bf(to_u(sum.x), to_u(sum.y)), pack_bf(to_u(sum.z), to_u(sum.w)));
+                } else {
+                    float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out_ptr) + at);
+                    if (a.type == MOE_OUT_F32_ADD) {
+                        const float4 old = *out;
+                        sum.x += old.x, sum.y += old.y, sum.z += old.z, sum.w += old.w;
+                    }
+                    *out = sum;
+                }
+            }
     }
     leave_pair(abort_flag, warp == 1, tbase);
 }
@@ -575,7 +617,8 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
-    const int rank = (int)cluster_rank();
+    const int place = (int)cluster_rank(), rank = place & 1;
+    const uint32_t lead = place & ~1, both = 3u << lead;
     constexpr int kGroups = work_groups(X8, M2);
     static_assert(kStages % kGroups == 0, "a stage is one group's");
 
@@ -601,7 +644,8 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
     __syncwarp();
     cluster_arrive_relaxed();
     pdl_wait();
-    WeightTile t = weight_tile<M2>(a, first);  // (there are as many tiles as pairs at least)
+    WeightTile t = {};
+    if (first < a.n_tiles) t = weight_tile<M2>(a, first);
     auto next_tile = [&](int i) {
         if (i + step < a.n_tiles) t = weight_tile<M2>(a, i + step);
     };
@@ -622,7 +666,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
     };
     const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed), ready_u = smem_u32(ready);
     const uint32_t stage_u = smem_u32(smem);
-    const uint32_t lead_full = leader_addr(full_u), lead_tempty = leader_addr(smem_u32(tempty)), lead_ready = leader_addr(ready_u);
+    const uint32_t lead_full = leader_addr(full_u, lead), lead_tempty = leader_addr(smem_u32(tempty), lead), lead_ready = leader_addr(ready_u, lead);
 
     if (warp == 0) {
         const uint64_t pol = policy_evict_normal();
@@ -744,11 +788,11 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                         __syncwarp();
                     },
                     [&](int st) {
-                        if (elect_one()) umma_commit_pair(empty_u + st * 8);
+                        if (elect_one()) umma_commit_pair(empty_u + st * 8, both);
                         __syncwarp();
                     },
                     [&](int v) {
-                        if (elect_one()) umma_commit_pair(smem_u32(&tfull[v & 1]));
+                        if (elect_one()) umma_commit_pair(smem_u32(&tfull[v & 1]), both);
                         __syncwarp();
                     });
             }
@@ -756,7 +800,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
             for (int v = max(0, u - 2); v < u && ok; ++v) ok = warp_wait(smem_u32(&tempty[v & 1]), (v >> 1) & 1, abort_flag, limit);
             if (!ok && lane == 0) give_up();
             // all products are complete before the tensor memory is freed
-            if (elect_one()) umma_commit_pair(smem_u32(done));
+            if (elect_one()) umma_commit_pair(smem_u32(done), both);
             __syncwarp();
         }
         mbar_wait(smem_u32(done), 0, limit);
@@ -765,7 +809,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
         // The leader hears of the other CTA's rows by copies.  (An arrival there holds its thread for
         // 1400 to 2000 cycles, until its release is seen by the cluster: one for each chunk, and codes
         // took 3087 us of 4096 tokens, 8 experts each, gate and up, where rows in bf16 took 1170.)
-        const uint32_t signals = smem_u32(full) + kSignals, lead_signals = leader_addr(signals);
+        const uint32_t signals = smem_u32(full) + kSignals, lead_signals = leader_addr(signals, lead);
         bool ok = true;
         int stage = 0, turn = 0;  // of the chunks that need work
         uint32_t land_phase = 0;
@@ -985,12 +1029,12 @@ int launched(cudaError_t e, const char* what) {
 }
 
 template <typename Kern, typename A>
-int launch_pairs(Kern kern, std::atomic<uint64_t>& configured, int threads, int smem, long pairs, cudaStream_t stream, const A& a,
-                 const char* what) {
+int launch_pairs(Kern kern, std::atomic<uint64_t>& configured, int threads, int smem, long pairs, int splits, cudaStream_t stream,
+                 const A& a, const char* what) {
     const int rc = launched(configure_once(configured,
                                            [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); }),
                             what);
-    return rc ? rc : launched(launch_pdl_cluster(kern, dim3(2 * (unsigned)pairs), dim3(threads), smem, stream, 2, a), what);
+    return rc ? rc : launched(launch_pdl_cluster(kern, dim3(2 * (unsigned)pairs), dim3(threads), smem, stream, 2 * splits, a), what);
 }
 
 constexpr long kBothTiles = 16;  // of a pair
@@ -1032,14 +1076,25 @@ int rows_args(const moe_project_t* p, int rows, const void* in, const int32_t* o
     a.cap = m_tiles * used > most_pairs() ? 256 : rows <= 48 * used ? 64 : rows <= 96 * used ? 128 : 256;
     a.stages = a.cap == 64 ? kMostStages : a.cap == 128 ? 8 : 6;
     *tiles = m_tiles * (rows / a.cap + used);
+    a.splits = 1;
     return MOE_OK;
 }
 
+// Pairs that share a tile's contraction: up to four (clusters of eight), with eight chunks each at least,
+// where they are resident: `share` percent of the device, and clusters do not cross its groups of
+// processors (36 of four and 15 of eight of 152).
+int splits_of(int chunks, long tiles, int share) {
+    const long sms = (long)num_sms() * share / 100;
+    if (chunks >= 32 && tiles <= sms * 15 / 152) return 4;
+    return chunks >= 16 && tiles <= sms * 36 / 152 ? 2 : 1;
+}
+
 template <bool DX>
-int launch_rows(const RowsArgs& a, long tiles, cudaStream_t stream) {
+int launch_rows(RowsArgs& a, long tiles, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
-    return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, std::min(tiles, most_pairs()), stream, a,
-                        DX ? "expert gradient" : "expert projection");
+    a.splits = splits_of(DX ? (a.N + 63) / 64 * a.P : (a.K + 63) / 64, tiles, 100);
+    return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, a.splits > 1 ? tiles * a.splits : std::min(tiles, most_pairs()),
+                        a.splits, stream, a, DX ? "expert gradient" : "expert projection");
 }
 
 template <bool X8>
@@ -1074,7 +1129,7 @@ template <bool X8, bool M2>
 int launch_weights(WeightArgs& a, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
     return launch_pairs(weights_kernel<X8, M2>, configured, weight_threads(X8, M2), kWeightSmem, std::min<long>(a.n_tiles, most_pairs()),
-                        stream, a, "expert weight gradient");
+                        1, stream, a, "expert weight gradient");
 }
 
 template <bool X8>
@@ -1107,14 +1162,16 @@ int gradients(const moe_project_t* p, int rows, const void* dy, const void* x, c
     if (dx && dw && dx_tiles + a.dw.n_tiles <= kBothTiles * most_pairs() && most_pairs() > 1) {
         const long used = std::min(rows, p->n_slots), each = (rows + used - 1) / used;
         const long height = std::max(200L, std::min<long>(a.dx.cap, each)), chunks = (each + 63) / 64;
-        const double dx_cost = (double)((a.dx.K + 255) / 256) * used * ((each + a.dx.cap - 1) / a.dx.cap) *
-                               (600.0 + 2.0 * height * a.dx.P * ((a.dx.N + 63) / 64));
+        const int dx_chunks = a.dx.P * ((a.dx.N + 63) / 64);
+        const int splits = a.dx.splits = splits_of(dx_chunks, dx_tiles, 50);
+        const double dx_cost = (double)((a.dx.K + 255) / 256) * used * ((each + a.dx.cap - 1) / a.dx.cap) * (600.0 + 2.0 * height * dx_chunks);
         const double dw_cost = (double)a.dw.n_tiles * (600.0 + std::max(2400L, chunks * (X8 ? 900 : 512)));
         const long dx_pairs = std::lround(most_pairs() * dx_cost / (dx_cost + dw_cost));
-        a.dx_pairs = (int)std::min(dx_tiles, std::max(1L, std::min(most_pairs() - 1, dx_pairs)));
-        const long dw_pairs = std::min<long>(a.dw.n_tiles, most_pairs() - a.dx_pairs);
+        a.dx_pairs = (int)(splits > 1 ? dx_tiles * splits : std::min(dx_tiles, std::max(1L, std::min(most_pairs() - 1, dx_pairs))));
+        // (clusters are of one kind: a multiple of the splits for dW too)
+        const long dw_pairs = std::max<long>(1, std::min<long>(a.dw.n_tiles, most_pairs() - a.dx_pairs) / splits) * splits;
         static std::atomic<uint64_t> configured{0};
-        return launch_pairs(gradients_kernel<X8>, configured, weight_threads(X8, false), kBothSmem, a.dx_pairs + dw_pairs, stream, a,
+        return launch_pairs(gradients_kernel<X8>, configured, weight_threads(X8, false), kBothSmem, a.dx_pairs + dw_pairs, splits, stream, a,
                             "expert gradients");
     }
     if (dx && (rc = launch_rows<true>(a.dx, dx_tiles, stream))) return rc;

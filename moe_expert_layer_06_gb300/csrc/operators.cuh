@@ -117,11 +117,23 @@ __device__ __forceinline__ void cluster_sync_read() {
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// ---- CTA pairs (cta_group::2): one product over the shared memory and tensor memory of both
-// The address of `addr` in the pair's leader.
-__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+// Four fp32 at the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr, uint32_t rank) {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(addr));
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// ---- CTA pairs (cta_group::2): one product over the shared memory and tensor memory of both
+// The address of `addr` in the pair's leader, CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr, uint32_t rank = 0) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
     return a;
 }
 
@@ -171,11 +183,12 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, 
         : "memory");
 }
 
-// Arrive on the mbarrier at this offset of both CTAs when this thread's products are done.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+// Arrive on the mbarrier at this offset of both CTAs (of the cluster, by their bits) when this thread's
+// products are done.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint32_t ctas = 3) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)ctas)
         : "memory");
 }
 

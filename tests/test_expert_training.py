@@ -133,6 +133,34 @@ def test_many_rows_of_a_slot_and_many_slots(R, K, N, S, P):
         close(got[1][p], dw[0][p], dw[1][p], name=f"dw{p}")
 
 
+# few tiles of a long contraction, which pairs of CTAs share (16 chunks of 64 and more for two, 32 for four)
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [1, 5, 70, 300])
+@pytest.mark.parametrize("K,N,S,P", [(2056, 136, 1, 1), (4104, 264, 2, 2), (1032, 8, 3, 1), (136, 2056, 2, 1), (264, 1544, 1, 2), (8, 4104, 3, 2)])
+def test_long_contractions_of_few_tiles(R, K, N, S, P):
+    c = Case(R, K, N, S, P, seed=14)
+    y, dx, dw = c.reference()
+    for dtype in (BF, F32):
+        close(c.forward(dtype), *y, name="y")
+        close(c.backward(dw=False, dx_type=dtype)[0], *dx, name="dx")
+        got = c.backward(dx_type=dtype)
+        close(got[0], *dx, name="dx beside dw")
+        for p in range(P):
+            close(got[1][p], dw[0][p], dw[1][p], name=f"dw{p}")
+    out = torch.full((R, P * N), 2.0, device="cuda")
+    c.forward(F32, add=True, out=out)
+    there = ~torch.isnan(y[0])
+    close(out, torch.where(there, y[0] + 2.0, 2.0), torch.where(there, y[1] + STEP * (y[0].abs() + 2.0), 0.0), name="y added")
+    first = c.forward()
+    assert torch.equal(first.nan_to_num(9.0), c.forward().nan_to_num(9.0))
+    assert m.moe_check_status() == 0
+    # rows of the next slot and of none beside it
+    if R >= 70:
+        c.x[-1, 3], c.dy[-1, 5] = float("inf"), float("nan")
+        close(c.forward()[:-1], y[0][:-1], y[1][:-1], name="y beside an infinity")
+        close(c.backward(dw=False)[0][:-1], dx[0][:-1], dx[1][:-1], name="dx beside a NaN")
+
+
 # counts that end at, before and after every unit in which a kernel may take rows
 @pytest.mark.gpu
 @pytest.mark.parametrize("P", [1, 2])
