@@ -556,7 +556,8 @@ MOE_API int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_
  * multiple of 16): exactly one of the two.  Products of bf16, sums in fp32, rounded once.
  * out, dx and dw are written as their type says: MOE_OUT_BF16; MOE_OUT_F32; MOE_OUT_F32_ADD adds to
  * the fp32 values that they hold (gradients of several batches, or of several paths to one input).
- * Rows of no slot are neither read nor written; a slot without rows gets dw = 0.  An infinity or
+ * Outputs overlap no input.  Rows of no slot are neither read nor written; a slot without rows gets
+ * dw = 0.  An infinity or
  * NaN in a row shows in that row's results and its slot's dw only.  Sums run in an order that the
  * sizes and counts fix: results repeat bit for bit on one GPU model.  rows = 0 writes dw alone.
  * Limits: K and N multiples of 8 and at most 2^24, n_slots <= 1024. */

@@ -121,11 +121,10 @@ struct Place {
     int block;
 };
 constexpr int kMostUnits = 64;  // of a CTA
-__device__ __forceinline__ Place place_of(size_t first, int u, Blocks b) {
-    const size_t row0 = first >> 32 ? first / b.n : (uint32_t)first / (uint32_t)b.n;
-    const uint32_t at = (uint32_t)(first - row0 * b.n) + u;
+__device__ __forceinline__ Place place_of(uint32_t first, int u, Blocks b) {
+    const uint32_t row0 = first / (uint32_t)b.n, at = first - row0 * b.n + u;
     const uint32_t q = b.reciprocal ? (b.n == 1 ? at : __umulhi(at, b.reciprocal)) : at >= (uint32_t)b.n;
-    return {row0 + q, (int)(at - q * b.n)};
+    return {(size_t)row0 + q, (int)(at - q * b.n)};
 }
 
 // EVEN: rows are whole blocks, which then follow one another whatever the row.
@@ -133,13 +132,14 @@ template <int U, bool EVEN>  // U: blocks of a group of lanes
 __global__ void __launch_bounds__(kThreads) keep_kernel(const uint16_t* __restrict__ x, size_t rows, int cols, Blocks blocks,
                                                         uint8_t* __restrict__ codes, float* __restrict__ scale) {
     pdl_begin();
-    const size_t first = (size_t)blockIdx.x * (kGroups * U), total = rows * blocks.n;
+    const uint32_t first = blockIdx.x * (kGroups * U);
+    const size_t total = rows * blocks.n;
     const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     uint4 v[U];
     size_t at[U];  // of the lane's columns; ~0: none
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const size_t b = first + i * kGroups + group;
+        const size_t b = (size_t)first + i * kGroups + group;
         if (EVEN) {
             at[i] = b < total ? b * kBlock + lane * 8 : ~size_t(0);
         } else {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const uint16_t* __restri
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         if (at[i] != ~size_t(0)) *reinterpret_cast<uint2*>(codes + at[i]) = encode8(v[i], e[i]);
-        if (lane == 0 && at[i] != ~size_t(0)) scale[first + i * kGroups + group] = pow2(e[i]);
+        if (lane == 0 && at[i] != ~size_t(0)) scale[(size_t)first + i * kGroups + group] = pow2(e[i]);
     }
 }
 
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const uint16_t* __restri
 struct GatePlace {
     size_t gate, h, scale;
 };
-__device__ __forceinline__ GatePlace gate_place(size_t first, int u, int lane, size_t rows, int inter, Blocks blocks) {
+__device__ __forceinline__ GatePlace gate_place(uint32_t first, int u, int lane, size_t rows, int inter, Blocks blocks) {
     const Place p = place_of(first, u, blocks);
     const int c = p.block * kBlock + lane * 8;
     if (p.row >= rows || c >= inter) return {~size_t(0), 0, 0};
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_keep_kernel(const uint16_t* _
                                                                uint8_t* __restrict__ codes, float* __restrict__ scale) {
     pdl_begin();
     const int lane = threadIdx.x % kLanes;
-    const GatePlace p = gate_place((size_t)blockIdx.x * kGroups, threadIdx.x / kLanes, lane, rows, inter, blocks);
+    const GatePlace p = gate_place(blockIdx.x * kGroups, threadIdx.x / kLanes, lane, rows, inter, blocks);
     const bool live = p.gate != ~size_t(0);
     uint4 g = make_uint4(0, 0, 0, 0), u = g;
     if (live) {
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t
                                                                    Blocks blocks, uint16_t* __restrict__ d_gate_up,
                                                                    uint16_t* __restrict__ h) {
     pdl_begin();
-    const GatePlace p = gate_place((size_t)blockIdx.x * kGroups, threadIdx.x / kLanes, threadIdx.x % kLanes, rows, inter, blocks);
+    const GatePlace p = gate_place(blockIdx.x * kGroups, threadIdx.x / kLanes, threadIdx.x % kLanes, rows, inter, blocks);
     if (p.gate == ~size_t(0)) return;
     const uint2 cg = __ldcs(reinterpret_cast<const uint2*>(codes + p.gate));
     const uint2 cu = __ldcs(reinterpret_cast<const uint2*>(codes + p.gate + inter));
@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t
 int check_rows(int rows, int cols, const char* name) {
     if (rows < 0 || cols <= 0 || cols % 8) return api_fail(MOE_ERR_INVALID_ARG, "rows >= 0 and %s > 0, a multiple of 8, required", name);
     if (cols > 1 << 24) return api_fail(MOE_ERR_UNSUPPORTED, "%s %d > %d", name, cols, 1 << 24);
-    if ((long long)rows * ((cols + kBlock - 1) / kBlock) / kGroups >= INT32_MAX)
-        return api_fail(MOE_ERR_UNSUPPORTED, "too many rows");
+    // (block numbers are of 32 bits: more of them than that are rows of 500 GB at least)
+    if ((long long)rows * ((cols + kBlock - 1) / kBlock) >= UINT32_MAX - kMostUnits) return api_fail(MOE_ERR_UNSUPPORTED, "too many rows");
     return MOE_OK;
 }
 

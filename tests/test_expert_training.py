@@ -121,7 +121,8 @@ def test_products_match_the_definition(R, K, N, S, P):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("R,K,N,S,P", [(1500, 264, 520, 2, 2), (2100, 136, 72, 1, 1), (1300, 2056, 1032, 3, 1), (900, 72, 2056, 300, 1)])
+@pytest.mark.parametrize("R,K,N,S,P", [(1500, 264, 520, 2, 2), (2100, 136, 72, 1, 1), (1300, 2056, 1032, 3, 1), (900, 72, 2056, 300, 1), (1100, 72, 136, 1024, 2),
+                                       (60, 8, 8, 1024, 1)])
 def test_many_rows_of_a_slot_and_many_slots(R, K, N, S, P):
     c = Case(R, K, N, S, P, seed=3)
     y, dx, dw = c.reference()
