@@ -579,6 +579,124 @@ def test_captured_in_a_graph_and_on_another_stream():
     assert m.moe_check_status() == 0
 
 
+@pytest.mark.gpu
+def test_several_threads_and_streams_at_once():
+    """Four host threads on streams of their own, different problems, no buffer shared: the results are those of calls alone."""
+    import threading
+
+    cases = [Case(300, 264, 136, 4, 2, seed=20), Case(60, 2056, 264, 2, 1, seed=21), Case(900, 136, 520, 40, 1, seed=22),
+             Case(5, 72, 4104, 3, 2, seed=23)]
+    want = [(c.forward().nan_to_num(9.0), *[t.nan_to_num(9.0) for t in (lambda g: [g[0], *g[1]])(c.backward())]) for c in cases]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(cases), []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(6):
+                    y, (dx, dw) = cases[i].forward(), cases[i].backward()
+                torch.cuda.current_stream().synchronize()
+                got[i] = [t.nan_to_num(9.0) for t in (y, dx, *dw)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # reported below, in the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert m.moe_check_status() == 0
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def rows_close(got, want, tol):
+    """The same as close() on the device."""
+    tol = tol + HALF * (want.abs() + tol) + 1e-30
+    assert bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+def test_outputs_of_more_than_2_31_elements():
+    """y, dx and dw past 32-bit offsets: the first, a middle and the last rows and slots."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)  # noqa: E731
+    S, K, N, P = 5, 72, 2048, 2
+    R = 2 ** 31 // (P * N) + 1003
+    off = torch.tensor([0, 17, 17, R // 2 + 5, R - 9, R - 2], dtype=torch.int32, device="cuda")
+    x, w = new(R, K), [new(S, N, K) for _ in range(P)]
+    y = torch.empty(R, P * N, dtype=BF, device="cuda")
+    m.moe_expert_project(m.Project(K, N, S, P), R, x, off, *w, y)
+    assert m.moe_check_status() == 0
+    for s, rows in ((0, slice(0, 17)), (2, slice(R // 2 - 60, R // 2 + 5)), (4, slice(R - 9, R - 2))):
+        for p in range(P):
+            want = x[rows].double() @ w[p][s].double().t()
+            rows_close(y[rows, p * N:(p + 1) * N], want, K * STEP * (x[rows].double().abs() @ w[p][s].double().abs().t()))
+    # dx, as wide as y was: one part, its contraction short
+    dx, dy = y, x[:, :64].contiguous()
+    w = new(S, 64, P * N)
+    m.moe_expert_project_backward(m.Project(P * N, 64, S), R, dy, None, None, None, off, w, None, dx, None)
+    assert m.moe_check_status() == 0
+    for s, rows in ((0, slice(0, 17)), (3, slice(R - 80, R - 9)), (4, slice(R - 9, R - 2))):
+        rows_close(dx[rows], dy[rows].double() @ w[s].double(), 64 * STEP * (dy[rows].double().abs() @ w[s].double().abs()))
+    del y, dx, x, dy, w
+    S, K, N, R = 1024, 1032, 2064, 3000
+    off = torch.linspace(0, R, S + 1, device="cuda").round().to(torch.int32)
+    x, dy, dw = new(R, K), new(R, N), torch.empty(S, N, K, dtype=BF, device="cuda")
+    m.moe_expert_project_backward(m.Project(K, N, S), R, dy, x, None, None, off, None, None, None, dw)
+    assert m.moe_check_status() == 0
+    for s in (0, 511, 1007, 1008, 1023):
+        rows = slice(int(off[s]), int(off[s + 1]))
+        a, b = dy[rows].double(), x[rows].double()
+        rows_close(dw[s], a.t() @ b, len(a) * STEP * (a.abs().t() @ b.abs()))
+
+
+@pytest.mark.gpu
+def test_kept_rows_and_combine_of_more_than_2_31_elements():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    H, k = 4096, 2
+    n = 2 ** 31 // H + 250
+    x = torch.randn(n, H, generator=g, device="cuda", dtype=BF)
+    codes, scale = torch.empty(n, H, dtype=torch.uint8, device="cuda"), torch.empty(n, H // 128, device="cuda")
+    m.moe_checkpoint_rows(n, H, x, codes, scale)
+    for rows in (slice(0, 3), slice(n // 2, n // 2 + 3), slice(n - 3, n)):
+        c, s = keep(x[rows].cpu())
+        assert torch.equal(scale[rows].cpu().double(), s) and torch.equal(codes[rows].cpu().view(torch.float8_e4m3fn).double(), c)
+    # the same memory as gate and up of 2048, and as what two experts gave each token
+    I = H // 2
+    h, dh = torch.empty(n, I, dtype=BF, device="cuda"), torch.randn(n, I, generator=g, device="cuda", dtype=BF)
+    m.moe_swiglu_checkpoint(n, I, x, h, codes, scale)
+    out, again = torch.empty_like(x), torch.empty_like(h)
+    m.moe_swiglu_backward(n, I, codes, scale, dh, out, again)
+    for rows in (slice(0, 3), slice(n - 3, n)):
+        gate, up = (kept(v)[2].double() for v in (x[rows, :I].cpu(), x[rows, I:].cpu()))
+        s, act = swiglu_values(gate, up)
+        d, bound = dh[rows].cpu().double(), 2.0 ** -15
+        assert bool(((again[rows].cpu().double() - act).abs() <= (HALF + bound) * act.abs() + 1e-30).all())
+        want = d * gate * s
+        assert bool(((out[rows, I:].cpu().double() - want).abs() <= (HALF + bound) * want.abs() + 1e-30).all())
+    T = n // k
+    shape = m.Shape(H, 8, 8, k, 0, 0, 8, 1)
+    dout, w = torch.randn(T, H, generator=g, device="cuda", dtype=BF), torch.rand(T, k, generator=g, device="cuda")
+    perm, dw = torch.randperm(T * k, generator=g, device="cuda").int(), torch.empty(T, k, device="cuda")
+    x = x[:T * k]
+    out = out[:T * k]
+    m.moe_combine_backward(shape, T, dout, x, perm, w, out, dw)
+    assert m.moe_check_status() == 0
+    for t in (0, T // 2, T - 1):
+        for j in range(k):
+            row = int(perm[t * k + j])
+            want = w[t, j].double() * dout[t].double()
+            assert bool(((out[row].double() - want).abs() <= (HALF + 2.0 ** -23) * want.abs() + 1e-40).all())
+            terms = dout[t].double() * x[row].double()
+            assert abs(float(dw[t, j]) - float(terms.sum())) <= H * 2.0 ** -24 * float(terms.abs().sum())
+    row = int((perm == T * k - 1).nonzero()[0])  # the very last row of y
+    want = w.view(-1)[row].double() * dout[row // k].double()
+    assert bool(((out[-1].double() - want).abs() <= (HALF + 2.0 ** -23) * want.abs() + 1e-40).all())
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 def project(p, rows=4, x=FAKE, off=FAKE, w=FAKE, w2=None, out=FAKE, kind=0):
     return m.lib().moe_expert_project(ctypes.byref(p) if p else None, rows, x, off, w, w2, out, kind, None)
