@@ -95,6 +95,20 @@ __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Four outputs of a sum that pairs shared.
+__device__ __forceinline__ void put4(void* out, int type, size_t at, float4 v) {
+    if (type == MOE_OUT_BF16) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf(to_u(v.x), to_u(v.y)), pack_bf(to_u(v.z), to_u(v.w)));
+        return;
+    }
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    if (type == MOE_OUT_F32_ADD) {
+        const float4 old = *p;
+        v.x += old.x, v.y += old.y, v.z += old.z, v.w += old.w;
+    }
+    *p = v;
+}
+
 // How the pair's kernels end.  On the way out nobody signals the other CTA any more (who waits for
 // signals has waited for all of them), so the barrier need not see them through; after a wait that
 // expired it does.
@@ -262,7 +276,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
-    const int place = (int)cluster_rank(), rank = place & 1, share = place >> 1;  // (the share of the contraction: 0 without splits)
+    const int place = (int)cluster_rank(), rank = place & 1, share = (place >> 1) % a.splits;  // of the contraction
     const uint32_t lead = place & ~1, both = 3u << lead;
     const int first = pair / a.splits;
     const int O = DX ? a.K : a.N, out_parts = DX ? 1 : a.P;
@@ -340,17 +354,21 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
         for (int i = first; i < n_tiles && ok; next_tile(i), i += step) {
             const int m0 = t.m0 + rank * 128, n16 = t.bn / 32, row0 = t.row0 + rank * n16 * 16;
             const uint64_t pol_w = t.shared_w ? pol : pol_once;
+            // y: a box of W wholly past the last output, which reaches only what is not stored, is left out, as
+            // boxes of nothing are slow (23840 rows, 448 features to 128, 24 us with them and 13 without; for dx
+            // and dW, with more and smaller boxes, the conditions cost as much as they gave)
+            const bool w_there = DX || m0 < O, both_there = DX || t.m0 + 128 < O;
             for (int c = c0; c < c1; ++c) {
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 const int part = DX ? (c >= kc1) : t.part, at = (DX && part ? c - kc1 : c) * 64;
                 if (elect_one()) {
                     const uint32_t sa = stage_u + stage * kStageBytes, fb = lead_full + stage * 8;
                     // the leader expects the bytes of both
-                    if (rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * kHalf + t.bn * 128);
+                    if (rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, (both_there ? 2 * kHalf : kHalf) + t.bn * 128);
                     if (DX) {
                         tma_load_3d_pair(sa, &a.w[part], fb, m0, at, t.s, pol_w);
                         tma_load_3d_pair(sa + kHalf / 2, &a.w[part], fb, m0 + 64, at, t.s, pol_w);
-                    } else {
+                    } else if (w_there) {
                         tma_load_3d_pair(sa, &a.w[part], fb, at, m0, t.s, pol_w);
                     }
                     for (int bit = 3, off = 0; bit >= 0; --bit)
@@ -451,25 +469,15 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
         cluster_sync();
         // every pair's CTA of this rank holds the same 128 outputs: the rows in turn, 4 outputs a lane
         const int f = t.m0 + rank * 128 + lane * 4;
+        const uint32_t base = (place >> 1) - share;
         if (first < n_tiles && f < O && !*abort_flag)
             for (int r = share + a.splits * warp; r < t.rows; r += a.splits * (blockDim.x / 32)) {
                 float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (int s = 0; s < a.splits; ++s) {
-                    const float4 v = ld_peer4(stage_u + (r * 128 + lane * 4) * 4, 2 * s + rank);
+                    const float4 v = ld_peer4(stage_u + (r * 128 + lane * 4) * 4, 2 * (base + s) + rank);
                     sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
                 }
-                const size_t at = ((size_t)(t.row0 + r) * out_parts + t.part) * O + f;
-                if (a.type == MOE_OUT_BF16) {
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out_ptr) + at) =
-                        make_uint2(pack_bf(to_u(sum.x), to_u(sum.y)), pack_bf(to_u(sum.z), to_u(sum.w)));
-                } else {
-                    float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out_ptr) + at);
-                    if (a.type == MOE_OUT_F32_ADD) {
-                        const float4 old = *out;
-                        sum.x += old.x, sum.y += old.y, sum.z += old.z, sum.w += old.w;
-                    }
-                    *out = sum;
-                }
+                put4(a.out_ptr, a.type, ((size_t)(t.row0 + r) * out_parts + t.part) * O + f, sum);
             }
     }
     leave_pair(abort_flag, warp == 1, tbase);
@@ -490,10 +498,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 struct WeightArgs {
     CUtensorMap dy[3];   // box {64, 1, 16 << j} of dy [R][P][N]
     CUtensorMap x[3];    // of x [R][1][K]; codes: box {128, 1, 16 << j}
+    void* out_ptr[2];
     CUtensorMap out[2];  // box {64, 16, 1} bf16, {32, 32, 1} fp32 of dw [S][N][K]
     const float* scale;  // [R][n_blk]
     const int32_t* offsets;
     int R, K, N, P, S, type, n_blk, n_tiles;
+    int splits;          // pairs of a cluster that share a tile's rows, as for y and dx
     DevStatus st;
 };
 template <bool M2>
@@ -566,11 +576,12 @@ static_assert(kWeightSmem <= 227 * 1024, "shared memory overflow");
 struct WeightTile {
     int s, part, n0, k0;
     int row0, rows;
-    bool two;  // halves (M2)
+    int r0, r1;  // this pair's share of the rows
+    bool two;    // halves (M2)
 };
 
-template <bool M2>
-__device__ __forceinline__ WeightTile weight_tile(const WeightArgs& a, int i) {
+template <bool M2, bool SHARED>
+__device__ __forceinline__ WeightTile weight_tile(const WeightArgs& a, int i, int share) {
     constexpr int kM = M2 ? 512 : 256;
     const int kt = (a.K + 255) / 256, nt = (a.N + kM - 1) / kM;
     WeightTile t;
@@ -584,6 +595,13 @@ __device__ __forceinline__ WeightTile weight_tile(const WeightArgs& a, int i) {
     int r1;
     slot_rows(a.offsets, t.s, a.R, t.row0, r1);
     t.rows = r1 - t.row0;
+    t.r0 = 0;
+    t.r1 = t.rows;
+    if (SHARED) {  // whole chunks, none perhaps
+        const long chunks = (t.rows + 63) / 64;
+        t.r0 = (int)min((long)t.rows, chunks * share / a.splits * 64);
+        t.r1 = (int)min((long)t.rows, chunks * (share + 1) / a.splits * 64);
+    }
     return t;
 }
 
@@ -599,8 +617,8 @@ __device__ __forceinline__ void decode16(const uint4& c, float scale, uint32_t (
     }
 }
 
-template <bool X8, bool M2>
-__device__ __forceinline__ void weights_pair(const WeightArgs& a, const int first, const int step) {
+template <bool X8, bool M2, bool SHARED>
+__device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair, const int pairs) {
     constexpr int kStages = WeightRing<M2>::kStages, kStageBytes = WeightRing<M2>::kStageBytes, kA = WeightRing<M2>::kA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -617,7 +635,8 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
-    const int place = (int)cluster_rank(), rank = place & 1;
+    const int place = (int)cluster_rank(), rank = place & 1, share = SHARED ? (place >> 1) % a.splits : 0;
+    const int first = SHARED ? pair / a.splits : pair, step = SHARED ? a.n_tiles : pairs;
     const uint32_t lead = place & ~1, both = 3u << lead;
     constexpr int kGroups = work_groups(X8, M2);
     static_assert(kStages % kGroups == 0, "a stage is one group's");
@@ -645,9 +664,9 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
     cluster_arrive_relaxed();
     pdl_wait();
     WeightTile t = {};
-    if (first < a.n_tiles) t = weight_tile<M2>(a, first);
+    if (first < a.n_tiles) t = weight_tile<M2, SHARED>(a, first, share);
     auto next_tile = [&](int i) {
-        if (i + step < a.n_tiles) t = weight_tile<M2>(a, i + step);
+        if (i + step < a.n_tiles) t = weight_tile<M2, SHARED>(a, i + step, share);
     };
     if (warp == 0 && first == 0)
         for (int s = lane; s < a.S; s += 32) {
@@ -675,8 +694,8 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
         uint32_t phase = 0, used = 0, used_land = 0, land_phase = 0;
         for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
             const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 128;
-            for (int r = 0; r < t.rows; r += 64) {
-                const int left = min(64, t.rows - r), n16 = (left + 15) / 16;
+            for (int r = t.r0; r < t.r1; r += 64) {
+                const int left = min(64, t.r1 - r), n16 = (left + 15) / 16;
                 const bool work = X8 || (left & 15);
                 if (!(ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit))) break;
                 if (elect_one()) {
@@ -748,13 +767,13 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
             const uint32_t idesc = umma_idesc_bf16(256, 256) | kIdescAMnMajor | kIdescBMnMajor;
             const uint64_t ad0 = umma_desc_mn_sw128(stage_u, kHalf / 2), bd0 = umma_desc_mn_sw128(stage_u + kA, kHalf / 2);
             for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
-                if (t.rows == 0) continue;
+                if (t.r0 >= t.r1) continue;
                 ok = tile_products<kStages>(
-                    t.two, (t.rows + 63) / 64, stage, u,
+                    t.two, (t.r1 - t.r0 + 63) / 64, stage, u,
                     [&](int c) {
                         // one wait a chunk: two or three of 180 cycles each held up the products of codes
                         bool got;
-                        if (X8 || (min(64, t.rows - c * 64) & 15)) {
+                        if (X8 || (min(64, t.r1 - t.r0 - c * 64) & 15)) {
                             got = warp_wait(ready_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit);
                             work_phase ^= 1u << at;
                         } else {
@@ -779,7 +798,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                         if (elect_one()) {
                             const uint64_t ad = ad0 + st * (kStageBytes >> 4) + half * (kHalf >> 4), bd = bd0 + st * (kStageBytes >> 4);
                             const uint32_t d = tbase + (v & 1) * 256;
-                            const int left = min(64, t.rows - c * 64);
+                            const int left = min(64, t.r1 - t.r0 - c * 64);
                             umma_bf16_pair(d, ad, bd, idesc, c > 0);
                             if (left > 16) umma_bf16_pair(d, ad + 128, bd + 128, idesc, 1);
                             if (left > 32) umma_bf16_pair(d, ad + 256, bd + 256, idesc, 1);
@@ -815,8 +834,8 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
         uint32_t land_phase = 0;
         for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
             const int blk = (t.k0 + rank * 128) / MOE_PAYLOAD_BLOCK;
-            for (int r = 0; r < t.rows; r += 64) {
-                const int left = min(64, t.rows - r), rows16 = (left + 15) & ~15;
+            for (int r = t.r0; r < t.r1; r += 64) {
+                const int left = min(64, t.r1 - r), rows16 = (left + 15) & ~15;
                 const bool work = X8 || (left & 15), mine = work && turn == group;
                 if (work && ++turn == kGroups) turn = 0;
                 if (mine) {
@@ -896,9 +915,37 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
         bool ok = true;
         int u = 0;
         for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
-            if (t.rows == 0 && a.type == MOE_OUT_F32_ADD) continue;
+            const bool some = t.r0 < t.r1;  // products to drain
+            if (SHARED) {
+                // [N][K] where the ring was (all its products are done), 16 bytes in the order of a swizzle
+                if (some && !(ok = warp_wait(smem_u32(&tfull[u & 1]), (u >> 1) & 1, abort_flag, limit))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = part * 128; c < part * 128 + 128; c += 32) {
+                    uint32_t v[32];
+                    if (some) {
+                        tmem_ld32(tbase + (u & 1) * 256 + ((uint32_t)(q * 32) << 16) + c, v);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 0;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st_shared4(stage_u + (q * 32 + lane) * 1024 + (((c >> 2) + (k ^ (lane & 7))) << 4), v[4 * k], v[4 * k + 1],
+                                   v[4 * k + 2], v[4 * k + 3]);
+                }
+                if (some) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed_cluster(lead_tempty + (u & 1) * 8);
+                    ++u;
+                }
+                continue;
+            }
+            if (!some && a.type == MOE_OUT_F32_ADD) continue;
             for (int half = 0; half < (t.two ? 2 : 1); ++half) {
-                if (t.rows) {
+                if (some) {
                     if (!(ok = warp_wait(smem_u32(&tfull[u & 1]), (u >> 1) & 1, abort_flag, limit))) break;
                     tc_fence_after();
                 }
@@ -912,7 +959,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
                             uint32_t v[32];
-                            if (t.rows) {
+                            if (some) {
                                 tmem_ld_16x256_64(tmem + c + ((uint32_t)(h * 16) << 16), v);
                                 tmem_ld_wait();
                             } else {
@@ -939,7 +986,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                 } else {
                     for (int c = part * 128; c < c_end; c += 32) {
                         uint32_t v[32];
-                        if (t.rows) {
+                        if (some) {
                             tmem_ld32(tmem + c, v);
                             tmem_ld_wait();
                         } else {
@@ -960,7 +1007,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
                         __syncwarp();
                     }
                 }
-                if (t.rows) {
+                if (some) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_relaxed_cluster(lead_tempty + (u & 1) * 8);
@@ -971,12 +1018,30 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int firs
         if (!ok && lane == 0) give_up();
         if (lane == 0) bulk_wait();
     }
+    if (SHARED) {
+        __syncwarp();
+        tc_fence_before();
+        cluster_sync();
+        // every pair's CTA of this rank holds the same 128 x 256: the rows of them in turn, 4 columns a lane
+        const uint32_t base = (place >> 1) - share;
+        if (first < a.n_tiles && !*abort_flag && (t.rows || a.type != MOE_OUT_F32_ADD))
+            for (int n = share + a.splits * warp; n < min(128, a.N - t.n0 - rank * 128); n += a.splits * (blockDim.x / 32))
+                for (int k = lane * 4; k < min(256, a.K - t.k0); k += 128) {
+                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int s = 0; s < a.splits && t.rows; ++s) {
+                        const float4 v = ld_peer4(stage_u + n * 1024 + (((k >> 2) ^ (n & 7)) << 4), 2 * (base + s) + rank);
+                        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                    }
+                    put4(a.out_ptr[t.part], a.type, ((size_t)t.s * a.N + t.n0 + rank * 128 + n) * a.K + t.k0 + k, sum);
+                }
+    }
     leave_pair(abort_flag, warp == 1, tbase);
 }
 
-template <bool X8, bool M2>
+// (SHARED: with it in every kernel dW of 38 rows, 1856 to 264 features of 16 slots, took 15.8 us, not 14.8)
+template <bool X8, bool M2, bool SHARED>
 __global__ void __launch_bounds__(weight_threads(X8, M2), 1) weights_kernel(const __grid_constant__ WeightArgs a) {
-    weights_pair<X8, M2>(a, blockIdx.x / 2, gridDim.x / 2);
+    weights_pair<X8, M2, SHARED>(a, blockIdx.x / 2, gridDim.x / 2);
 }
 
 // dx and dW in one launch, `dx_pairs` of its pairs for dx: where neither fills the device for long, one
@@ -987,11 +1052,11 @@ struct BothArgs {
     int dx_pairs;
 };
 constexpr int kBothSmem = kRowsSmem > kWeightSmem ? kRowsSmem : kWeightSmem;
-template <bool X8>
+template <bool X8, bool SHARED>
 __global__ void __launch_bounds__(weight_threads(X8, false), 1) gradients_kernel(const __grid_constant__ BothArgs a) {
     const int pair = blockIdx.x / 2;
     if (pair < a.dx_pairs) rows_pair<true>(a.dx, pair, a.dx_pairs);
-    else weights_pair<X8, false>(a.dw, pair - a.dx_pairs, gridDim.x / 2 - a.dx_pairs);
+    else weights_pair<X8, false, SHARED>(a.dw, pair - a.dx_pairs, gridDim.x / 2 - a.dx_pairs);
 }
 
 int check_project(const moe_project_t* p, int rows) {
@@ -1080,19 +1145,27 @@ int rows_args(const moe_project_t* p, int rows, const void* in, const int32_t* o
     return MOE_OK;
 }
 
-// Pairs that share a tile's contraction: up to four (clusters of eight), with eight chunks each at least,
-// where they are resident: `share` percent of the device, and clusters do not cross its groups of
-// processors (36 of four and 15 of eight of 152).
-int splits_of(int chunks, long tiles, int share) {
-    const long sms = (long)num_sms() * share / 100;
-    if (chunks >= 32 && tiles <= sms * 15 / 152) return 4;
-    return chunks >= 16 && tiles <= sms * 36 / 152 ? 2 : 1;
+// Clusters of two or four pairs that are resident: they do not cross the device's groups of processors
+// (36 and 15 of 152).
+long resident(int pairs) { return (long)num_sms() * (pairs == 2 ? 36 : 15) / 152; }
+
+// Pairs that share a tile's contraction: up to four, with eight chunks each at least, where clusters for
+// all tiles are resident.
+int splits_of(int chunks, long tiles) {
+    if (chunks >= 32 && tiles <= resident(4)) return 4;
+    return chunks >= 16 && tiles <= resident(2) ? 2 : 1;
+}
+
+// Chunks of 64 rows of a slot, of slots of equal counts.
+int chunks_of_slot(int rows, int slots) {
+    const int used = std::min(rows, slots);
+    return ((rows + used - 1) / used + 63) / 64;
 }
 
 template <bool DX>
 int launch_rows(RowsArgs& a, long tiles, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
-    a.splits = splits_of(DX ? (a.N + 63) / 64 * a.P : (a.K + 63) / 64, tiles, 100);
+    a.splits = splits_of(DX ? (a.N + 63) / 64 * a.P : (a.K + 63) / 64, tiles);
     return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, a.splits > 1 ? tiles * a.splits : std::min(tiles, most_pairs()),
                         a.splits, stream, a, DX ? "expert gradient" : "expert projection");
 }
@@ -1121,15 +1194,19 @@ int weight_args(const moe_project_t* p, int rows, const void* dy, const void* x,
     a.type = type;
     a.n_blk = (p->in_features + MOE_PAYLOAD_BLOCK - 1) / MOE_PAYLOAD_BLOCK;
     a.st = st;
+    a.out_ptr[0] = dw;
+    a.out_ptr[1] = dw2;
     a.n_tiles = (int)((K + 255) / 256 * ((N + 255) / 256) * P * S);
+    a.splits = 1;
     return MOE_OK;
 }
 
-template <bool X8, bool M2>
-int launch_weights(WeightArgs& a, cudaStream_t stream) {
+template <bool X8, bool M2, bool SHARED>
+int launch_weights(const WeightArgs& a, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
-    return launch_pairs(weights_kernel<X8, M2>, configured, weight_threads(X8, M2), kWeightSmem, std::min<long>(a.n_tiles, most_pairs()),
-                        1, stream, a, "expert weight gradient");
+    return launch_pairs(weights_kernel<X8, M2, SHARED>, configured, weight_threads(X8, M2), kWeightSmem,
+                        SHARED ? (long)a.n_tiles * a.splits : std::min<long>(a.n_tiles, most_pairs()), a.splits, stream, a,
+                        "expert weight gradient");
 }
 
 template <bool X8>
@@ -1140,9 +1217,65 @@ int launch_weights(WeightArgs& a, cudaStream_t stream) {
     // 512 396 and 329; codes, which are turned half as often, 187 and 171, 266 and 244, 447 and 428.  16
     // slots of 1024 to 1024, 512 rows each: 19.1 and 21.1).
     const long tiles = (long)((a.K + 255) / 256) * ((a.N + 511) / 512) * a.P * a.S;
-    if (tiles < 4 * most_pairs() || !(X8 || a.R >= 384L * a.S)) return launch_weights<X8, false>(a, stream);
-    a.n_tiles = (int)tiles;
-    return launch_weights<X8, true>(a, stream);
+    if (tiles >= 4 * most_pairs() && (X8 || a.R >= 384L * a.S)) {
+        a.n_tiles = (int)tiles;
+        return launch_weights<X8, true, false>(a, stream);
+    }
+    a.splits = splits_of(chunks_of_slot(a.R, a.S), a.n_tiles);
+    return a.splits > 1 ? launch_weights<X8, false, true>(a, stream) : launch_weights<X8, false, false>(a, stream);
+}
+
+// How dx and dW share the pairs of one launch: what they cost, in cycles, is 600 a tile and, for each
+// chunk of its sum, of dx 2 for each row and 400 at least, of dW 512, or the turning of its codes, and a
+// tile's drain at least, of dx 10 for each row, of dW 2400; sharing a sum costs 1500.  Slots are not equal, so the pairs' last tiles count by
+// half.  The plan is the one that ends first, and of those that end together the one that does the other
+// part sooner.  (In place of pairs by the sums of the costs, and dW never shared: 10062 rows, 144 to 248
+// features of 3 slots, gate and up, codes, 52 us and 21 so; 56 rows, 424 to 2856 of 7 slots, 27 and 16; 26
+// rows, 112 to 6064 of 29 slots, 52 both; 2771 rows, 504 to 3672 of 2 slots, 57 and 61.)
+struct Work {
+    int tiles, chunks, chunk, least;
+    int64_t time(int pairs, int splits) const {
+        const int64_t sum = std::max<int64_t>(least, (int64_t)((chunks + splits - 1) / splits) * chunk);
+        const int64_t tile = 600 + sum + (splits > 1 ? 1500 : 0), at_once = pairs / splits;
+        return ((tiles + at_once - 1) / at_once * tile + std::max(tile, tiles * tile / at_once)) / 2;
+    }
+};
+struct Plan {
+    int x_pairs, w_pairs, x_splits, w_splits;
+    int64_t time;
+};
+Plan best_plan(const Work& x, const Work& w) {
+    Plan best{0, 0, 1, 1, INT64_MAX};
+    auto offer = [&](int x_pairs, int w_pairs, int xs, int ws) {
+        const int64_t xt = x.time(x_pairs, xs), wt = w.time(w_pairs, ws), time = std::max(xt, wt) + std::min(xt, wt) / 8;
+        if (time < best.time) best = {x_pairs, w_pairs, xs, ws, time};
+    };
+    for (int xs = 1; xs <= 4; xs *= 2)
+        for (int ws = 1; ws <= 4; ws *= 2) {
+            const int group = std::max(xs, ws), there = group == 1 ? (int)most_pairs() : (int)resident(group) * group;
+            if ((xs > 1 && x.chunks < 8 * xs) || (ws > 1 && w.chunks < 8 * ws)) continue;
+            auto whole = [&](int pairs) { return (pairs + group - 1) / group * group; };  // of whole clusters
+            const long x_need = (long)x.tiles * xs, w_need = (long)w.tiles * ws;
+            if ((xs > 1 && x_need > there - group) || (ws > 1 && w_need > there - group)) continue;
+            const int x_pairs = whole((int)std::min<long>(x_need, there)), w_pairs = whole((int)std::min<long>(w_need, there));
+            if (xs > 1 && ws > 1) {
+                if (x_pairs + w_pairs <= there) offer(x_pairs, w_pairs, xs, ws);
+            } else if (xs > 1) {
+                if (x_pairs < there) offer(x_pairs, std::min(w_pairs, there - x_pairs), xs, ws);
+            } else if (ws > 1) {
+                if (w_pairs < there) offer(std::min(x_pairs, there - w_pairs), w_pairs, xs, ws);
+            } else {
+                for (int n = 1; n < there && n <= x_pairs; ++n) offer(n, std::min(w_pairs, there - n), 1, 1);
+            }
+        }
+    return best;
+}
+
+template <bool X8, bool SHARED>
+int launch_both(const BothArgs& a, const Plan& plan, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    return launch_pairs(gradients_kernel<X8, SHARED>, configured, weight_threads(X8, false), kBothSmem, plan.x_pairs + plan.w_pairs,
+                        std::max(plan.x_splits, plan.w_splits), stream, a, "expert gradients");
 }
 
 template <bool X8>
@@ -1153,26 +1286,21 @@ int gradients(const moe_project_t* p, int rows, const void* dy, const void* x, c
     int rc;
     if (dx && (rc = rows_args<true>(p, rows, dy, offsets, w, w2, dx, dx_type, st, a.dx, &dx_tiles))) return rc;
     if (dw && (rc = weight_args<X8>(p, rows, dy, x, scale, offsets, dw, dw2, dw_type, st, a.dw))) return rc;
-    // Both in one launch up to a few tiles a pair, the pairs shared by what the tiles cost, in cycles: a
-    // chunk of dx 2 for each row and 400 at least, a chunk of dW 512, or turning its codes, and a tile of
-    // dW its drain at least.  (100 rows, 328 to 600 features of 16 slots, a tile or two a pair, 12.2 us
-    // one after the other and 8.3 beside each other; 8000 rows, 2048 to 1024 of 16 slots, 12 tiles, 65 and
-    // 55; 4096 rows, 2048 to 7168 of 32 slots, a hundred, 332 and 383: there one reads memory and the
-    // other writes it, and each takes all the pairs.)
+    // Both in one launch up to a few tiles a pair.  (100 rows, 328 to 600 features of 16 slots, a tile or
+    // two a pair, 12.2 us one after the other and 8.3 beside each other; 8000 rows, 2048 to 1024 of 16
+    // slots, 12 tiles, 65 and 55; 4096 rows, 2048 to 7168 of 32 slots, a hundred, 332 and 383: there one
+    // reads memory and the other writes it, and each takes all the pairs.)
     if (dx && dw && dx_tiles + a.dw.n_tiles <= kBothTiles * most_pairs() && most_pairs() > 1) {
-        const long used = std::min(rows, p->n_slots), each = (rows + used - 1) / used;
-        const long height = std::max(200L, std::min<long>(a.dx.cap, each)), chunks = (each + 63) / 64;
-        const int dx_chunks = a.dx.P * ((a.dx.N + 63) / 64);
-        const int splits = a.dx.splits = splits_of(dx_chunks, dx_tiles, 50);
-        const double dx_cost = (double)((a.dx.K + 255) / 256) * used * ((each + a.dx.cap - 1) / a.dx.cap) * (600.0 + 2.0 * height * dx_chunks);
-        const double dw_cost = (double)a.dw.n_tiles * (600.0 + std::max(2400L, chunks * (X8 ? 900 : 512)));
-        const long dx_pairs = std::lround(most_pairs() * dx_cost / (dx_cost + dw_cost));
-        a.dx_pairs = (int)(splits > 1 ? dx_tiles * splits : std::min(dx_tiles, std::max(1L, std::min(most_pairs() - 1, dx_pairs))));
-        // (clusters are of one kind: a multiple of the splits for dW too)
-        const long dw_pairs = std::max<long>(1, std::min<long>(a.dw.n_tiles, most_pairs() - a.dx_pairs) / splits) * splits;
-        static std::atomic<uint64_t> configured{0};
-        return launch_pairs(gradients_kernel<X8>, configured, weight_threads(X8, false), kBothSmem, a.dx_pairs + dw_pairs, splits, stream, a,
-                            "expert gradients");
+        const int used = std::min(rows, p->n_slots), each = (rows + used - 1) / used, dx_most = (int)dx_tiles;
+        const int height = std::min(a.dx.cap, each);
+        // (dx's tiles: as many as there may be; chunks of dW: of equal slots)
+        Work x{dx_most, a.dx.P * ((a.dx.N + 63) / 64), std::max(400, 2 * height), 10 * height};
+        Work w{a.dw.n_tiles, chunks_of_slot(rows, p->n_slots), X8 ? 900 : 512, 2400};
+        const Plan plan = best_plan(x, w);
+        a.dx.splits = plan.x_splits;
+        a.dw.splits = plan.w_splits;
+        a.dx_pairs = plan.x_pairs;
+        return plan.w_splits > 1 ? launch_both<X8, true>(a, plan, stream) : launch_both<X8, false>(a, plan, stream);
     }
     if (dx && (rc = launch_rows<true>(a.dx, dx_tiles, stream))) return rc;
     return dw ? launch_weights<X8>(a.dw, stream) : MOE_OK;

@@ -162,6 +162,46 @@ def test_long_contractions_of_few_tiles(R, K, N, S, P):
         close(c.backward(dw=False)[0][:-1], dx[0][:-1], dx[1][:-1], name="dx beside a NaN")
 
 
+# few tiles of dw with long sums, which pairs of CTAs share too; slots with fewer chunks than pairs, or none
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[2500], [3000, 0, 70], [1, 2200, 64, 1900], [130, 4000]])
+@pytest.mark.parametrize("K,N,P", [(136, 200, 1), (272, 40, 2), (16, 8, 1)])
+def test_long_sums_of_few_tiles(counts, K, N, P):
+    off = np.concatenate([[0], np.cumsum(counts)])
+    c = Case(int(off[-1]) + 9, K, N, len(counts), P, off, seed=15)
+    _, dx, dw = c.reference()
+    for beside in (False, True):
+        for dtype in (BF, F32):
+            got = c.backward(dx=beside, dw_type=dtype)
+            if beside:
+                close(got[0], *dx, name="dx")
+            for p in range(P):
+                close(got[1][p], dw[0][p], dw[1][p], name=f"dw{p}")
+    added = c.backward(dx=False, dw_type=F32, add_dw=True, fill=1.0)[1]
+    for p in range(P):
+        close(added[p], dw[0][p] + 1.0, dw[1][p] + STEP * (dw[0][p].abs() + 1.0), name=f"dw{p} added")
+    if K % 16 == 0:
+        g = torch.Generator().manual_seed(K)
+        codes = torch.randint(0, 256, (c.R, K), generator=g).to(torch.uint8)
+        codes = torch.where((codes & 0x7F) == 0x7F, codes - 1, codes)
+        scales = torch.exp2(torch.randint(-12, 4, (c.R, -(-K // 128)), generator=g).float())
+        values = (codes.view(torch.float8_e4m3fn).double() * scales.double().repeat_interleave(128, 1)[:, :K]).to(BF)
+        kept_dw = c.reference(values)[2]
+        for beside in (False, True):
+            got = c.backward(dx=beside, eight=(codes, scales))
+            for p in range(P):
+                close(got[1][p], kept_dw[0][p], kept_dw[1][p], name=f"dw{p} of codes")
+    assert m.moe_check_status() == 0
+    # the row behind the last slot, and one of the largest slot: the others' gradients do not see them
+    big = int(np.argmax(counts))
+    c.x[-1, 3], c.dy[-1, 5] = float("inf"), float("nan")
+    c.x[off[big] + 1, 3], c.dy[off[big] + 1, 5] = float("inf"), float("nan")
+    got = c.backward(dx=False)[1]
+    for s in range(len(counts)):
+        if s != big:
+            close(got[0][s], dw[0][0][s], dw[1][0][s], name="dw beside infinities")
+
+
 # counts that end at, before and after every unit in which a kernel may take rows
 @pytest.mark.gpu
 @pytest.mark.parametrize("P", [1, 2])
