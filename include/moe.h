@@ -532,7 +532,8 @@ MOE_API int moe_adapter_project_backward(const moe_adapter_t* adapter, int T, co
  *   dy_disp[inv_perm[t*k+j], :] = bf16( topk_w[t,j] * d_out[t,:] ),
  *   d_topk_w[t,j] = sum over the columns of d_out[t,:] * y_disp[inv_perm[t*k+j], :]   (fp32).
  * d_out [T,H], y_disp and dy_disp [T*k,H] bf16; the sums run in a fixed order.  A row index outside
- * [0, T*k) sets the device status, writes no row and gives the gradient 0. */
+ * [0, T*k) sets the device status, writes no row and gives the gradient 0.  Each row is named
+ * once, as moe_dispatch does: what dy_disp holds in a row that two assignments name is not defined. */
 MOE_API int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_out, const void* y_disp,
                          const int32_t* inv_perm, const float* topk_w, void* dy_disp, float* d_topk_w, void* stream);
 
@@ -557,9 +558,9 @@ MOE_API int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_
  * out, dx and dw are written as their type says: MOE_OUT_BF16; MOE_OUT_F32; MOE_OUT_F32_ADD adds to
  * the fp32 values that they hold (gradients of several batches, or of several paths to one input).
  * Outputs overlap no input.  Rows of no slot are neither read nor written; a slot without rows gets
- * dw = 0.  An infinity or
- * NaN in a row shows in that row's results and its slot's dw only.  Sums run in an order that the
- * sizes and counts fix: results repeat bit for bit on one GPU model.  rows = 0 writes dw alone.
+ * dw = 0.  An infinity or NaN in a row shows in that row's results and its slot's dw only.  Sums run in
+ * an order that the sizes and counts fix: results repeat bit for bit on one GPU model.  rows = 0 writes
+ * dw alone.
  * Limits: K and N multiples of 8 and at most 2^24, n_slots <= 1024. */
 #define MOE_OUT_BF16 0
 #define MOE_OUT_F32 1
@@ -580,8 +581,9 @@ MOE_API int moe_expert_project_backward(const moe_project_t* project, int rows, 
 /* Activations kept in 8 bits: a row is cut into blocks of MOE_PAYLOAD_BLOCK columns (the last one
  * shorter), and a block stored as E4M3 codes and one fp32 scale, the least power of two from
  * 2^-117 to 2^119 with amax / scale <= 448 (amax: its largest finite magnitude; 1 for a block of
- * zeros; 2^119 where none has); code = e4m3(x / scale), rounded to nearest even, saturating.  code * scale is a bf16 value, so the
- * backward products use the kept values themselves.  Infinities and NaN are kept as NaN.
+ * zeros; 2^119 where none has); code = e4m3(x / scale), rounded to nearest even, saturating.
+ * code * scale is a bf16 value, so the backward products use the kept values themselves.  Infinities
+ * and NaN are kept as NaN.
  * moe_checkpoint_rows: x [rows,cols] bf16 -> codes [rows,cols], scale [rows, ceil(cols/128)].
  * moe_swiglu_checkpoint: gate_up [rows, 2*inter] bf16 (gate, then up: moe_expert_project's out) ->
  *   h [rows,inter] = bf16( silu(gate) * up ), and gate and up kept: codes [rows, 2*inter], scale
