@@ -202,6 +202,76 @@ def test_long_sums_of_few_tiles(counts, K, N, P):
             close(got[0][s], dw[0][0][s], dw[1][0][s], name="dw beside infinities")
 
 
+# shared memory that a call of NaNs left is not seen where a narrow output's copies are left out
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [8, 64, 128, 136, 192, 320, 392])
+@pytest.mark.parametrize("R,K,S,P", [(700, 328, 2, 1), (30, 2056, 1, 2), (2000, 72, 3, 2)])
+def test_narrow_outputs_after_a_call_of_nans(R, K, S, P, N):
+    nan = Case(3000, 520, 520, 2, 2, seed=16)
+    nan.x.fill_(float("nan"))
+    nan.dy.fill_(float("nan"))
+    c = Case(R, K, N, S, P, seed=17)
+    y, dx, dw = c.reference()
+    for dtype in (BF, F32):
+        nan.forward()
+        close(c.forward(dtype), *y, name="y")
+        nan.backward()
+        got = c.backward(dx_type=dtype, dw_type=dtype)
+        close(got[0], *dx, name="dx")
+        for p in range(P):
+            close(got[1][p], dw[0][p], dw[1][p], name=f"dw{p}")
+        nan.backward()
+        got = c.backward(dx=False, dw_type=dtype)[1]
+        for p in range(P):
+            close(got[p], dw[0][p], dw[1][p], name=f"dw{p} alone")
+    assert m.moe_check_status() == 0
+
+
+# sums that pairs share: a captured call takes the counts of its replay, repeats bit for bit, on two streams too
+@pytest.mark.gpu
+def test_shared_sums_captured_repeated_and_beside_each_other():
+    R, K, N, S = 2600, 144, 200, 3
+    c = Case(R, K, N, S, 2, [0, 2000, 2000, 2600], seed=18)
+    x, dy, off, (w, w2) = c.x.cuda(), c.dy.cuda(), c.offsets(), c.weights()
+
+    def outputs():
+        return [torch.zeros(R, K, dtype=BF, device="cuda")] + [torch.zeros_like(w) for _ in range(4)]
+
+    def step(dx, dw, dw2, alone, alone2):
+        m.moe_expert_project_backward(c.p, R, dy, x, None, None, off, w, w2, dx, dw, dw2)
+        m.moe_expert_project_backward(c.p, R, dy, x, None, None, off, None, None, None, alone, alone2)
+
+    first = outputs()
+    step(*first)
+    graph, side, replayed = torch.cuda.CUDAGraph(), torch.cuda.Stream(), outputs()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step(*replayed)
+    for offsets in ([0, 2000, 2000, 2600], [0, 0, 2600, 2600], [0, 1, 100, 2500]):
+        off.copy_(torch.tensor(offsets, dtype=torch.int32))
+        c.off = np.asarray(offsets, dtype=np.int32)
+        _, dx, dw = c.reference()
+        graph.replay()
+        torch.cuda.synchronize()
+        n = offsets[-1]
+        close(replayed[0][:n], dx[0][:n], dx[1][:n], name="dx")
+        for p in range(2):
+            close(replayed[1 + p], dw[0][p], dw[1][p], name=f"dw{p}")
+            close(replayed[3 + p], dw[0][p], dw[1][p], name=f"dw{p} alone")
+        if offsets == [0, 2000, 2000, 2600]:
+            assert all(torch.equal(a, b) for a, b in zip(first, replayed))
+        here, there = outputs(), outputs()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            step(*here)
+            with torch.cuda.stream(side):
+                step(*there)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[:n] if a.shape[0] == R else a, b[:n] if b.shape[0] == R else b)
+                   for got in (here, there) for a, b in zip(got, replayed))
+    assert m.moe_check_status() == 0
+
+
 # counts that end at, before and after every unit in which a kernel may take rows
 @pytest.mark.gpu
 @pytest.mark.parametrize("P", [1, 2])
