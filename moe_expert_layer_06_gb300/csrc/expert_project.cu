@@ -109,6 +109,17 @@ __device__ __forceinline__ void put4(void* out, int type, size_t at, float4 v) {
     *p = v;
 }
 
+// What `splits` pairs hold of four sums, from the CTA of rank `first` on, added in the pairs' order.  The
+// loads are on their way together.
+__device__ __forceinline__ float4 sum_of_pairs(uint32_t addr, uint32_t first, int splits) {
+    float4 v[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = s < splits ? ld_peer4(addr, first + 2 * s) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int s = 1; s < 4; ++s) v[0].x += v[s].x, v[0].y += v[s].y, v[0].z += v[s].z, v[0].w += v[s].w;
+    return v[0];
+}
+
 // How the pair's kernels end.  On the way out nobody signals the other CTA any more (who waits for
 // signals has waited for all of them), so the barrier need not see them through; after a wait that
 // expired it does.
@@ -472,11 +483,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
         const uint32_t base = (place >> 1) - share;
         if (first < n_tiles && f < O && !*abort_flag)
             for (int r = share + a.splits * warp; r < t.rows; r += a.splits * (blockDim.x / 32)) {
-                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int s = 0; s < a.splits; ++s) {
-                    const float4 v = ld_peer4(stage_u + (r * 128 + lane * 4) * 4, 2 * (base + s) + rank);
-                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-                }
+                const float4 sum = sum_of_pairs(stage_u + (r * 128 + lane * 4) * 4, 2 * base + rank, a.splits);
                 put4(a.out_ptr, a.type, ((size_t)(t.row0 + r) * out_parts + t.part) * O + f, sum);
             }
     }
@@ -1025,15 +1032,16 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
         // every pair's CTA of this rank holds the same 128 x 256: the rows of them in turn, 4 columns a lane
         const uint32_t base = (place >> 1) - share;
         if (first < a.n_tiles && !*abort_flag && (t.rows || a.type != MOE_OUT_F32_ADD))
-            for (int n = share + a.splits * warp; n < min(128, a.N - t.n0 - rank * 128); n += a.splits * (blockDim.x / 32))
-                for (int k = lane * 4; k < min(256, a.K - t.k0); k += 128) {
-                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int s = 0; s < a.splits && t.rows; ++s) {
-                        const float4 v = ld_peer4(stage_u + n * 1024 + (((k >> 2) ^ (n & 7)) << 4), 2 * (base + s) + rank);
-                        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-                    }
-                    put4(a.out_ptr[t.part], a.type, ((size_t)t.s * a.N + t.n0 + rank * 128 + n) * a.K + t.k0 + k, sum);
-                }
+            for (int n = share + a.splits * warp; n < min(128, a.N - t.n0 - rank * 128); n += a.splits * (blockDim.x / 32)) {
+                const int k = lane * 4, most = a.K - t.k0;
+                const uint32_t row = stage_u + n * 1024, at = (lane ^ (n & 7)) << 4;
+                float4 low = make_float4(0.0f, 0.0f, 0.0f, 0.0f), high = low;
+                if (t.rows && k < most) low = sum_of_pairs(row + at, 2 * base + rank, a.splits);
+                if (t.rows && k + 128 < most) high = sum_of_pairs(row + at + 512, 2 * base + rank, a.splits);
+                const size_t out = ((size_t)t.s * a.N + t.n0 + rank * 128 + n) * a.K + t.k0 + k;
+                if (k < most) put4(a.out_ptr[t.part], a.type, out, low);
+                if (k + 128 < most) put4(a.out_ptr[t.part], a.type, out + 128, high);
+            }
     }
     leave_pair(abort_flag, warp == 1, tbase);
 }
@@ -1149,11 +1157,14 @@ int rows_args(const moe_project_t* p, int rows, const void* in, const int32_t* o
 // (36 and 15 of 152).
 long resident(int pairs) { return (long)num_sms() * (pairs == 2 ? 36 : 15) / 152; }
 
-// Pairs that share a tile's contraction: up to four, with eight chunks each at least, where clusters for
-// all tiles are resident.
-int splits_of(int chunks, long tiles) {
-    if (chunks >= 32 && tiles <= resident(4)) return 4;
-    return chunks >= 16 && tiles <= resident(2) ? 2 : 1;
+// Pairs that share a tile's contraction, where clusters for all tiles are resident: four from 16 chunks
+// on, else two from 16 (y and dx) or 24 (dW, whose sums are larger).  (One pair, two and four, us: y of 64
+// rows, 1024 to 256 (16 chunks), 6.9, 6.7 and 5.6, of 2048 features 10.2, 8.4 and 6.4, of 512 5.3 and 5.8
+// with two; dW of 1024 rows, 256 by 256, 8.6, 9.3 and 8.6, in 8 bits 10.1, 9.9 and 9.3, of 2048 rows 12.8,
+// 11.5 and 9.7, of 512 6.5 and 8.2 with two.)
+int splits_of(int chunks, long tiles, int two) {
+    if (chunks >= 16 && tiles <= resident(4)) return 4;
+    return chunks >= two && tiles <= resident(2) ? 2 : 1;
 }
 
 // Chunks of 64 rows of a slot, of slots of equal counts.
@@ -1165,7 +1176,7 @@ int chunks_of_slot(int rows, int slots) {
 template <bool DX>
 int launch_rows(RowsArgs& a, long tiles, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
-    a.splits = splits_of(DX ? (a.N + 63) / 64 * a.P : (a.K + 63) / 64, tiles);
+    a.splits = splits_of(DX ? (a.N + 63) / 64 * a.P : (a.K + 63) / 64, tiles, 16);
     return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, a.splits > 1 ? tiles * a.splits : std::min(tiles, most_pairs()),
                         a.splits, stream, a, DX ? "expert gradient" : "expert projection");
 }
@@ -1221,22 +1232,22 @@ int launch_weights(WeightArgs& a, cudaStream_t stream) {
         a.n_tiles = (int)tiles;
         return launch_weights<X8, true, false>(a, stream);
     }
-    a.splits = splits_of(chunks_of_slot(a.R, a.S), a.n_tiles);
+    a.splits = splits_of(chunks_of_slot(a.R, a.S), a.n_tiles, 24);
     return a.splits > 1 ? launch_weights<X8, false, true>(a, stream) : launch_weights<X8, false, false>(a, stream);
 }
 
 // How dx and dW share the pairs of one launch: what they cost, in cycles, is 600 a tile and, for each
 // chunk of its sum, of dx 2 for each row and 400 at least, of dW 512, or the turning of its codes, and a
-// tile's drain at least, of dx 10 for each row, of dW 2400; sharing a sum costs 1500.  Slots are not equal, so the pairs' last tiles count by
+// tile's drain at least, of dx 10 for each row, of dW 2400; sharing a sum costs 2300 and 5500.  Slots are not equal, so the pairs' last tiles count by
 // half.  The plan is the one that ends first, and of those that end together the one that does the other
 // part sooner.  (In place of pairs by the sums of the costs, and dW never shared: 10062 rows, 144 to 248
 // features of 3 slots, gate and up, codes, 52 us and 21 so; 56 rows, 424 to 2856 of 7 slots, 27 and 16; 26
 // rows, 112 to 6064 of 29 slots, 52 both; 2771 rows, 504 to 3672 of 2 slots, 57 and 61.)
 struct Work {
-    int tiles, chunks, chunk, least;
+    int tiles, chunks, chunk, least, join;
     int64_t time(int pairs, int splits) const {
         const int64_t sum = std::max<int64_t>(least, (int64_t)((chunks + splits - 1) / splits) * chunk);
-        const int64_t tile = 600 + sum + (splits > 1 ? 1500 : 0), at_once = pairs / splits;
+        const int64_t tile = 600 + sum + (splits > 1 ? join : 0), at_once = pairs / splits;
         return ((tiles + at_once - 1) / at_once * tile + std::max(tile, tiles * tile / at_once)) / 2;
     }
 };
@@ -1253,7 +1264,7 @@ Plan best_plan(const Work& x, const Work& w) {
     for (int xs = 1; xs <= 4; xs *= 2)
         for (int ws = 1; ws <= 4; ws *= 2) {
             const int group = std::max(xs, ws), there = group == 1 ? (int)most_pairs() : (int)resident(group) * group;
-            if ((xs > 1 && x.chunks < 8 * xs) || (ws > 1 && w.chunks < 8 * ws)) continue;
+            if ((xs > 1 && x.chunks < 16) || (ws > 1 && w.chunks < 16)) continue;
             auto whole = [&](int pairs) { return (pairs + group - 1) / group * group; };  // of whole clusters
             const long x_need = (long)x.tiles * xs, w_need = (long)w.tiles * ws;
             if ((xs > 1 && x_need > there - group) || (ws > 1 && w_need > there - group)) continue;
@@ -1294,8 +1305,8 @@ int gradients(const moe_project_t* p, int rows, const void* dy, const void* x, c
         const int used = std::min(rows, p->n_slots), each = (rows + used - 1) / used, dx_most = (int)dx_tiles;
         const int height = std::min(a.dx.cap, each);
         // (dx's tiles: as many as there may be; chunks of dW: of equal slots)
-        Work x{dx_most, a.dx.P * ((a.dx.N + 63) / 64), std::max(400, 2 * height), 10 * height};
-        Work w{a.dw.n_tiles, chunks_of_slot(rows, p->n_slots), X8 ? 900 : 512, 2400};
+        Work x{dx_most, a.dx.P * ((a.dx.N + 63) / 64), std::max(400, 2 * height), 10 * height, 2300};
+        Work w{a.dw.n_tiles, chunks_of_slot(rows, p->n_slots), X8 ? 900 : 512, 2400, 5500};
         const Plan plan = best_plan(x, w);
         a.dx.splits = plan.x_splits;
         a.dw.splits = plan.w_splits;
