@@ -545,7 +545,8 @@ MOE_API int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_
  * moe_expert_layer_06_gb300.training runs the whole layer this way.
  *
  * Rows of slot s are [offsets[s], offsets[s+1]) (moe_dispatch; offsets [n_slots+1] at least, on the
- * device).  Offsets outside [0, rows] or running backwards set the device status and are cut to it.
+ * device).  Offsets outside [0, rows] or running backwards set the device status and are cut to it (each
+ * value of a row that several slots then name is that of one of them).
  * moe_expert_project: for each part p (two: gate and up),
  *   out[r, p*N + n] = sum over k of x[r,k] * w_p[s,n,k]        (r in slot s)
  * moe_expert_project_backward:

@@ -142,7 +142,9 @@ __device__ __forceinline__ void leave_pair(const volatile int* abort_flag, bool 
 // a slot in chunks of equal height, a multiple of 32 up to `cap` (half of them in each CTA).
 // dx's W is read MN-major, as its contraction runs over W's rows.
 // Few tiles with a long contraction: the pairs of a cluster take a share of it each, and their sums meet
-// in distributed shared memory, added in the pairs' order.
+// in distributed shared memory, added in the pairs' order.  The launch has pairs for as many tiles as
+// offsets in order give; offsets that run backwards may name rows again and give more, which the pairs
+// then take whole and in turn.
 struct RowsArgs {
     CUtensorMap w[2];  // box {64, 128} of [S][N][K], dx: {64, 64}
     CUtensorMap in[4]; // box {64, 1, 16 << j} of x [R][1][K], dx: dy [R][P][N]
@@ -151,7 +153,7 @@ struct RowsArgs {
     void* out_ptr;
     int R, K, N, P, S, type;
     int cap, stages;   // rows of a chunk at most (64, 128, 256); stages of the ring that then fit
-    int splits;        // pairs of a cluster, which share a tile's contraction; above 1, one tile each
+    int splits;        // pairs of a cluster, which share a tile's contraction; above 1, pairs for every tile
     DevStatus st;
 };
 constexpr int kMostStages = 9;
@@ -269,7 +271,7 @@ __device__ __forceinline__ void drain_f32(const RowsArgs& a, const RowsTile& t, 
     }
 }
 
-// The pair `first` of `step`, which share the tiles.
+// Pair `pair` of `pairs`, which share the tiles.
 template <bool DX>
 __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, const int pairs) {
     extern __shared__ uint8_t smem_raw[];
@@ -287,13 +289,11 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
-    const int place = (int)cluster_rank(), rank = place & 1, share = (place >> 1) % a.splits;  // of the contraction
+    const int place = (int)cluster_rank(), rank = place & 1;
     const uint32_t lead = place & ~1, both = 3u << lead;
-    const int first = pair / a.splits;
     const int O = DX ? a.K : a.N, out_parts = DX ? 1 : a.P;
     const int m_tiles = (O + 255) / 256 * out_parts;
     const int kc1 = ((DX ? a.N : a.K) + 63) / 64, kc = kc1 * (DX ? a.P : 1);  // chunks of a part, of a tile
-    const int c0 = a.splits > 1 ? kc * share / a.splits : 0, c1 = a.splits > 1 ? kc * (share + 1) / a.splits : kc;  // this pair's
     const int kStages = a.stages, kStageBytes = stage_bytes(a.cap);
 
     if (warp == 0 && lane == 0) {
@@ -328,7 +328,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
             pre[s] = sum;
             sum += chunks_of(r1 - r0, a.cap) * m_tiles;
         }
-        if (!fits && first == 0) raise_status(a.st, kStatusBadShape);
+        if (!fits && pair < a.splits) raise_status(a.st, kStatusBadShape);
         int incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -342,7 +342,9 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    const int n_tiles = pre[a.S], step = a.splits > 1 ? max(1, n_tiles) : pairs;
+    const int n_tiles = pre[a.S], splits = n_tiles <= pairs / a.splits ? a.splits : 1;
+    const int first = pair / splits, step = splits > 1 ? max(1, n_tiles) : pairs;
+    const int share = (place >> 1) % splits, c0 = kc * share / splits, c1 = kc * (share + 1) / splits;  // of the contraction
     RowsTile t = {};
     if (first < n_tiles) t = rows_tile<DX>(a, pre, start, first);
     auto next_tile = [&](int i) {
@@ -455,7 +457,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
             if (!(ok = named_and(2 + (q >> 1), 64, ok))) break;  // (the two warps that share drain_bf16's barrier)
             tc_fence_after();
             const uint32_t tmem = tbase + (n & 1) * 256 + ((uint32_t)(q * 32) << 16), out = stage_u + kRing;
-            if (a.splits > 1) {
+            if (splits > 1) {
                 // [row][128 outputs] where the ring was: all its products are done
                 for (int r = 0; r < t.rows; r += 16) {
                     float v[16];
@@ -474,7 +476,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
         if (!ok && lane == 0) give_up();
         if (lane == 0) bulk_wait();
     }
-    if (a.splits > 1) {
+    if (splits > 1) {
         __syncwarp();
         tc_fence_before();
         cluster_sync();
@@ -482,8 +484,8 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
         const int f = t.m0 + rank * 128 + lane * 4;
         const uint32_t base = (place >> 1) - share;
         if (first < n_tiles && f < O && !*abort_flag)
-            for (int r = share + a.splits * warp; r < t.rows; r += a.splits * (blockDim.x / 32)) {
-                const float4 sum = sum_of_pairs(stage_u + (r * 128 + lane * 4) * 4, 2 * base + rank, a.splits);
+            for (int r = share + splits * warp; r < t.rows; r += splits * (blockDim.x / 32)) {
+                const float4 sum = sum_of_pairs(stage_u + (r * 128 + lane * 4) * 4, 2 * base + rank, splits);
                 put4(a.out_ptr, a.type, ((size_t)(t.row0 + r) * out_parts + t.part) * O + f, sum);
             }
     }
