@@ -993,6 +993,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_pair_kernel(const __grid_
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) settle_after_timeout();  // (a stage's copies signal the leader, whatever their own CTA has seen)
+    __syncwarp();
     cluster_sync();  // neither CTA leaves while the other may signal it or read its memory
     pdl_wait();      // the grid is complete only when the v kernel is
     tc_fence_after();

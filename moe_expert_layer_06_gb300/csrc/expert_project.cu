@@ -120,14 +120,25 @@ __device__ __forceinline__ float4 sum_of_pairs(uint32_t addr, uint32_t first, in
     return v[0];
 }
 
-// How the pair's kernels end.  On the way out nobody signals the other CTA any more (who waits for
+// How the pair's kernels end; `owner`: the warp that took the tensor memory, and has waited on `done` for the last
+// products (`complete`: they were).  On the way out nobody signals the other CTA any more (who waits for
 // signals has waited for all of them), so the barrier need not see them through; after a wait that
-// expired it does.
-__device__ __forceinline__ void leave_pair(const volatile int* abort_flag, bool owner, uint32_t tmem) {
+// expired it does, when everything has had the time to land.
+__device__ __forceinline__ void leave_pair(const volatile int* abort_flag, const DevStatus& st, bool owner, bool complete, uint32_t done,
+                                           uint32_t tmem) {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    // (In the CTA that issues no products this warp has waited since the kernel began, which may take longer than a
+    // wait's limit.  The other warps are through by now, and the issuing one is or gives up.)
+    if (owner && !complete && !mbar_wait(done, 0, max(st.limit_ns, kSettleNs))) {
+        raise_status(st, kStatusWaitTimeout);
+        settle_after_timeout();
+    }
+    __syncwarp();
     if (*abort_flag) {
+        settle_after_timeout();
+        __syncwarp();
         cluster_sync();
     } else {
         cluster_arrive_relaxed();
@@ -356,6 +367,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
         *abort_flag = 1;
         raise_status(a.st, kStatusWaitTimeout);
     };
+    bool complete = true;  // (warp 1: the products are)
     const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), stage_u = smem_u32(smem);
     const uint32_t lead_full = leader_addr(full_u, lead), lead_tempty = leader_addr(smem_u32(tempty), lead);
 
@@ -398,15 +410,15 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
                 }
             }
         }
-        if (!ok && lane == 0) give_up();
         // every stage's last products are done, so its copies have landed
-        for (int s = 0; s < kStages; ++s) {
-            if ((used >> stage) & 1u) mbar_wait(empty_u + stage * 8, phase ^ 1, limit);
+        for (int s = 0; s < kStages && ok; ++s) {
+            if ((used >> stage) & 1u) ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit);
             if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1;
             }
         }
+        if (!ok && lane == 0) give_up();
     } else if (warp == 1) {
         if (rank == 0) {
             const uint64_t ad0 = DX ? umma_desc_mn_sw128(stage_u, kHalf / 2) : umma_desc_sw128(stage_u);
@@ -447,7 +459,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
             if (elect_one()) umma_commit_pair(smem_u32(done), both);
             __syncwarp();
         }
-        mbar_wait(smem_u32(done), 0, limit);
+        complete = mbar_wait(smem_u32(done), 0, limit);
     } else if (warp < 6) {  // (a launch for dW too has more)
         const int q = warp & 3;
         bool ok = true;
@@ -489,7 +501,7 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
                 put4(a.out_ptr, a.type, ((size_t)(t.row0 + r) * out_parts + t.part) * O + f, sum);
             }
     }
-    leave_pair(abort_flag, warp == 1, tbase);
+    leave_pair(abort_flag, a.st, warp == 1, complete, smem_u32(done), tbase);
 }
 
 template <bool DX>
@@ -692,6 +704,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
         *abort_flag = 1;
         raise_status(a.st, kStatusWaitTimeout);
     };
+    bool complete = true;  // (warp 1: the products are)
     const uint32_t full_u = smem_u32(full), empty_u = smem_u32(empty), landed_u = smem_u32(landed), ready_u = smem_u32(ready);
     const uint32_t stage_u = smem_u32(smem);
     const uint32_t lead_full = leader_addr(full_u, lead), lead_tempty = leader_addr(smem_u32(tempty), lead), lead_ready = leader_addr(ready_u, lead);
@@ -700,7 +713,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
         const uint64_t pol = policy_evict_normal();
         bool ok = true;
         int stage = 0;
-        uint32_t phase = 0, used = 0, used_land = 0, land_phase = 0;
+        uint32_t phase = 0, used = 0;
         for (int i = first; i < a.n_tiles && ok; next_tile(i), i += step) {
             const int n0 = t.n0 + rank * 128, k0 = t.k0 + rank * 128;
             for (int r = t.r0; r < t.r1; r += 64) {
@@ -745,26 +758,21 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
                 }
                 __syncwarp();
                 used |= 1u << stage;
-                used_land = work ? used_land | 1u << stage : used_land & ~(1u << stage);
-                if (work) land_phase ^= 1u << stage;
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
         }
-        if (!ok && lane == 0) give_up();
         // every stage's last products are done, so its copies have landed
-        for (int s = 0; s < kStages; ++s) {
-            if ((used >> stage) & 1u) {
-                if (!ok && ((used_land >> stage) & 1u)) mbar_wait(landed_u + stage * 8, ((land_phase >> stage) & 1u) ^ 1, limit);
-                mbar_wait(empty_u + stage * 8, phase ^ 1, limit);
-            }
+        for (int s = 0; s < kStages && ok; ++s) {
+            if ((used >> stage) & 1u) ok = warp_wait(empty_u + stage * 8, phase ^ 1, abort_flag, limit);
             if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1;
             }
         }
+        if (!ok && lane == 0) give_up();
     } else if (warp == 1) {
         // What it waits for is read by the tensor cores alone, each CTA's half in its own shared
         // memory: the waits do not acquire for the cluster (100 to 200 ns each; three of them held the
@@ -831,7 +839,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
             if (elect_one()) umma_commit_pair(smem_u32(done), both);
             __syncwarp();
         }
-        mbar_wait(smem_u32(done), 0, limit);
+        complete = mbar_wait(smem_u32(done), 0, limit);
     } else if (warp < 2 + kWork * kGroups) {
         const int group = (warp - 2) / kWork, sub = (warp - 2) % kWork;
         // The leader hears of the other CTA's rows by copies.  (An arrival there holds its thread for
@@ -912,11 +920,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
                 if (++stage == kStages) stage = 0;
             }
         }
-        if (!ok) {
-            if (lane == 0) give_up();
-            // (the last signals are on their way: time enough for them to arrive)
-            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;) {}
-        }
+        if (!ok && lane == 0) give_up();
     } else {
         // two warps for each quarter of the accumulators, half of the columns each
         const int q = warp & 3, part = (warp - 2 - kWork * kGroups) >> 2;
@@ -1045,7 +1049,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
                 if (k + 128 < most) put4(a.out_ptr[t.part], a.type, out + 128, high);
             }
     }
-    leave_pair(abort_flag, warp == 1, tbase);
+    leave_pair(abort_flag, a.st, warp == 1, complete, smem_u32(done), tbase);
 }
 
 // (SHARED: with it in every kernel dW of 38 rows, 1856 to 264 features of 16 slots, took 15.8 us, not 14.8)

@@ -93,6 +93,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
     return ok;
 }
 
+// After a wait that expired, before a CTA of a pair leaves: what is still on its way to shared memory (copies
+// that signal the other CTA's barrier, signals, commits) cannot all be waited for by itself, as some of it is
+// counted by barriers that the one who gave up no longer completes.  10 ms is a thousand times what any of it takes,
+// however short the waits' own limit.
+constexpr unsigned long long kSettleNs = 10000000;
+__device__ __forceinline__ void settle_after_timeout() {
+    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kSettleNs;) {}
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

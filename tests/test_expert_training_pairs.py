@@ -1,5 +1,5 @@
-"""Sums that pairs of CTAs share (moe_expert_project and its backward pass), beside test_expert_training.py,
-whose cases, definitions and tolerances these tests take."""
+"""The CTA pairs of moe_expert_project and its backward pass: sums that several of them share, the limit of their
+waits.  Beside test_expert_training.py, whose cases, definitions and tolerances these tests take."""
 import numpy as np
 import pytest
 import torch
@@ -57,3 +57,33 @@ def test_offsets_that_run_backwards(K, N, P):
                 close(both[1][p][s], *dw[s][p], name=f"dw{p} of slot {s}")
                 close(alone[1][p][s], *dw[s][p], name=f"dw{p} of slot {s} alone")
     assert m.moe_check_status() == m.MOE_ERR_DEVICE_STATUS
+
+
+@pytest.mark.gpu
+def test_a_limit_of_the_waits_below_the_time_of_a_call():
+    """The limit is of each wait, not of the kernel: calls of some milliseconds give the same bits under 0.5 ms."""
+    R, K, N, S = 32768, 7168, 2048, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF)  # noqa: E731
+    p, off = m.Project(K, N, S, 2), torch.linspace(0, R, S + 1, device="cuda").round().to(torch.int32)
+    x, dy, w, w2 = new(R, K), new(R, 2 * N), new(S, N, K), new(S, N, K)
+    codes, scale = torch.empty(R, K, dtype=torch.uint8, device="cuda"), torch.empty(R, K // 128, device="cuda")
+    m.moe_checkpoint_rows(R, K, x, codes, scale)
+
+    def step():
+        y, dx = torch.empty(R, 2 * N, dtype=BF, device="cuda"), torch.empty(R, K, dtype=BF, device="cuda")
+        dw = [torch.empty(S, N, K, dtype=BF, device="cuda") for _ in range(4)]
+        m.moe_expert_project(p, R, x, off, w, w2, y)
+        m.moe_expert_project_backward(p, R, dy, x, None, None, off, w, w2, dx, *dw[:2])
+        m.moe_expert_project_backward(p, R, dy, None, codes, scale, off, None, None, None, *dw[2:])
+        return [y, dx, *dw]
+
+    want = step()
+    assert m.moe_check_status() == m.MOE_OK
+    m.moe_set_wait_limit_ns(500_000)
+    try:
+        got = step()
+        assert m.moe_check_status() == m.MOE_OK
+    finally:
+        m.moe_set_wait_limit_ns(2_000_000_000)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
