@@ -579,6 +579,15 @@ MOE_API int moe_expert_project_backward(const moe_project_t* project, int rows, 
                                         const void* w2, void* dx, int dx_type, void* dw, void* dw2, int dw_type,
                                         void* stream);
 
+/* For tests: how a call of moe_expert_project (outputs 0) or of its backward pass (outputs: MOE_PLAN_DX, MOE_PLAN_DW
+ * or both, and MOE_PLAN_ROWS8 where the rows are given in 8 bits) runs on the current device.  plan [4], host
+ * memory: how many pairs of CTAs share a sum of y or dx, and one of dw (0: not asked for); 1 where dx and dw
+ * are one launch; 1 where dw's tiles are twice as high. */
+#define MOE_PLAN_DX 1
+#define MOE_PLAN_DW 2
+#define MOE_PLAN_ROWS8 4
+MOE_API int moe_debug_project_plan(const moe_project_t* project, int rows, int outputs, int32_t* plan);
+
 /* Activations kept in 8 bits: a row is cut into blocks of MOE_PAYLOAD_BLOCK columns (the last one
  * shorter), and a block stored as E4M3 codes and one fp32 scale, the least power of two from
  * 2^-117 to 2^119 with amax / scale <= 448 (amax: its largest finite magnitude; 1 for a block of

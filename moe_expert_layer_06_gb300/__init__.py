@@ -42,7 +42,7 @@ EXPORTS = (
     "moe_expert_down_fp8_payload", "moe_combine_fp8", "moe_ep_plan", "moe_gather_rows",
     "moe_route_scored", "moe_route_scored_backward", "moe_adapter_workspace_size", "moe_adapter_project",
     "moe_adapter_project_backward", "moe_expert_project", "moe_expert_project_backward", "moe_checkpoint_rows",
-    "moe_swiglu_checkpoint", "moe_swiglu_backward", "moe_combine_backward",
+    "moe_swiglu_checkpoint", "moe_swiglu_backward", "moe_combine_backward", "moe_debug_project_plan",
 )
 
 # router scores and group scores of moe_route_scored
@@ -55,6 +55,11 @@ MOE_GROUP_TOP2 = 1
 MOE_OUT_BF16 = 0
 MOE_OUT_F32 = 1
 MOE_OUT_F32_ADD = 2
+
+# what moe_debug_project_plan is asked for (MOE_PLAN_* in include/moe.h)
+MOE_PLAN_DX = 1
+MOE_PLAN_DW = 2
+MOE_PLAN_ROWS8 = 4
 
 # columns per scale of the E4M3 combine payload and of activations kept in 8 bits (MOE_PAYLOAD_BLOCK in include/moe.h)
 MOE_PAYLOAD_BLOCK = 128
@@ -123,6 +128,7 @@ _SIG = {
     "moe_adapter_project_backward": (_I, [_P, _I] + [_P] * 12 + [_Z, _P]),
     "moe_expert_project": (_I, [_P, _I] + [_P] * 5 + [_I, _P]),
     "moe_expert_project_backward": (_I, [_P, _I] + [_P] * 8 + [_I, _P, _P, _I, _P]),
+    "moe_debug_project_plan": (_I, [_P, _I, _I, _P]),
     "moe_checkpoint_rows": (_I, [_I, _I] + [_P] * 4),
     "moe_swiglu_checkpoint": (_I, [_I, _I] + [_P] * 5),
     "moe_swiglu_backward": (_I, [_I, _I] + [_P] * 6),
@@ -482,6 +488,13 @@ def moe_expert_project_backward(project, rows, dy, x, x8, x8_scale, offsets, w, 
         _offsets(offsets, S), _dense(w, "w", (S, N, K), bf16), _dense(w2, "w2", (S, N, K), bf16),
         _dense(dx, "dx", (rows, K), f32 if x_kind else bf16), x_kind, _dense(dw, "dw", (S, N, K), w_type),
         _dense(dw2, "dw2", (S, N, K), w_type), w_kind, _stream(stream)))
+
+
+def moe_debug_project_plan(project, rows, outputs=0):
+    """For tests: (pairs that share a sum of y or dx, of dw, one launch, twice as high tiles of dw) of such a call."""
+    plan = (ctypes.c_int32 * 4)()
+    _check(lib().moe_debug_project_plan(ctypes.byref(project), rows, outputs, ctypes.addressof(plan)))
+    return tuple(plan)
 
 
 def moe_checkpoint_rows(rows, cols, x, codes, scale, stream=None):

@@ -1126,10 +1126,24 @@ int out_map(CUtensorMap* map, void* out, uint64_t d0, uint64_t d1, uint64_t d2, 
                                 : make_tmap_f32(map, out, d0, d1, d2, 32, box1, box2);
 }
 
-// y or dx; *tiles: as many as there may be
+// Tiles of y or dx (as many as there may be), the rows of a chunk at most, 64-wide chunks of a sum.
+struct RowsPlan {
+    long tiles;
+    int cap, chunks;
+};
+template <bool DX>
+RowsPlan rows_plan(const moe_project_t* p, int rows) {
+    // Where there is about a tile for each pair, what counts is how soon its chunks are there: lower ones,
+    // of which more fit the ring, where slots have few rows (400 rows of 16 slots, gate and up of 600 to
+    // 328: 6.8 us with 256 rows, 6.5 with 64).
+    const long m_tiles = ((DX ? p->in_features : p->out_features) + 255L) / 256 * (DX ? 1 : p->n_parts), used = std::min(rows, p->n_slots);
+    const int cap = m_tiles * used > most_pairs() ? 256 : rows <= 48 * used ? 64 : rows <= 96 * used ? 128 : 256;
+    return {m_tiles * (rows / cap + used), cap, DX ? (p->out_features + 63) / 64 * p->n_parts : (p->in_features + 63) / 64};
+}
+
 template <bool DX>
 int rows_args(const moe_project_t* p, int rows, const void* in, const int32_t* offsets, const void* w, const void* w2, void* out, int type,
-              const DevStatus& st, RowsArgs& a, long* tiles) {
+              const DevStatus& st, int cap, int splits, RowsArgs& a) {
     const uint64_t K = p->in_features, N = p->out_features, S = p->n_slots, P = p->n_parts, R = rows;
     int rc = make_tmap_3d(&a.w[0], w, K, N, S, K * 2, K * N * 2, 64, DX ? 64 : 128, 1);
     if (rc) return rc;
@@ -1148,14 +1162,9 @@ int rows_args(const moe_project_t* p, int rows, const void* in, const int32_t* o
     a.S = p->n_slots;
     a.type = type;
     a.st = st;
-    // Where there is about a tile for each pair, what counts is how soon its chunks are there: lower ones,
-    // of which more fit the ring, where slots have few rows (400 rows of 16 slots, gate and up of 600 to
-    // 328: 6.8 us with 256 rows, 6.5 with 64).
-    const long m_tiles = (long)((O + 255) / 256 * OP), used = std::min(rows, p->n_slots);
-    a.cap = m_tiles * used > most_pairs() ? 256 : rows <= 48 * used ? 64 : rows <= 96 * used ? 128 : 256;
+    a.cap = cap;
     a.stages = a.cap == 64 ? kMostStages : a.cap == 128 ? 8 : 6;
-    *tiles = m_tiles * (rows / a.cap + used);
-    a.splits = 1;
+    a.splits = splits;
     return MOE_OK;
 }
 
@@ -1180,16 +1189,15 @@ int chunks_of_slot(int rows, int slots) {
 }
 
 template <bool DX>
-int launch_rows(RowsArgs& a, long tiles, cudaStream_t stream) {
+int launch_rows(const RowsArgs& a, long tiles, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
-    a.splits = splits_of(DX ? (a.N + 63) / 64 * a.P : (a.K + 63) / 64, tiles, 16);
     return launch_pairs(rows_kernel<DX>, configured, kRowsThreads, kRowsSmem, a.splits > 1 ? tiles * a.splits : std::min(tiles, most_pairs()),
                         a.splits, stream, a, DX ? "expert gradient" : "expert projection");
 }
 
 template <bool X8>
 int weight_args(const moe_project_t* p, int rows, const void* dy, const void* x, const float* scale, const int32_t* offsets, void* dw,
-                void* dw2, int type, const DevStatus& st, WeightArgs& a) {
+                void* dw2, int type, const DevStatus& st, int n_tiles, int splits, WeightArgs& a) {
     const uint64_t K = p->in_features, N = p->out_features, S = p->n_slots, P = p->n_parts, R = rows;
     int rc;
     for (int j = 0; j < 3; ++j)
@@ -1213,8 +1221,8 @@ int weight_args(const moe_project_t* p, int rows, const void* dy, const void* x,
     a.st = st;
     a.out_ptr[0] = dw;
     a.out_ptr[1] = dw2;
-    a.n_tiles = (int)((K + 255) / 256 * ((N + 255) / 256) * P * S);
-    a.splits = 1;
+    a.n_tiles = n_tiles;
+    a.splits = splits;
     return MOE_OK;
 }
 
@@ -1226,29 +1234,13 @@ int launch_weights(const WeightArgs& a, cudaStream_t stream) {
                         "expert weight gradient");
 }
 
-template <bool X8>
-int launch_weights(WeightArgs& a, cudaStream_t stream) {
-    // Twice 256 of N where that leaves every pair several tiles and, rows in bf16, where a slot has many
-    // rows: the products of a tile hide the drain of one accumulator, not of the first of two (16 slots,
-    // gate and up of 7168 to 2048: 128 rows a slot 163 us with 256 and 167 with twice that, 256 both 226,
-    // 512 396 and 329; codes, which are turned half as often, 187 and 171, 266 and 244, 447 and 428.  16
-    // slots of 1024 to 1024, 512 rows each: 19.1 and 21.1).
-    const long tiles = (long)((a.K + 255) / 256) * ((a.N + 511) / 512) * a.P * a.S;
-    if (tiles >= 4 * most_pairs() && (X8 || a.R >= 384L * a.S)) {
-        a.n_tiles = (int)tiles;
-        return launch_weights<X8, true, false>(a, stream);
-    }
-    a.splits = splits_of(chunks_of_slot(a.R, a.S), a.n_tiles, 24);
-    return a.splits > 1 ? launch_weights<X8, false, true>(a, stream) : launch_weights<X8, false, false>(a, stream);
-}
-
-// How dx and dW share the pairs of one launch: what they cost, in cycles, is 600 a tile and, for each
-// chunk of its sum, of dx 2 for each row and 400 at least, of dW 512, or the turning of its codes, and a
-// tile's drain at least, of dx 10 for each row, of dW 2400; sharing a sum costs 2300 and 5500.  Slots are not equal, so the pairs' last tiles count by
-// half.  The plan is the one that ends first, and of those that end together the one that does the other
-// part sooner.  (In place of pairs by the sums of the costs, and dW never shared: 10062 rows, 144 to 248
-// features of 3 slots, gate and up, codes, 52 us and 21 so; 56 rows, 424 to 2856 of 7 slots, 27 and 16; 26
-// rows, 112 to 6064 of 29 slots, 52 both; 2771 rows, 504 to 3672 of 2 slots, 57 and 61.)
+// How dx and dW share the pairs of one launch: what they cost, in cycles, is 600 a tile and, for each chunk of its
+// sum, of dx 2 for each row and 400 at least, of dW 512, or the turning of its codes, and a tile's drain at least,
+// of dx 10 for each row, of dW 2400; sharing a sum costs 2300 and 5500.  Slots are not equal, so the pairs' last
+// tiles count by half.  The plan is the one that ends first, and of those that end together the one that does the
+// other part sooner.  (In place of pairs by the sums of the costs, and dW never shared: 10062 rows, 144 to 248
+// features of 3 slots, gate and up, codes, 52 us and 21 so; 56 rows, 424 to 2856 of 7 slots, 27 and 16; 26 rows,
+// 112 to 6064 of 29 slots, 52 both; 2771 rows, 504 to 3672 of 2 slots, 57 and 61.)
 struct Work {
     int tiles, chunks, chunk, least, join;
     int64_t time(int pairs, int splits) const {
@@ -1288,6 +1280,45 @@ Plan best_plan(const Work& x, const Work& w) {
     return best;
 }
 
+// How a backward pass runs: dx and dW in one launch (`one`), dW in tiles of twice 256 of N (`tall`), how many pairs
+// share a sum.
+struct BackwardPlan {
+    RowsPlan rows;
+    int w_tiles;
+    bool one, tall;
+    Plan plan;
+};
+BackwardPlan backward_plan(const moe_project_t* p, int rows, bool dx, bool dw, bool x8) {
+    BackwardPlan b{rows_plan<true>(p, rows), 0, false, false, {0, 0, 1, 1, 0}};
+    auto tiles = [&](int height) { return (p->in_features + 255L) / 256 * ((p->out_features + height - 1) / height) * p->n_parts * p->n_slots; };
+    b.w_tiles = (int)tiles(256);
+    const int w_chunks = chunks_of_slot(rows, p->n_slots);
+    // Both in one launch up to a few tiles a pair.  (100 rows, 328 to 600 features of 16 slots, a tile or
+    // two a pair, 12.2 us one after the other and 8.3 beside each other; 8000 rows, 2048 to 1024 of 16
+    // slots, 12 tiles, 65 and 55; 4096 rows, 2048 to 7168 of 32 slots, a hundred, 332 and 383: there one
+    // reads memory and the other writes it, and each takes all the pairs.)
+    if (dx && dw && b.rows.tiles + b.w_tiles <= kBothTiles * most_pairs() && most_pairs() > 1) {
+        const int used = std::min(rows, p->n_slots), each = (rows + used - 1) / used, height = std::min(b.rows.cap, each);
+        // (dx's tiles: as many as there may be; chunks of dW: of equal slots)
+        Work x{(int)b.rows.tiles, b.rows.chunks, std::max(400, 2 * height), 10 * height, 2300};
+        Work w{b.w_tiles, w_chunks, x8 ? 900 : 512, 2400, 5500};
+        b.one = true;
+        b.plan = best_plan(x, w);
+        return b;
+    }
+    if (dx) b.plan.x_splits = splits_of(b.rows.chunks, b.rows.tiles, 16);
+    if (!dw) return b;
+    // Twice 256 of N where that leaves every pair several tiles and, rows in bf16, where a slot has many
+    // rows: the products of a tile hide the drain of one accumulator, not of the first of two (16 slots,
+    // gate and up of 7168 to 2048: 128 rows a slot 163 us with 256 and 167 with twice that, 256 both 226,
+    // 512 396 and 329; codes, which are turned half as often, 187 and 171, 266 and 244, 447 and 428.  16
+    // slots of 1024 to 1024, 512 rows each: 19.1 and 21.1).
+    b.tall = tiles(512) >= 4 * most_pairs() && (x8 || rows >= 384L * p->n_slots);
+    if (b.tall) b.w_tiles = (int)tiles(512);
+    else b.plan.w_splits = splits_of(w_chunks, b.w_tiles, 24);
+    return b;
+}
+
 template <bool X8, bool SHARED>
 int launch_both(const BothArgs& a, const Plan& plan, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
@@ -1298,29 +1329,19 @@ int launch_both(const BothArgs& a, const Plan& plan, cudaStream_t stream) {
 template <bool X8>
 int gradients(const moe_project_t* p, int rows, const void* dy, const void* x, const float* scale, const int32_t* offsets, const void* w,
               const void* w2, void* dx, int dx_type, void* dw, void* dw2, int dw_type, const DevStatus& st, cudaStream_t stream) {
+    const BackwardPlan b = backward_plan(p, rows, dx, dw, X8);
     BothArgs a;
-    long dx_tiles = 0;
     int rc;
-    if (dx && (rc = rows_args<true>(p, rows, dy, offsets, w, w2, dx, dx_type, st, a.dx, &dx_tiles))) return rc;
-    if (dw && (rc = weight_args<X8>(p, rows, dy, x, scale, offsets, dw, dw2, dw_type, st, a.dw))) return rc;
-    // Both in one launch up to a few tiles a pair.  (100 rows, 328 to 600 features of 16 slots, a tile or
-    // two a pair, 12.2 us one after the other and 8.3 beside each other; 8000 rows, 2048 to 1024 of 16
-    // slots, 12 tiles, 65 and 55; 4096 rows, 2048 to 7168 of 32 slots, a hundred, 332 and 383: there one
-    // reads memory and the other writes it, and each takes all the pairs.)
-    if (dx && dw && dx_tiles + a.dw.n_tiles <= kBothTiles * most_pairs() && most_pairs() > 1) {
-        const int used = std::min(rows, p->n_slots), each = (rows + used - 1) / used, dx_most = (int)dx_tiles;
-        const int height = std::min(a.dx.cap, each);
-        // (dx's tiles: as many as there may be; chunks of dW: of equal slots)
-        Work x{dx_most, a.dx.P * ((a.dx.N + 63) / 64), std::max(400, 2 * height), 10 * height, 2300};
-        Work w{a.dw.n_tiles, chunks_of_slot(rows, p->n_slots), X8 ? 900 : 512, 2400, 5500};
-        const Plan plan = best_plan(x, w);
-        a.dx.splits = plan.x_splits;
-        a.dw.splits = plan.w_splits;
-        a.dx_pairs = plan.x_pairs;
-        return plan.w_splits > 1 ? launch_both<X8, true>(a, plan, stream) : launch_both<X8, false>(a, plan, stream);
+    if (dx && (rc = rows_args<true>(p, rows, dy, offsets, w, w2, dx, dx_type, st, b.rows.cap, b.plan.x_splits, a.dx))) return rc;
+    if (dw && (rc = weight_args<X8>(p, rows, dy, x, scale, offsets, dw, dw2, dw_type, st, b.w_tiles, b.plan.w_splits, a.dw))) return rc;
+    if (b.one) {
+        a.dx_pairs = b.plan.x_pairs;
+        return b.plan.w_splits > 1 ? launch_both<X8, true>(a, b.plan, stream) : launch_both<X8, false>(a, b.plan, stream);
     }
-    if (dx && (rc = launch_rows<true>(a.dx, dx_tiles, stream))) return rc;
-    return dw ? launch_weights<X8>(a.dw, stream) : MOE_OK;
+    if (dx && (rc = launch_rows<true>(a.dx, b.rows.tiles, stream))) return rc;
+    if (!dw) return MOE_OK;
+    if (b.tall) return launch_weights<X8, true, false>(a.dw, stream);
+    return b.plan.w_splits > 1 ? launch_weights<X8, false, true>(a.dw, stream) : launch_weights<X8, false, false>(a.dw, stream);
 }
 
 }  // namespace
@@ -1341,10 +1362,11 @@ int moe_expert_project(const moe_project_t* project, int rows, const void* x, co
     PdlScope pdl(rows);
     DevStatus st;
     if ((rc = api_device_status(&st))) return rc;
+    const RowsPlan plan = rows_plan<false>(project, rows);
     RowsArgs a;
-    long tiles;
-    if ((rc = rows_args<false>(project, rows, x, offsets, w, w2, out, out_type, st, a, &tiles))) return rc;
-    return launch_rows<false>(a, tiles, reinterpret_cast<cudaStream_t>(stream));
+    if ((rc = rows_args<false>(project, rows, x, offsets, w, w2, out, out_type, st, plan.cap, splits_of(plan.chunks, plan.tiles, 16), a)))
+        return rc;
+    return launch_rows<false>(a, plan.tiles, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int moe_expert_project_backward(const moe_project_t* project, int rows, const void* dy, const void* x, const uint8_t* x8,
@@ -1375,6 +1397,25 @@ int moe_expert_project_backward(const moe_project_t* project, int rows, const vo
     if ((rc = api_device_status(&st))) return rc;
     return x8 ? gradients<true>(project, rows, dy, x8, x8_scale, offsets, w, w2, dx, dx_type, dw, dw2, dw_type, st, s)
               : gradients<false>(project, rows, dy, x, nullptr, offsets, w, w2, dx, dx_type, dw, dw2, dw_type, st, s);
+}
+
+int moe_debug_project_plan(const moe_project_t* project, int rows, int outputs, int32_t* plan) {
+    const int rc = check_project(project, rows);
+    if (rc) return rc;
+    if (rows == 0 || outputs < 0 || outputs > 7 || outputs == MOE_PLAN_ROWS8 || !plan)
+        return api_fail(MOE_ERR_INVALID_ARG, "rows > 0, MOE_PLAN_* of an output, and plan required");
+    if (outputs == 0) {
+        const RowsPlan y = rows_plan<false>(project, rows);
+        plan[0] = splits_of(y.chunks, y.tiles, 16);
+        plan[1] = plan[2] = plan[3] = 0;
+        return MOE_OK;
+    }
+    const BackwardPlan b = backward_plan(project, rows, outputs & MOE_PLAN_DX, outputs & MOE_PLAN_DW, outputs & MOE_PLAN_ROWS8);
+    plan[0] = outputs & MOE_PLAN_DX ? b.plan.x_splits : 0;
+    plan[1] = outputs & MOE_PLAN_DW ? b.plan.w_splits : 0;
+    plan[2] = b.one;
+    plan[3] = b.tall;
+    return MOE_OK;
 }
 
 }  // extern "C"

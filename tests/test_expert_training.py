@@ -134,7 +134,8 @@ def test_many_rows_of_a_slot_and_many_slots(R, K, N, S, P):
         close(got[1][p], dw[0][p], dw[1][p], name=f"dw{p}")
 
 
-# few tiles of a long contraction, which pairs of CTAs share (16 chunks of 64 and more for two, 32 for four)
+# few tiles of a long contraction, which pairs of CTAs share (from 16 chunks of 64 on: four, or two where there are more
+# tiles; test_expert_training_pairs.py asks for the plan of each call)
 @pytest.mark.gpu
 @pytest.mark.parametrize("R", [1, 5, 70, 300])
 @pytest.mark.parametrize("K,N,S,P", [(2056, 136, 1, 1), (4104, 264, 2, 2), (1032, 8, 3, 1), (136, 2056, 2, 1), (264, 1544, 1, 2), (8, 4104, 3, 2)])
