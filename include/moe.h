@@ -601,6 +601,7 @@ MOE_API int moe_debug_project_plan(const moe_project_t* project, int rows, int o
  * moe_swiglu_backward: with g and u the kept values, s = sigmoid(g) and dh [rows,inter] bf16,
  *   d_gate_up[:, :inter] = dh * u * s * (1 + g * (1 - s)),  d_gate_up[:, inter:] = dh * g * s,
  *   h [rows,inter] (NULL to skip) = bf16( g * s * u ), what the down projection's dw multiplies.
+ * A sigmoid below 2^-126 (gates from about -88 down) counts as 0.
  * cols and inter: multiples of 8. */
 MOE_API int moe_checkpoint_rows(int rows, int cols, const void* x, uint8_t* codes, float* scale, void* stream);
 MOE_API int moe_swiglu_checkpoint(int rows, int inter, const void* gate_up, void* h, uint8_t* codes, float* scale,

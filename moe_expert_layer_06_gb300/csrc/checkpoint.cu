@@ -226,7 +226,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t
         const float s = sigmoid(g[j]), silu = g[j] * s;
         act[j] = silu * u[j];
         du[j] = up * silu;
-        dg[j] = up * u[j] * (s * fmaf(g[j], 1.0f - s, 1.0f));
+        // (u times what is 1.1 at most stays below fp32's largest, as a kept u is 448 * 2^119 at most: no product
+        // overflows but the result's own)
+        dg[j] = up * (u[j] * (s * fmaf(g[j], 1.0f - s, 1.0f)));
     }
     uint16_t* out = d_gate_up + p.gate;
     *reinterpret_cast<uint4*>(out) =

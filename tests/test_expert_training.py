@@ -4,9 +4,10 @@ in 8 bits, SwiGLU on them, the combine's gradient) against their definitions in 
 Tolerances, element by element.  An output rounds once (bf16: half a step, 2^-8 of its value; fp32:
 2^-24); an fp32 sum of n products is off by at most n steps of 2^-23 of the sum of their magnitudes
 (2^-24 for a rounded sum; twice that where a tensor core truncates).  Codes and scales are equal.
-SwiGLU: __expf is off by 2 + 1.173 |g| steps of 2^-23; up to |g| = 70 (beyond, what it gives is below
-the 1e-30 that every comparison allows) that is 84 of them, and the division and the few products
-beside it add less than 10: 2^-16 of the factors in all."""
+SwiGLU: the sigmoid is 1 / (1 + 2^(-g log2 e)).  log2 e and its product with g are rounded, 2^-24 each of up to
+70 * 1.45 (beyond |g| = 70 what it gives is below the 1e-30 that every comparison allows): 71 steps of 2^-23 of
+the power; ex2.approx adds 2, the sum half of one, rcp.approx 1 and the few products beside it less than 10:
+2^-16 (128 steps) of the factors in all."""
 import ctypes
 
 import numpy as np
