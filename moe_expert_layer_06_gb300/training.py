@@ -11,8 +11,11 @@
 Between the passes `Buffers` keeps, for each of a token's k rows, the dispatched row and gate and up in
 8 bits (with a power of two for each 128 columns) and the expert's output in bf16; for each token the
 shared gate and up in 8 bits; and the routing.  h is computed again from what was kept.  The other
-buffers are scratch, which layers may share.  Everything runs on one stream without host
-synchronisation and may be captured in a CUDA graph.
+buffers are scratch, which layers may share.  A pass runs on one stream, the current one or `stream`,
+without host synchronisation, and may be captured in a CUDA graph.  Buffers may be made on another
+stream than the passes run on (they are ready when they are made); who changes the stream between a
+layer's passes orders the two, and who drops Buffers waits for the passes or records the stream, as for
+any tensor.
 
 The products are of bf16 operands with fp32 sums; the gradient of the logits is rounded to bf16 once
 for the router's products.  The routing's selection has no gradient, nor has select_bias.
@@ -60,6 +63,8 @@ class Buffers:
         self.ones = torch.ones((T, s.top_k), device=device)
         self.all_tokens = torch.tensor([0, T], dtype=i32, device=device)  # offsets of the one slot of dense products
         self.ws = new(u8, max(moe_route_workspace_size(s, T), moe_dispatch_workspace_size(s, T), 16))
+        # ones and all_tokens are filled, and what held this memory before is over, whatever stream reads them first
+        torch.cuda.current_stream(self.ws.device).synchronize()
 
 
 def _check(s: Shape, buffers: Buffers, T: int):
