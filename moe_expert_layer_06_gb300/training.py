@@ -10,7 +10,10 @@
 
 Between the passes `Buffers` keeps, for each of a token's k rows, the dispatched row and gate and up in
 8 bits (with a power of two for each 128 columns) and the expert's output in bf16; for each token the
-shared gate and up in 8 bits; and the routing.  h is computed again from what was kept.  The other
+shared gate and up in 8 bits; and the routing.  h is computed again from what was kept.  With
+keep_rows=False the dispatched rows are not kept but gathered again from x, which layer_backward takes
+anyway: k * hidden bytes a token less between the passes, for a scratch of twice as many, and the gate's and up's
+gradients are of the rows themselves instead of rows rounded to 8 bits.  The other
 buffers are scratch, which layers may share.  A pass runs on one stream, the current one or `stream`,
 without host synchronisation, and may be captured in a CUDA graph.  Buffers may be made on another
 stream than the passes run on (they are ready when they are made); who changes the stream between a
@@ -22,21 +25,32 @@ for the router's products.  The routing's selection has no gradient, nor has sel
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (MOE_PAYLOAD_BLOCK, Project, Shape, moe_checkpoint_rows, moe_combine, moe_combine_backward, moe_dispatch,
-               moe_dispatch_workspace_size, moe_expert_project, moe_expert_project_backward, moe_route_scored,
-               moe_route_scored_backward, moe_route_workspace_size, moe_swiglu_backward, moe_swiglu_checkpoint)
+               moe_dispatch_workspace_size, moe_expert_project, moe_expert_project_backward, moe_gather_rows,
+               moe_route_scored, moe_route_scored_backward, moe_route_workspace_size, moe_swiglu_backward,
+               moe_swiglu_checkpoint)
 
 
 def _blocks(cols: int) -> int:
     return -(-cols // MOE_PAYLOAD_BLOCK)
 
 
-class Buffers:
-    """What layer_forward leaves for layer_backward, and their scratch, for batches of T tokens."""
+def _on(stream):
+    """The context in which torch's own operations run on `stream`."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
 
-    def __init__(self, shape, T: int, device="cuda"):
+
+class Buffers:
+    """What layer_forward leaves for layer_backward, and their scratch, for batches of T tokens.
+    keep_rows: whether the dispatched rows are kept (in 8 bits), or gathered again from x."""
+
+    def __init__(self, shape, T: int, device="cuda", keep_rows=True):
         s = Shape.of(shape)
         n, H, I, Is = T * s.top_k, s.hidden, s.inter, s.n_shared * s.inter_shared
         new = lambda dtype, *size: torch.empty(size, dtype=dtype, device=device)  # noqa: E731
@@ -46,12 +60,13 @@ class Buffers:
         self.logits, self.topk_idx, self.topk_w = new(f32, T, s.n_experts), new(i32, T, s.top_k), new(f32, T, s.top_k)
         self.slot_of, self.perm, self.inv_perm = (new(i32, n) for _ in range(3))
         self.counts, self.offsets, self.blocks = new(i32, s.n_slots + 1), new(i32, s.n_slots + 2), new(i32, s.n_blocks)
-        self.x8, self.x8_scale = new(u8, n, H), new(f32, n, _blocks(H))
+        self.x8, self.x8_scale = (new(u8, n, H), new(f32, n, _blocks(H))) if keep_rows else (None, None)
         self.act8, self.act8_scale = new(u8, n, 2 * I), new(f32, n, 2 * _blocks(I))
         self.y_disp = new(bf16, n, H)
         if Is:
             self.shared8, self.shared8_scale = new(u8, T, 2 * Is), new(f32, T, 2 * _blocks(Is))
         # scratch
+        self.token_of, self.x_rows = (None, None) if keep_rows else (new(i32, n), new(bf16, n, H))
         self.rows = new(bf16, n, H)           # x_disp; dy_disp; dx_disp
         self.gate_up = new(bf16, n, 2 * I)    # and its gradient
         self.h, self.dh = new(bf16, n, I), new(bf16, n, I)
@@ -86,7 +101,8 @@ def layer_forward(shape, router, T: int, x, w_router, select_bias, w_gate, w_up,
     moe_route_scored(s, router, T, x, w_router, select_bias, None, b.logits, b.topk_idx, b.topk_w, b.ws, stream=stream)
     moe_dispatch(s, T, x, b.topk_idx, None, b.slot_of, b.counts, b.blocks, b.offsets, b.perm, b.inv_perm, b.rows, b.ws,
                  stream=stream)
-    moe_checkpoint_rows(n, H, b.rows, b.x8, b.x8_scale, stream=stream)
+    if b.x8 is not None:
+        moe_checkpoint_rows(n, H, b.rows, b.x8, b.x8_scale, stream=stream)
     moe_expert_project(Project(H, I, s.n_slots, 2), n, b.rows, b.offsets, w_gate, w_up, b.gate_up, stream=stream)
     moe_swiglu_checkpoint(n, I, b.gate_up, b.h, b.act8, b.act8_scale, stream=stream)
     moe_expert_project(Project(I, H, s.n_slots), n, b.h, b.offsets, w_down, None, b.y_disp, stream=stream)
@@ -101,8 +117,8 @@ def layer_forward(shape, router, T: int, x, w_router, select_bias, w_gate, w_up,
 
 def layer_backward(shape, router, T: int, d_out, x, w_router, w_gate, w_up, w_down, ws_gate, ws_up, w_shared_down, dx, d_w_router,
                    d_w_gate, d_w_up, d_w_down, d_ws_gate, d_ws_up, d_w_shared_down, buffers: Buffers, add=False, stream=None):
-    """Gradients of layer_forward's last call on these buffers: dx [T, H] bf16, and every weight's as the
-    weight (bf16 or fp32; with add, fp32 values that they are added to)."""
+    """Gradients of layer_forward's last call on these buffers, with the same x: dx [T, H] bf16, and every weight's as
+    the weight (bf16 or fp32; with add, fp32 values that they are added to)."""
     s, b = Shape.of(shape), buffers
     _check(s, b, T)
     n, H, I, E, Is = T * s.top_k, s.hidden, s.inter, s.n_experts, s.n_shared * s.inter_shared
@@ -112,15 +128,16 @@ def layer_backward(shape, router, T: int, d_out, x, w_router, w_gate, w_up, w_do
     moe_expert_project_backward(down, n, b.rows, None, None, None, b.offsets, w_down, None, b.dh, None, stream=stream)
     moe_swiglu_backward(n, I, b.act8, b.act8_scale, b.dh, b.gate_up, b.h, stream=stream)
     moe_expert_project_backward(down, n, b.rows, b.h, None, None, b.offsets, None, None, None, d_w_down, add_dw=add, stream=stream)
-    moe_expert_project_backward(gate_up, n, b.gate_up, None, b.x8, b.x8_scale, b.offsets, w_gate, w_up, b.rows, d_w_gate, d_w_up,
+    if b.x8 is None and n:
+        with _on(stream):
+            torch.floor_divide(b.perm, s.top_k, out=b.token_of)
+        moe_gather_rows(x, b.token_of, b.x_rows, stream=stream)
+    moe_expert_project_backward(gate_up, n, b.gate_up, b.x_rows, b.x8, b.x8_scale, b.offsets, w_gate, w_up, b.rows, d_w_gate, d_w_up,
                                 add_dw=add, stream=stream)
     # router
     moe_route_scored_backward(s, router, T, b.logits, b.topk_idx, b.d_topk_w, b.d_logits, stream=stream)
-    if stream is None:
+    with _on(stream):
         b.d_logits16.copy_(b.d_logits)
-    else:
-        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)):
-            b.d_logits16.copy_(b.d_logits)
     moe_expert_project_backward(logits, T, b.d_logits16, x, None, None, b.all_tokens, w_router.view(1, E, H), None, b.x32,
                                 d_w_router.view(1, E, H), add_dw=add, stream=stream)
     # shared experts: their dx is added to the router's
