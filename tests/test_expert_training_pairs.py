@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import moe_expert_layer_06_gb300 as m
-from test_expert_training import BF, F32, Case, close
+from test_expert_training import BF, F32, HALF, STEP, Case, close, ragged
 
 
 def slots_of(c):
@@ -103,7 +103,7 @@ def test_every_plan_of_shared_sums(sizes, outputs, plan):
         out = torch.full((c.R, c.P * c.N), 2.0, device="cuda")
         c.forward(F32, add=True, out=out)
         there = ~torch.isnan(y[0])
-        close(out, torch.where(there, y[0] + 2.0, 2.0), torch.where(there, y[1] + 2.0 ** -23 * (y[0].abs() + 2.0), 0.0), name="y added")
+        close(out, torch.where(there, y[0] + 2.0, 2.0), torch.where(there, y[1] + STEP * (y[0].abs() + 2.0), 0.0), name="y added")
         assert torch.equal(c.forward().nan_to_num(9.0), c.forward().nan_to_num(9.0))
         assert m.moe_check_status() == 0
         return
@@ -120,9 +120,9 @@ def test_every_plan_of_shared_sums(sizes, outputs, plan):
     got = c.backward(want_x, want_w, F32, F32, eight, want_x, want_w, fill=1.0)
     if want_x:
         there = ~torch.isnan(dx[0])
-        close(got[0], torch.where(there, dx[0] + 1.0, 1.0), torch.where(there, dx[1] + 2.0 ** -23 * (dx[0].abs() + 1.0), 0.0), name="dx added")
+        close(got[0], torch.where(there, dx[0] + 1.0, 1.0), torch.where(there, dx[1] + STEP * (dx[0].abs() + 1.0), 0.0), name="dx added")
     for p in range(c.P if want_w else 0):
-        close(got[1][p], dw[0][p] + 1.0, dw[1][p] + 2.0 ** -23 * (dw[0][p].abs() + 1.0), name=f"dw{p} added")
+        close(got[1][p], dw[0][p] + 1.0, dw[1][p] + STEP * (dw[0][p].abs() + 1.0), name=f"dw{p} added")
     assert m.moe_check_status() == 0
 
 
@@ -222,3 +222,67 @@ def test_a_limit_of_the_waits_below_the_time_of_a_call():
     finally:
         m.moe_set_wait_limit_ns(2_000_000_000)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [37, 4096, 12321])
+def test_products_at_the_width_of_a_large_layer(R):
+    """7168 to gate and up of 2048 for 32 slots, 2048 to 7168 for the way back: slots with the most and the fewest rows and one
+    without any, all of their outputs against fp64."""
+    S, H, I = 32, 7168, 2048
+    off = ragged(R, S, seed=40)
+    counts = np.diff(off)
+    some = counts > 0
+    look = {int(np.argmax(counts)), int(np.argmin(np.where(some, counts, R + 1))), int(np.argmin(counts))}
+    g = torch.Generator(device="cuda").manual_seed(R)
+    for K, N, P in ((H, I, 2), (I, H, 1)):
+        new = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(BF)  # noqa: E731
+        p, offsets = m.Project(K, N, S, P), torch.from_numpy(off).cuda()
+        x, dy, w = new(R, K), new(R, P * N), [new(S, N, K, std=K ** -0.5) for _ in range(P)]
+        codes, scale = torch.empty(R, K, dtype=torch.uint8, device="cuda"), torch.empty(R, K // 128, device="cuda")
+        m.moe_checkpoint_rows(R, K, x, codes, scale)
+        kept = (codes.view(torch.float8_e4m3fn).float() * scale.repeat_interleave(128, 1)).to(BF)
+        y, dx = torch.empty(R, P * N, dtype=BF, device="cuda"), torch.empty(R, K, dtype=BF, device="cuda")
+        dw, dw8 = ([torch.full((S, N, K), float("nan"), dtype=BF, device="cuda") for _ in range(P)] for _ in range(2))
+        m.moe_expert_project(p, R, x, offsets, *(w + [None])[:2], y)
+        m.moe_expert_project_backward(p, R, dy, x, None, None, offsets, *(w + [None])[:2], dx, *dw)
+        m.moe_expert_project_backward(p, R, dy, None, codes, scale, offsets, None, None, None, *dw8)
+        assert m.moe_check_status() == 0
+
+        def near(got, want, tol):
+            assert bool(((got.double() - want).abs() <= tol + HALF * (want.abs() + tol) + 1e-30).all())
+
+        for s in look:
+            rows, n = slice(int(off[s]), int(off[s + 1])), int(counts[s])
+            a, want, bound = x[rows].double(), 0.0, 0.0
+            for q in range(P):
+                cols, ws, d = slice(q * N, (q + 1) * N), w[q][s].double(), dy[rows, q * N:(q + 1) * N].double()
+                near(y[rows, cols], a @ ws.t(), K * STEP * (a.abs() @ ws.abs().t()))
+                want, bound = want + d @ ws, bound + P * N * STEP * (d.abs() @ ws.abs())
+                for rows_of, got in ((a, dw[q][s]), (kept[rows].double(), dw8[q][s])):
+                    near(got, d.t() @ rows_of, n * STEP * (d.abs().t() @ rows_of.abs()))
+            near(dx[rows], want, bound)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N", [(1 << 24, 8), (8, 1 << 24)])
+def test_the_most_features(K, N):
+    """2^24 on either side: sums of -1, 0 and 1, which are whole numbers below 2^8 and so exact in bf16, too."""
+    R, S = 5, 2
+    g = torch.Generator(device="cuda").manual_seed(K)
+    few = lambda *s: torch.where(torch.rand(*s, generator=g, device="cuda") < 1e-4,  # noqa: E731
+                                 torch.randint(0, 2, s, generator=g, device="cuda") * 2.0 - 1.0, 0.0)
+    many = lambda *s: torch.randint(-1, 2, s, generator=g, device="cuda").float()  # noqa: E731
+    x, dy, w = (few if K > N else many)(R, K), (many if K > N else few)(R, N), many(S, N, K)
+    off = [0, 2, 4]  # (the last row is of no slot)
+    p, offsets = m.Project(K, N, S), torch.tensor(off, dtype=torch.int32, device="cuda")
+    y, dx, dw = (torch.full(s, 7.0, dtype=BF, device="cuda") for s in ((R, N), (R, K), (S, N, K)))
+    m.moe_expert_project(p, R, x.to(BF), offsets, w.to(BF), None, y)
+    m.moe_expert_project_backward(p, R, dy.to(BF), x.to(BF), None, None, offsets, w.to(BF), None, dx, dw)
+    assert m.moe_check_status() == 0
+    for s in range(S):
+        rows = slice(off[s], off[s + 1])
+        for got, a, b in ((y[rows], x[rows], w[s].t()), (dx[rows], dy[rows], w[s]), (dw[s], dy[rows].t(), x[rows])):
+            want = a.double() @ b.double()
+            assert float(want.abs().max()) < 256 and torch.equal(got.double(), want)
+    assert bool((y[4] == 7.0).all()) and bool((dx[4] == 7.0).all())

@@ -97,3 +97,42 @@ def test_gates_over_the_whole_range():
     check(d[:, :8], dd * u * s * (1.0 + g * rest), (dd * u * s).abs() * (1.0 + (g * rest).abs()), "d_gate")
     check(d[:, 8:], dd * g * s, (dd * g * s).abs(), "d_up")
     check(again, g * s * u, (g * s * u).abs(), "h again")
+
+
+def keep_wide(x):
+    """keep() of finite rows, vectorised: the least power of two (from 2^-117 on) that brings a block to 448 at most."""
+    R, C = x.shape
+    nb = -(-C // 128)
+    v = torch.nn.functional.pad(x.double(), (0, nb * 128 - C)).view(R, nb, 128)
+    frac, e = torch.frexp(v.abs().amax(2))  # (448 is 0.875 * 2^9)
+    e = torch.where(frac == 0.0, 0, (e - 9 + (frac > 0.875).int()).clamp(min=-117))
+    scale = torch.ldexp(torch.ones_like(frac), e)
+    q = v / scale[:, :, None]
+    step = torch.ldexp(torch.ones_like(q), (torch.frexp(q)[1] - 1).clamp(min=-6) - 3)
+    return (torch.round(q / step) * step).view(R, nb * 128)[:, :C], scale
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [128 * 4095, 128 * 4095 + 8, 128 * 4096, 128 * 4096 + 8, 128 * 9001 + 72])
+def test_rows_of_many_blocks(C):
+    """Around 4096 blocks a row, where a block's row is found in another way."""
+    R = 3
+    gen = torch.Generator().manual_seed(C)
+    x = (torch.randn(R, C, generator=gen) * torch.exp2(torch.randint(-9, 10, (R, 1), generator=gen).float())).to(BF)
+    want, scales = keep_wide(x)
+    assert torch.equal(keep(x[:, -200:])[1], keep_wide(x[:, -200:])[1]) and torch.equal(keep(x[:, -200:])[0], keep_wide(x[:, -200:])[0])
+    codes, scale = torch.full((R, C), 0x55, dtype=torch.uint8, device="cuda"), torch.full(scales.shape, 5.0, device="cuda")
+    m.moe_checkpoint_rows(R, C, x.cuda(), codes, scale)
+    assert torch.equal(scale.cpu().double(), scales) and torch.equal(codes.cpu().view(torch.float8_e4m3fn).double(), want)
+    up, dh = torch.randn(R, C, generator=gen).to(BF), torch.randn(R, C, generator=gen).to(BF)
+    h, codes, scale, d, again = run(torch.cat([x, up], 1), dh)
+    ku = keep_wide(up)
+    assert torch.equal(scale.cpu().double(), torch.cat([scales, ku[1]], 1))
+    assert torch.equal(codes.cpu().view(torch.float8_e4m3fn).double(), torch.cat([want, ku[0]], 1))
+    g, u = x.double(), up.double()
+    check(h, g * sigmoid(g) * u, (g * sigmoid(g) * u).abs(), "h")
+    g, u = (k[0] * k[1].repeat_interleave(128, 1)[:, :C] for k in ((want, scales), ku))
+    s, rest, dd = sigmoid(g), torch.sigmoid(-g), dh.double()
+    check(d[:, :C], dd * u * s * (1.0 + g * rest), (dd * u * s).abs() * (1.0 + (g * rest).abs()), "d_gate")
+    check(d[:, C:], dd * g * s, (dd * g * s).abs(), "d_up")
+    check(again, g * s * u, (g * s * u).abs(), "h again")
