@@ -540,8 +540,9 @@ MOE_API int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_
 /* ---------------------------------------------------------------- training the experts
  * The expert products by themselves, with their gradients, and the activations
  * between them kept in 8 bits.  A layer's experts forward: moe_expert_project (gate and
- * up as two parts), moe_swiglu_checkpoint, moe_expert_down; backward: moe_combine_backward,
- * moe_expert_project_backward (down), moe_swiglu_backward, moe_expert_project_backward (gate and up);
+ * up as two parts), moe_swiglu_checkpoint, moe_expert_project (down); backward: moe_combine_backward,
+ * moe_expert_project_backward (down: dx), moe_swiglu_backward, moe_expert_project_backward (down: dw, which takes the
+ * h that moe_swiglu_backward gives; then gate and up);
  * moe_expert_layer_06_gb300.training runs the whole layer this way.
  *
  * Rows of slot s are [offsets[s], offsets[s+1]) (moe_dispatch; offsets [n_slots+1] at least, on the
@@ -558,7 +559,8 @@ MOE_API int moe_combine_backward(const moe_shape_t* shape, int T, const void* d_
  * multiple of 16): exactly one of the two.  Products of bf16, sums in fp32, rounded once.
  * out, dx and dw are written as their type says: MOE_OUT_BF16; MOE_OUT_F32; MOE_OUT_F32_ADD adds to
  * the fp32 values that they hold (gradients of several batches, or of several paths to one input).
- * Outputs overlap no input.  Rows of no slot are neither read nor written; a slot without rows gets
+ * Outputs overlap no input.  Rows of no slot are not written, and no result depends on them (they may
+ * be read, as rows are fetched 16 or 32 at a time); a slot without rows gets
  * dw = 0.  An infinity or NaN in a row shows in that row's results and its slot's dw only.  Sums run in
  * an order that the sizes and counts fix: results repeat bit for bit on one GPU model.  rows = 0 writes
  * dw alone.

@@ -23,10 +23,7 @@ constexpr int kGroups = kThreads / kLanes;    // blocks of a CTA side by side
 
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
+__device__ __forceinline__ uint32_t pack_two(float lo, float hi) { return pack_bf(__float_as_uint(lo), __float_as_uint(hi)); }
 
 // |x| of two bf16, infinities and NaN as 0
 __device__ __forceinline__ uint32_t finite_abs(uint32_t w) {
@@ -191,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_keep_kernel(const uint16_t* _
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float a = lo_of(gw[j]), b = hi_of(gw[j]);
-        out[j] = pack_bf(a * sigmoid(a) * lo_of(uw[j]), b * sigmoid(b) * hi_of(uw[j]));
+        out[j] = pack_two(a * sigmoid(a) * lo_of(uw[j]), b * sigmoid(b) * hi_of(uw[j]));
     }
     int eg, eu;
     block_exponents(g, u, eg, eu);
@@ -232,12 +229,12 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const uint8_t
     }
     uint16_t* out = d_gate_up + p.gate;
     *reinterpret_cast<uint4*>(out) =
-        make_uint4(pack_bf(dg[0], dg[1]), pack_bf(dg[2], dg[3]), pack_bf(dg[4], dg[5]), pack_bf(dg[6], dg[7]));
+        make_uint4(pack_two(dg[0], dg[1]), pack_two(dg[2], dg[3]), pack_two(dg[4], dg[5]), pack_two(dg[6], dg[7]));
     *reinterpret_cast<uint4*>(out + inter) =
-        make_uint4(pack_bf(du[0], du[1]), pack_bf(du[2], du[3]), pack_bf(du[4], du[5]), pack_bf(du[6], du[7]));
+        make_uint4(pack_two(du[0], du[1]), pack_two(du[2], du[3]), pack_two(du[4], du[5]), pack_two(du[6], du[7]));
     if (h)
         *reinterpret_cast<uint4*>(h + p.h) =
-            make_uint4(pack_bf(act[0], act[1]), pack_bf(act[2], act[3]), pack_bf(act[4], act[5]), pack_bf(act[6], act[7]));
+            make_uint4(pack_two(act[0], act[1]), pack_two(act[2], act[3]), pack_two(act[4], act[5]), pack_two(act[6], act[7]));
 }
 
 int check_rows(int rows, int cols, const char* name) {
@@ -259,10 +256,6 @@ dim3 grid_of(int rows, Blocks blocks) {
     return dim3((unsigned)(((size_t)rows * blocks.n + kGroups * U - 1) / (kGroups * U)));
 }
 
-int launched(cudaError_t e, const char* what) {
-    return e == cudaSuccess ? MOE_OK : api_fail(MOE_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -276,9 +269,10 @@ int moe_checkpoint_rows(int rows, int cols, const void* x, uint8_t* codes, float
     if ((rc = api_need(x, "x")) || (rc = api_need(codes, "codes")) || (rc = api_need(scale, "scale", 4))) return rc;
     PdlScope pdl(rows);
     const Blocks blocks = blocks_of(cols);
-    return launched(launch_pdl(cols % kBlock ? keep_kernel<4, false> : keep_kernel<4, true>, grid_of<4>(rows, blocks), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream),
-                               static_cast<const uint16_t*>(x), (size_t)rows, cols, blocks, codes, scale),
-                    "checkpoint");
+    return launched(launch_pdl(cols % kBlock ? keep_kernel<4, false> : keep_kernel<4, true>, grid_of<4>(rows, blocks),
+                               dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const uint16_t*>(x),
+                               (size_t)rows, cols, blocks, codes, scale),
+                    "checkpoint launch");
 }
 
 int moe_swiglu_checkpoint(int rows, int inter, const void* gate_up, void* h, uint8_t* codes, float* scale, void* stream) {
@@ -292,7 +286,7 @@ int moe_swiglu_checkpoint(int rows, int inter, const void* gate_up, void* h, uin
     return launched(launch_pdl(swiglu_keep_kernel, grid_of<1>(rows, blocks), dim3(kThreads), 0,
                                reinterpret_cast<cudaStream_t>(stream), static_cast<const uint16_t*>(gate_up), (size_t)rows, inter,
                                blocks, static_cast<uint16_t*>(h), codes, scale),
-                    "SwiGLU");
+                    "SwiGLU launch");
 }
 
 int moe_swiglu_backward(int rows, int inter, const uint8_t* codes, const float* scale, const void* dh, void* d_gate_up, void* h,
@@ -308,7 +302,7 @@ int moe_swiglu_backward(int rows, int inter, const uint8_t* codes, const float* 
     return launched(launch_pdl(swiglu_backward_kernel, grid_of<1>(rows, blocks), dim3(kThreads), 0,
                                reinterpret_cast<cudaStream_t>(stream), codes, scale, static_cast<const uint16_t*>(dh), (size_t)rows,
                                inter, blocks, static_cast<uint16_t*>(d_gate_up), static_cast<uint16_t*>(h)),
-                    "SwiGLU gradient");
+                    "SwiGLU gradient launch");
 }
 
 }  // extern "C"

@@ -52,7 +52,11 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
 }
 
 // 16 bytes of this CTA's shared memory to another CTA's, which a barrier there hears of: a signal that
-// nobody waits for here, and that is sent when what the thread did before is done.
+// nobody waits for here.  The copy itself orders its own 16 bytes and nothing that the thread stored before.
+// What the signal says rests on the proxy fence: rows are stored, each lane ends its stores by
+// fence.proxy.async.shared::cta, __syncwarp has seen every lane past its fence, and only then is the copy issued; the
+// rows are read by the tensor cores through that proxy alone, from the shared memory of the CTA that stored
+// them, never by the threads of the CTA that hears of it.
 __device__ __forceinline__ void signal_by_copy(uint32_t dst, uint32_t src, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst), "r"(src),
                  "r"(bar)
@@ -1101,10 +1105,6 @@ int need_parts(const moe_project_t* p, const void* a, const void* b, const char*
     if (rc) return rc;
     if (p->n_parts == 2) return api_need(b, name2);
     return b ? api_fail(MOE_ERR_INVALID_ARG, "%s is given, but n_parts is 1", name2) : MOE_OK;
-}
-
-int launched(cudaError_t e, const char* what) {
-    return e == cudaSuccess ? MOE_OK : api_fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
 template <typename Kern, typename A>

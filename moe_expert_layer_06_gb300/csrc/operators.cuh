@@ -1,4 +1,4 @@
-// What the operators around the layer (scored_route.cu, adapter.cu) share.
+// What the operators around the layer (scored_route.cu, adapter.cu, expert_project.cu, checkpoint.cu) share.
 #pragma once
 
 #include "kernels.h"
@@ -259,5 +259,8 @@ int api_router_gemm(const moe_shape_t* shape, int T, const void* x, const void* 
                     int* ksplit, cudaStream_t stream);
 // Pointer checks: 0, or the error code with its text set.
 int api_need(const void* p, const char* name, unsigned align = 16);
+inline int launched(cudaError_t e, const char* what) {
+    return e == cudaSuccess ? MOE_OK : api_fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
 
 }  // namespace moe
