@@ -168,7 +168,7 @@ struct RowsArgs {
     void* out_ptr;
     int R, K, N, P, S, type;
     int cap, stages;   // rows of a chunk at most (64, 128, 256); stages of the ring that then fit
-    int splits;        // pairs of a cluster, which share a tile's contraction; above 1, pairs for every tile
+    int splits;        // pairs of a cluster, which share a tile's contraction (1, 2, 4); above 1, pairs for every tile
     DevStatus st;
 };
 constexpr int kMostStages = 9;
@@ -357,9 +357,10 @@ __device__ __forceinline__ void rows_pair(const RowsArgs& a, const int pair, con
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    const int n_tiles = pre[a.S], splits = n_tiles <= pairs / a.splits ? a.splits : 1;
-    const int first = pair / splits, step = splits > 1 ? max(1, n_tiles) : pairs;
-    const int share = (place >> 1) % splits, c0 = kc * share / splits, c1 = kc * (share + 1) / splits;  // of the contraction
+    // (1, 2 or 4: without divisions, which cost a call of few tiles 0.3 us here)
+    const int n_tiles = pre[a.S], splits = n_tiles <= pairs >> (a.splits >> 1) ? a.splits : 1, bits = splits >> 1;
+    const int first = pair >> bits, step = splits > 1 ? max(1, n_tiles) : pairs;
+    const int share = (place >> 1) & (splits - 1), c0 = kc * share >> bits, c1 = kc * (share + 1) >> bits;  // of the contraction
     RowsTile t = {};
     if (first < n_tiles) t = rows_tile<DX>(a, pre, start, first);
     auto next_tile = [&](int i) {
