@@ -51,18 +51,6 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
     return v;
 }
 
-// 16 bytes of this CTA's shared memory to another CTA's, which a barrier there hears of: a signal that
-// nobody waits for here.  The copy itself orders its own 16 bytes and nothing that the thread stored before.
-// What the signal says rests on the proxy fence: rows are stored, each lane ends its stores by
-// fence.proxy.async.shared::cta, __syncwarp has seen every lane past its fence, and only then is the copy issued; the
-// rows are read by the tensor cores through that proxy alone, from the shared memory of the CTA that stored
-// them, never by the threads of the CTA that hears of it.
-__device__ __forceinline__ void signal_by_copy(uint32_t dst, uint32_t src, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst), "r"(src),
-                 "r"(bar)
-                 : "memory");
-}
-
 // 16 lanes x 64 columns: as tmem_ld_16x256, i up to 7
 __device__ __forceinline__ void tmem_ld_16x256_64(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -97,6 +85,37 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 // 1600 to 3400 cycles of a tile of dW that takes 5500 with it.)
 __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// An arrival that releases what was written to this CTA's shared memory, and a wait for such arrivals: fences
+// at cluster scope that are restricted to shared memory, and so wait for no store to global memory.  (A full
+// release holds a thread for 1400 to 2000 cycles: one for each chunk, and codes took 3087 us of 4096 tokens, 8
+// experts each, gate and up, where rows in bf16 took 1170; handed on by one warp of the CTA, 1376 against 1127 us.)
+__device__ __forceinline__ void mbar_arrive_shared_cluster(uint32_t bar) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    mbar_arrive_relaxed_cluster(bar);
+}
+__device__ __forceinline__ bool mbar_try_wait_relaxed_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait_shared_cluster(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
+                                                         unsigned long long limit) {
+    bool ok = mbar_try_wait_relaxed_cluster(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!ok && !*abort_flag && globaltimer_ns() - t0 <= limit) ok = mbar_try_wait_relaxed_cluster(bar, parity);
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+    return ok;
 }
 
 // Four outputs of a sum that pairs shared.
@@ -595,8 +614,6 @@ constexpr int kWeightOut = kDrainWarps * 4096;  // a block of 32 x 128 bytes of 
 constexpr int work_groups(bool x8, bool m2) { return !x8 ? 1 : m2 ? 2 : 3; }
 constexpr int weight_threads(bool x8, bool m2) { return 64 + 32 * kWork * work_groups(x8, m2) + 32 * kDrainWarps; }
 constexpr int kWeightSmem = 1024 + kRing + kWeightOut + 512;
-constexpr int kSignals = 384;  // of those 512 bytes: 16 for each stage, and 16 to send
-static_assert(kSignals + 16 * (WeightRing<false>::kStages + 1) <= 512, "signals");
 static_assert(kWeightSmem <= 227 * 1024, "shared memory overflow");
 
 struct WeightTile {
@@ -657,7 +674,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
     uint64_t* done = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((4 * kStages + 5) * 8 + 8 <= kSignals, "barriers");
+    static_assert((4 * kStages + 5) * 8 + 8 <= 512, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned long long limit = a.st.limit_ns;
@@ -672,7 +689,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
             mbar_init(smem_u32(&landed[s]), 1);
-            mbar_init(smem_u32(&ready[s]), kWork + 1);  // the leader's workers and its wait for the others' copies
+            mbar_init(smem_u32(&ready[s]), 2 * kWork);  // the workers of both
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&tfull[s]), 1);
@@ -730,7 +747,6 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
                     const uint32_t fb = lead_full + stage * 8, lb = landed_u + stage * 8;
                     const uint32_t dy_bytes = (t.two ? 2 : 1) * n16 * 4096, x_bytes = X8 ? n16 * 2048 : n16 * 4096;
                     if (!work && rank == 0) mbar_arrive_expect_tx(full_u + stage * 8, 2 * (dy_bytes + x_bytes));
-                    if (work && rank == 0) mbar_arrive_expect_tx(ready_u + stage * 8, kWork * 16);
                     if (work) mbar_arrive_expect_tx(lb, dy_bytes + x_bytes);
                     for (int bit = 2, off = 0; bit >= 0; --bit)
                         if (n16 & (1 << bit)) {
@@ -780,8 +796,8 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
         if (!ok && lane == 0) give_up();
     } else if (warp == 1) {
         // What it waits for is read by the tensor cores alone, each CTA's half in its own shared
-        // memory: the waits do not acquire for the cluster (100 to 200 ns each; three of them held the
-        // products of codes up).
+        // memory.  Rows that threads stored are acquired from both CTAs, by fences restricted to shared memory;
+        // the waits for copies alone do not acquire for the cluster (100 to 200 ns each where unrestricted).
         bool ok = true;
         int stage = 0, at = 0, u = 0;
         uint32_t full_phase = 0, work_phase = 0;  // (of each stage: not every chunk uses both)
@@ -796,7 +812,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
                         // one wait a chunk: two or three of 180 cycles each held up the products of codes
                         bool got;
                         if (X8 || (min(64, t.r1 - t.r0 - c * 64) & 15)) {
-                            got = warp_wait(ready_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit);
+                            got = warp_wait_shared_cluster(ready_u + at * 8, (work_phase >> at) & 1u, abort_flag, limit);
                             work_phase ^= 1u << at;
                         } else {
                             got = warp_wait(full_u + at * 8, (full_phase >> at) & 1u, abort_flag, limit);
@@ -847,10 +863,6 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
         complete = mbar_wait(smem_u32(done), 0, limit);
     } else if (warp < 2 + kWork * kGroups) {
         const int group = (warp - 2) / kWork, sub = (warp - 2) % kWork;
-        // The leader hears of the other CTA's rows by copies.  (An arrival there holds its thread for
-        // 1400 to 2000 cycles, until its release is seen by the cluster: one for each chunk, and codes
-        // took 3087 us of 4096 tokens, 8 experts each, gate and up, where rows in bf16 took 1170.)
-        const uint32_t signals = smem_u32(full) + kSignals, lead_signals = leader_addr(signals, lead);
         bool ok = true;
         int stage = 0, turn = 0;  // of the chunks that need work
         uint32_t land_phase = 0;
@@ -917,7 +929,7 @@ __device__ __forceinline__ void weights_pair(const WeightArgs& a, const int pair
                     __syncwarp();
                     if (lane == 0) {
                         if (rank == 0) mbar_arrive(ready_u + stage * 8);
-                        else signal_by_copy(lead_signals + stage * 16, signals + kStages * 16, lead_ready + stage * 8);
+                        else mbar_arrive_shared_cluster(lead_ready + stage * 8);
                     }
                     __syncwarp();
                 }
